@@ -12,6 +12,9 @@ _EXPORTS = (
     "grouped_fp8_contiguous", "grouped_fp8_masked", "check_status",
     "mk_alignment_for_contiguous", "sfa_bytes", "sfb_bytes", "sfa_shape", "sfb_shape",
     "set_wait_timeout_ms", "set_pdl", "selftest_wait_timeout", "last_error", "last_tile", "version", "FGF8Error", "SCALE_F32", "SCALE_UE8M0",
+    "quantize_fp4", "gemm_fp4_blockscaled", "fp4_sf_shape", "FP4_MX", "FP4_NV",
+    "gated_f16", "gated_f16_backward", "gated_backward_ws_bytes", "gemv_fp4", "gated_gemv_fp4", "GEMV_MAX_ROWS",
+    "ACT_SILU", "ACT_GELU_TANH",
 )
 
 

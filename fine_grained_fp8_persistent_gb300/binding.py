@@ -22,6 +22,9 @@ FP4_MX = 0     # MXFP4: E2M1 + E8M0 scale per 32 elements along K
 FP4_NV = 1     # NVFP4: E2M1 + E4M3 scale per 16 elements along K
 F16 = 0
 BF16 = 1
+ACT_SILU = 0
+ACT_GELU_TANH = 1
+GEMV_MAX_ROWS = 16   # rows of X that the 4-bit matrix-vector operators take
 
 OK = 0
 ERR_DEVICE_TIMEOUT = 5
@@ -54,6 +57,11 @@ _SIGS = {
     "grouped_fp8_masked": ([_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P], _I),
     "quantize_fp4": ([_P, _P, _P, _I, _I, _I, _P], _I),
     "gemm_fp4_blockscaled": ([_P, _P, _P, _P, _P, _I, _I, _I, _I, _P], _I),
+    "gated_f16": ([_P] * 6 + [_I] * 5 + [_P], _I),
+    "gated_f16_backward": ([_P] * 10 + [_I] * 5 + [_P], _I),
+    "gemv_fp4": ([_P] * 4 + [_I] * 5 + [_P], _I),
+    "gated_gemv_fp4": ([_P] * 6 + [_I] * 6 + [_P], _I),
+    "fgf8_gated_backward_ws_bytes": ([_I, _I], _LL),
     "fgf8_fp4_sf_bytes": ([_I, _I, _I], _LL),
     "fgf8_mk_alignment_for_contiguous": ([], _I),
     "fgf8_sfa_bytes": ([_I, _I, _I], _LL),
@@ -369,6 +377,138 @@ def gemm_fp4_blockscaled(aq, sfa, bq, sfb, fmt, out: torch.Tensor | None = None,
     _need_out(out, (M, N), (torch.bfloat16,), "out")
     st = _stream(stream, aq=aq, sfa=sfa, bq=bq, sfb=sfb, out=out)
     _call("gemm_fp4_blockscaled", st, _ptr(aq), _ptr(sfa), _ptr(bq), _ptr(sfb), _ptr(out), M, N, K, _fp4(fmt))
+    return out
+
+
+# --------------------------------------------------------------------------- gated block, matrix-vector
+def _act(act) -> int:
+    if isinstance(act, str):
+        return {"silu": ACT_SILU, "gelu_tanh": ACT_GELU_TANH}[act.lower()]
+    return int(act)
+
+
+def _dtype16(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"{name} must be fp16 or bf16")
+    return BF16 if t.dtype == torch.bfloat16 else F16
+
+
+def _need_like(t: torch.Tensor, shape: tuple, dtype: torch.dtype, name: str) -> None:
+    """A 16-bit operand: exactly this shape and type."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _empty(shape: tuple, like: torch.Tensor, stream, dtype: torch.dtype | None = None) -> torch.Tensor:
+    """torch.empty on `like`'s device, from the memory pool of the stream the call
+    runs on: memory that is given back while the kernel still runs must not be
+    handed to work on another stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
+
+
+def gated_f16(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, act="silu", save: bool = False,
+              out: torch.Tensor | None = None, g: torch.Tensor | None = None, u: torch.Tensor | None = None,
+              stream=None):
+    """H = act(X Wg^T) * (X Wu^T) for fp16/bf16 X (M, K), Wg and Wu (N, K), in one kernel.
+    act: "silu" or "gelu_tanh".  With save (or g and u given) also returns the projections
+    G and U in the same type, which gated_f16_backward reads: (h, g, u)."""
+    M, K = x.shape
+    N = wg.shape[0]
+    dt = _dtype16(x, "x")
+    _need_like(wg, (N, K), x.dtype, "wg")
+    _need_like(wu, (N, K), x.dtype, "wu")
+    if (g is None) != (u is None):
+        raise ValueError("g and u: give both or neither")
+    if out is None:
+        out = _empty((M, N), x, stream)
+    if save and g is None:
+        g, u = _empty((M, N), x, stream), _empty((M, N), x, stream)
+    _need_out(out, (M, N), (x.dtype,), "out")
+    if g is not None:
+        _need_out(g, (M, N), (x.dtype,), "g")
+        _need_out(u, (M, N), (x.dtype,), "u")
+    st = _stream(stream, x=x, wg=wg, wu=wu, out=out, g=g, u=u)
+    _call("gated_f16", st, _ptr(x), _ptr(wg), _ptr(wu), _ptr(out), _ptr(g), _ptr(u), M, N, K, dt, _act(act))
+    return out if g is None else (out, g, u)
+
+
+def gated_f16_backward(dh: torch.Tensor, x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, g: torch.Tensor,
+                       u: torch.Tensor, act="silu", dx: torch.Tensor | None = None,
+                       dwg: torch.Tensor | None = None, dwu: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, stream=None):
+    """Gradients (dX, dWg, dWu) of gated_f16 from dH (M, N) and the G, U it kept.
+    `workspace` (uint8, gated_backward_ws_bytes(M, N) bytes) is taken from torch when not given."""
+    M, K = x.shape
+    N = wg.shape[0]
+    dt = _dtype16(x, "x")
+    _need_like(wg, (N, K), x.dtype, "wg")
+    _need_like(wu, (N, K), x.dtype, "wu")
+    for name, t in (("dh", dh), ("g", g), ("u", u)):
+        _need_like(t, (M, N), x.dtype, name)
+    if dx is None:
+        dx = _empty((M, K), x, stream)
+    if dwg is None:
+        dwg = _empty((N, K), x, stream)
+    if dwu is None:
+        dwu = _empty((N, K), x, stream)
+    _need_out(dx, (M, K), (x.dtype,), "dx")
+    _need_out(dwg, (N, K), (x.dtype,), "dwg")
+    _need_out(dwu, (N, K), (x.dtype,), "dwu")
+    ws_bytes = gated_backward_ws_bytes(M, N)
+    if workspace is None:
+        workspace = _empty((max(ws_bytes, 0),), x, stream, torch.uint8)
+    if workspace.numel() * workspace.element_size() < ws_bytes:
+        raise ValueError(f"workspace: expected {ws_bytes} bytes, got {workspace.numel() * workspace.element_size()}")
+    st = _stream(stream, dh=dh, x=x, wg=wg, wu=wu, g=g, u=u, dx=dx, dwg=dwg, dwu=dwu, workspace=workspace)
+    _call("gated_f16_backward", st, _ptr(dh), _ptr(x), _ptr(wg), _ptr(wu), _ptr(g), _ptr(u), _ptr(dx), _ptr(dwg),
+          _ptr(dwu), _ptr(workspace), M, N, K, dt, _act(act))
+    return dx, dwg, dwu
+
+
+def gated_backward_ws_bytes(M: int, N: int) -> int:
+    """Bytes of the gated_f16_backward workspace (dG and dU)."""
+    return int(_lib.fgf8_gated_backward_ws_bytes(int(M), int(N)))
+
+
+def _need_fp4(wq: torch.Tensor, sf: torch.Tensor, N: int, K: int, fmt, names: tuple) -> None:
+    _need(wq, N * (K // 2), 1, names[0])
+    _need(sf, _numel(fp4_sf_shape(N, K, fmt)[0]), 4, names[1])
+
+
+def gemv_fp4(x: torch.Tensor, wq: torch.Tensor, sf: torch.Tensor, fmt, out: torch.Tensor | None = None,
+             stream=None) -> torch.Tensor:
+    """Y = X W^T for at most GEMV_MAX_ROWS rows of fp16/bf16 X (M, K) and MXFP4 or NVFP4
+    weights (N, K) as quantize_fp4 writes them; Y has the type of X."""
+    M, K = x.shape
+    N = wq.shape[0]
+    dt = _dtype16(x, "x")
+    _need_fp4(wq, sf, N, K, fmt, ("wq", "sf"))
+    if out is None:
+        out = _empty((M, N), x, stream)
+    _need_out(out, (M, N), (x.dtype,), "out")
+    st = _stream(stream, x=x, wq=wq, sf=sf, out=out)
+    _call("gemv_fp4", st, _ptr(x), _ptr(wq), _ptr(sf), _ptr(out), M, N, K, _fp4(fmt), dt)
+    return out
+
+
+def gated_gemv_fp4(x: torch.Tensor, wgq: torch.Tensor, sfg: torch.Tensor, wuq: torch.Tensor, sfu: torch.Tensor, fmt,
+                   act="silu", out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """H = act(X Wg^T) * (X Wu^T) for at most GEMV_MAX_ROWS rows of fp16/bf16 X (M, K) and
+    MXFP4 or NVFP4 weights (N, K) as quantize_fp4 writes them, in one kernel."""
+    M, K = x.shape
+    N = wgq.shape[0]
+    dt = _dtype16(x, "x")
+    _need_fp4(wgq, sfg, N, K, fmt, ("wgq", "sfg"))
+    _need_fp4(wuq, sfu, N, K, fmt, ("wuq", "sfu"))
+    if out is None:
+        out = _empty((M, N), x, stream)
+    _need_out(out, (M, N), (x.dtype,), "out")
+    st = _stream(stream, x=x, wgq=wgq, sfg=sfg, wuq=wuq, sfu=sfu, out=out)
+    _call("gated_gemv_fp4", st, _ptr(x), _ptr(wgq), _ptr(sfg), _ptr(wuq), _ptr(sfu), _ptr(out), M, N, K, _fp4(fmt),
+          dt, _act(act))
     return out
 
 

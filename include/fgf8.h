@@ -82,6 +82,11 @@ typedef enum { FGF8_SCALE_F32 = 0, FGF8_SCALE_UE8M0 = 1 } fgf8_scale_fmt;
 /* 4-bit block-scaled formats ([TC5] section 6.3): E2M1 elements with an E8M0
  * scale per 32 elements along K (MXFP4) or an E4M3 scale per 16 (NVFP4). */
 typedef enum { FGF8_FP4_MX = 0, FGF8_FP4_NV = 1 } fgf8_fp4_fmt;
+/* Activations of the gated operators:
+ *   SILU      : a(g) = g * sigma(g),  sigma(g) = 1 / (1 + exp(-g))
+ *   GELU_TANH : a(g) = g/2 * (1 + tanh(z)) = g * sigma(2 z),
+ *               z = sqrt(2/pi) * (g + 0.044715 g^3) */
+typedef enum { FGF8_ACT_SILU = 0, FGF8_ACT_GELU_TANH = 1 } fgf8_act;
 
 /*
  * quantize_1x128 -- activation quantization, 1x128 groups ([DG] "fine-grained
@@ -212,6 +217,60 @@ FGF8_API int quantize_fp4(const void* X, void* Xq, void* SF, int R, int K, int f
  */
 FGF8_API int gemm_fp4_blockscaled(const void* Aq, const void* SFA, const void* Bq, const void* SFB,
                                   void* D, int M, int N, int K, int fmt, void* stream);
+
+/*
+ * gated_f16 -- the gated half of a feed-forward block in one kernel:
+ *   G = X Wg^T,  U = X Wu^T,  H = a(G) * U   (element by element)
+ * FP32 accumulation; the activation and the product are taken on the FP32
+ * accumulators and H is rounded once, to nearest even.
+ *   X  : [M][K] tokens;  Wg, Wu : [N][K] gate and up weights;  H : [M][N]
+ *   G, U : [M][N] (outputs, both or neither may be NULL): the projections rounded
+ *          to the same type, which gated_f16_backward reads
+ * All of one type, fp16 or bf16 (dtype, an fgf8_dtype); act is an fgf8_act.
+ * Requires K % 8 == 0, N % 8 == 0, M >= 0, N, K >= 1.
+ */
+FGF8_API int gated_f16(const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U, int M, int N,
+                       int K, int dtype, int act, void* stream);
+
+/*
+ * gated_f16_backward -- gradients of gated_f16 from dH and the kept G, U:
+ *   dG = dH * U * a'(G),  dU = dH * a(G)
+ *   dX = dG Wg + dU Wu,   dWg = dG^T X,   dWu = dU^T X
+ * dG and dU are computed in FP32 and rounded to the operands' type, the type the
+ * tensor cores read; the three products accumulate in FP32 and round once.
+ *   dH, G, U : [M][N];  X, dX : [M][K];  Wg, Wu, dWg, dWu : [N][K]
+ *   workspace : fgf8_gated_backward_ws_bytes(M, N) bytes of device memory, holding
+ *               dG and dU for the length of the call
+ * M == 0 writes zeros to dWg and dWu.  Requires what gated_f16 requires.
+ */
+FGF8_API int gated_f16_backward(const void* dH, const void* X, const void* Wg, const void* Wu, const void* G,
+                                const void* U, void* dX, void* dWg, void* dWu, void* workspace, int M, int N,
+                                int K, int dtype, int act, void* stream);
+
+/* Bytes of the gated_f16_backward workspace; -1 on invalid arguments. */
+FGF8_API long long fgf8_gated_backward_ws_bytes(int M, int N);
+
+/*
+ * gemv_fp4 -- Y = X W^T for a few rows of X and a 4-bit weight matrix in the
+ * layouts of quantize_fp4 (group scales along K): the form of a linear layer that
+ * generates one token per sequence, whose time is the reading of W.
+ *   X  : fp16 or bf16 [M][K] (dtype);  Wq : uint8 [N][K/2];  SF : scale table of N rows
+ *   Y  : [M][N], the type of X, rounded to nearest even from FP32 sums
+ * X is not quantized.  Requires K % 64 == 0, N, K >= 1, 0 <= M <= 16 (more rows
+ * return FGF8_ERR_UNSUPPORTED: quantize_fp4 X and call gemm_fp4_blockscaled).
+ */
+FGF8_API int gemv_fp4(const void* X, const void* Wq, const void* SF, void* Y, int M, int N, int K, int fmt,
+                      int dtype, void* stream);
+
+/*
+ * gated_gemv_fp4 -- the gated block of gated_f16 for a few rows of X and 4-bit
+ * weights, in one kernel: H = a(X Wg^T) * (X Wu^T).
+ *   X : fp16 or bf16 [M][K];  WgQ, WuQ : uint8 [N][K/2];  SFg, SFu : scale tables of N rows
+ *   H : [M][N], the type of X, rounded once from FP32
+ * Both weights in the same format.  Requires what gemv_fp4 requires.
+ */
+FGF8_API int gated_gemv_fp4(const void* X, const void* WgQ, const void* SFg, const void* WuQ, const void* SFu,
+                            void* H, int M, int N, int K, int fmt, int dtype, int act, void* stream);
 
 /* Bytes of a quantize_fp4 scale table for R rows; -1 on invalid arguments. */
 FGF8_API long long fgf8_fp4_sf_bytes(int R, int K, int fmt);
