@@ -1,138 +1,229 @@
 // gated_f16.cu -- the gated feed-forward block in 16-bit types and its backward pass.
 //
-// Forward:   G = X Wg^T, U = X Wu^T, H = a(G) * U.
-// Backward:  dG = dH * U * a'(G), dU = dH * a(G); dX = dG Wg + dU Wu,
-//            dWg = dG^T X, dWu = dU^T X.
+// Forward:   G = X Wg^T, U = X Wu^T, H = a(G) * U, one launch.
+// Backward:  dG = dH * U * a'(G), dU = dH * a(G) element by element, then
+//            dX = dG Wg + dU Wu and dWg = dG^T X, dWu = dU^T X: three launches.
+// The products are gated_gemm.cuh's; this file holds the elementwise kernel, the tensor
+// maps, the choice of tile and the launches.
+#include <cstdio>
+#include <cstdlib>
 #include <cstring>
 
 #include "activation.cuh"
 #include "gated.h"
+#include "gated_gemm.cuh"
 
 namespace fgf8 {
 namespace {
 
-// A strided view of a 16-bit matrix: element (i, k) at base[i * si + k * sk].
-struct View {
-  const uint16_t* p;
-  long long si, sk;
-  __device__ __forceinline__ float at(int i, int k, int ni, int nk, bool bf16) const {
-    return i < ni && k < nk ? act::to_float(p[i * si + k * sk], bf16) : 0.0f;
-  }
-};
-
-constexpr int kTile = 64, kDepth = 16;
-
-// One 64 x 64 tile per CTA of 256 threads, 4 x 4 outputs per thread and accumulator.
-// GATED: acc[0] = A B0^T, acc[1] = A B1^T, out = a(acc[0]) * acc[1]; else
-// out = A0 B0^T + A1 B1^T (the second product only when nk1 > 0).
-template <bool GATED>
-__global__ void __launch_bounds__(256) tile_kernel(View a0, View b0, View a1, View b1, int M, int N, int K, int terms,
-                                                   uint16_t* out, uint16_t* g, uint16_t* u, bool bf16, int act_code) {
-  __shared__ float sa[kDepth][kTile + 1], sb[2][kDepth][kTile + 1];
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  const int m0 = blockIdx.y * kTile, n0 = blockIdx.x * kTile;
-  float acc[2][4][4] = {};
-  for (int term = 0; term < (GATED ? 1 : terms); ++term) {
-    const View a = term ? a1 : a0, b = term ? b1 : b0;
-    for (int k0 = 0; k0 < K; k0 += kDepth) {
-      for (int i = threadIdx.x; i < kTile * kDepth; i += 256) {
-        const int r = i / kDepth, k = i % kDepth;
-        sa[k][r] = a.at(m0 + r, k0 + k, M, K, bf16);
-        sb[0][k][r] = b.at(n0 + r, k0 + k, N, K, bf16);
-        if (GATED) sb[1][k][r] = b1.at(n0 + r, k0 + k, N, K, bf16);
-      }
-      __syncthreads();
-      for (int k = 0; k < kDepth; ++k)
-        for (int i = 0; i < 4; ++i)
-          for (int j = 0; j < 4; ++j) {
-            acc[0][i][j] = fmaf(sa[k][ty + 16 * i], sb[0][k][tx + 16 * j], acc[0][i][j]);
-            if (GATED) acc[1][i][j] = fmaf(sa[k][ty + 16 * i], sb[1][k][tx + 16 * j], acc[1][i][j]);
-          }
-      __syncthreads();
-    }
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m >= M || n >= N) continue;
-      const size_t at = static_cast<size_t>(m) * N + n;
-      float v = acc[0][i][j];
-      if (GATED) {
-        if (g != nullptr) {
-          g[at] = act::from_float(v, bf16);
-          u[at] = act::from_float(acc[1][i][j], bf16);
-        }
-        v = (act_code == act::kSilu ? act::value<act::kSilu>(v) : act::value<act::kGeluTanh>(v)) * acc[1][i][j];
-      }
-      out[at] = act::from_float(v, bf16);
-    }
-}
-
 // dG, dU from dH, G, U.  Eight elements (16 bytes) per thread; n8 = M * N / 8.
-template <int ACT>
+template <int ACT, bool BF16>
 __global__ void __launch_bounds__(256) slope_kernel(const uint4* __restrict__ dh, const uint4* __restrict__ g,
                                                     const uint4* __restrict__ u, uint4* __restrict__ dg,
-                                                    uint4* __restrict__ du, long long n8, bool bf16) {
+                                                    uint4* __restrict__ du, long long n8) {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
   for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n8; i += gridDim.x * 256LL) {
     const uint4 a = dh[i], b = g[i], c = u[i];
     const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w}, cw[4] = {c.x, c.y, c.z, c.w};
     uint32_t gw[4], uw[4];
+#pragma unroll
     for (int j = 0; j < 4; ++j) {
-      uint32_t go = 0, uo = 0;
+      float dgv[2], duv[2];
+#pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float d = act::to_float(aw[j] >> (16 * h) & 0xFFFFu, bf16);
+        const float d = act::to_float((aw[j] >> (16 * h)) & 0xFFFFu, BF16);
         float v, s;
-        act::value_slope<ACT>(act::to_float(bw[j] >> (16 * h) & 0xFFFFu, bf16), v, s);
-        go |= static_cast<uint32_t>(act::from_float(d * act::to_float(cw[j] >> (16 * h) & 0xFFFFu, bf16) * s, bf16)) << (16 * h);
-        uo |= static_cast<uint32_t>(act::from_float(d * v, bf16)) << (16 * h);
+        act::value_slope<ACT>(act::to_float((bw[j] >> (16 * h)) & 0xFFFFu, BF16), v, s);
+        dgv[h] = d * act::to_float((cw[j] >> (16 * h)) & 0xFFFFu, BF16) * s;
+        duv[h] = d * v;
       }
-      gw[j] = go;
-      uw[j] = uo;
+      gw[j] = pack_2x16(dgv[0], dgv[1], BF16);
+      uw[j] = pack_2x16(duv[0], duv[1], BF16);
     }
     dg[i] = make_uint4(gw[0], gw[1], gw[2], gw[3]);
     du[i] = make_uint4(uw[0], uw[1], uw[2], uw[3]);
   }
 }
 
-int check_launch(const char* who) {
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? 0 : set_error(4, "%s launch: %s", who, cudaGetErrorString(e));
+// ----------------------------------------------------------------- launches
+// Launch configuration with a cluster of `cluster` CTAs and, when enabled,
+// programmatic stream serialization.
+struct Launch {
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  Launch(unsigned grid, unsigned threads, size_t smem, int cluster, cudaStream_t stream) {
+    std::memset(&cfg, 0, sizeof(cfg));
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  }
+};
+
+template <GatedOp OP, int ACT, int NCTA, int BN, int STAGES>
+int launch_gemm(const GatedMaps& tm, const GatedGemmArgs& args, cudaStream_t stream) {
+  using C = GatedCfg<OP, NCTA, BN, STAGES>;
+  static_assert(C::SMEM_BYTES <= 232448, "shared memory budget");
+  auto* fn = &gated_gemm<OP, ACT, NCTA, BN, STAGES>;
+  static int max_clusters[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return set_error(2, "device id %d", dev);
+  if (max_clusters[dev] == 0) {
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    int clusters = device_sm_count();
+    if (e == cudaSuccess && NCTA > 1) {
+      Launch probe(static_cast<unsigned>(device_sm_count() / NCTA * NCTA), C::THREADS, C::SMEM_BYTES, NCTA, stream);
+      probe.cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&clusters, fn, &probe.cfg);
+    }
+    if (e != cudaSuccess || clusters <= 0) return set_error(4, "gated_f16 occupancy: %s", cudaGetErrorString(e));
+    max_clusters[dev] = clusters;
+  }
+  const long long num_m = static_cast<long long>((args.rows + C::TILE_M - 1) / C::TILE_M) * (OP == GatedOp::GradW ? 2 : 1);
+  const long long tiles = num_m * ((args.cols + C::OUT_N - 1) / C::OUT_N);
+  if (tiles > 0x7F000000LL) return set_error(2, "gated_f16: problem too large");
+  const long long clusters = persistent_clusters(tiles, NCTA, device_sm_count(), max_clusters[dev], sm_cap_enabled());
+  set_last_tile("f16", OP == GatedOp::Forward ? "gated" : OP == GatedOp::GradX ? "grad_x" : "grad_w", NCTA, BN);
+  Launch l(static_cast<unsigned>(clusters * NCTA), C::THREADS, C::SMEM_BYTES, NCTA, stream);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, fn, tm, args);
+  return e == cudaSuccess ? 0 : set_error(4, "gated_f16 launch: %s", cudaGetErrorString(e));
 }
 
-dim3 tiles(int M, int N) { return dim3((N + kTile - 1) / kTile, (M + kTile - 1) / kTile); }
-const uint16_t* u16(const void* p) { return static_cast<const uint16_t*>(p); }
+// A map of a row-major 16-bit matrix: K-major operand boxes of 64 columns x box_rows,
+// or MN-major boxes of 64 x 64, both 128 bytes wide and swizzled.
+bool operand_map(CUtensorMap* m, const GatedArgs& a, const void* p, long long rows, long long cols, int box_rows) {
+  return encode_tmap_2d(m, a.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p, cols, rows, cols * 2, 64,
+                        box_rows, true);
+}
+bool output_map(CUtensorMap* m, const void* p, long long rows, long long cols, int box_cols) {
+  return encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, p, cols, rows, cols * 2, box_cols, 32, false);
+}
+
+int gemm_args(GatedGemmArgs& g, const GatedArgs& a, int rows, int cols, int reduce) {
+  std::memset(&g, 0, sizeof(g));
+  g.rows = rows;
+  g.cols = cols;
+  g.nkb = (reduce + 63) / 64;
+  g.a_box_rows = rows >= 128 ? 128 : (rows + 7) / 8 * 8;
+  g.bf16 = a.bf16;
+  g.act = a.act;
+  g.status = device_status_ptr();
+  g.timeout_ns = wait_timeout_ns();
+  return g.status ? 0 : 4;
+}
+
+// One tile configuration and its relative time per K block and tile.
+struct Choice {
+  int ncta, bn;
+  double t_kb;
+};
+int pick(const Choice* c, int n, long long rows, long long cols_of_bn, int mats, int divide) {
+  // FGF8_FORCE_TILE="<ctas per cluster>x<bn>" selects that tile when it is among the candidates
+  if (const char* f = std::getenv("FGF8_FORCE_TILE")) {
+    int nc = 0, bn = 0;
+    if (std::sscanf(f, "%dx%d", &nc, &bn) == 2)
+      for (int i = 0; i < n; ++i)
+        if (c[i].ncta == nc && c[i].bn == bn) return i;
+  }
+  int best = 0;
+  double cost = -1.0;
+  for (int i = 0; i < n; ++i) {
+    const long long tm = 128LL * c[i].ncta, tn = c[i].bn / divide;
+    const long long tiles = mats * ((rows + tm - 1) / tm) * ((cols_of_bn + tn - 1) / tn);
+    const long long units = device_sm_count() / c[i].ncta;
+    const double t = static_cast<double>((tiles + units - 1) / units) * c[i].t_kb;
+    if (cost < 0 || t < cost) {
+      cost = t;
+      best = i;
+    }
+  }
+  return best;
+}
+
+template <int ACT>
+int forward(const GatedArgs& a, const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U, cudaStream_t stream) {
+  static const Choice c[] = {{2, 256, 2.0}, {1, 128, 1.2}, {1, 64, 0.9}, {1, 32, 0.7}};
+  const Choice& ch = c[pick(c, 4, a.M, a.N, 1, 2)];
+  GatedGemmArgs g;
+  if (gemm_args(g, a, a.M, a.N, a.K)) return 4;
+  g.save = G != nullptr;
+  GatedMaps tm;
+  std::memset(&tm, 0, sizeof(tm));
+  const int half = ch.bn / 2, cw = half < 32 ? half : 32;
+  if (!operand_map(&tm.a[0], a, X, a.M, a.K, g.a_box_rows) || !operand_map(&tm.b[0], a, Wg, a.N, a.K, half) ||
+      !operand_map(&tm.b[1], a, Wu, a.N, a.K, half) || !output_map(&tm.d[0], H, a.M, a.N, cw))
+    return 4;
+  if (g.save && (!output_map(&tm.d[1], G, a.M, a.N, cw) || !output_map(&tm.d[2], U, a.M, a.N, cw))) return 4;
+  if (ch.ncta == 2) return launch_gemm<GatedOp::Forward, ACT, 2, 256, 6>(tm, g, stream);
+  if (ch.bn == 128) return launch_gemm<GatedOp::Forward, ACT, 1, 128, 6>(tm, g, stream);
+  if (ch.bn == 64) return launch_gemm<GatedOp::Forward, ACT, 1, 64, 8>(tm, g, stream);
+  return launch_gemm<GatedOp::Forward, ACT, 1, 32, 10>(tm, g, stream);
+}
+
+int grad_x(const GatedArgs& a, const void* dG, const void* dU, const void* Wg, const void* Wu, void* dX, cudaStream_t stream) {
+  static const Choice c[] = {{2, 256, 2.0}, {1, 128, 1.2}, {1, 64, 0.9}};
+  const Choice& ch = c[pick(c, 3, a.M, a.K, 1, 1)];
+  GatedGemmArgs g;
+  if (gemm_args(g, a, a.M, a.K, a.N)) return 4;
+  GatedMaps tm;
+  std::memset(&tm, 0, sizeof(tm));
+  if (!operand_map(&tm.a[0], a, dG, a.M, a.N, g.a_box_rows) || !operand_map(&tm.a[1], a, dU, a.M, a.N, g.a_box_rows) ||
+      !operand_map(&tm.b[0], a, Wg, a.N, a.K, 64) || !operand_map(&tm.b[1], a, Wu, a.N, a.K, 64) || !output_map(&tm.d[0], dX, a.M, a.K, 32))
+    return 4;
+  if (ch.ncta == 2) return launch_gemm<GatedOp::GradX, act::kSilu, 2, 256, 6>(tm, g, stream);
+  if (ch.bn == 128) return launch_gemm<GatedOp::GradX, act::kSilu, 1, 128, 6>(tm, g, stream);
+  return launch_gemm<GatedOp::GradX, act::kSilu, 1, 64, 8>(tm, g, stream);
+}
+
+int grad_w(const GatedArgs& a, const void* dG, const void* dU, const void* X, void* dWg, void* dWu, cudaStream_t stream) {
+  static const Choice c[] = {{2, 256, 2.0}, {1, 128, 1.2}};
+  const Choice& ch = c[pick(c, 2, a.N, a.K, 2, 1)];
+  GatedGemmArgs g;
+  if (gemm_args(g, a, a.N, a.K, a.M)) return 4;
+  GatedMaps tm;
+  std::memset(&tm, 0, sizeof(tm));
+  if (!operand_map(&tm.a[0], a, dG, a.M, a.N, 64) || !operand_map(&tm.a[1], a, dU, a.M, a.N, 64) || !operand_map(&tm.b[0], a, X, a.M, a.K, 64) ||
+      !output_map(&tm.d[0], dWg, a.N, a.K, 32) || !output_map(&tm.d[1], dWu, a.N, a.K, 32))
+    return 4;
+  if (ch.ncta == 2) return launch_gemm<GatedOp::GradW, act::kSilu, 2, 256, 6>(tm, g, stream);
+  return launch_gemm<GatedOp::GradW, act::kSilu, 1, 128, 6>(tm, g, stream);
+}
+
+template <int ACT>
+int slopes(const GatedArgs& a, const void* dH, const void* G, const void* U, void* dG, void* dU, cudaStream_t stream) {
+  const long long n8 = static_cast<long long>(a.M) * a.N / 8;
+  const long long want = (n8 + 255) / 256, cap = 8LL * device_sm_count();
+  Launch l(static_cast<unsigned>(want < cap ? want : cap), 256, 0, 1, stream);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, a.bf16 ? slope_kernel<ACT, true> : slope_kernel<ACT, false>, static_cast<const uint4*>(dH),
+                                           static_cast<const uint4*>(G), static_cast<const uint4*>(U), static_cast<uint4*>(dG),
+                                           static_cast<uint4*>(dU), n8);
+  return e == cudaSuccess ? 0 : set_error(4, "gated_f16_backward launch: %s", cudaGetErrorString(e));
+}
 
 }  // namespace
 
 int launch_gated_forward(const GatedArgs& a, const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U,
                          cudaStream_t stream) {
-  const View x{u16(X), a.K, 1}, wg{u16(Wg), a.K, 1}, wu{u16(Wu), a.K, 1};
-  tile_kernel<true><<<tiles(a.M, a.N), 256, 0, stream>>>(x, wg, x, wu, a.M, a.N, a.K, 1, static_cast<uint16_t*>(H),
-                                                         static_cast<uint16_t*>(G), static_cast<uint16_t*>(U), a.bf16 != 0, a.act);
-  return check_launch("gated_f16");
+  return a.act == act::kSilu ? forward<act::kSilu>(a, X, Wg, Wu, H, G, U, stream) : forward<act::kGeluTanh>(a, X, Wg, Wu, H, G, U, stream);
 }
 
 int launch_gated_backward(const GatedArgs& a, const void* dH, const void* X, const void* Wg, const void* Wu,
                           const void* G, const void* U, void* dX, void* dWg, void* dWu, void* dG, void* dU,
                           cudaStream_t stream) {
-  const long long n8 = static_cast<long long>(a.M) * a.N / 8;
-  const long long want = (n8 + 255) / 256, cap = 8LL * device_sm_count();
-  const int grid = static_cast<int>(want < cap ? want : cap);
-  auto* k = a.act == act::kSilu ? slope_kernel<act::kSilu> : slope_kernel<act::kGeluTanh>;
-  k<<<grid, 256, 0, stream>>>(static_cast<const uint4*>(dH), static_cast<const uint4*>(G), static_cast<const uint4*>(U),
-                              static_cast<uint4*>(dG), static_cast<uint4*>(dU), n8, a.bf16 != 0);
-  if (int r = check_launch("gated_f16_backward")) return r;
-  // dX[m][k] = sum_n dG[m][n] Wg[n][k] + dU[m][n] Wu[n][k]
-  const View dg{u16(dG), a.N, 1}, du{u16(dU), a.N, 1}, wgt{u16(Wg), 1, a.K}, wut{u16(Wu), 1, a.K};
-  tile_kernel<false><<<tiles(a.M, a.K), 256, 0, stream>>>(dg, wgt, du, wut, a.M, a.K, a.N, 2, static_cast<uint16_t*>(dX),
-                                                          nullptr, nullptr, a.bf16 != 0, a.act);
-  // dW[n][k] = sum_m dG[m][n] X[m][k]
-  const View xt{u16(X), 1, a.K}, dgt{u16(dG), 1, a.N}, dut{u16(dU), 1, a.N};
-  tile_kernel<false><<<tiles(a.N, a.K), 256, 0, stream>>>(dgt, xt, dgt, xt, a.N, a.K, a.M, 1, static_cast<uint16_t*>(dWg),
-                                                          nullptr, nullptr, a.bf16 != 0, a.act);
-  tile_kernel<false><<<tiles(a.N, a.K), 256, 0, stream>>>(dut, xt, dut, xt, a.N, a.K, a.M, 1, static_cast<uint16_t*>(dWu),
-                                                          nullptr, nullptr, a.bf16 != 0, a.act);
-  return check_launch("gated_f16_backward");
+  int r = a.act == act::kSilu ? slopes<act::kSilu>(a, dH, G, U, dG, dU, stream) : slopes<act::kGeluTanh>(a, dH, G, U, dG, dU, stream);
+  if (r == 0) r = grad_x(a, dG, dU, Wg, Wu, dX, stream);
+  if (r == 0) r = grad_w(a, dG, dU, X, dWg, dWu, stream);
+  return r;
 }
 
 }  // namespace fgf8
