@@ -7,8 +7,6 @@
 
 namespace {
 
-constexpr int kGemvMaxRows = 16;
-
 // Every tensor pointer is 16-byte aligned device (or managed) memory of the current
 // device, checked before anything is launched.
 int check_pointers(const char* who, std::initializer_list<const void*> ptrs) {
@@ -53,8 +51,8 @@ int check_gemv(const char* who, int M, int N, int K, int fmt, int dtype) {
   if (fmt != FGF8_FP4_MX && fmt != FGF8_FP4_NV) return fgf8::set_error(FGF8_ERR_INVALID_ARG, "%s: bad format %d", who, fmt);
   if (dtype != FGF8_F16 && dtype != FGF8_BF16) return fgf8::set_error(FGF8_ERR_INVALID_ARG, "%s: bad dtype %d", who, dtype);
   if (K % 64 != 0) return fgf8::set_error(FGF8_ERR_UNSUPPORTED, "%s: K=%d not a multiple of 64", who, K);
-  if (M > kGemvMaxRows)
-    return fgf8::set_error(FGF8_ERR_UNSUPPORTED, "%s: M=%d above %d rows", who, M, kGemvMaxRows);
+  if (M > fgf8::kGemvMaxRows)
+    return fgf8::set_error(FGF8_ERR_UNSUPPORTED, "%s: M=%d above %d rows", who, M, fgf8::kGemvMaxRows);
   return FGF8_OK;
 }
 

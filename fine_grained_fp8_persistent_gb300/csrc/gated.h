@@ -5,6 +5,8 @@
 
 namespace fgf8 {
 
+constexpr int kGemvMaxRows = 16;   // rows of X the matrix-vector kernels take
+
 // One gated_f16 / gated_f16_backward call: M tokens, N inner columns, K hidden size.
 struct GatedArgs {
   int M, N, K;
@@ -28,6 +30,9 @@ int launch_gated_forward(const GatedArgs& a, const void* X, const void* Wg, cons
                          cudaStream_t stream);
 int launch_gated_backward(const GatedArgs& a, const void* dH, const void* X, const void* Wg, const void* Wu,
                           const void* G, const void* U, void* dX, void* dWg, void* dWu, void* dG, void* dU,
+                          cudaStream_t stream);
+// The forward pass for a few tokens (M <= kGemvMaxRows), bound by reading the weights.
+int launch_gated_gemv_f16(const GatedArgs& a, const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U,
                           cudaStream_t stream);
 int launch_gemv_fp4(const GemvArgs& a, cudaStream_t stream);
 

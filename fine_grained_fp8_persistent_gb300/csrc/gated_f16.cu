@@ -214,6 +214,7 @@ int slopes(const GatedArgs& a, const void* dH, const void* G, const void* U, voi
 
 int launch_gated_forward(const GatedArgs& a, const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U,
                          cudaStream_t stream) {
+  if (a.M <= kGemvMaxRows) return launch_gated_gemv_f16(a, X, Wg, Wu, H, G, U, stream);
   return a.act == act::kSilu ? forward<act::kSilu>(a, X, Wg, Wu, H, G, U, stream) : forward<act::kGeluTanh>(a, X, Wg, Wu, H, G, U, stream);
 }
 

@@ -1,67 +1,41 @@
-// gemv_fp4.cu -- products of a few rows of X with 4-bit weights (the layouts of
-// quantize_fp4), plain or gated.
-//
-//   Y[m][n] = sum_k X[m][k] * E2M1(code[n][k]) * scale[n][k / SV]
-//
-// SV = 32 with E8M0 scales (MXFP4) or 16 with E4M3 scales (NVFP4).
-#include "activation.cuh"
-#include "gated.h"
-#include "ptx.cuh"
+// gemv_fp4.cu -- launcher of the products of a few rows of X with 4-bit weights, plain
+// or gated (gemv.cuh).
+#include "gemv.cuh"
 
 namespace fgf8 {
 namespace {
 
-constexpr int kMaxRows = 16;
-
-// The value of an E2M1 code (bit 3 sign, bits 2-1 exponent, bit 0 mantissa).
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-  const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-  const float v = e == 0 ? 0.5f * m : (1.0f + 0.5f * m) * static_cast<float>(1u << (e - 1));
-  return (c & 8u) ? -v : v;
+// A CTA reads M * 2 bytes of X per element of K beside ROWS / 2 bytes of weights, so the
+// rows per CTA grow with M: 16 up to 4 tokens, 32 up to 8, 64 up to 16.
+template <WType WT, bool BF16, int MATS>
+int by_rows(const GemvKArgs& k, cudaStream_t stream) {
+  if (k.M <= 4) return launch_gemv<WT, BF16, MATS, 1, 1>(k, stream);
+  if (k.M <= 8) return launch_gemv<WT, BF16, MATS, 1, 2>(k, stream);
+  return launch_gemv<WT, BF16, MATS, 2, 4>(k, stream);
 }
 
-// The value of a scale byte: 2^(b - 127), or E4M3.
-__device__ __forceinline__ float scale_value(uint32_t b, int fmt) {
-  if (fmt != 0) return ptx::e4m3_value(b);
-  return b == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(b << 23);
-}
-
-// One warp per output column n; lane l takes the 8-code words l, l + 32, ... of the row.
-__global__ void __launch_bounds__(128) gemv_kernel(GemvArgs a) {
-  const int n = blockIdx.x * 4 + threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (n >= a.N) return;
-  const int sv = a.fmt == 0 ? 32 : 16, ld = (a.N + 3) / 4 * 4, mats = a.act >= 0 ? 2 : 1;
-  const uint16_t* X = static_cast<const uint16_t*>(a.X);
-  for (int m = 0; m < a.M; ++m) {
-    float sum[2] = {0.0f, 0.0f};
-    for (int j = 0; j < mats; ++j) {
-      const uint32_t* w = static_cast<const uint32_t*>(a.W[j]) + static_cast<size_t>(n) * (a.K / 8);
-      const uint8_t* sf = static_cast<const uint8_t*>(a.SF[j]);
-      for (int i = lane; i < a.K / 8; i += 32) {
-        const uint32_t codes = w[i];
-        const int group = i * 8 / sv;
-        const float s = scale_value(sf[(static_cast<size_t>(group / 4) * ld + n) * 4 + group % 4], a.fmt);
-        float part = 0.0f;
-        for (int c = 0; c < 8; ++c)
-          part = fmaf(act::to_float(X[static_cast<size_t>(m) * a.K + 8 * i + c], a.bf16 != 0), e2m1_value(codes >> (4 * c) & 15u), part);
-        sum[j] = fmaf(part, s, sum[j]);
-      }
-      for (int off = 16; off > 0; off >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], off);
-    }
-    if (lane == 0) {
-      float v = sum[0];
-      if (a.act >= 0) v = (a.act == act::kSilu ? act::value<act::kSilu>(v) : act::value<act::kGeluTanh>(v)) * sum[1];
-      static_cast<uint16_t*>(a.out)[static_cast<size_t>(m) * a.N + n] = act::from_float(v, a.bf16 != 0);
-    }
-  }
+template <WType WT>
+int by_type(const GemvArgs& a, const GemvKArgs& k, cudaStream_t stream) {
+  if (a.act >= 0) return a.bf16 ? by_rows<WT, true, 2>(k, stream) : by_rows<WT, false, 2>(k, stream);
+  return a.bf16 ? by_rows<WT, true, 1>(k, stream) : by_rows<WT, false, 1>(k, stream);
 }
 
 }  // namespace
 
 int launch_gemv_fp4(const GemvArgs& a, cudaStream_t stream) {
-  gemv_kernel<<<(a.N + 3) / 4, 128, 0, stream>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? 0 : set_error(4, "gemv_fp4 launch: %s", cudaGetErrorString(e));
+  GemvKArgs k;
+  std::memset(&k, 0, sizeof(k));
+  k.X = a.X;
+  for (int j = 0; j < 2; ++j) {
+    k.W[j] = a.W[j];
+    k.SF[j] = a.SF[j];
+  }
+  k.out = a.out;
+  k.M = a.M;
+  k.N = a.N;
+  k.K = a.K;
+  k.act = a.act;
+  return a.fmt == 0 ? by_type<WType::MX>(a, k, stream) : by_type<WType::NV>(a, k, stream);
 }
 
 }  // namespace fgf8
