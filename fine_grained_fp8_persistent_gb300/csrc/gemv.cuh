@@ -16,18 +16,25 @@
 // 2 t + 8 + {0, 1}.  The sum over k does not care for the order, so X needs no shuffle
 // either: lane t's share of a row of X is 16 contiguous bytes.
 //
-// bf16 X is scaled per row by the power of two that puts its largest finite |x| into
-// [2^14, 2^15) and rounded to fp16, the type E2M1 decodes to.  Every |x| of at least 2^-31
-// of that largest one stays exact; smaller ones move by at most 2^-39 of it, below the FP32
-// accumulation's own rounding.
+// bf16 X is scaled, for each row and chunk of 256 columns, by the power of two that puts
+// the largest finite |x| there into [2^14, 2^15), and rounded to fp16, the type E2M1 decodes
+// to.  Every |x| of at least 2^-31 of that largest one stays exact; smaller ones move by at
+// most 2^-39 of it, below the FP32 accumulation's own rounding.  The chunk's sums are
+// multiplied by the power's inverse as they are added to the totals.
 //
-// Work split.  A CTA is 8 warps: WR groups of 16 weight rows times WK = 8 / WR interleaved
-// shares of the reduction; a cluster of CTAs splits the reduction further when there
-// are few rows.  Each warp streams 64-byte pieces of its 16 rows (one "chunk") through a
-// ring of its own with cp.async, so the main loop has no barrier.  The partial sums are
-// joined in shared memory, then over the cluster, always in the same order.
+// Work split.  One or two CTAs per SM, walking tiles of 16 weight rows; X (or as much of it as
+// fits) is converted and kept in shared memory once per CTA.  A round is up to WARPS tiles:
+// the 128-byte pieces ("chunks") of all their rows, tile after tile, are dealt to the warps
+// in equal contiguous runs, so every warp has the same work whatever the number of rows,
+// and a run meets at most two tiles.  Each warp streams its run through a ring of its own
+// with cp.async, which goes on across rounds, so the loop has no barrier; at a tile's end
+// it leaves its partial sums in a slot, and after the round the slots of each tile are
+// added in the warps' order.  With few rows, or with more of X than fits, a cluster of
+// CTAs splits the reduction and adds its sums through distributed shared memory, also in
+// a fixed order.
 #pragma once
 #include <cstring>
+#include <type_traits>
 
 #include "activation.cuh"
 #include "gated.h"
@@ -45,35 +52,43 @@ struct GemvKArgs {
   void* keep[2];     // gated 16-bit: G and U, or null
   int M, N, K;
   int act;
+  int tiles;         // tiles of 16 weight rows: cta_tiles per cluster, one more for the
+  int cta_tiles;     //   first `extra` clusters
+  int extra;
+  int round_tiles;   // tiles of one round, at most WARPS
   int chunks;        // chunks of the whole reduction
-  int per_cta;       // chunks of one CTA (a multiple of WK)
-  int x_chunks;      // chunks of X in shared memory at a time (a multiple of WK)
+  int cta_chunks;    // chunks of one CTA's share of it (every CTA has at least one)
+  int x_chunks;      // chunks of X in shared memory at a time
   int x_stride;      // bytes between rows of X in shared memory
+  int off_sum;       // offsets of the joined sums (two buffers, read by the cluster), of
+  int off_scale;     //   2^p of each chunk and row of X, and of X
+  int off_x;
 };
 
-template <WType WT, bool BF16, int MATS, int NT, int WR>
+template <WType WT, int MATS, int NT>
 struct GemvCfg {
-  static constexpr int WARPS = 8, THREADS = 32 * WARPS;
-  static constexpr int WK = WARPS / WR;
-  static constexpr int ROWS = 16 * WR;
-  static constexpr int CK = WT == WType::W16 ? 32 : 128;     // elements of K per chunk (64 bytes of a row)
-  static constexpr int SF_BYTES = WT == WType::MX ? 64 : WT == WType::NV ? 128 : 0;
-  static constexpr int STAGE = MATS * (1024 + SF_BYTES);
-  static constexpr int DEPTH = MATS == 2 ? 4 : 6;            // chunks in flight per warp
+  static constexpr int WARPS = MATS == 2 ? 8 : 12, THREADS = 32 * WARPS;
+  static constexpr int MIN_CTAS = NT == 1 ? 2 : 1;           // per SM
+  static constexpr int CK = WT == WType::W16 ? 64 : 256;     // elements of K per chunk (128 bytes of a row)
+  static constexpr int WPC = WT == WType::MX ? 2 : 4;        // scale words per row and chunk
+  static constexpr int SF_BYTES = WT == WType::W16 ? 0 : WPC * 64;
+  static constexpr int STAGE = MATS * (2048 + SF_BYTES);
+  static constexpr int DEPTH = 3;                            // ring slots of a warp
   static constexpr int RING = WARPS * DEPTH * STAGE;
-  static constexpr int COLS = 8 * NT;
-  static constexpr int RED = WARPS * MATS * 16 * COLS * 4;   // partial sums, over the ring
-  static_assert(RED <= RING, "the partial sums reuse the ring");
-  static constexpr int SUM = MATS * ROWS * COLS * 4;         // joined sums of the CTA, read by the cluster
-  static constexpr int OFF_SUM = RING;
-  static constexpr int OFF_MISC = OFF_SUM + SUM;             // per row of X: largest |x| bits, then 2^p
-  static constexpr int OFF_X = OFF_MISC + 128;
+  static constexpr int OFF_SLOTS = RING;                     // [warp][2][MATS][M][16] partial sums
+  static constexpr int slots_bytes(int M) { return WARPS * 2 * MATS * M * 64; }
 };
 
 namespace gemv {
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp16_full(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp4_full(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
@@ -94,6 +109,11 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
   else
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// D = A B, no addend.
+__device__ __forceinline__ void mma16816_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 // Eight E2M1 codes (low nibble first) to four fp16 pairs.
 __device__ __forceinline__ void e2m1x8(uint32_t v, uint32_t (&h)[4]) {
@@ -130,37 +150,79 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
 }
 
 }  // namespace gemv
 
-template <WType WT, bool BF16, int MATS, int NT, int WR>
-__global__ void __launch_bounds__(256, MATS == 2 ? 2 : 3) gemv_kernel(const GemvKArgs args) {
-  using C = GemvCfg<WT, BF16, MATS, NT, WR>;
+// Four outputs (weight rows n .. n + 3, token m) from their FP32 sums.
+__device__ __forceinline__ void store4(void* base, const GemvKArgs& args, int n, int m, const float4& v, bool bf16) {
+  uint16_t* p = static_cast<uint16_t*>(base) + static_cast<size_t>(m) * args.N + n;
+  const uint32_t lo = pack_2x16(v.x, v.y, bf16), hi = pack_2x16(v.z, v.w, bf16);
+  if (args.N % 4 == 0) {                                  // 8-byte aligned, and all four rows or none
+    *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
+    return;
+  }
+  p[0] = static_cast<uint16_t>(lo);
+  if (n + 1 < args.N) p[1] = static_cast<uint16_t>(lo >> 16);
+  if (n + 2 < args.N) p[2] = static_cast<uint16_t>(hi);
+  if (n + 3 < args.N) p[3] = static_cast<uint16_t>(hi >> 16);
+}
+template <bool BF16, int MATS>
+__device__ __forceinline__ void gemv_store(const GemvKArgs& args, int n, int m, float4 (&v)[MATS]) {
+  if (n >= args.N) return;
+  if constexpr (MATS == 2) {
+    if (args.keep[0] != nullptr) {
+      store4(args.keep[0], args, n, m, v[0], BF16);
+      store4(args.keep[1], args, n, m, v[1], BF16);
+    }
+    auto a = [&](float g) { return args.act == act::kSilu ? act::value<act::kSilu>(g) : act::value<act::kGeluTanh>(g); };
+    v[0] = make_float4(a(v[0].x) * v[1].x, a(v[0].y) * v[1].y, a(v[0].z) * v[1].z, a(v[0].w) * v[1].w);
+  }
+  store4(args.out, args, n, m, v[0], BF16);
+}
+
+template <WType WT, bool BF16, int MATS, int NT>
+__global__ void __launch_bounds__(GemvCfg<WT, MATS, NT>::THREADS, GemvCfg<WT, MATS, NT>::MIN_CTAS) gemv_kernel(const GemvKArgs args) {
+  using C = GemvCfg<WT, MATS, NT>;
   using namespace gemv;
   constexpr bool kScaleX = WT != WType::W16 && BF16;   // bf16 X against fp16 weight values
   constexpr bool kMmaBf16 = WT == WType::W16 && BF16;
+  constexpr int W = C::WARPS;
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t sbase = ptx::smem_u32(smem);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane >> 2, t = lane & 3;
-  const int wr = warp % WR, wk = warp / WR;
   const int S = static_cast<int>(gridDim.y);            // CTAs of the cluster: shares of the reduction
   const int rank = static_cast<int>(blockIdx.y);
   const int M = args.M, N = args.N, K = args.K;
-  const int row0 = static_cast<int>(blockIdx.x) * C::ROWS;
-  const int c0 = rank * args.per_cta;                    // first chunk of this CTA
-  const int nc = min(args.per_cta, args.chunks - c0);    // may be <= 0 for the last ranks
-  const int mine = nc > wk ? (nc - wk + C::WK - 1) / C::WK : 0;   // chunks of this warp: wk, wk + WK, ...
+  const int tile0 = static_cast<int>(blockIdx.x) * args.cta_tiles + min(static_cast<int>(blockIdx.x), args.extra);
+  const int my_tiles = args.cta_tiles + (static_cast<int>(blockIdx.x) < args.extra ? 1 : 0);
+  const int c0 = rank * args.cta_chunks;                 // first chunk of this CTA
+  const int nc = min(args.cta_chunks, args.chunks - c0);
+  const int pieces = (nc + args.x_chunks - 1) / args.x_chunks;
   constexpr int ELEM_BITS = WT == WType::W16 ? 16 : 4;
   const size_t row_bytes = static_cast<size_t>(K) * ELEM_BITS / 8;
   constexpr int SV = WT == WType::MX ? 32 : 16;
   const int sf_words = WT == WType::W16 ? 0 : (K / SV + 3) / 4;
   const int sf_ld = (N + 3) / 4 * 4;
+
+  // A run: this warp's chunks of one round and piece of X.
+  struct Run {
+    int round, piece;
+    int tile, chunk, left, pc;   // tile within the round, chunk within the piece, chunks left, chunks per piece
+  };
+  auto run_set = [&](Run& r) {
+    const int T = min(args.round_tiles, my_tiles - r.round * args.round_tiles);
+    r.pc = min(args.x_chunks, nc - r.piece * args.x_chunks);
+    const int U = T * r.pc, b = warp * U / W;
+    r.left = (warp + 1) * U / W - b;
+    r.tile = b / r.pc;
+    r.chunk = b - r.tile * r.pc;
+  };
 
   // X and the weights may come from the previous kernel
   ptx::griddep_wait();
@@ -168,321 +230,473 @@ __global__ void __launch_bounds__(256, MATS == 2 ? 2 : 3) gemv_kernel(const Gemv
 
   // ------------------------------------------------------------ weight stream
   const uint32_t ring = sbase + static_cast<uint32_t>(warp * C::DEPTH * C::STAGE);
-  // copies: lane = row l / 4 (and + 8), piece l % 4; the pieces of row r are stored
-  // rotated by r / 2 so that ldmatrix reads eight rows without bank conflicts
-  const int cr = lane >> 2, cp = lane & 3;
-  const int wrow = row0 + 16 * wr;
-  auto issue = [&](int i) {                               // i-th chunk of this warp
-    if (i < mine) {
-      const int c = c0 + wk + i * C::WK;
-      const uint32_t st = ring + static_cast<uint32_t>((i % C::DEPTH) * C::STAGE);
-      const size_t at = static_cast<size_t>(c) * 64 + static_cast<size_t>(cp) * 16;
-      const bool in_k = at < row_bytes;
+  // copies: lane = row l / 8 (and + 4, + 8, + 12), piece l % 8; piece p of row r is stored
+  // at p ^ (r % 8) so that ldmatrix reads eight rows without bank conflicts
+  const int cr = lane >> 3, cp = lane & 7;
+  const uint32_t dst_a = static_cast<uint32_t>(cr * 128 + ((cp ^ cr) << 4)), dst_b = dst_a ^ 64u;
+  const size_t rows4 = 4 * row_bytes;
+  const int full_chunks = static_cast<int>(row_bytes / 128);   // chunks with no column past K
+  Run pf{0, 0, 0, 0, 0, 0};
+  run_set(pf);
+  bool pf_end = false, pf_new = true, pf_rows = false;
+  int pf_slot = 0, gc = 0, row0 = 0;
+  const uint8_t* wp[MATS] = {};
+  const uint32_t* sp[MATS] = {};
+  auto issue = [&]() {
+    while (pf.left == 0 && !pf_end) {                     // the next piece or round with work for this warp
+      if (++pf.piece >= pieces) {
+        pf.piece = 0;
+        if (++pf.round * args.round_tiles >= my_tiles) { pf_end = true; break; }
+      }
+      run_set(pf);
+      pf_new = true;
+    }
+    if (!pf_end) {
+      if (pf_new) {                                       // a new tile: row pointers
+        row0 = (tile0 + pf.round * args.round_tiles + pf.tile) * 16;
+        gc = c0 + pf.piece * args.x_chunks + pf.chunk;
+        pf_rows = row0 + 16 <= N;
 #pragma unroll
-      for (int j = 0; j < MATS; ++j) {
-        const uint8_t* w = static_cast<const uint8_t*>(args.W[j]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = cr + 8 * h;
-          const bool ok = in_k && wrow + r < N;
-          cp16(st + j * 1024 + r * 64 + ((cp ^ ((r >> 1) & 3)) << 4), ok ? w + static_cast<size_t>(wrow + r) * row_bytes + at : w, ok);
+        for (int j = 0; j < MATS; ++j) {
+          wp[j] = static_cast<const uint8_t*>(args.W[j]) + static_cast<size_t>(row0 + cr) * row_bytes + static_cast<size_t>(gc) * 128 + cp * 16;
+          if constexpr (WT != WType::W16)
+            sp[j] = static_cast<const uint32_t*>(args.SF[j]) + static_cast<size_t>(gc * C::WPC + (lane >> 4)) * sf_ld + row0 + (lane & 15);
         }
-        if constexpr (WT != WType::W16) {
-          // scale words of the chunk's 16 rows: one (MXFP4) or two (NVFP4) per row
-          constexpr int WPC = WT == WType::MX ? 1 : 2;
-          if (lane < 16 * WPC) {
-            const int word = c * WPC + (lane >> 4), r = wrow + (lane & 15);
-            const bool ok = word < sf_words && r < N;
-            const uint32_t* sf = static_cast<const uint32_t*>(args.SF[j]);
-            cp4(st + MATS * 1024 + j * C::SF_BYTES + lane * 4, ok ? sf + static_cast<size_t>(word) * sf_ld + r : sf, ok);
+        pf_new = false;
+      }
+      const uint32_t st = ring + static_cast<uint32_t>(pf_slot * C::STAGE);
+      if (pf_rows && gc < full_chunks) {
+#pragma unroll
+        for (int j = 0; j < MATS; ++j) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) cp16_full(st + j * 2048 + (i & 1 ? dst_b : dst_a) + 512 * i, wp[j] + i * rows4);
+          if constexpr (WT != WType::W16) {
+#pragma unroll
+            for (int i = 0; i < C::WPC / 2; ++i)
+              cp4_full(st + MATS * 2048 + j * C::SF_BYTES + lane * 4 + 128 * i, sp[j] + static_cast<size_t>(2 * i) * sf_ld);
+          }
+        }
+      } else {                                            // rows past N and columns past K are zero
+        const bool in_k = static_cast<size_t>(gc) * 128 + cp * 16 < row_bytes;
+#pragma unroll
+        for (int j = 0; j < MATS; ++j) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool ok = in_k && row0 + cr + 4 * i < N;
+            cp16(st + j * 2048 + (i & 1 ? dst_b : dst_a) + 512 * i, ok ? wp[j] + i * rows4 : static_cast<const uint8_t*>(args.W[j]), ok);
+          }
+          if constexpr (WT != WType::W16) {
+#pragma unroll
+            for (int i = 0; i < C::WPC / 2; ++i) {
+              const bool ok = gc * C::WPC + (lane >> 4) + 2 * i < sf_words && row0 + (lane & 15) < N;
+              cp4(st + MATS * 2048 + j * C::SF_BYTES + lane * 4 + 128 * i,
+                  ok ? sp[j] + static_cast<size_t>(2 * i) * sf_ld : static_cast<const uint32_t*>(args.SF[j]), ok);
+            }
           }
         }
       }
+#pragma unroll
+      for (int j = 0; j < MATS; ++j) {
+        wp[j] += 128;
+        if constexpr (WT != WType::W16) sp[j] += static_cast<size_t>(C::WPC) * sf_ld;
+      }
+      ++gc;
+      --pf.left;
+      if (++pf.chunk == pf.pc) {
+        pf.chunk = 0;
+        ++pf.tile;
+        pf_new = true;
+      }
+      if (++pf_slot == C::DEPTH) pf_slot = 0;
     }
     cp_commit();
   };
 #pragma unroll
-  for (int i = 0; i < C::DEPTH - 1; ++i) issue(i);
+  for (int i = 0; i < C::DEPTH - 1; ++i) issue();
 
-  float acc[MATS][NT][4] = {};
-  float tot[MATS][NT][4] = {};                            // NVFP4 with scaled X: sums over the pieces of X
-  const uint32_t xs = sbase + C::OFF_X;
-  uint32_t* amax = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
-  float* pw = reinterpret_cast<float*>(smem + C::OFF_MISC + 64);
+  const uint32_t xs = sbase + static_cast<uint32_t>(args.off_x);
+  float* slots = reinterpret_cast<float*>(smem + C::OFF_SLOTS);
+  float* xscale = reinterpret_cast<float*>(smem + args.off_scale);   // [chunk][M]
+  int slot = 0;                                           // ring slot of the next chunk
 
-  int i = 0;                                              // next chunk of this warp
-  for (int x0 = 0; x0 < nc; x0 += args.x_chunks) {
-    // ---------------------------------------------------------- a piece of X
-    const int xn = min(args.x_chunks, nc - x0);           // chunks
-    const int k0 = (c0 + x0) * C::CK;
-    const int vecs = xn * (C::CK / 8);                    // 16-byte vectors per row, zeros past K
-    const int blocks = (vecs + 31) / 32;
-    if (x0 > 0) __syncthreads();                          // the previous piece has been read
-    if constexpr (kScaleX) {
-      if (threadIdx.x < 16) amax[threadIdx.x] = 0u;
-      __syncthreads();
-    }
-    for (int it = warp; it < M * blocks; it += C::WARPS) {
-      const int m = it / blocks, v = (it - m * blocks) * 32 + lane;
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      const bool in = v < vecs;
-      if (in && k0 + 8 * v < K)
-        w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(args.X) + static_cast<size_t>(m) * K + k0 + 8 * v));
-      if constexpr (WT == WType::W16) {
-        // element 8 s + 2 t + i of each 32 goes to 8 t + 2 s + i: lane t's four pairs side by side
-        if (in) {
-          const uint32_t d = xs + static_cast<uint32_t>(m * args.x_stride + (v >> 2) * 64 + (v & 3) * 4);
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  // this lane's rows of X (columns of the MMA); columns past M repeat the last row and
+  // are never stored
+  uint32_t xl[NT];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) asm volatile("st.shared.b32 [%0], %1;" ::"r"(d + 16 * j), "r"(u[j]) : "memory");
-        }
-      } else if (in) {
-        st_shared_v4(xs + static_cast<uint32_t>(m * args.x_stride + v * 16), w.x, w.y, w.z, w.w);
-      }
-      if constexpr (kScaleX) {
-        // largest finite |x| of the row, as FP32 bits
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-        uint32_t a = 0u;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t lo = (u[j] << 16) & 0x7FFFFFFFu, hi = u[j] & 0x7FFF0000u;
-          a = max(a, lo < 0x7F800000u ? lo : 0u);
-          a = max(a, hi < 0x7F800000u ? hi : 0u);
-        }
-        a = __reduce_max_sync(0xffffffffu, a);
-        if (lane == 0) atomicMax(amax + m, a);
-      }
-    }
-    __syncthreads();
-    float xp[NT][2];                                      // 2^p of this lane's columns
-#pragma unroll
-    for (int n = 0; n < NT; ++n) xp[n][0] = xp[n][1] = 1.0f;
-    if constexpr (kScaleX) {
-      for (int it = warp; it < M * blocks; it += C::WARPS) {
-        const int m = it / blocks, v = (it - m * blocks) * 32 + lane;
-        // x * 2^sh in two exact steps (sh reaches 141); 2^-sh is an FP32 value
-        const int e = amax[m] ? static_cast<int>(amax[m] >> 23) : 127;
-        const int sh = 141 - e, s1 = sh / 2, s2 = sh - s1;
-        const float f1 = __uint_as_float(static_cast<uint32_t>(127 + s1) << 23), f2 = __uint_as_float(static_cast<uint32_t>(127 + s2) << 23);
-        if (v < vecs) {
-          const uint32_t at = xs + static_cast<uint32_t>(m * args.x_stride + v * 16);
-          uint32_t u[4];
-          lds128(at, u);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            u[j] = pack_2x16(__uint_as_float(u[j] << 16) * f1 * f2, __uint_as_float(u[j] & 0xFFFF0000u) * f1 * f2, false);
-          st_shared_v4(at, u[0], u[1], u[2], u[3]);
-        }
-        if (v == 0) {                                     // the row's first vector: record 2^-sh, subnormal from sh = 127
-          pw[m] = sh < 127 ? __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) : __uint_as_float(1u << (149 - sh));
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int m = 8 * n + 2 * t + j;
-          xp[n][j] = m < M ? pw[m] : 1.0f;
-        }
-    }
+  for (int n = 0; n < NT; ++n) xl[n] = xs + static_cast<uint32_t>(min(8 * n + g, M - 1) * args.x_stride + t * 16);
 
-    // ---------------------------------------------------------- main loop
-    const int lr = (lane & 7) + ((lane >> 3) & 1) * 8;    // ldmatrix: row and piece this lane addresses
-    const int lp = lane >> 4, lx = (lr >> 1) & 3;
-    for (; i < mine && wk + i * C::WK < x0 + xn; ++i) {
-      cp_wait<C::DEPTH - 2>();
-      __syncwarp();
-      issue(i + C::DEPTH - 1);
-      const uint32_t st = ring + static_cast<uint32_t>((i % C::DEPTH) * C::STAGE);
-      const uint32_t xc = xs + static_cast<uint32_t>((wk + i * C::WK - x0) * (C::CK * 2) + t * 16);
-      uint32_t a[MATS][2][4];
+  for (int round = 0; round * args.round_tiles < my_tiles; ++round) {
+    const int T = min(args.round_tiles, my_tiles - round * args.round_tiles);
+    for (int piece = 0; piece < pieces; ++piece) {
+      // -------------------------------------------------------- a piece of X
+      if (pieces > 1 || round == 0) {
+        const int xn = min(args.x_chunks, nc - piece * args.x_chunks);
+        const int k0 = (c0 + piece * args.x_chunks) * C::CK;
+        // one warp takes 256 columns of a row, 8 per lane (zeros past K)
+        const int blocks = (xn * C::CK + 255) / 256;
+        for (int it = warp; it < M * blocks; it += W) {
+          const int m = it / blocks, blk = it - m * blocks, v = blk * 32 + lane;
+          uint4 w = make_uint4(0u, 0u, 0u, 0u);
+          if (k0 + 8 * v < K)
+            w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(args.X) + static_cast<size_t>(m) * K + k0 + 8 * v));
+          uint32_t u[4] = {w.x, w.y, w.z, w.w};
+          if constexpr (WT == WType::W16) {
+            // element 8 s + 2 t + i of each 32 goes to 8 t + 2 s + i: lane t's four pairs side by side
+            if (8 * v < xn * C::CK) {
+              const uint32_t d = xs + static_cast<uint32_t>(m * args.x_stride + (v >> 2) * 64 + (v & 3) * 4);
 #pragma unroll
-      for (int j = 0; j < MATS; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) ldmatrix_x4(st + j * 1024 + lr * 64 + (((2 * h + lp) ^ lx) << 4), a[j][h]);
-      if constexpr (WT == WType::W16) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          uint32_t b[4] = {0u, 0u, 0u, 0u};
-          if (8 * n + g < M) lds128(xc + static_cast<uint32_t>((8 * n + g) * args.x_stride), b);
-#pragma unroll
-          for (int j = 0; j < MATS; ++j) {
-            mma16816<kMmaBf16>(acc[j][n], a[j][0][0], a[j][0][1], a[j][0][2], a[j][0][3], b[0], b[1]);
-            mma16816<kMmaBf16>(acc[j][n], a[j][1][0], a[j][1][1], a[j][1][2], a[j][1][3], b[2], b[3]);
-          }
-        }
-      } else {
-        // scale words of rows g and g + 8
-        uint32_t sw[MATS][2][2];
-        float sf[MATS][2][4];
-#pragma unroll
-        for (int j = 0; j < MATS; ++j)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const uint8_t* p = smem + (st - sbase) + MATS * 1024 + j * C::SF_BYTES + (g + 8 * r) * 4;
-            sw[j][r][0] = *reinterpret_cast<const uint32_t*>(p);
-            if constexpr (WT == WType::NV) {
-              sw[j][r][1] = *reinterpret_cast<const uint32_t*>(p + 64);
-              sw[j][r][0] >>= 8 * (t >> 1);
-              sw[j][r][1] >>= 8 * (t >> 1);
-            } else {
-              e8m0x4(sw[j][r][0], sf[j][r]);
+              for (int j = 0; j < 4; ++j) asm volatile("st.shared.b32 [%0], %1;" ::"r"(d + 16 * j), "r"(u[j]) : "memory");
             }
-          }
+          } else {
+            if constexpr (kScaleX) {
+              uint32_t a = 0u;                            // largest finite |x|, as bf16 bits
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {                     // 32 codes of each row
-          uint32_t b[NT][4];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            b[n][0] = b[n][1] = b[n][2] = b[n][3] = 0u;
-            if (8 * n + g < M) lds128(xc + static_cast<uint32_t>((8 * n + g) * args.x_stride + 64 * s), b[n]);
-          }
-#pragma unroll
-          for (int j = 0; j < MATS; ++j) {
-            uint32_t lo[4], hi[4];
-            e2m1x8(a[j][s >> 1][2 * (s & 1)], lo);
-            e2m1x8(a[j][s >> 1][2 * (s & 1) + 1], hi);
-            if constexpr (WT == WType::NV) {
-              // lanes t = 0, 1 hold the piece's first group, t = 2, 3 its second
-              const uint32_t s0 = e4m3_pair(sw[j][0][s >> 1], 2 * (s & 1)), s1 = e4m3_pair(sw[j][1][s >> 1], 2 * (s & 1));
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                lo[q] = mul2(lo[q], s0);
-                hi[q] = mul2(hi[q], s1);
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t lo = u[j] & 0x7FFFu, hi = (u[j] >> 16) & 0x7FFFu;
+                a = max(a, lo < 0x7F80u ? lo : 0u);
+                a = max(a, hi < 0x7F80u ? hi : 0u);
               }
-            }
+              a = __reduce_max_sync(0xffffffffu, a);
+              // x * 2^sh in two exact steps (sh reaches 141); 2^-sh is an FP32 value, a
+              // subnormal from sh = 127 on
+              const int sh = 141 - (a ? static_cast<int>(a >> 7) : 127), s1 = sh / 2, s2 = sh - s1;
+              const float f1 = __uint_as_float(static_cast<uint32_t>(127 + s1) << 23), f2 = __uint_as_float(static_cast<uint32_t>(127 + s2) << 23);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              if constexpr (WT == WType::NV) {
-                mma16816<false>(acc[j][n], lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
-                mma16816<false>(acc[j][n], lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
-              } else {
-                float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma16816<false>(p, lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
-                mma16816<false>(p, lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  acc[j][n][q] = fmaf(kScaleX ? p[q] * xp[n][q & 1] : p[q], sf[j][q >> 1][s], acc[j][n][q]);
-              }
+              for (int j = 0; j < 4; ++j)
+                u[j] = pack_2x16(__uint_as_float(u[j] << 16) * f1 * f2, __uint_as_float(u[j] & 0xFFFF0000u) * f1 * f2, false);
+              if (lane == 0) xscale[blk * M + m] = sh < 127 ? __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) : __uint_as_float(1u << (149 - sh));
             }
+            st_shared_v4(xs + static_cast<uint32_t>(m * args.x_stride + v * 16), u[0], u[1], u[2], u[3]);
           }
         }
+        __syncthreads();
       }
-    }
-    if constexpr (kScaleX && WT == WType::NV) {
+
+      // -------------------------------------------------------- this warp's run
+      float acc[MATS][NT][4];
 #pragma unroll
       for (int j = 0; j < MATS; ++j)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            tot[j][n][q] = fmaf(acc[j][n][q], xp[n][q & 1], tot[j][n][q]);
-            acc[j][n][q] = 0.0f;
+          for (int q = 0; q < 4; ++q) acc[j][n][q] = 0.0f;
+      Run r{round, piece, 0, 0, 0, 0};
+      run_set(r);
+      int part = 0;                                       // which of the run's tiles
+      // the partial sums of a finished tile (or of the run's end)
+      auto flush = [&]() {
+#pragma unroll
+        for (int j = 0; j < MATS; ++j)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int col = 8 * n + 2 * t + (q & 1), row = g + 8 * (q >> 1);
+              if (col < M) slots[(((warp * 2 + part) * MATS + j) * M + col) * 16 + row] = acc[j][n][q];
+              acc[j][n][q] = 0.0f;
+            }
+        ++part;
+      };
+      const int lr = (lane & 7) + ((lane >> 3) & 1) * 8;  // ldmatrix: row and piece this lane addresses
+      const uint32_t la = static_cast<uint32_t>(lr * 128 + (((lane >> 4) ^ (lr & 7)) << 4));
+      while (r.left > 0) {
+        cp_wait<C::DEPTH - 2>();
+        __syncwarp();
+        issue();
+        const uint32_t so = static_cast<uint32_t>((warp * C::DEPTH + slot) * C::STAGE);
+        const uint32_t st = sbase + so;
+        if (++slot == C::DEPTH) slot = 0;
+        const uint32_t xc = static_cast<uint32_t>(r.chunk * (C::CK * 2));
+        if constexpr (WT == WType::W16) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {                   // 32 columns
+            uint32_t b[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) lds128(xl[n] + xc + 64 * h, b[n]);
+#pragma unroll
+            for (int j = 0; j < MATS; ++j)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                uint32_t a[4];
+                ldmatrix_x4(st + j * 2048 + (la ^ ((2 * h + i) << 5)), a);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16816<kMmaBf16>(acc[j][n], a[0], a[1], a[2], a[3], b[n][2 * i], b[n][2 * i + 1]);
+              }
           }
-    }
-  }
-
-  // -------------------------------------------------------------- join
-  cp_wait<0>();
-  __syncthreads();                                        // every warp is done with its ring
-  float* red = reinterpret_cast<float*>(smem);            // [wk][mat][col][ROWS]
+        } else {
+          float xp[NT][2];                                // 2^p of this lane's columns
+          if constexpr (kScaleX) {
 #pragma unroll
-  for (int j = 0; j < MATS; ++j)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+              for (int j = 0; j < 2; ++j) xp[n][j] = xscale[r.chunk * M + min(8 * n + 2 * t + j, M - 1)];
+          }
+          // the chunk's sums: of scaled X where X is scaled, else straight into the totals
+          float part_acc[MATS][NT][4];
+          float(&sums)[MATS][NT][4] = kScaleX ? part_acc : acc;
+          if constexpr (kScaleX) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int col = 8 * n + 2 * t + (q & 1), row = 16 * wr + g + 8 * (q >> 1);
-        red[((wk * MATS + j) * C::COLS + col) * C::ROWS + row] = (kScaleX && WT == WType::NV) ? tot[j][n][q] : acc[j][n][q];
-      }
-  __syncthreads();
-  float* sum = reinterpret_cast<float*>(smem + C::OFF_SUM);   // [mat][col][ROWS]
-  for (int o = threadIdx.x; o < MATS * C::COLS * C::ROWS; o += C::THREADS) {
-    float v = 0.0f;
+            for (int j = 0; j < MATS; ++j)
 #pragma unroll
-    for (int k = 0; k < C::WK; ++k) v += red[k * MATS * C::COLS * C::ROWS + o];
-    sum[o] = v;
-  }
-  if (S > 1) cluster_sync_all();
-  else __syncthreads();
-  // outputs o = m * ROWS + row, split over the cluster
-  const int all = M * C::ROWS;
-  for (int o = rank * C::THREADS + static_cast<int>(threadIdx.x); o < all; o += S * C::THREADS) {
-    const int m = o / C::ROWS, n = row0 + o % C::ROWS;
-    float v[MATS];
+              for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int j = 0; j < MATS; ++j) {
-      if (S > 1) {
-        const uint32_t at = sbase + C::OFF_SUM + static_cast<uint32_t>(j * C::COLS * C::ROWS + o) * 4u;
-        v[j] = 0.0f;
-        for (int r = 0; r < S; ++r) v[j] += ld_cluster_f32(map_to_rank(at, static_cast<uint32_t>(r)));
-      } else {
-        v[j] = sum[j * C::COLS * C::ROWS + o];
-      }
-    }
-    if (n < N) {
-      const size_t at = static_cast<size_t>(m) * N + n;
-      uint16_t* out = static_cast<uint16_t*>(args.out);
-      if constexpr (MATS == 2) {
-        if (args.keep[0] != nullptr) {
-          static_cast<uint16_t*>(args.keep[0])[at] = act::from_float(v[0], BF16);
-          static_cast<uint16_t*>(args.keep[1])[at] = act::from_float(v[1], BF16);
+                for (int q = 0; q < 4; ++q) part_acc[j][n][q] = 0.0f;
+          }
+          const uint8_t* scales = smem + so + MATS * 2048;
+          // MXFP4 on scaled X: a scale of 2^65 or more could overflow sums whose product
+          // with 2^p is finite; such a chunk multiplies each group by 2^p first
+          bool large = false;
+          if constexpr (kScaleX && WT == WType::MX) {
+#pragma unroll
+            for (int j = 0; j < MATS; ++j) {
+              const uint32_t w = *reinterpret_cast<const uint32_t*>(scales + j * C::SF_BYTES + lane * 4);
+              large = large || (w & (w << 1) & 0x80808080u) != 0u;
+            }
+            large = __any_sync(0xffffffffu, large);
+          }
+          auto body = [&](auto large_c) {
+            constexpr bool kLarge = decltype(large_c)::value;
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {                 // 128 codes of each row
+              // scales of rows g and g + 8
+              uint32_t sw[MATS][2][2];
+              [[maybe_unused]] float sf[MATS][2][4];
+#pragma unroll
+              for (int j = 0; j < MATS; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const uint8_t* p = scales + j * C::SF_BYTES + f * (C::WPC * 32) + (g + 8 * h) * 4;
+                  sw[j][h][0] = *reinterpret_cast<const uint32_t*>(p);
+                  if constexpr (WT == WType::NV) {
+                    sw[j][h][1] = *reinterpret_cast<const uint32_t*>(p + 64);
+                    sw[j][h][0] >>= 8 * (t >> 1);
+                    sw[j][h][1] >>= 8 * (t >> 1);
+                  } else {
+                    e8m0x4(sw[j][h][0], sf[j][h]);
+                  }
+                }
+#pragma unroll
+              for (int p2 = 0; p2 < 2; ++p2) {            // 64 codes
+                uint32_t a[MATS][4];
+#pragma unroll
+                for (int j = 0; j < MATS; ++j) ldmatrix_x4(st + j * 2048 + (la ^ ((2 * f + p2) << 5)), a[j]);
+#pragma unroll
+                for (int s2 = 0; s2 < 2; ++s2) {          // 32 codes
+                  const int s = 2 * p2 + s2;
+                  uint32_t b[NT][4];
+#pragma unroll
+                  for (int n = 0; n < NT; ++n) lds128(xl[n] + xc + 256 * f + 64 * s, b[n]);
+#pragma unroll
+                  for (int j = 0; j < MATS; ++j) {
+                    uint32_t lo[4], hi[4];
+                    e2m1x8(a[j][2 * s2], lo);
+                    e2m1x8(a[j][2 * s2 + 1], hi);
+                    if constexpr (WT == WType::NV) {
+                      // lanes t = 0, 1 hold the piece's first group, t = 2, 3 its second
+                      const uint32_t s0 = e4m3_pair(sw[j][0][p2], 2 * s2), s1 = e4m3_pair(sw[j][1][p2], 2 * s2);
+#pragma unroll
+                      for (int q = 0; q < 4; ++q) {
+                        lo[q] = mul2(lo[q], s0);
+                        hi[q] = mul2(hi[q], s1);
+                      }
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                      if constexpr (WT == WType::NV) {
+                        mma16816<false>(sums[j][n], lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
+                        mma16816<false>(sums[j][n], lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
+                      } else {
+                        float p[4];
+                        mma16816_f16_zero(p, lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
+                        mma16816<false>(p, lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                          if constexpr (kLarge) acc[j][n][q] = fmaf(p[q] * xp[n][q & 1], sf[j][q >> 1][s], acc[j][n][q]);
+                          else sums[j][n][q] = fmaf(p[q], sf[j][q >> 1][s], sums[j][n][q]);
+                        }
+                      }
+                    }
+                  }
+                }
+              }
+            }
+            if constexpr (kScaleX && !kLarge) {
+#pragma unroll
+              for (int j = 0; j < MATS; ++j)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) acc[j][n][q] = fmaf(part_acc[j][n][q], xp[n][q & 1], acc[j][n][q]);
+            }
+          };
+          if (kScaleX && WT == WType::MX && large) body(std::true_type{});
+          else body(std::false_type{});
         }
-        v[0] = (args.act == act::kSilu ? act::value<act::kSilu>(v[0]) : act::value<act::kGeluTanh>(v[0])) * v[1];
+        --r.left;
+        if (++r.chunk == r.pc) {
+          r.chunk = 0;
+          flush();
+        }
       }
-      out[at] = act::from_float(v[0], BF16);
+      if (r.chunk != 0) flush();                          // an unfinished tile (a run that stops at a tile's end has flushed it)
+
+      // -------------------------------------------------------- join the round
+      // Four weight rows of one token per thread: cell = (token * 4 + row / 4) of a tile.
+      __syncthreads();
+      const int pc = r.pc, U = T * pc;
+      const int cells = 4 * M;
+      const bool last_piece = piece == pieces - 1;
+      float4* sum4 = reinterpret_cast<float4*>(smem + args.off_sum) + (round & 1) * (MATS * args.round_tiles * cells);
+      const float4* slots4 = reinterpret_cast<const float4*>(slots);
+      const int first_row = (tile0 + round * args.round_tiles) * 16;
+      for (int o = threadIdx.x; o < T * cells; o += C::THREADS) {
+        const int tile = o / cells, cell = o - tile * cells;
+        // the warps whose runs meet this tile: run w starts at w U / W
+        const int w0 = ((tile * pc + 1) * W - 1) / U, w1 = ((tile * pc + pc) * W - 1) / U;
+        float4 v[MATS];
+#pragma unroll
+        for (int j = 0; j < MATS; ++j) v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int w = w0, b = w0 * U / W; w <= w1; ++w) {
+          const int e = (w + 1) * U / W;
+          if (e > b) {                                    // not an empty run
+            const int li = b >= tile * pc ? 0 : 1;        // the run's first tile, or its second
+#pragma unroll
+            for (int j = 0; j < MATS; ++j) {
+              const float4 p = slots4[((w * 2 + li) * MATS + j) * cells + cell];
+              v[j].x += p.x;
+              v[j].y += p.y;
+              v[j].z += p.z;
+              v[j].w += p.w;
+            }
+          }
+          b = e;
+        }
+        if (S > 1 || pieces > 1) {
+#pragma unroll
+          for (int j = 0; j < MATS; ++j) {
+            float4& d = sum4[(j * args.round_tiles + tile) * cells + cell];
+            if (piece > 0) v[j] = make_float4(d.x + v[j].x, d.y + v[j].y, d.z + v[j].z, d.w + v[j].w);
+            d = v[j];
+          }
+        }
+        if (S == 1 && last_piece) gemv_store<BF16, MATS>(args, first_row + tile * 16 + (cell & 3) * 4, cell >> 2, v);
+      }
+      if (S > 1 && last_piece) {
+        // one barrier per round: the next round's sums go to the other buffer
+        cluster_sync_all();
+        for (int o = rank * C::THREADS + static_cast<int>(threadIdx.x); o < T * cells; o += S * C::THREADS) {
+          const int tile = o / cells, cell = o - tile * cells;
+          float4 v[MATS];
+#pragma unroll
+          for (int j = 0; j < MATS; ++j) {
+            const uint32_t at = ptx::smem_u32(sum4 + (j * args.round_tiles + tile) * cells + cell);
+            v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int q = 0; q < S; ++q) {
+              const float4 p = ld_cluster_f32x4(map_to_rank(at, static_cast<uint32_t>(q)));
+              v[j].x += p.x;
+              v[j].y += p.y;
+              v[j].z += p.z;
+              v[j].w += p.w;
+            }
+          }
+          gemv_store<BF16, MATS>(args, first_row + tile * 16 + (cell & 3) * 4, cell >> 2, v);
+        }
+      } else {
+        __syncthreads();                                  // slots and X are free again
+      }
     }
   }
-  if (S > 1) cluster_sync_all();                          // the sums stay until every CTA has read them
+  if (S > 1) cluster_sync_all();                          // every CTA has read this one's sums
+  cp_wait<0>();
 }
 
-// Launch: rows per CTA, shares of the reduction, and how much of X stays in shared memory.
-template <WType WT, bool BF16, int MATS, int NT, int WR>
+// Launch: shares of the reduction, tiles per CTA, and how much of X stays in shared memory.
+template <WType WT, bool BF16, int MATS, int NT>
 int launch_gemv(GemvKArgs a, cudaStream_t stream) {
-  using C = GemvCfg<WT, BF16, MATS, NT, WR>;
-  auto* fn = &gemv_kernel<WT, BF16, MATS, NT, WR>;
-  constexpr int kXBytes = 56 * 1024;
-  constexpr int kMaxSmem = C::OFF_X + kXBytes + 16 * 64;
-  static_assert(kMaxSmem <= 232448, "shared memory budget");
-  static bool ready[64] = {};
+  using C = GemvCfg<WT, MATS, NT>;
+  auto* fn = &gemv_kernel<WT, BF16, MATS, NT>;
+  constexpr int kSmem = 232448;
+  constexpr int kHalf = 115712;                           // two CTAs per SM (227 KB with 1 KB reserved each)
+  static int max_clusters[64][4] = {};                    // by device and log2 of the cluster size
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return set_error(2, "device id %d", dev);
-  if (!ready[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    if (e != cudaSuccess) return set_error(4, "matrix-vector set-up: %s", cudaGetErrorString(e));
-    ready[dev] = true;
-  }
-  a.chunks = (a.K + C::CK - 1) / C::CK;
-  const long long tiles = (a.N + C::ROWS - 1) / C::ROWS;
-  // split the reduction while the CTAs do not fill the SMs twice over and every warp
-  // keeps at least four chunks
-  int S = 1;
-  while (S < 8 && tiles * S < 2LL * device_sm_count() && a.chunks / (2 * S * C::WK) >= 4) S *= 2;
-  auto round_up = [](int v, int to) { return (v + to - 1) / to * to; };
-  a.per_cta = round_up((a.chunks + S - 1) / S, C::WK);
-  // rows of X are an odd number of 64-byte units apart (bank conflicts); at most kXBytes of X
-  const int most = kXBytes / (C::CK * 2) / a.M / C::WK * C::WK;
-  a.x_chunks = a.per_cta < most ? a.per_cta : most;
-  const int units = a.x_chunks * (C::CK * 2 / 64);
-  a.x_stride = (units | 1) * 64;
-  if (a.x_chunks <= 0) return set_error(2, "matrix-vector: no room for X");
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = static_cast<unsigned>(S);
+  attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(S), 1);
   cfg.blockDim = dim3(C::THREADS, 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(C::OFF_X) + static_cast<size_t>(a.M) * a.x_stride;
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
+  if (max_clusters[dev][0] == 0) {
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    cfg.numAttrs = 1;
+    for (int i = 3; e == cudaSuccess && i >= 0; --i) {
+      attr[0].val.clusterDim.y = 1u << i;
+      cfg.gridDim = dim3(static_cast<unsigned>(device_sm_count() >> i), 1u << i, 1);
+      int n = 0;
+      e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
+      if (e == cudaSuccess && n <= 0) e = cudaErrorInvalidConfiguration;
+      if (e == cudaSuccess) max_clusters[dev][i] = n;
+    }
+    if (e != cudaSuccess) return set_error(4, "matrix-vector set-up: %s", cudaGetErrorString(e));
+  }
+  a.chunks = (a.K + C::CK - 1) / C::CK;
+  a.tiles = (a.N + 15) / 16;
+  const int slots = C::OFF_SLOTS + C::slots_bytes(a.M);
+  // Shares of the reduction: the split with the least time by this model (ns): chunks of
+  // the busiest SM at its share of the memory rate, X to stage, a cluster's joins.
+  double best = -1.0;
+  int S = 1, log_s = 0, per_sm = 1;
+  for (int i = 0; i < 4; ++i) {
+    const int s = 1 << i, per = (a.chunks + s - 1) / s;
+    if ((s - 1) * per >= a.chunks) continue;              // a CTA without work
+    const double x_bytes = static_cast<double>(per) * (C::CK * 2 + 4) * a.M;
+    for (int two = 0; two < C::MIN_CTAS; ++two) {
+      const double room = (two ? kHalf : kSmem) - slots - 16384.0 - 128.0 - 64.0 * a.M;
+      if (two && x_bytes > room) continue;
+      const int tiles = (a.tiles + max_clusters[dev][i] - 1) / max_clusters[dev][i];   // of an SM, over its CTAs
+      if (two && tiles < 2) continue;
+      const double pieces = x_bytes > room ? static_cast<double>((tiles + C::WARPS - 1) / C::WARPS) : 1.0;
+      const double ns = static_cast<double>(tiles) * per * (C::STAGE / 40.0) + pieces * x_bytes / 50.0 + (s > 1 ? 2500.0 : 0.0) - two;
+      if (best < 0 || ns < best) {
+        best = ns;
+        S = s;
+        log_s = i;
+        per_sm = 1 << two;
+      }
+    }
+  }
+  a.cta_chunks = (a.chunks + S - 1) / S;
+  const int slots_cap = max_clusters[dev][log_s] * per_sm;
+  const int clusters = a.tiles < slots_cap ? a.tiles : slots_cap;
+  a.cta_tiles = a.tiles / clusters;
+  a.extra = a.tiles % clusters;
+  // rounds of equal size, at most WARPS tiles and 8 KB of joined sums
+  const int sum_cap = 8192 / (MATS * a.M * 64);
+  const int most = C::WARPS < sum_cap ? C::WARPS : sum_cap;
+  const int cta_most = a.cta_tiles + (a.extra > 0 ? 1 : 0);
+  const int rounds = (cta_most + most - 1) / most;
+  a.round_tiles = (cta_most + rounds - 1) / rounds;
+  a.off_sum = slots;
+  a.off_scale = slots + 2 * MATS * a.round_tiles * a.M * 64;
+  // X: rows an odd number of 64-byte units apart (bank conflicts), and a scale per row and chunk
+  const int room = ((per_sm == 2 ? kHalf : kSmem) - a.off_scale - 128) / a.M - 64;
+  const int fit = room / (C::CK * 2 + 4);
+  if (fit <= 0) return set_error(2, "matrix-vector: no room for X");
+  a.x_chunks = a.cta_chunks < fit ? a.cta_chunks : fit;
+  a.x_stride = (a.x_chunks * (C::CK * 2 / 64) | 1) * 64;
+  a.off_x = (a.off_scale + a.x_chunks * a.M * 4 + 127) / 128 * 128;
+  attr[0].val.clusterDim.y = static_cast<unsigned>(S);
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters), static_cast<unsigned>(S), 1);
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  cfg.dynamicSmemBytes = static_cast<size_t>(a.off_x) + static_cast<size_t>(a.M) * a.x_stride;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, a);
   return e == cudaSuccess ? 0 : set_error(4, "matrix-vector launch: %s", cudaGetErrorString(e));
 }

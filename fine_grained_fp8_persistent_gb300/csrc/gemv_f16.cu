@@ -4,12 +4,9 @@
 namespace fgf8 {
 namespace {
 
-// rows of weights per CTA by tokens, as for the 4-bit weights (gemv_fp4.cu); the weights
-// are four times the bytes, so 16 rows carry the traffic of X up to 8 tokens
 template <bool BF16>
 int by_rows(const GemvKArgs& k, cudaStream_t stream) {
-  if (k.M <= 8) return launch_gemv<WType::W16, BF16, 2, 1, 1>(k, stream);
-  return launch_gemv<WType::W16, BF16, 2, 2, 2>(k, stream);
+  return k.M <= 8 ? launch_gemv<WType::W16, BF16, 2, 1>(k, stream) : launch_gemv<WType::W16, BF16, 2, 2>(k, stream);
 }
 
 }  // namespace

@@ -5,13 +5,10 @@
 namespace fgf8 {
 namespace {
 
-// A CTA reads M * 2 bytes of X per element of K beside ROWS / 2 bytes of weights, so the
-// rows per CTA grow with M: 16 up to 4 tokens, 32 up to 8, 64 up to 16.
+// eight tokens per N = 8 instruction
 template <WType WT, bool BF16, int MATS>
 int by_rows(const GemvKArgs& k, cudaStream_t stream) {
-  if (k.M <= 4) return launch_gemv<WT, BF16, MATS, 1, 1>(k, stream);
-  if (k.M <= 8) return launch_gemv<WT, BF16, MATS, 1, 2>(k, stream);
-  return launch_gemv<WT, BF16, MATS, 2, 4>(k, stream);
+  return k.M <= 8 ? launch_gemv<WT, BF16, MATS, 1>(k, stream) : launch_gemv<WT, BF16, MATS, 2>(k, stream);
 }
 
 template <WType WT>
