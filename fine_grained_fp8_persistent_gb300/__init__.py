@@ -21,7 +21,8 @@ _EXPORTS = (
 def __getattr__(name):
     if name in _EXPORTS:
         from . import binding
-        return getattr(binding, name)
+        value = globals()[name] = getattr(binding, name)   # found at once from the next use on
+        return value
     raise AttributeError(name)
 
 

@@ -381,32 +381,68 @@ def gemm_fp4_blockscaled(aq, sfa, bq, sfb, fmt, out: torch.Tensor | None = None,
 
 
 # --------------------------------------------------------------------------- gated block, matrix-vector
+_ACTS = {"silu": ACT_SILU, "gelu_tanh": ACT_GELU_TANH}
+_CODE16 = {torch.float16: F16, torch.bfloat16: BF16}
+
+
 def _act(act) -> int:
-    if isinstance(act, str):
-        return {"silu": ACT_SILU, "gelu_tanh": ACT_GELU_TANH}[act.lower()]
-    return int(act)
+    return _ACTS[act.lower()] if isinstance(act, str) else int(act)
 
 
 def _dtype16(t: torch.Tensor, name: str) -> int:
-    if t.dtype not in (torch.float16, torch.bfloat16):
+    code = _CODE16.get(t.dtype)
+    if code is None:
         raise ValueError(f"{name} must be fp16 or bf16")
-    return BF16 if t.dtype == torch.bfloat16 else F16
+    return code
 
 
 def _need_like(t: torch.Tensor, shape: tuple, dtype: torch.dtype, name: str) -> None:
     """A 16-bit operand: exactly this shape and type."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
 
 
-def _empty(shape: tuple, like: torch.Tensor, stream, dtype: torch.dtype | None = None) -> torch.Tensor:
-    """torch.empty on `like`'s device, from the memory pool of the stream the call
+def _empty(shape: tuple, dtype: torch.dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """An empty tensor on `like`'s device, from the memory pool of the stream the call
     runs on: memory that is given back while the kernel still runs must not be
     handed to work on another stream."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _launch(name: str, stream, tensors: tuple, ints: tuple) -> None:
+    """Run one library entry point on `stream` (None: the current stream of the tensors'
+    device): pointers of `tensors`, then `ints`, then the stream.  A matrix-vector kernel
+    takes a few microseconds, so this does what _stream, _ptr and _call do without their
+    objects; the raw stream handle and the device come from the calls those make."""
+    device = tensors[0].get_device()
+    pointers = []
+    for t in tensors:
+        if t is None:
+            pointers.append(None)
+            continue
+        if t.get_device() != device or not t.is_contiguous():
+            _ptr(t)                                       # says why, unless the device is another one
+            raise ValueError(f"{name}: a tensor is on {t.device}, another one on {tensors[0].device}")
+        pointers.append(t.data_ptr())
+    if device < 0:
+        raise ValueError("tensors must live on a CUDA device")
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        if stream.device.index != device:
+            raise ValueError(f"{name}: the tensors are on {tensors[0].device} but the launch stream is on {stream.device}")
+        handle = stream.cuda_stream
+    fn = getattr(_lib, name)
+    if torch._C._cuda_getDevice() == device:
+        rc = fn(*pointers, *ints, handle)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*pointers, *ints, handle)
+    if rc != OK:
+        _check(rc, name)
 
 
 def gated_f16(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, act="silu", save: bool = False,
@@ -417,21 +453,21 @@ def gated_f16(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, act="silu", s
     G and U in the same type, which gated_f16_backward reads: (h, g, u)."""
     M, K = x.shape
     N = wg.shape[0]
-    dt = _dtype16(x, "x")
-    _need_like(wg, (N, K), x.dtype, "wg")
-    _need_like(wu, (N, K), x.dtype, "wu")
+    code, dtype = _dtype16(x, "x"), x.dtype
+    _need_like(wg, (N, K), dtype, "wg")
+    _need_like(wu, (N, K), dtype, "wu")
     if (g is None) != (u is None):
         raise ValueError("g and u: give both or neither")
     if out is None:
-        out = _empty((M, N), x, stream)
-    if save and g is None:
-        g, u = _empty((M, N), x, stream), _empty((M, N), x, stream)
-    _need_out(out, (M, N), (x.dtype,), "out")
+        out = _empty((M, N), dtype, x, stream)
+    else:
+        _need_like(out, (M, N), dtype, "out")
     if g is not None:
-        _need_out(g, (M, N), (x.dtype,), "g")
-        _need_out(u, (M, N), (x.dtype,), "u")
-    st = _stream(stream, x=x, wg=wg, wu=wu, out=out, g=g, u=u)
-    _call("gated_f16", st, _ptr(x), _ptr(wg), _ptr(wu), _ptr(out), _ptr(g), _ptr(u), M, N, K, dt, _act(act))
+        _need_like(g, (M, N), dtype, "g")
+        _need_like(u, (M, N), dtype, "u")
+    elif save:
+        g, u = _empty((M, N), dtype, x, stream), _empty((M, N), dtype, x, stream)
+    _launch("gated_f16", stream, (x, wg, wu, out, g, u), (M, N, K, code, _act(act)))
     return out if g is None else (out, g, u)
 
 
@@ -443,29 +479,24 @@ def gated_f16_backward(dh: torch.Tensor, x: torch.Tensor, wg: torch.Tensor, wu: 
     `workspace` (uint8, gated_backward_ws_bytes(M, N) bytes) is taken from torch when not given."""
     M, K = x.shape
     N = wg.shape[0]
-    dt = _dtype16(x, "x")
-    _need_like(wg, (N, K), x.dtype, "wg")
-    _need_like(wu, (N, K), x.dtype, "wu")
-    for name, t in (("dh", dh), ("g", g), ("u", u)):
-        _need_like(t, (M, N), x.dtype, name)
-    if dx is None:
-        dx = _empty((M, K), x, stream)
-    if dwg is None:
-        dwg = _empty((N, K), x, stream)
-    if dwu is None:
-        dwu = _empty((N, K), x, stream)
-    _need_out(dx, (M, K), (x.dtype,), "dx")
-    _need_out(dwg, (N, K), (x.dtype,), "dwg")
-    _need_out(dwu, (N, K), (x.dtype,), "dwu")
+    code, dtype = _dtype16(x, "x"), x.dtype
+    for name, t, shape in (("wg", wg, (N, K)), ("wu", wu, (N, K)), ("dh", dh, (M, N)), ("g", g, (M, N)),
+                           ("u", u, (M, N))):
+        _need_like(t, shape, dtype, name)
+    grads = []
+    for name, t, shape in (("dx", dx, (M, K)), ("dwg", dwg, (N, K)), ("dwu", dwu, (N, K))):
+        if t is None:
+            t = _empty(shape, dtype, x, stream)
+        else:
+            _need_like(t, shape, dtype, name)
+        grads.append(t)
     ws_bytes = gated_backward_ws_bytes(M, N)
     if workspace is None:
-        workspace = _empty((max(ws_bytes, 0),), x, stream, torch.uint8)
-    if workspace.numel() * workspace.element_size() < ws_bytes:
+        workspace = _empty((max(ws_bytes, 0),), torch.uint8, x, stream)
+    elif workspace.numel() * workspace.element_size() < ws_bytes:
         raise ValueError(f"workspace: expected {ws_bytes} bytes, got {workspace.numel() * workspace.element_size()}")
-    st = _stream(stream, dh=dh, x=x, wg=wg, wu=wu, g=g, u=u, dx=dx, dwg=dwg, dwu=dwu, workspace=workspace)
-    _call("gated_f16_backward", st, _ptr(dh), _ptr(x), _ptr(wg), _ptr(wu), _ptr(g), _ptr(u), _ptr(dx), _ptr(dwg),
-          _ptr(dwu), _ptr(workspace), M, N, K, dt, _act(act))
-    return dx, dwg, dwu
+    _launch("gated_f16_backward", stream, (dh, x, wg, wu, g, u, *grads, workspace), (M, N, K, code, _act(act)))
+    return tuple(grads)
 
 
 def gated_backward_ws_bytes(M: int, N: int) -> int:
@@ -473,9 +504,10 @@ def gated_backward_ws_bytes(M: int, N: int) -> int:
     return int(_lib.fgf8_gated_backward_ws_bytes(int(M), int(N)))
 
 
-def _need_fp4(wq: torch.Tensor, sf: torch.Tensor, N: int, K: int, fmt, names: tuple) -> None:
-    _need(wq, N * (K // 2), 1, names[0])
-    _need(sf, _numel(fp4_sf_shape(N, K, fmt)[0]), 4, names[1])
+def _need_fp4(wq: torch.Tensor, sf: torch.Tensor, N: int, K: int, fmt: int, wname: str, sname: str) -> None:
+    """Codes and scale table of quantize_fp4 for an N x K matrix."""
+    _need(wq, N * (K // 2), 1, wname)
+    _need(sf, (K // (32 if fmt == FP4_MX else 16) + 3) // 4 * ((N + 3) // 4 * 4), 4, sname)
 
 
 def gemv_fp4(x: torch.Tensor, wq: torch.Tensor, sf: torch.Tensor, fmt, out: torch.Tensor | None = None,
@@ -484,13 +516,13 @@ def gemv_fp4(x: torch.Tensor, wq: torch.Tensor, sf: torch.Tensor, fmt, out: torc
     weights (N, K) as quantize_fp4 writes them; Y has the type of X."""
     M, K = x.shape
     N = wq.shape[0]
-    dt = _dtype16(x, "x")
-    _need_fp4(wq, sf, N, K, fmt, ("wq", "sf"))
+    code, f = _dtype16(x, "x"), _fp4(fmt)
+    _need_fp4(wq, sf, N, K, f, "wq", "sf")
     if out is None:
-        out = _empty((M, N), x, stream)
-    _need_out(out, (M, N), (x.dtype,), "out")
-    st = _stream(stream, x=x, wq=wq, sf=sf, out=out)
-    _call("gemv_fp4", st, _ptr(x), _ptr(wq), _ptr(sf), _ptr(out), M, N, K, _fp4(fmt), dt)
+        out = _empty((M, N), x.dtype, x, stream)
+    else:
+        _need_like(out, (M, N), x.dtype, "out")
+    _launch("gemv_fp4", stream, (x, wq, sf, out), (M, N, K, f, code))
     return out
 
 
@@ -500,15 +532,14 @@ def gated_gemv_fp4(x: torch.Tensor, wgq: torch.Tensor, sfg: torch.Tensor, wuq: t
     MXFP4 or NVFP4 weights (N, K) as quantize_fp4 writes them, in one kernel."""
     M, K = x.shape
     N = wgq.shape[0]
-    dt = _dtype16(x, "x")
-    _need_fp4(wgq, sfg, N, K, fmt, ("wgq", "sfg"))
-    _need_fp4(wuq, sfu, N, K, fmt, ("wuq", "sfu"))
+    code, f = _dtype16(x, "x"), _fp4(fmt)
+    _need_fp4(wgq, sfg, N, K, f, "wgq", "sfg")
+    _need_fp4(wuq, sfu, N, K, f, "wuq", "sfu")
     if out is None:
-        out = _empty((M, N), x, stream)
-    _need_out(out, (M, N), (x.dtype,), "out")
-    st = _stream(stream, x=x, wgq=wgq, sfg=sfg, wuq=wuq, sfu=sfu, out=out)
-    _call("gated_gemv_fp4", st, _ptr(x), _ptr(wgq), _ptr(sfg), _ptr(wuq), _ptr(sfu), _ptr(out), M, N, K, _fp4(fmt),
-          dt, _act(act))
+        out = _empty((M, N), x.dtype, x, stream)
+    else:
+        _need_like(out, (M, N), x.dtype, "out")
+    _launch("gated_gemv_fp4", stream, (x, wgq, sfg, wuq, sfu, out), (M, N, K, f, code, _act(act)))
     return out
 
 

@@ -22,7 +22,7 @@
 // most 2^-39 of it, below the FP32 accumulation's own rounding.  The chunk's sums are
 // multiplied by the power's inverse as they are added to the totals.
 //
-// Work split.  One or two CTAs per SM, walking tiles of 16 weight rows; X (or as much of it as
+// Work split.  One CTA per SM, walking tiles of 16 weight rows; X (or as much of it as
 // fits) is converted and kept in shared memory once per CTA.  A round is up to WARPS tiles:
 // the 128-byte pieces ("chunks") of all their rows, tile after tile, are dealt to the warps
 // in equal contiguous runs, so every warp has the same work whatever the number of rows,
@@ -63,17 +63,20 @@ struct GemvKArgs {
   int off_sum;       // offsets of the joined sums (two buffers, read by the cluster), of
   int off_scale;     //   2^p of each chunk and row of X, and of X
   int off_x;
+  int prefetch;      // chunks of a warp's first run to ask into L2 ahead of the previous kernel's end
 };
 
-template <WType WT, int MATS, int NT>
+// DEEP: one CTA per SM with as many bytes in flight as fit; else half an SM's registers
+// and shared memory.
+template <WType WT, int MATS, int NT, bool DEEP>
 struct GemvCfg {
-  static constexpr int WARPS = MATS == 2 ? 8 : 12, THREADS = 32 * WARPS;
-  static constexpr int MIN_CTAS = NT == 1 ? 2 : 1;           // per SM
+  static constexpr int WARPS = MATS == 2 ? (DEEP && NT == 1 ? 12 : 8) : DEEP && NT == 1 ? 16 : 12, THREADS = 32 * WARPS;
+  static constexpr int MIN_CTAS = DEEP ? 1 : 2;              // per SM: bounds the registers
   static constexpr int CK = WT == WType::W16 ? 64 : 256;     // elements of K per chunk (128 bytes of a row)
   static constexpr int WPC = WT == WType::MX ? 2 : 4;        // scale words per row and chunk
   static constexpr int SF_BYTES = WT == WType::W16 ? 0 : WPC * 64;
   static constexpr int STAGE = MATS * (2048 + SF_BYTES);
-  static constexpr int DEPTH = 3;                            // ring slots of a warp
+  static constexpr int DEPTH = DEEP && MATS == 1 && NT == 1 ? 5 : 3;   // ring slots of a warp
   static constexpr int RING = WARPS * DEPTH * STAGE;
   static constexpr int OFF_SLOTS = RING;                     // [warp][2][MATS][M][16] partial sums
   static constexpr int slots_bytes(int M) { return WARPS * 2 * MATS * M * 64; }
@@ -93,6 +96,7 @@ __device__ __forceinline__ void cp4_full(uint32_t dst, const void* src) {
 __device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -185,9 +189,9 @@ __device__ __forceinline__ void gemv_store(const GemvKArgs& args, int n, int m, 
   store4(args.out, args, n, m, v[0], BF16);
 }
 
-template <WType WT, bool BF16, int MATS, int NT>
-__global__ void __launch_bounds__(GemvCfg<WT, MATS, NT>::THREADS, GemvCfg<WT, MATS, NT>::MIN_CTAS) gemv_kernel(const GemvKArgs args) {
-  using C = GemvCfg<WT, MATS, NT>;
+template <WType WT, bool BF16, int MATS, int NT, bool DEEP>
+__global__ void __launch_bounds__(GemvCfg<WT, MATS, NT, DEEP>::THREADS, GemvCfg<WT, MATS, NT, DEEP>::MIN_CTAS) gemv_kernel(const GemvKArgs args) {
+  using C = GemvCfg<WT, MATS, NT, DEEP>;
   using namespace gemv;
   constexpr bool kScaleX = WT != WType::W16 && BF16;   // bf16 X against fp16 weight values
   constexpr bool kMmaBf16 = WT == WType::W16 && BF16;
@@ -224,7 +228,27 @@ __global__ void __launch_bounds__(GemvCfg<WT, MATS, NT>::THREADS, GemvCfg<WT, MA
     r.chunk = b - r.tile * r.pc;
   };
 
-  // X and the weights may come from the previous kernel
+  // Under a programmatic dependent launch the previous kernel may still be running.  Its
+  // outputs (X, perhaps the weights) are read only after the wait below; until then this
+  // warp asks for the weights of its first run to be brought into L2, the memory's point of
+  // coherence, which reads nothing into the kernel.
+  if (args.prefetch > 0) {
+    Run r{0, 0, 0, 0, 0, 0};
+    run_set(r);
+    const int half = lane >> 4;                            // two chunks at a time, a row per lane
+    for (int i = half; i < r.left && i < args.prefetch; i += 2) {
+      const int at = r.tile * r.pc + r.chunk + i, tile = at / r.pc, gc = c0 + at - tile * r.pc;
+      const int row = (tile0 + tile) * 16 + (lane & 15);
+#pragma unroll
+      for (int j = 0; j < MATS; ++j) {
+        if (row < N) {
+          prefetch_l2(static_cast<const uint8_t*>(args.W[j]) + static_cast<size_t>(row) * row_bytes + static_cast<size_t>(gc) * 128);
+          if (WT != WType::W16 && (lane & 15) < C::WPC && gc * C::WPC + (lane & 15) < sf_words)
+            prefetch_l2(static_cast<const uint32_t*>(args.SF[j]) + static_cast<size_t>(gc * C::WPC + (lane & 15)) * sf_ld + (tile0 + tile) * 16);
+        }
+      }
+    }
+  }
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
 
@@ -334,39 +358,50 @@ __global__ void __launch_bounds__(GemvCfg<WT, MATS, NT>::THREADS, GemvCfg<WT, MA
         const int k0 = (c0 + piece * args.x_chunks) * C::CK;
         // one warp takes 256 columns of a row, 8 per lane (zeros past K)
         const int blocks = (xn * C::CK + 255) / 256;
-        for (int it = warp; it < M * blocks; it += W) {
-          const int m = it / blocks, blk = it - m * blocks, v = blk * 32 + lane;
-          uint4 w = make_uint4(0u, 0u, 0u, 0u);
-          if (k0 + 8 * v < K)
-            w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(args.X) + static_cast<size_t>(m) * K + k0 + 8 * v));
-          uint32_t u[4] = {w.x, w.y, w.z, w.w};
-          if constexpr (WT == WType::W16) {
-            // element 8 s + 2 t + i of each 32 goes to 8 t + 2 s + i: lane t's four pairs side by side
-            if (8 * v < xn * C::CK) {
-              const uint32_t d = xs + static_cast<uint32_t>(m * args.x_stride + (v >> 2) * 64 + (v & 3) * 4);
+        // four loads in flight per lane
+        for (int it0 = warp; it0 < M * blocks; it0 += 4 * W) {
+          uint4 w[4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) asm volatile("st.shared.b32 [%0], %1;" ::"r"(d + 16 * j), "r"(u[j]) : "memory");
-            }
-          } else {
-            if constexpr (kScaleX) {
-              uint32_t a = 0u;                            // largest finite |x|, as bf16 bits
+          for (int q = 0; q < 4; ++q) {
+            const int it = it0 + q * W, m = it / blocks, v = (it - m * blocks) * 32 + lane;
+            w[q] = make_uint4(0u, 0u, 0u, 0u);
+            if (it < M * blocks && k0 + 8 * v < K)
+              w[q] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(args.X) + static_cast<size_t>(m) * K + k0 + 8 * v));
+          }
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const uint32_t lo = u[j] & 0x7FFFu, hi = (u[j] >> 16) & 0x7FFFu;
-                a = max(a, lo < 0x7F80u ? lo : 0u);
-                a = max(a, hi < 0x7F80u ? hi : 0u);
+          for (int q = 0; q < 4; ++q) {
+            const int it = it0 + q * W;
+            if (it >= M * blocks) break;
+            const int m = it / blocks, blk = it - m * blocks, v = blk * 32 + lane;
+            uint32_t u[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+            if constexpr (WT == WType::W16) {
+              // element 8 s + 2 t + i of each 32 goes to 8 t + 2 s + i: lane t's four pairs side by side
+              if (8 * v < xn * C::CK) {
+                const uint32_t d = xs + static_cast<uint32_t>(m * args.x_stride + (v >> 2) * 64 + (v & 3) * 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) asm volatile("st.shared.b32 [%0], %1;" ::"r"(d + 16 * j), "r"(u[j]) : "memory");
               }
-              a = __reduce_max_sync(0xffffffffu, a);
-              // x * 2^sh in two exact steps (sh reaches 141); 2^-sh is an FP32 value, a
-              // subnormal from sh = 127 on
-              const int sh = 141 - (a ? static_cast<int>(a >> 7) : 127), s1 = sh / 2, s2 = sh - s1;
-              const float f1 = __uint_as_float(static_cast<uint32_t>(127 + s1) << 23), f2 = __uint_as_float(static_cast<uint32_t>(127 + s2) << 23);
+            } else {
+              if constexpr (kScaleX) {
+                uint32_t a = 0u;                            // largest finite |x|, as bf16 bits
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                u[j] = pack_2x16(__uint_as_float(u[j] << 16) * f1 * f2, __uint_as_float(u[j] & 0xFFFF0000u) * f1 * f2, false);
-              if (lane == 0) xscale[blk * M + m] = sh < 127 ? __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) : __uint_as_float(1u << (149 - sh));
+                for (int j = 0; j < 4; ++j) {
+                  const uint32_t lo = u[j] & 0x7FFFu, hi = (u[j] >> 16) & 0x7FFFu;
+                  a = max(a, lo < 0x7F80u ? lo : 0u);
+                  a = max(a, hi < 0x7F80u ? hi : 0u);
+                }
+                a = __reduce_max_sync(0xffffffffu, a);
+                // x * 2^sh in two exact steps (sh reaches 141); 2^-sh is an FP32 value, a
+                // subnormal from sh = 127 on
+                const int sh = 141 - (a ? static_cast<int>(a >> 7) : 127), s1 = sh / 2, s2 = sh - s1;
+                const float f1 = __uint_as_float(static_cast<uint32_t>(127 + s1) << 23), f2 = __uint_as_float(static_cast<uint32_t>(127 + s2) << 23);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  u[j] = pack_2x16(__uint_as_float(u[j] << 16) * f1 * f2, __uint_as_float(u[j] & 0xFFFF0000u) * f1 * f2, false);
+                if (lane == 0) xscale[blk * M + m] = sh < 127 ? __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) : __uint_as_float(1u << (149 - sh));
+              }
+              st_shared_v4(xs + static_cast<uint32_t>(m * args.x_stride + v * 16), u[0], u[1], u[2], u[3]);
             }
-            st_shared_v4(xs + static_cast<uint32_t>(m * args.x_stride + v * 16), u[0], u[1], u[2], u[3]);
           }
         }
         __syncthreads();
@@ -610,95 +645,144 @@ __global__ void __launch_bounds__(GemvCfg<WT, MATS, NT>::THREADS, GemvCfg<WT, MA
   cp_wait<0>();
 }
 
-// Launch: shares of the reduction, tiles per CTA, and how much of X stays in shared memory.
-template <WType WT, bool BF16, int MATS, int NT>
-int launch_gemv(GemvKArgs a, cudaStream_t stream) {
-  using C = GemvCfg<WT, MATS, NT>;
-  auto* fn = &gemv_kernel<WT, BF16, MATS, NT>;
-  constexpr int kSmem = 232448;
-  constexpr int kHalf = 115712;                           // two CTAs per SM (227 KB with 1 KB reserved each)
-  static int max_clusters[64][4] = {};                    // by device and log2 of the cluster size
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64) return set_error(2, "device id %d", dev);
+// How a call is laid out: log2 of the cluster, clusters, shared memory, tiles and X per CTA.
+struct GemvPlan {
+  double ns;
+  int log_s, clusters, smem;
+  GemvKArgs a;
+};
+
+template <WType WT, bool BF16, int MATS, int NT, bool DEEP>
+struct GemvLaunch {
+  using C = GemvCfg<WT, MATS, NT, DEEP>;
+  static constexpr int kSmem = 232448;
+  static constexpr auto kernel = &gemv_kernel<WT, BF16, MATS, NT, DEEP>;
+
   cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof(cfg));
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.blockDim = dim3(C::THREADS, 1, 1);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  if (max_clusters[dev][0] == 0) {
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    cfg.numAttrs = 1;
-    for (int i = 3; e == cudaSuccess && i >= 0; --i) {
-      attr[0].val.clusterDim.y = 1u << i;
-      cfg.gridDim = dim3(static_cast<unsigned>(device_sm_count() >> i), 1u << i, 1);
-      int n = 0;
-      e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
-      if (e == cudaSuccess && n <= 0) e = cudaErrorInvalidConfiguration;
-      if (e == cudaSuccess) max_clusters[dev][i] = n;
-    }
-    if (e != cudaSuccess) return set_error(4, "matrix-vector set-up: %s", cudaGetErrorString(e));
+  GemvLaunch(int log_s, int clusters, int smem, cudaStream_t stream) {
+    std::memset(&cfg, 0, sizeof(cfg));
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = 1u << log_s;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters), 1u << log_s, 1);
+    cfg.blockDim = dim3(C::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
   }
-  a.chunks = (a.K + C::CK - 1) / C::CK;
-  a.tiles = (a.N + 15) / 16;
-  const int slots = C::OFF_SLOTS + C::slots_bytes(a.M);
-  // Shares of the reduction: the split with the least time by this model (ns): chunks of
-  // the busiest SM at its share of the memory rate, X to stage, a cluster's joins.
-  double best = -1.0;
-  int S = 1, log_s = 0, per_sm = 1;
-  for (int i = 0; i < 4; ++i) {
-    const int s = 1 << i, per = (a.chunks + s - 1) / s;
-    if ((s - 1) * per >= a.chunks) continue;              // a CTA without work
-    const double x_bytes = static_cast<double>(per) * (C::CK * 2 + 4) * a.M;
-    for (int two = 0; two < C::MIN_CTAS; ++two) {
-      const double room = (two ? kHalf : kSmem) - slots - 16384.0 - 128.0 - 64.0 * a.M;
-      if (two && x_bytes > room) continue;
-      const int tiles = (a.tiles + max_clusters[dev][i] - 1) / max_clusters[dev][i];   // of an SM, over its CTAs
-      if (two && tiles < 2) continue;
-      const double pieces = x_bytes > room ? static_cast<double>((tiles + C::WARPS - 1) / C::WARPS) : 1.0;
-      const double ns = static_cast<double>(tiles) * per * (C::STAGE / 40.0) + pieces * x_bytes / 50.0 + (s > 1 ? 2500.0 : 0.0) - two;
-      if (best < 0 || ns < best) {
-        best = ns;
-        S = s;
-        log_s = i;
-        per_sm = 1 << two;
+
+  // Clusters of 2^log_s CTAs that fit the device at one CTA per SM; null on an error.
+  static const int* max_clusters() {
+    static int fit[64][4] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) {
+      set_error(2, "device id %d", dev);
+      return nullptr;
+    }
+    if (fit[dev][0] == 0) {
+      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      for (int i = 3; e == cudaSuccess && i >= 0; --i) {
+        GemvLaunch l(i, device_sm_count() >> i, kSmem, nullptr);
+        l.cfg.numAttrs = 1;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, kernel, &l.cfg);
+        if (e == cudaSuccess && n <= 0) e = cudaErrorInvalidConfiguration;
+        if (e == cudaSuccess) fit[dev][i] = n;
+      }
+      if (e != cudaSuccess) {
+        fit[dev][0] = 0;
+        set_error(4, "matrix-vector set-up: %s", cudaGetErrorString(e));
+        return nullptr;
       }
     }
+    return fit[dev];
   }
-  a.cta_chunks = (a.chunks + S - 1) / S;
-  const int slots_cap = max_clusters[dev][log_s] * per_sm;
-  const int clusters = a.tiles < slots_cap ? a.tiles : slots_cap;
-  a.cta_tiles = a.tiles / clusters;
-  a.extra = a.tiles % clusters;
-  // rounds of equal size, at most WARPS tiles and 8 KB of joined sums
-  const int sum_cap = 8192 / (MATS * a.M * 64);
-  const int most = C::WARPS < sum_cap ? C::WARPS : sum_cap;
-  const int cta_most = a.cta_tiles + (a.extra > 0 ? 1 : 0);
-  const int rounds = (cta_most + most - 1) / most;
-  a.round_tiles = (cta_most + rounds - 1) / rounds;
-  a.off_sum = slots;
-  a.off_scale = slots + 2 * MATS * a.round_tiles * a.M * 64;
-  // X: rows an odd number of 64-byte units apart (bank conflicts), and a scale per row and chunk
-  const int room = ((per_sm == 2 ? kHalf : kSmem) - a.off_scale - 128) / a.M - 64;
-  const int fit = room / (C::CK * 2 + 4);
-  if (fit <= 0) return set_error(2, "matrix-vector: no room for X");
-  a.x_chunks = a.cta_chunks < fit ? a.cta_chunks : fit;
-  a.x_stride = (a.x_chunks * (C::CK * 2 / 64) | 1) * 64;
-  a.off_x = (a.off_scale + a.x_chunks * a.M * 4 + 127) / 128 * 128;
-  attr[0].val.clusterDim.y = static_cast<unsigned>(S);
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters), static_cast<unsigned>(S), 1);
-  cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  cfg.dynamicSmemBytes = static_cast<size_t>(a.off_x) + static_cast<size_t>(a.M) * a.x_stride;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, a);
-  return e == cudaSuccess ? 0 : set_error(4, "matrix-vector launch: %s", cudaGetErrorString(e));
+
+  // The layout with the least time by a simple model (ns): the chunks of the busiest SM, X
+  // to stage, a cluster's joins.  Measured on a GB300: 40 bytes per ns and SM on half an
+  // SM's resources; 48 with the deep rings, which cost 1 us more (the next kernel's CTAs
+  // find no room before this one's exit).  One token at N = K = 7168 in MXFP4 (three tiles
+  // per SM) takes 8.5 us shallow and 9.3 us deep, N = 32768 28.8 and 23.1 us.
+  static bool plan(GemvPlan& best, const GemvKArgs& args) {
+    const int* fit = max_clusters();
+    if (fit == nullptr) return false;
+    const int chunks = (args.K + C::CK - 1) / C::CK, all_tiles = (args.N + 15) / 16;
+    const int slots = C::OFF_SLOTS + C::slots_bytes(args.M);
+    // 8 KB of joined sums in each of the two buffers, padding of X
+    const double room = kSmem - slots - 16384.0 - 128.0 - 64.0 * args.M;
+    if (room < 2.0 * (C::CK * 2 + 4) * args.M) return true;
+    int log_s = -1;
+    for (int i = 0; i < 4; ++i) {
+      const int s = 1 << i, per = (chunks + s - 1) / s;
+      if ((s - 1) * per >= chunks) continue;              // a CTA without work
+      const double x_bytes = static_cast<double>(per) * (C::CK * 2 + 4) * args.M;
+      const int tiles = (all_tiles + fit[i] - 1) / fit[i];
+      const double pieces = x_bytes > room ? static_cast<double>((tiles + C::WARPS - 1) / C::WARPS) : 1.0;
+      const double ns = static_cast<double>(tiles) * per * C::STAGE / (DEEP ? 48.0 : 40.0) + pieces * x_bytes / 50.0 +
+                        (s > 1 ? 2500.0 : 0.0) + (DEEP ? 1000.0 : 0.0);
+      if (best.ns >= 0 && ns >= best.ns) continue;
+      best.ns = ns;
+      log_s = i;
+    }
+    if (log_s < 0) return true;                           // the other variant is ahead
+    GemvKArgs& a = best.a;
+    a = args;
+    a.chunks = chunks;
+    a.tiles = all_tiles;
+    a.cta_chunks = (chunks + (1 << log_s) - 1) >> log_s;
+    best.log_s = log_s;
+    best.clusters = all_tiles < fit[log_s] ? all_tiles : fit[log_s];
+    a.cta_tiles = all_tiles / best.clusters;
+    a.extra = all_tiles % best.clusters;
+    // rounds of equal size, at most WARPS tiles and 8 KB of joined sums
+    const int sum_cap = 8192 / (MATS * args.M * 64);
+    const int most = C::WARPS < sum_cap ? C::WARPS : sum_cap;
+    const int cta_most = a.cta_tiles + (a.extra > 0 ? 1 : 0);
+    const int rounds = (cta_most + most - 1) / most;
+    a.round_tiles = (cta_most + rounds - 1) / rounds;
+    a.off_sum = slots;
+    a.off_scale = slots + 2 * MATS * a.round_tiles * args.M * 64;
+    // X: rows an odd number of 64-byte units apart (bank conflicts), a scale per row and chunk
+    const int fit_x = ((kSmem - a.off_scale - 128) / args.M - 64) / (C::CK * 2 + 4);
+    a.x_chunks = a.cta_chunks < fit_x ? a.cta_chunks : fit_x;
+    a.x_stride = (a.x_chunks * (C::CK * 2 / 64) | 1) * 64;
+    a.off_x = (a.off_scale + a.x_chunks * args.M * 4 + 127) / 128 * 128;
+    a.prefetch = pdl_enabled() ? 4 : 0;
+    best.smem = a.off_x + args.M * a.x_stride;
+    return true;
+  }
+
+  static int launch(const GemvPlan& p, cudaStream_t stream) {
+    GemvLaunch l(p.log_s, p.clusters, p.smem, stream);
+    const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kernel, p.a);
+    return e == cudaSuccess ? 0 : set_error(4, "matrix-vector launch: %s", cudaGetErrorString(e));
+  }
+};
+
+template <WType WT, bool BF16, int MATS, int NT>
+int launch_gemv(const GemvKArgs& args, cudaStream_t stream) {
+  GemvPlan p;
+  p.ns = -1.0;
+  if constexpr (NT == 2) {
+    using D = GemvLaunch<WT, BF16, MATS, NT, true>;
+    if (!D::plan(p, args)) return 4;
+    if (p.ns < 0) return set_error(2, "matrix-vector: no room for X");
+    return D::launch(p, stream);
+  } else {
+    using D = GemvLaunch<WT, BF16, MATS, NT, true>;
+    using L = GemvLaunch<WT, BF16, MATS, NT, false>;
+    if (!L::plan(p, args)) return 4;
+    const double shallow = p.ns;
+    if (!D::plan(p, args)) return 4;
+    if (p.ns < 0) return set_error(2, "matrix-vector: no room for X");
+    return p.ns < shallow || shallow < 0 ? D::launch(p, stream) : L::launch(p, stream);
+  }
 }
 
 }  // namespace fgf8

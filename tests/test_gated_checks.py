@@ -98,9 +98,7 @@ class _Recorder:
 def fg(monkeypatch):
     from fine_grained_fp8_persistent_gb300 import binding
     rec = _Recorder()
-    monkeypatch.setattr(binding, "_ptr", lambda t: None if t is None else t.data_ptr())
-    monkeypatch.setattr(binding, "_stream", lambda stream=None, **t: binding._Stream(0, None))
-    monkeypatch.setattr(binding, "_call", lambda name, st, *args: rec.calls.append(name))
+    monkeypatch.setattr(binding, "_launch", lambda name, stream, tensors, ints: rec.calls.append(name))
     binding.recorder = rec
     return binding
 
@@ -167,8 +165,13 @@ def test_non_contiguous_tensors_are_refused():
 
         def is_contiguous(self):
             return False
+
+        def get_device(self):
+            return 0
     with pytest.raises(ValueError, match="contiguous"):
-        binding._ptr(Fake())
+        binding._launch("gemv_fp4", None, (Fake(),), ())
+    with pytest.raises(ValueError, match="CUDA device"):
+        binding._launch("gemv_fp4", None, (z(2, 2),), ())
 
 
 def test_package_exports():
