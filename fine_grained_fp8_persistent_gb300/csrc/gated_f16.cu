@@ -21,8 +21,6 @@ template <int ACT, bool BF16>
 __global__ void __launch_bounds__(256) slope_kernel(const uint4* __restrict__ dh, const uint4* __restrict__ g,
                                                     const uint4* __restrict__ u, uint4* __restrict__ dg,
                                                     uint4* __restrict__ du, long long n8) {
-  ptx::griddep_wait();
-  ptx::griddep_launch_dependents();
   for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n8; i += gridDim.x * 256LL) {
     const uint4 a = dh[i], b = g[i], c = u[i];
     const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w}, cw[4] = {c.x, c.y, c.z, c.w};
@@ -47,12 +45,12 @@ __global__ void __launch_bounds__(256) slope_kernel(const uint4* __restrict__ dh
 }
 
 // ----------------------------------------------------------------- launches
-// Launch configuration with a cluster of `cluster` CTAs and, when enabled,
-// programmatic stream serialization.
+// Launch configuration with a cluster of `cluster` CTAs and, for the forward pass when
+// enabled, programmatic stream serialization.
 struct Launch {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  Launch(unsigned grid, unsigned threads, size_t smem, int cluster, cudaStream_t stream) {
+  Launch(unsigned grid, unsigned threads, size_t smem, int cluster, cudaStream_t stream, bool pdl) {
     std::memset(&cfg, 0, sizeof(cfg));
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
@@ -65,7 +63,7 @@ struct Launch {
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    cfg.numAttrs = pdl ? 2 : 1;
   }
 };
 
@@ -82,8 +80,7 @@ int launch_gemm(const GatedMaps& tm, const GatedGemmArgs& args, cudaStream_t str
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
     int clusters = device_sm_count();
     if (e == cudaSuccess && NCTA > 1) {
-      Launch probe(static_cast<unsigned>(device_sm_count() / NCTA * NCTA), C::THREADS, C::SMEM_BYTES, NCTA, stream);
-      probe.cfg.numAttrs = 1;
+      Launch probe(static_cast<unsigned>(device_sm_count() / NCTA * NCTA), C::THREADS, C::SMEM_BYTES, NCTA, stream, false);
       e = cudaOccupancyMaxActiveClusters(&clusters, fn, &probe.cfg);
     }
     if (e != cudaSuccess || clusters <= 0) return set_error(4, "gated_f16 occupancy: %s", cudaGetErrorString(e));
@@ -94,7 +91,7 @@ int launch_gemm(const GatedMaps& tm, const GatedGemmArgs& args, cudaStream_t str
   if (tiles > 0x7F000000LL) return set_error(2, "gated_f16: problem too large");
   const long long clusters = persistent_clusters(tiles, NCTA, device_sm_count(), max_clusters[dev], sm_cap_enabled());
   set_last_tile("f16", OP == GatedOp::Forward ? "gated" : OP == GatedOp::GradX ? "grad_x" : "grad_w", NCTA, BN);
-  Launch l(static_cast<unsigned>(clusters * NCTA), C::THREADS, C::SMEM_BYTES, NCTA, stream);
+  Launch l(static_cast<unsigned>(clusters * NCTA), C::THREADS, C::SMEM_BYTES, NCTA, stream, C::kFwd && pdl_enabled());
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, fn, tm, args);
   return e == cudaSuccess ? 0 : set_error(4, "gated_f16 launch: %s", cudaGetErrorString(e));
 }
@@ -203,7 +200,7 @@ template <int ACT>
 int slopes(const GatedArgs& a, const void* dH, const void* G, const void* U, void* dG, void* dU, cudaStream_t stream) {
   const long long n8 = static_cast<long long>(a.M) * a.N / 8;
   const long long want = (n8 + 255) / 256, cap = 8LL * device_sm_count();
-  Launch l(static_cast<unsigned>(want < cap ? want : cap), 256, 0, 1, stream);
+  Launch l(static_cast<unsigned>(want < cap ? want : cap), 256, 0, 1, stream, false);
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, a.bf16 ? slope_kernel<ACT, true> : slope_kernel<ACT, false>, static_cast<const uint4*>(dH),
                                            static_cast<const uint4*>(G), static_cast<const uint4*>(U), static_cast<uint4*>(dG),
                                            static_cast<uint4*>(dU), n8);

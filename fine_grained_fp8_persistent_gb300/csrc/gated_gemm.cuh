@@ -151,9 +151,12 @@ __global__ void __launch_bounds__(GatedCfg<OP, NCTA, BN, STAGES>::THREADS, 1)
     tc_alloc<NCTA>(ptx::smem_u32(tmem_slot), C::TMEM_ALLOC);
     ptx::tc_fence_before();
   }
-  // nothing above reads global memory: it overlaps the tail of the previous kernel
-  ptx::griddep_wait();
-  ptx::griddep_launch_dependents();
+  // Forward: nothing above reads global memory, so it overlaps the tail of the previous
+  // kernel.  No kernel here lets the next one start early: with programmatic launches
+  // through the backward pass (elementwise kernel, GradX, GradW, and the next call's
+  // elementwise kernel waiting beside GradW, more CTAs than fit) a queue of calls at
+  // 4096 x 7168 x 2048 stopped for good, outside any wait of these kernels.
+  if constexpr (C::kFwd) ptx::griddep_wait();
   __syncthreads();
   if constexpr (NCTA == 2) cluster_sync_all();
   ptx::tc_fence_after();
@@ -317,8 +320,11 @@ __global__ void __launch_bounds__(GatedCfg<OP, NCTA, BN, STAGES>::THREADS, 1)
                      pack_2x16(v[8 * j + 4], v[8 * j + 5], bf16), pack_2x16(v[8 * j + 6], v[8 * j + 7], bf16));
       ptx::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0 && y < args.rows && x < args.cols) ptx::tma_store_2d(map, buf, x, y);
-      if (lane == 0) ptx::bulk_commit_group();
+      if (lane == 0) {
+        if (y < args.rows && x < args.cols) ptx::tma_store_2d(map, buf, x, y);
+        ptx::bulk_commit_group();
+      }
+      __syncwarp();                                       // the next TMEM load is a whole-warp instruction
       ++stored;
     };
     for (int t = first; t < num_tiles; t += step) {

@@ -315,8 +315,8 @@ FGF8_API const char* fgf8_last_tile(void);
 FGF8_API int fgf8_selftest_wait_timeout(void* stream);
 
 /* Programmatic dependent launch (on by default; the environment variable
- * FGF8_PDL=0 turns it off at first use).  When on, every kernel is launched with
- * programmatic stream serialization: its set-up (barriers, TMEM, descriptor
+ * FGF8_PDL=0 turns it off at first use).  When on, every kernel but those of
+ * gated_f16_backward is launched with programmatic stream serialization: its set-up (barriers, TMEM, descriptor
  * prefetch) overlaps the end of the previous kernel on the stream, and it reads no
  * global data before that kernel has completed.  enable: 1 on, 0 off, anything
  * else leaves it unchanged.  Returns the previous setting. */
