@@ -55,13 +55,14 @@ struct GemvKArgs {
   int tiles;         // tiles of 16 weight rows: cta_tiles per cluster, one more for the
   int cta_tiles;     //   first `extra` clusters
   int extra;
+  int group_tiles;   // tiles whose sums are kept while X goes through in pieces
   int round_tiles;   // tiles of one round, at most WARPS
   int chunks;        // chunks of the whole reduction
   int cta_chunks;    // chunks of one CTA's share of it (every CTA has at least one)
   int x_chunks;      // chunks of X in shared memory at a time
   int x_stride;      // bytes between rows of X in shared memory
-  int off_sum;       // offsets of the joined sums (two buffers, read by the cluster), of
-  int off_scale;     //   2^p of each chunk and row of X, and of X
+  int off_sum;       // offsets of a group's joined sums (read by the cluster), of 2^p of
+  int off_scale;     //   each chunk and row of X, and of X
   int off_x;
   int prefetch;      // chunks of a warp's first run to ask into L2 ahead of the previous kernel's end
 };
@@ -70,7 +71,7 @@ struct GemvKArgs {
 // and shared memory.
 template <WType WT, int MATS, int NT, bool DEEP>
 struct GemvCfg {
-  static constexpr int WARPS = MATS == 2 ? (DEEP && NT == 1 ? 12 : 8) : DEEP && NT == 1 ? 16 : 12, THREADS = 32 * WARPS;
+  static constexpr int WARPS = MATS == 2 ? (DEEP && NT == 1 ? 12 : 8) : DEEP ? 16 : 12, THREADS = 32 * WARPS;
   static constexpr int MIN_CTAS = DEEP ? 1 : 2;              // per SM: bounds the registers
   static constexpr int CK = WT == WType::W16 ? 64 : 256;     // elements of K per chunk (128 bytes of a row)
   static constexpr int WPC = WT == WType::MX ? 2 : 4;        // scale words per row and chunk
@@ -108,15 +109,15 @@ __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   if constexpr (BF16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // D = A B, no addend.
 __device__ __forceinline__ void mma16816_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
                : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 // Eight E2M1 codes (low nibble first) to four fp16 pairs.
@@ -151,8 +152,12 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-__device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+__device__ __forceinline__ void lds128(const uint8_t* p, uint32_t (&r)[4]) {
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
+  r[0] = v.x;
+  r[1] = v.y;
+  r[2] = v.z;
+  r[3] = v.w;
 }
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
   float4 v;
@@ -214,13 +219,16 @@ __global__ void __launch_bounds__(GemvCfg<WT, MATS, NT, DEEP>::THREADS, GemvCfg<
   const int sf_words = WT == WType::W16 ? 0 : (K / SV + 3) / 4;
   const int sf_ld = (N + 3) / 4 * 4;
 
-  // A run: this warp's chunks of one round and piece of X.
+  // A run: this warp's chunks of one round and piece of X.  The order is: groups of tiles,
+  // pieces of X, rounds of a group (all but the rounds are usually one).
   struct Run {
-    int round, piece;
+    int group, piece, round;     // first tile of the group, piece, first tile of the round (of this CTA's)
     int tile, chunk, left, pc;   // tile within the round, chunk within the piece, chunks left, chunks per piece
   };
+  auto group_end = [&](int group) { return min(group + args.group_tiles, my_tiles); };
+  auto round_size = [&](int group, int round) { return min(args.round_tiles, group_end(group) - round); };
   auto run_set = [&](Run& r) {
-    const int T = min(args.round_tiles, my_tiles - r.round * args.round_tiles);
+    const int T = round_size(r.group, r.round);
     r.pc = min(args.x_chunks, nc - r.piece * args.x_chunks);
     const int U = T * r.pc, b = warp * U / W;
     r.left = (warp + 1) * U / W - b;
@@ -233,7 +241,7 @@ __global__ void __launch_bounds__(GemvCfg<WT, MATS, NT, DEEP>::THREADS, GemvCfg<
   // warp asks for the weights of its first run to be brought into L2, the memory's point of
   // coherence, which reads nothing into the kernel.
   if (args.prefetch > 0) {
-    Run r{0, 0, 0, 0, 0, 0};
+    Run r{0, 0, 0, 0, 0, 0, 0};
     run_set(r);
     const int half = lane >> 4;                            // two chunks at a time, a row per lane
     for (int i = half; i < r.left && i < args.prefetch; i += 2) {
@@ -260,24 +268,29 @@ __global__ void __launch_bounds__(GemvCfg<WT, MATS, NT, DEEP>::THREADS, GemvCfg<
   const uint32_t dst_a = static_cast<uint32_t>(cr * 128 + ((cp ^ cr) << 4)), dst_b = dst_a ^ 64u;
   const size_t rows4 = 4 * row_bytes;
   const int full_chunks = static_cast<int>(row_bytes / 128);   // chunks with no column past K
-  Run pf{0, 0, 0, 0, 0, 0};
+  Run pf{0, 0, 0, 0, 0, 0, 0};
   run_set(pf);
   bool pf_end = false, pf_new = true, pf_rows = false;
   int pf_slot = 0, gc = 0, row0 = 0;
   const uint8_t* wp[MATS] = {};
   const uint32_t* sp[MATS] = {};
   auto issue = [&]() {
-    while (pf.left == 0 && !pf_end) {                     // the next piece or round with work for this warp
-      if (++pf.piece >= pieces) {
-        pf.piece = 0;
-        if (++pf.round * args.round_tiles >= my_tiles) { pf_end = true; break; }
+    while (pf.left == 0 && !pf_end) {                     // the next run with work for this warp
+      pf.round += args.round_tiles;
+      if (pf.round >= group_end(pf.group)) {
+        pf.round = pf.group;
+        if (++pf.piece >= pieces) {
+          pf.piece = 0;
+          pf.round = pf.group += args.group_tiles;
+          if (pf.group >= my_tiles) { pf_end = true; break; }
+        }
       }
       run_set(pf);
       pf_new = true;
     }
     if (!pf_end) {
       if (pf_new) {                                       // a new tile: row pointers
-        row0 = (tile0 + pf.round * args.round_tiles + pf.tile) * 16;
+        row0 = (tile0 + pf.round + pf.tile) * 16;
         gc = c0 + pf.piece * args.x_chunks + pf.chunk;
         pf_rows = row0 + 16 <= N;
 #pragma unroll
@@ -345,15 +358,16 @@ __global__ void __launch_bounds__(GemvCfg<WT, MATS, NT, DEEP>::THREADS, GemvCfg<
 
   // this lane's rows of X (columns of the MMA); columns past M repeat the last row and
   // are never stored
-  uint32_t xl[NT];
+  const uint8_t* xl[NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) xl[n] = xs + static_cast<uint32_t>(min(8 * n + g, M - 1) * args.x_stride + t * 16);
+  for (int n = 0; n < NT; ++n) xl[n] = smem + args.off_x + static_cast<uint32_t>(min(8 * n + g, M - 1) * args.x_stride + t * 16);
 
-  for (int round = 0; round * args.round_tiles < my_tiles; ++round) {
-    const int T = min(args.round_tiles, my_tiles - round * args.round_tiles);
-    for (int piece = 0; piece < pieces; ++piece) {
+  for (int group = 0; group < my_tiles; group += args.group_tiles) {
+   for (int piece = 0; piece < pieces; ++piece) {
+    for (int round = group; round < group_end(group); round += args.round_tiles) {
+      const int T = round_size(group, round);
       // -------------------------------------------------------- a piece of X
-      if (pieces > 1 || round == 0) {
+      if (round == group && (pieces > 1 || group == 0)) {
         const int xn = min(args.x_chunks, nc - piece * args.x_chunks);
         const int k0 = (c0 + piece * args.x_chunks) * C::CK;
         // one warp takes 256 columns of a row, 8 per lane (zeros past K)
@@ -383,21 +397,36 @@ __global__ void __launch_bounds__(GemvCfg<WT, MATS, NT, DEEP>::THREADS, GemvCfg<
               }
             } else {
               if constexpr (kScaleX) {
-                uint32_t a = 0u;                            // largest finite |x|, as bf16 bits
+                // largest |x| of the 256 columns as bf16 bits; infinities and NaN are left
+                // out of it, in a second look that only rows with them take
+                uint32_t a2 = 0u;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) a2 = __vmaxu2(a2, u[j] & 0x7FFF7FFFu);
+                uint32_t a = __reduce_max_sync(0xffffffffu, max(a2 & 0xFFFFu, a2 >> 16));
+                if (a >= 0x7F80u) {
+                  a = 0u;
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    const uint32_t lo = u[j] & 0x7FFFu, hi = (u[j] >> 16) & 0x7FFFu;
+                    a = max(a, lo < 0x7F80u ? lo : 0u);
+                    a = max(a, hi < 0x7F80u ? hi : 0u);
+                  }
+                  a = __reduce_max_sync(0xffffffffu, a);
+                }
+                // x * 2^sh is exact; 2^sh is not an FP32 value above sh = 127 (it reaches
+                // 141), where 2^14 of it is applied first; 2^-sh always is one, a subnormal
+                // from sh = 127 on
+                const int sh = 141 - (a ? static_cast<int>(a >> 7) : 127);
+                const float f = __uint_as_float(static_cast<uint32_t>(127 + (sh > 127 ? sh - 14 : sh)) << 23);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                  const uint32_t lo = u[j] & 0x7FFFu, hi = (u[j] >> 16) & 0x7FFFu;
-                  a = max(a, lo < 0x7F80u ? lo : 0u);
-                  a = max(a, hi < 0x7F80u ? hi : 0u);
+                  float lo = __uint_as_float(u[j] << 16), hi = __uint_as_float(u[j] & 0xFFFF0000u);
+                  if (sh > 127) {
+                    lo *= 16384.0f;
+                    hi *= 16384.0f;
+                  }
+                  u[j] = pack_2x16(lo * f, hi * f, false);
                 }
-                a = __reduce_max_sync(0xffffffffu, a);
-                // x * 2^sh in two exact steps (sh reaches 141); 2^-sh is an FP32 value, a
-                // subnormal from sh = 127 on
-                const int sh = 141 - (a ? static_cast<int>(a >> 7) : 127), s1 = sh / 2, s2 = sh - s1;
-                const float f1 = __uint_as_float(static_cast<uint32_t>(127 + s1) << 23), f2 = __uint_as_float(static_cast<uint32_t>(127 + s2) << 23);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  u[j] = pack_2x16(__uint_as_float(u[j] << 16) * f1 * f2, __uint_as_float(u[j] & 0xFFFF0000u) * f1 * f2, false);
                 if (lane == 0) xscale[blk * M + m] = sh < 127 ? __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) : __uint_as_float(1u << (149 - sh));
               }
               st_shared_v4(xs + static_cast<uint32_t>(m * args.x_stride + v * 16), u[0], u[1], u[2], u[3]);
@@ -415,7 +444,7 @@ __global__ void __launch_bounds__(GemvCfg<WT, MATS, NT, DEEP>::THREADS, GemvCfg<
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int q = 0; q < 4; ++q) acc[j][n][q] = 0.0f;
-      Run r{round, piece, 0, 0, 0, 0};
+      Run r{group, piece, round, 0, 0, 0, 0};
       run_set(r);
       int part = 0;                                       // which of the run's tiles
       // the partial sums of a finished tile (or of the run's end)
@@ -581,9 +610,8 @@ __global__ void __launch_bounds__(GemvCfg<WT, MATS, NT, DEEP>::THREADS, GemvCfg<
       const int pc = r.pc, U = T * pc;
       const int cells = 4 * M;
       const bool last_piece = piece == pieces - 1;
-      float4* sum4 = reinterpret_cast<float4*>(smem + args.off_sum) + (round & 1) * (MATS * args.round_tiles * cells);
+      float4* sum4 = reinterpret_cast<float4*>(smem + args.off_sum);   // [MATS][tile of the group][cells]
       const float4* slots4 = reinterpret_cast<const float4*>(slots);
-      const int first_row = (tile0 + round * args.round_tiles) * 16;
       for (int o = threadIdx.x; o < T * cells; o += C::THREADS) {
         const int tile = o / cells, cell = o - tile * cells;
         // the warps whose runs meet this tile: run w starts at w U / W
@@ -609,39 +637,41 @@ __global__ void __launch_bounds__(GemvCfg<WT, MATS, NT, DEEP>::THREADS, GemvCfg<
         if (S > 1 || pieces > 1) {
 #pragma unroll
           for (int j = 0; j < MATS; ++j) {
-            float4& d = sum4[(j * args.round_tiles + tile) * cells + cell];
+            float4& d = sum4[(j * args.group_tiles + round - group + tile) * cells + cell];
             if (piece > 0) v[j] = make_float4(d.x + v[j].x, d.y + v[j].y, d.z + v[j].z, d.w + v[j].w);
             d = v[j];
           }
         }
-        if (S == 1 && last_piece) gemv_store<BF16, MATS>(args, first_row + tile * 16 + (cell & 3) * 4, cell >> 2, v);
+        if (S == 1 && last_piece) gemv_store<BF16, MATS>(args, (tile0 + round + tile) * 16 + (cell & 3) * 4, cell >> 2, v);
       }
-      if (S > 1 && last_piece) {
-        // one barrier per round: the next round's sums go to the other buffer
-        cluster_sync_all();
-        for (int o = rank * C::THREADS + static_cast<int>(threadIdx.x); o < T * cells; o += S * C::THREADS) {
-          const int tile = o / cells, cell = o - tile * cells;
-          float4 v[MATS];
+      __syncthreads();                                    // slots and X are free again
+    }
+   }
+   if (S > 1) {
+      cluster_sync_all();                                 // every share's sums are there
+      const int cells = 4 * M;
+      const float4* sum4 = reinterpret_cast<const float4*>(smem + args.off_sum);
+      const int all = (group_end(group) - group) * cells;
+      for (int o = rank * C::THREADS + static_cast<int>(threadIdx.x); o < all; o += S * C::THREADS) {
+        const int tile = o / cells, cell = o - tile * cells;
+        float4 v[MATS];
 #pragma unroll
-          for (int j = 0; j < MATS; ++j) {
-            const uint32_t at = ptx::smem_u32(sum4 + (j * args.round_tiles + tile) * cells + cell);
-            v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int q = 0; q < S; ++q) {
-              const float4 p = ld_cluster_f32x4(map_to_rank(at, static_cast<uint32_t>(q)));
-              v[j].x += p.x;
-              v[j].y += p.y;
-              v[j].z += p.z;
-              v[j].w += p.w;
-            }
+        for (int j = 0; j < MATS; ++j) {
+          const uint32_t at = ptx::smem_u32(sum4 + (j * args.group_tiles + tile) * cells + cell);
+          v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int q = 0; q < S; ++q) {
+            const float4 p = ld_cluster_f32x4(map_to_rank(at, static_cast<uint32_t>(q)));
+            v[j].x += p.x;
+            v[j].y += p.y;
+            v[j].z += p.z;
+            v[j].w += p.w;
           }
-          gemv_store<BF16, MATS>(args, first_row + tile * 16 + (cell & 3) * 4, cell >> 2, v);
         }
-      } else {
-        __syncthreads();                                  // slots and X are free again
+        gemv_store<BF16, MATS>(args, (tile0 + group + tile) * 16 + (cell & 3) * 4, cell >> 2, v);
       }
+      cluster_sync_all();                                 // and stay until every CTA has read them
     }
   }
-  if (S > 1) cluster_sync_all();                          // every CTA has read this one's sums
   cp_wait<0>();
 }
 
@@ -656,6 +686,7 @@ template <WType WT, bool BF16, int MATS, int NT, bool DEEP>
 struct GemvLaunch {
   using C = GemvCfg<WT, MATS, NT, DEEP>;
   static constexpr int kSmem = 232448;
+  static constexpr int kSumBytes = 16384;                 // at most, of joined sums
   static constexpr auto kernel = &gemv_kernel<WT, BF16, MATS, NT, DEEP>;
 
   cudaLaunchConfig_t cfg;
@@ -714,18 +745,25 @@ struct GemvLaunch {
     if (fit == nullptr) return false;
     const int chunks = (args.K + C::CK - 1) / C::CK, all_tiles = (args.N + 15) / 16;
     const int slots = C::OFF_SLOTS + C::slots_bytes(args.M);
-    // 8 KB of joined sums in each of the two buffers, padding of X
-    const double room = kSmem - slots - 16384.0 - 128.0 - 64.0 * args.M;
-    if (room < 2.0 * (C::CK * 2 + 4) * args.M) return true;
+    // shared memory for X (with its padding) and joined sums
+    const double room = kSmem - slots - 128.0 - 64.0 * args.M;
+    const double x_chunk = static_cast<double>(C::CK * 2 + 4) * args.M, tile_sum = MATS * 64.0 * args.M;
+    if (room < kSumBytes + 2.0 * x_chunk) return true;
     int log_s = -1;
     for (int i = 0; i < 4; ++i) {
       const int s = 1 << i, per = (chunks + s - 1) / s;
       if ((s - 1) * per >= chunks) continue;              // a CTA without work
-      const double x_bytes = static_cast<double>(per) * (C::CK * 2 + 4) * args.M;
+      const double x_bytes = static_cast<double>(per) * x_chunk;
       const int tiles = (all_tiles + fit[i] - 1) / fit[i];
-      const double pieces = x_bytes > room ? static_cast<double>((tiles + C::WARPS - 1) / C::WARPS) : 1.0;
-      const double ns = static_cast<double>(tiles) * per * C::STAGE / (DEEP ? 48.0 : 40.0) + pieces * x_bytes / 50.0 +
-                        (s > 1 ? 2500.0 : 0.0) + (DEEP ? 1000.0 : 0.0);
+      double groups = 1.0, pieces = 1.0;
+      if (s > 1 || x_bytes > room) {
+        const double sums = tiles * tile_sum < kSumBytes ? tiles * tile_sum : kSumBytes;
+        groups = tiles * tile_sum / sums;
+        pieces = x_bytes > room - sums ? x_bytes / (room - sums) + 1.0 : 1.0;
+      }
+      const double stagings = pieces > 1.0 ? groups * pieces : 1.0;
+      const double ns = static_cast<double>(tiles) * per * C::STAGE / (DEEP ? 48.0 : 40.0) + (pieces > 1.0 ? groups : 1.0) * x_bytes / 50.0 +
+                        1500.0 * (stagings - 1.0) + (s > 1 ? 2500.0 * groups : 0.0) + (DEEP ? 1000.0 : 0.0);
       if (best.ns >= 0 && ns >= best.ns) continue;
       best.ns = ns;
       log_s = i;
@@ -740,17 +778,20 @@ struct GemvLaunch {
     best.clusters = all_tiles < fit[log_s] ? all_tiles : fit[log_s];
     a.cta_tiles = all_tiles / best.clusters;
     a.extra = all_tiles % best.clusters;
-    // rounds of equal size, at most WARPS tiles and 8 KB of joined sums
-    const int sum_cap = 8192 / (MATS * args.M * 64);
-    const int most = C::WARPS < sum_cap ? C::WARPS : sum_cap;
     const int cta_most = a.cta_tiles + (a.extra > 0 ? 1 : 0);
-    const int rounds = (cta_most + most - 1) / most;
-    a.round_tiles = (cta_most + rounds - 1) / rounds;
+    const bool sums = log_s > 0 || a.cta_chunks * x_chunk > room;   // kept in shared memory
+    const int sum_cap = static_cast<int>(kSumBytes / tile_sum);
+    a.group_tiles = sums && sum_cap < cta_most ? sum_cap : cta_most;
+    // rounds of equal size, at most WARPS tiles
+    const int rounds = (a.group_tiles + C::WARPS - 1) / C::WARPS;
+    a.round_tiles = (a.group_tiles + rounds - 1) / rounds;
     a.off_sum = slots;
-    a.off_scale = slots + 2 * MATS * a.round_tiles * args.M * 64;
-    // X: rows an odd number of 64-byte units apart (bank conflicts), a scale per row and chunk
+    a.off_scale = slots + (sums ? a.group_tiles * MATS * args.M * 64 : 0);
+    // X: rows an odd number of 64-byte units apart (bank conflicts), a scale per row and
+    // chunk; pieces of equal size
     const int fit_x = ((kSmem - a.off_scale - 128) / args.M - 64) / (C::CK * 2 + 4);
-    a.x_chunks = a.cta_chunks < fit_x ? a.cta_chunks : fit_x;
+    const int pieces = (a.cta_chunks + fit_x - 1) / fit_x;
+    a.x_chunks = (a.cta_chunks + pieces - 1) / pieces;
     a.x_stride = (a.x_chunks * (C::CK * 2 / 64) | 1) * 64;
     a.off_x = (a.off_scale + a.x_chunks * args.M * 4 + 127) / 128 * 128;
     a.prefetch = pdl_enabled() ? 4 : 0;
