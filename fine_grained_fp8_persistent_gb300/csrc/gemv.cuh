@@ -22,16 +22,15 @@
 // most 2^-39 of it, below the FP32 accumulation's own rounding.  The chunk's sums are
 // multiplied by the power's inverse as they are added to the totals.
 //
-// Work split.  One CTA per SM, walking tiles of 16 weight rows; X (or as much of it as
-// fits) is converted and kept in shared memory once per CTA.  A round is up to WARPS tiles:
-// the 128-byte pieces ("chunks") of all their rows, tile after tile, are dealt to the warps
-// in equal contiguous runs, so every warp has the same work whatever the number of rows,
-// and a run meets at most two tiles.  Each warp streams its run through a ring of its own
-// with cp.async, which goes on across rounds, so the loop has no barrier; at a tile's end
-// it leaves its partial sums in a slot, and after the round the slots of each tile are
-// added in the warps' order.  With few rows, or with more of X than fits, a cluster of
-// CTAs splits the reduction and adds its sums through distributed shared memory, also in
-// a fixed order.
+// Work split.  One CTA per SM, walking tiles of 16 weight rows in rounds; a warp takes one
+// tile of the round, or, when there are fewer tiles than warps, every KS-th of the tile's
+// 128-byte pieces ("chunks").  X (or as much of it as fits: a "piece") is converted and
+// kept in shared memory once per CTA.  Each warp streams its chunks through a ring of its
+// own with cp.async, which goes on across pieces and rounds, so the loop has no barrier,
+// and keeps its sums in registers to the round's end.  The KS shares of a tile are then
+// added in shared memory, in order.  With few rows, or with much more of X than fits, a
+// cluster of CTAs splits the reduction further and adds its sums through distributed
+// shared memory, also in order.
 #pragma once
 #include <cstring>
 #include <type_traits>
@@ -52,35 +51,31 @@ struct GemvKArgs {
   void* keep[2];     // gated 16-bit: G and U, or null
   int M, N, K;
   int act;
-  int tiles;         // tiles of 16 weight rows: cta_tiles per cluster, one more for the
-  int cta_tiles;     //   first `extra` clusters
+  int cta_tiles;     // tiles of 16 weight rows per cluster, one more for the first `extra`
   int extra;
-  int group_tiles;   // tiles whose sums are kept while X goes through in pieces
-  int round_tiles;   // tiles of one round, at most WARPS
+  int round_tiles;   // tiles of one round
+  int ks;            // warps per tile: a CTA has round_tiles * ks warps
   int chunks;        // chunks of the whole reduction
   int cta_chunks;    // chunks of one CTA's share of it (every CTA has at least one)
   int x_chunks;      // chunks of X in shared memory at a time
   int x_stride;      // bytes between rows of X in shared memory
-  int off_sum;       // offsets of a group's joined sums (read by the cluster), of 2^p of
-  int off_scale;     //   each chunk and row of X, and of X
+  int off_slots;     // offsets of the warps' sums [warp][MATS][M][16], of 2^p of each chunk
+  int off_scale;     //   and row of X, and of X
   int off_x;
-  int prefetch;      // chunks of a warp's first run to ask into L2 ahead of the previous kernel's end
+  int prefetch;      // chunks per warp to ask into L2 ahead of the previous kernel's end
 };
 
 // DEEP: one CTA per SM with as many bytes in flight as fit; else half an SM's registers
 // and shared memory.
 template <WType WT, int MATS, int NT, bool DEEP>
 struct GemvCfg {
-  static constexpr int WARPS = MATS == 2 ? (DEEP && NT == 1 ? 12 : 8) : DEEP ? 16 : 12, THREADS = 32 * WARPS;
+  static constexpr int WARPS = DEEP ? (MATS == 2 ? 12 : 16) : (MATS == 2 ? 8 : 12);   // at most
   static constexpr int MIN_CTAS = DEEP ? 1 : 2;              // per SM: bounds the registers
   static constexpr int CK = WT == WType::W16 ? 64 : 256;     // elements of K per chunk (128 bytes of a row)
   static constexpr int WPC = WT == WType::MX ? 2 : 4;        // scale words per row and chunk
   static constexpr int SF_BYTES = WT == WType::W16 ? 0 : WPC * 64;
   static constexpr int STAGE = MATS * (2048 + SF_BYTES);
   static constexpr int DEPTH = DEEP && MATS == 1 && NT == 1 ? 5 : 3;   // ring slots of a warp
-  static constexpr int RING = WARPS * DEPTH * STAGE;
-  static constexpr int OFF_SLOTS = RING;                     // [warp][2][MATS][M][16] partial sums
-  static constexpr int slots_bytes(int M) { return WARPS * 2 * MATS * M * 64; }
 };
 
 namespace gemv {
@@ -167,6 +162,12 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
 
 }  // namespace gemv
 
+__device__ __forceinline__ void add4(float4& a, const float4& b) {
+  a.x += b.x;
+  a.y += b.y;
+  a.z += b.z;
+  a.w += b.w;
+}
 // Four outputs (weight rows n .. n + 3, token m) from their FP32 sums.
 __device__ __forceinline__ void store4(void* base, const GemvKArgs& args, int n, int m, const float4& v, bool bf16) {
   uint16_t* p = static_cast<uint16_t*>(base) + static_cast<size_t>(m) * args.N + n;
@@ -195,64 +196,44 @@ __device__ __forceinline__ void gemv_store(const GemvKArgs& args, int n, int m, 
 }
 
 template <WType WT, bool BF16, int MATS, int NT, bool DEEP>
-__global__ void __launch_bounds__(GemvCfg<WT, MATS, NT, DEEP>::THREADS, GemvCfg<WT, MATS, NT, DEEP>::MIN_CTAS) gemv_kernel(const GemvKArgs args) {
+__global__ void __launch_bounds__(32 * GemvCfg<WT, MATS, NT, DEEP>::WARPS, GemvCfg<WT, MATS, NT, DEEP>::MIN_CTAS) gemv_kernel(const GemvKArgs args) {
   using C = GemvCfg<WT, MATS, NT, DEEP>;
   using namespace gemv;
   constexpr bool kScaleX = WT != WType::W16 && BF16;   // bf16 X against fp16 weight values
   constexpr bool kMmaBf16 = WT == WType::W16 && BF16;
-  constexpr int W = C::WARPS;
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t sbase = ptx::smem_u32(smem);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int W = static_cast<int>(blockDim.x) / 32;
   const int g = lane >> 2, t = lane & 3;
   const int S = static_cast<int>(gridDim.y);            // CTAs of the cluster: shares of the reduction
   const int rank = static_cast<int>(blockIdx.y);
-  const int M = args.M, N = args.N, K = args.K;
+  const int M = args.M, N = args.N, K = args.K, KS = args.ks;
   const int tile0 = static_cast<int>(blockIdx.x) * args.cta_tiles + min(static_cast<int>(blockIdx.x), args.extra);
   const int my_tiles = args.cta_tiles + (static_cast<int>(blockIdx.x) < args.extra ? 1 : 0);
+  const int wt = warp / KS, ks = warp - wt * KS;         // tile of the round and share of it
   const int c0 = rank * args.cta_chunks;                 // first chunk of this CTA
   const int nc = min(args.cta_chunks, args.chunks - c0);
-  const int pieces = (nc + args.x_chunks - 1) / args.x_chunks;
   constexpr int ELEM_BITS = WT == WType::W16 ? 16 : 4;
   const size_t row_bytes = static_cast<size_t>(K) * ELEM_BITS / 8;
   constexpr int SV = WT == WType::MX ? 32 : 16;
   const int sf_words = WT == WType::W16 ? 0 : (K / SV + 3) / 4;
   const int sf_ld = (N + 3) / 4 * 4;
 
-  // A run: this warp's chunks of one round and piece of X.  The order is: groups of tiles,
-  // pieces of X, rounds of a group (all but the rounds are usually one).
-  struct Run {
-    int group, piece, round;     // first tile of the group, piece, first tile of the round (of this CTA's)
-    int tile, chunk, left, pc;   // tile within the round, chunk within the piece, chunks left, chunks per piece
-  };
-  auto group_end = [&](int group) { return min(group + args.group_tiles, my_tiles); };
-  auto round_size = [&](int group, int round) { return min(args.round_tiles, group_end(group) - round); };
-  auto run_set = [&](Run& r) {
-    const int T = round_size(r.group, r.round);
-    r.pc = min(args.x_chunks, nc - r.piece * args.x_chunks);
-    const int U = T * r.pc, b = warp * U / W;
-    r.left = (warp + 1) * U / W - b;
-    r.tile = b / r.pc;
-    r.chunk = b - r.tile * r.pc;
-  };
-
   // Under a programmatic dependent launch the previous kernel may still be running.  Its
   // outputs (X, perhaps the weights) are read only after the wait below; until then this
   // warp asks for the weights of its first run to be brought into L2, the memory's point of
   // coherence, which reads nothing into the kernel.
-  if (args.prefetch > 0) {
-    Run r{0, 0, 0, 0, 0, 0, 0};
-    run_set(r);
-    const int half = lane >> 4;                            // two chunks at a time, a row per lane
-    for (int i = half; i < r.left && i < args.prefetch; i += 2) {
-      const int at = r.tile * r.pc + r.chunk + i, tile = at / r.pc, gc = c0 + at - tile * r.pc;
-      const int row = (tile0 + tile) * 16 + (lane & 15);
+  if (args.prefetch > 0 && wt < my_tiles) {
+    const int row = (tile0 + wt) * 16 + (lane & 15);       // a row per lane, two chunks at a time
+    for (int i = lane >> 4; i < args.prefetch && ks + i * KS < nc; i += 2) {
+      const int gc = c0 + ks + i * KS;
 #pragma unroll
       for (int j = 0; j < MATS; ++j) {
         if (row < N) {
           prefetch_l2(static_cast<const uint8_t*>(args.W[j]) + static_cast<size_t>(row) * row_bytes + static_cast<size_t>(gc) * 128);
           if (WT != WType::W16 && (lane & 15) < C::WPC && gc * C::WPC + (lane & 15) < sf_words)
-            prefetch_l2(static_cast<const uint32_t*>(args.SF[j]) + static_cast<size_t>(gc * C::WPC + (lane & 15)) * sf_ld + (tile0 + tile) * 16);
+            prefetch_l2(static_cast<const uint32_t*>(args.SF[j]) + static_cast<size_t>(gc * C::WPC + (lane & 15)) * sf_ld + (tile0 + wt) * 16);
         }
       }
     }
@@ -268,30 +249,18 @@ __global__ void __launch_bounds__(GemvCfg<WT, MATS, NT, DEEP>::THREADS, GemvCfg<
   const uint32_t dst_a = static_cast<uint32_t>(cr * 128 + ((cp ^ cr) << 4)), dst_b = dst_a ^ 64u;
   const size_t rows4 = 4 * row_bytes;
   const int full_chunks = static_cast<int>(row_bytes / 128);   // chunks with no column past K
-  Run pf{0, 0, 0, 0, 0, 0, 0};
-  run_set(pf);
-  bool pf_end = false, pf_new = true, pf_rows = false;
-  int pf_slot = 0, gc = 0, row0 = 0;
+  const size_t sf_step = static_cast<size_t>(sf_ld) * C::WPC * KS;
+  int pf_tile = wt, pf_q = ks;                             // tile (of this CTA's) and chunk (of its share) to load next
+  int pf_slot = 0, row0 = 0;
+  bool pf_rows = false, pf_new = true;
   const uint8_t* wp[MATS] = {};
   const uint32_t* sp[MATS] = {};
+  if (pf_q >= nc) pf_tile = my_tiles;                      // more shares than chunks: nothing to do
   auto issue = [&]() {
-    while (pf.left == 0 && !pf_end) {                     // the next run with work for this warp
-      pf.round += args.round_tiles;
-      if (pf.round >= group_end(pf.group)) {
-        pf.round = pf.group;
-        if (++pf.piece >= pieces) {
-          pf.piece = 0;
-          pf.round = pf.group += args.group_tiles;
-          if (pf.group >= my_tiles) { pf_end = true; break; }
-        }
-      }
-      run_set(pf);
-      pf_new = true;
-    }
-    if (!pf_end) {
+    if (pf_tile < my_tiles) {
+      const int gc = c0 + pf_q;
       if (pf_new) {                                       // a new tile: row pointers
-        row0 = (tile0 + pf.round + pf.tile) * 16;
-        gc = c0 + pf.piece * args.x_chunks + pf.chunk;
+        row0 = (tile0 + pf_tile) * 16;
         pf_rows = row0 + 16 <= N;
 #pragma unroll
         for (int j = 0; j < MATS; ++j) {
@@ -334,14 +303,13 @@ __global__ void __launch_bounds__(GemvCfg<WT, MATS, NT, DEEP>::THREADS, GemvCfg<
       }
 #pragma unroll
       for (int j = 0; j < MATS; ++j) {
-        wp[j] += 128;
-        if constexpr (WT != WType::W16) sp[j] += static_cast<size_t>(C::WPC) * sf_ld;
+        wp[j] += 128 * KS;
+        if constexpr (WT != WType::W16) sp[j] += sf_step;
       }
-      ++gc;
-      --pf.left;
-      if (++pf.chunk == pf.pc) {
-        pf.chunk = 0;
-        ++pf.tile;
+      pf_q += KS;
+      if (pf_q >= nc) {
+        pf_q = ks;
+        pf_tile += args.round_tiles;
         pf_new = true;
       }
       if (++pf_slot == C::DEPTH) pf_slot = 0;
@@ -352,7 +320,6 @@ __global__ void __launch_bounds__(GemvCfg<WT, MATS, NT, DEEP>::THREADS, GemvCfg<
   for (int i = 0; i < C::DEPTH - 1; ++i) issue();
 
   const uint32_t xs = sbase + static_cast<uint32_t>(args.off_x);
-  float* slots = reinterpret_cast<float*>(smem + C::OFF_SLOTS);
   float* xscale = reinterpret_cast<float*>(smem + args.off_scale);   // [chunk][M]
   int slot = 0;                                           // ring slot of the next chunk
 
@@ -362,14 +329,21 @@ __global__ void __launch_bounds__(GemvCfg<WT, MATS, NT, DEEP>::THREADS, GemvCfg<
 #pragma unroll
   for (int n = 0; n < NT; ++n) xl[n] = smem + args.off_x + static_cast<uint32_t>(min(8 * n + g, M - 1) * args.x_stride + t * 16);
 
-  for (int group = 0; group < my_tiles; group += args.group_tiles) {
-   for (int piece = 0; piece < pieces; ++piece) {
-    for (int round = group; round < group_end(group); round += args.round_tiles) {
-      const int T = round_size(group, round);
+  for (int round = 0; round < my_tiles; round += args.round_tiles) {
+    float acc[MATS][NT][4];
+#pragma unroll
+    for (int j = 0; j < MATS; ++j)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[j][n][q] = 0.0f;
+    int q = round + wt < my_tiles ? ks : nc;              // this warp's next chunk
+    for (int x0 = 0; x0 < nc; x0 += args.x_chunks) {
       // -------------------------------------------------------- a piece of X
-      if (round == group && (pieces > 1 || group == 0)) {
-        const int xn = min(args.x_chunks, nc - piece * args.x_chunks);
-        const int k0 = (c0 + piece * args.x_chunks) * C::CK;
+      if (round == 0 || nc > args.x_chunks) {
+        if (round > 0 || x0 > 0) __syncthreads();         // the previous piece has been read
+        const int xn = min(args.x_chunks, nc - x0);
+        const int k0 = (c0 + x0) * C::CK;
         // one warp takes 256 columns of a row, 8 per lane (zeros past K)
         const int blocks = (xn * C::CK + 255) / 256;
         // four loads in flight per lane
@@ -436,41 +410,17 @@ __global__ void __launch_bounds__(GemvCfg<WT, MATS, NT, DEEP>::THREADS, GemvCfg<
         __syncthreads();
       }
 
-      // -------------------------------------------------------- this warp's run
-      float acc[MATS][NT][4];
-#pragma unroll
-      for (int j = 0; j < MATS; ++j)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) acc[j][n][q] = 0.0f;
-      Run r{group, piece, round, 0, 0, 0, 0};
-      run_set(r);
-      int part = 0;                                       // which of the run's tiles
-      // the partial sums of a finished tile (or of the run's end)
-      auto flush = [&]() {
-#pragma unroll
-        for (int j = 0; j < MATS; ++j)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int col = 8 * n + 2 * t + (q & 1), row = g + 8 * (q >> 1);
-              if (col < M) slots[(((warp * 2 + part) * MATS + j) * M + col) * 16 + row] = acc[j][n][q];
-              acc[j][n][q] = 0.0f;
-            }
-        ++part;
-      };
+      // -------------------------------------------------------- this warp's chunks of it
       const int lr = (lane & 7) + ((lane >> 3) & 1) * 8;  // ldmatrix: row and piece this lane addresses
       const uint32_t la = static_cast<uint32_t>(lr * 128 + (((lane >> 4) ^ (lr & 7)) << 4));
-      while (r.left > 0) {
+      for (const int end = min(nc, x0 + args.x_chunks); q < end; q += KS) {
         cp_wait<C::DEPTH - 2>();
         __syncwarp();
         issue();
         const uint32_t so = static_cast<uint32_t>((warp * C::DEPTH + slot) * C::STAGE);
         const uint32_t st = sbase + so;
         if (++slot == C::DEPTH) slot = 0;
-        const uint32_t xc = static_cast<uint32_t>(r.chunk * (C::CK * 2));
+        const uint32_t xc = static_cast<uint32_t>((q - x0) * (C::CK * 2));
         if constexpr (WT == WType::W16) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {                   // 32 columns
@@ -493,7 +443,7 @@ __global__ void __launch_bounds__(GemvCfg<WT, MATS, NT, DEEP>::THREADS, GemvCfg<
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int j = 0; j < 2; ++j) xp[n][j] = xscale[r.chunk * M + min(8 * n + 2 * t + j, M - 1)];
+              for (int j = 0; j < 2; ++j) xp[n][j] = xscale[(q - x0) * M + min(8 * n + 2 * t + j, M - 1)];
           }
           // the chunk's sums: of scaled X where X is scaled, else straight into the totals
           float part_acc[MATS][NT][4];
@@ -596,80 +546,64 @@ __global__ void __launch_bounds__(GemvCfg<WT, MATS, NT, DEEP>::THREADS, GemvCfg<
           if (kScaleX && WT == WType::MX && large) body(std::true_type{});
           else body(std::false_type{});
         }
-        --r.left;
-        if (++r.chunk == r.pc) {
-          r.chunk = 0;
-          flush();
-        }
       }
-      if (r.chunk != 0) flush();                          // an unfinished tile (a run that stops at a tile's end has flushed it)
-
-      // -------------------------------------------------------- join the round
-      // Four weight rows of one token per thread: cell = (token * 4 + row / 4) of a tile.
-      __syncthreads();
-      const int pc = r.pc, U = T * pc;
-      const int cells = 4 * M;
-      const bool last_piece = piece == pieces - 1;
-      float4* sum4 = reinterpret_cast<float4*>(smem + args.off_sum);   // [MATS][tile of the group][cells]
-      const float4* slots4 = reinterpret_cast<const float4*>(slots);
-      for (int o = threadIdx.x; o < T * cells; o += C::THREADS) {
-        const int tile = o / cells, cell = o - tile * cells;
-        // the warps whose runs meet this tile: run w starts at w U / W
-        const int w0 = ((tile * pc + 1) * W - 1) / U, w1 = ((tile * pc + pc) * W - 1) / U;
-        float4 v[MATS];
-#pragma unroll
-        for (int j = 0; j < MATS; ++j) v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int w = w0, b = w0 * U / W; w <= w1; ++w) {
-          const int e = (w + 1) * U / W;
-          if (e > b) {                                    // not an empty run
-            const int li = b >= tile * pc ? 0 : 1;        // the run's first tile, or its second
-#pragma unroll
-            for (int j = 0; j < MATS; ++j) {
-              const float4 p = slots4[((w * 2 + li) * MATS + j) * cells + cell];
-              v[j].x += p.x;
-              v[j].y += p.y;
-              v[j].z += p.z;
-              v[j].w += p.w;
-            }
-          }
-          b = e;
-        }
-        if (S > 1 || pieces > 1) {
-#pragma unroll
-          for (int j = 0; j < MATS; ++j) {
-            float4& d = sum4[(j * args.group_tiles + round - group + tile) * cells + cell];
-            if (piece > 0) v[j] = make_float4(d.x + v[j].x, d.y + v[j].y, d.z + v[j].z, d.w + v[j].w);
-            d = v[j];
-          }
-        }
-        if (S == 1 && last_piece) gemv_store<BF16, MATS>(args, (tile0 + round + tile) * 16 + (cell & 3) * 4, cell >> 2, v);
-      }
-      __syncthreads();                                    // slots and X are free again
     }
-   }
-   if (S > 1) {
+
+    // ---------------------------------------------------------- the round's outputs
+    // four weight rows of one token per thread: cell = token * 4 + row / 4 of a tile
+    float* slots = reinterpret_cast<float*>(smem + args.off_slots);
+#pragma unroll
+    for (int j = 0; j < MATS; ++j)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int col = 8 * n + 2 * t + (e & 1), row = g + 8 * (e >> 1);
+          if (col < M) slots[((warp * MATS + j) * M + col) * 16 + row] = acc[j][n][e];
+        }
+    const int T = min(args.round_tiles, my_tiles - round), cells = 4 * M;
+    float4* slots4 = reinterpret_cast<float4*>(slots);
+    if (KS == 1 && S == 1) {                              // a warp's own tile
+      __syncwarp();
+      if (wt < T)
+        for (int cell = lane; cell < cells; cell += 32) {
+          float4 v[MATS];
+#pragma unroll
+          for (int j = 0; j < MATS; ++j) v[j] = slots4[(warp * MATS + j) * cells + cell];
+          gemv_store<BF16, MATS>(args, (tile0 + round + wt) * 16 + (cell & 3) * 4, cell >> 2, v);
+        }
+      __syncwarp();
+      continue;
+    }
+    __syncthreads();
+    for (int o = threadIdx.x; o < T * cells; o += static_cast<int>(blockDim.x)) {
+      const int tile = o / cells, cell = o - tile * cells;
+      float4 v[MATS];
+#pragma unroll
+      for (int j = 0; j < MATS; ++j) {
+        float4& first = slots4[(tile * KS * MATS + j) * cells + cell];
+        v[j] = first;
+        for (int k = 1; k < KS; ++k) add4(v[j], slots4[((tile * KS + k) * MATS + j) * cells + cell]);
+        if (S > 1) first = v[j];
+      }
+      if (S == 1) gemv_store<BF16, MATS>(args, (tile0 + round + tile) * 16 + (cell & 3) * 4, cell >> 2, v);
+    }
+    if (S > 1) {
       cluster_sync_all();                                 // every share's sums are there
-      const int cells = 4 * M;
-      const float4* sum4 = reinterpret_cast<const float4*>(smem + args.off_sum);
-      const int all = (group_end(group) - group) * cells;
-      for (int o = rank * C::THREADS + static_cast<int>(threadIdx.x); o < all; o += S * C::THREADS) {
+      for (int o = rank * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x); o < T * cells; o += S * static_cast<int>(blockDim.x)) {
         const int tile = o / cells, cell = o - tile * cells;
         float4 v[MATS];
 #pragma unroll
         for (int j = 0; j < MATS; ++j) {
-          const uint32_t at = ptx::smem_u32(sum4 + (j * args.group_tiles + tile) * cells + cell);
+          const uint32_t at = ptx::smem_u32(slots4 + (tile * KS * MATS + j) * cells + cell);
           v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int q = 0; q < S; ++q) {
-            const float4 p = ld_cluster_f32x4(map_to_rank(at, static_cast<uint32_t>(q)));
-            v[j].x += p.x;
-            v[j].y += p.y;
-            v[j].z += p.z;
-            v[j].w += p.w;
-          }
+          for (int r = 0; r < S; ++r) add4(v[j], ld_cluster_f32x4(map_to_rank(at, static_cast<uint32_t>(r))));
         }
-        gemv_store<BF16, MATS>(args, (tile0 + group + tile) * 16 + (cell & 3) * 4, cell >> 2, v);
+        gemv_store<BF16, MATS>(args, (tile0 + round + tile) * 16 + (cell & 3) * 4, cell >> 2, v);
       }
       cluster_sync_all();                                 // and stay until every CTA has read them
+    } else {
+      __syncthreads();                                    // the slots are free again
     }
   }
   cp_wait<0>();
@@ -678,7 +612,7 @@ __global__ void __launch_bounds__(GemvCfg<WT, MATS, NT, DEEP>::THREADS, GemvCfg<
 // How a call is laid out: log2 of the cluster, clusters, shared memory, tiles and X per CTA.
 struct GemvPlan {
   double ns;
-  int log_s, clusters, smem;
+  int log_s, clusters, threads, smem;
   GemvKArgs a;
 };
 
@@ -686,12 +620,11 @@ template <WType WT, bool BF16, int MATS, int NT, bool DEEP>
 struct GemvLaunch {
   using C = GemvCfg<WT, MATS, NT, DEEP>;
   static constexpr int kSmem = 232448;
-  static constexpr int kSumBytes = 16384;                 // at most, of joined sums
   static constexpr auto kernel = &gemv_kernel<WT, BF16, MATS, NT, DEEP>;
 
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  GemvLaunch(int log_s, int clusters, int smem, cudaStream_t stream) {
+  GemvLaunch(int log_s, int clusters, int threads, int smem, cudaStream_t stream) {
     std::memset(&cfg, 0, sizeof(cfg));
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 1;
@@ -700,7 +633,7 @@ struct GemvLaunch {
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(clusters), 1u << log_s, 1);
-    cfg.blockDim = dim3(C::THREADS, 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -719,7 +652,7 @@ struct GemvLaunch {
     if (fit[dev][0] == 0) {
       cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
       for (int i = 3; e == cudaSuccess && i >= 0; --i) {
-        GemvLaunch l(i, device_sm_count() >> i, kSmem, nullptr);
+        GemvLaunch l(i, device_sm_count() >> i, 32 * C::WARPS, kSmem, nullptr);
         l.cfg.numAttrs = 1;
         int n = 0;
         e = cudaOccupancyMaxActiveClusters(&n, kernel, &l.cfg);
@@ -744,63 +677,54 @@ struct GemvLaunch {
     const int* fit = max_clusters();
     if (fit == nullptr) return false;
     const int chunks = (args.K + C::CK - 1) / C::CK, all_tiles = (args.N + 15) / 16;
-    const int slots = C::OFF_SLOTS + C::slots_bytes(args.M);
-    // shared memory for X (with its padding) and joined sums
-    const double room = kSmem - slots - 128.0 - 64.0 * args.M;
-    const double x_chunk = static_cast<double>(C::CK * 2 + 4) * args.M, tile_sum = MATS * 64.0 * args.M;
-    if (room < kSumBytes + 2.0 * x_chunk) return true;
-    int log_s = -1;
+    const int x_chunk = (C::CK * 2 + 4) * args.M;          // bytes of X and its scales
     for (int i = 0; i < 4; ++i) {
       const int s = 1 << i, per = (chunks + s - 1) / s;
       if ((s - 1) * per >= chunks) continue;              // a CTA without work
-      const double x_bytes = static_cast<double>(per) * x_chunk;
+      // tiles per round and warps per tile: all warps busy, as few rounds as can be, and no
+      // more shares of a tile than shorten the longest one
       const int tiles = (all_tiles + fit[i] - 1) / fit[i];
-      double groups = 1.0, pieces = 1.0;
-      if (s > 1 || x_bytes > room) {
-        const double sums = tiles * tile_sum < kSumBytes ? tiles * tile_sum : kSumBytes;
-        groups = tiles * tile_sum / sums;
-        pieces = x_bytes > room - sums ? x_bytes / (room - sums) + 1.0 : 1.0;
-      }
-      const double stagings = pieces > 1.0 ? groups * pieces : 1.0;
-      const double ns = static_cast<double>(tiles) * per * C::STAGE / (DEEP ? 48.0 : 40.0) + (pieces > 1.0 ? groups : 1.0) * x_bytes / 50.0 +
-                        1500.0 * (stagings - 1.0) + (s > 1 ? 2500.0 * groups : 0.0) + (DEEP ? 1000.0 : 0.0);
+      const int rounds = (tiles + C::WARPS - 1) / C::WARPS;
+      const int round_tiles = (tiles + rounds - 1) / rounds;
+      int ks = C::WARPS / round_tiles < per ? C::WARPS / round_tiles : per;
+      const int longest = (per + ks - 1) / ks;
+      ks = (per + longest - 1) / longest;
+      const int warps = round_tiles * ks;
+      // shared memory: ring, sums, X (rows an odd number of 64-byte units apart) and scales
+      const int slots = warps * C::DEPTH * C::STAGE;
+      const int scale = slots + warps * MATS * args.M * 64;
+      const int fit_x = ((kSmem - scale - 128) / args.M - 64) / (C::CK * 2 + 4);
+      if (fit_x < 1) continue;
+      const int pieces = (per + fit_x - 1) / fit_x;
+      const double stagings = pieces > 1 ? pieces * rounds : 1.0;
+      const double ns = static_cast<double>(rounds) * longest * warps * C::STAGE / (DEEP ? 48.0 : 40.0) +
+                        stagings * (per / pieces * static_cast<double>(x_chunk) / 50.0 + 500.0) + (s > 1 ? 2500.0 * rounds : 0.0) + (DEEP ? 1000.0 : 0.0);
       if (best.ns >= 0 && ns >= best.ns) continue;
       best.ns = ns;
-      log_s = i;
+      best.log_s = i;
+      best.threads = 32 * warps;
+      best.clusters = all_tiles < fit[i] ? all_tiles : fit[i];
+      GemvKArgs& a = best.a;
+      a = args;
+      a.cta_tiles = all_tiles / best.clusters;
+      a.extra = all_tiles % best.clusters;
+      a.round_tiles = round_tiles;
+      a.ks = ks;
+      a.chunks = chunks;
+      a.cta_chunks = per;
+      a.x_chunks = (per + pieces - 1) / pieces;
+      a.x_stride = (a.x_chunks * (C::CK * 2 / 64) | 1) * 64;
+      a.off_slots = slots;
+      a.off_scale = scale;
+      a.off_x = (scale + a.x_chunks * args.M * 4 + 127) / 128 * 128;
+      a.prefetch = pdl_enabled() ? 4 : 0;
+      best.smem = a.off_x + args.M * a.x_stride;
     }
-    if (log_s < 0) return true;                           // the other variant is ahead
-    GemvKArgs& a = best.a;
-    a = args;
-    a.chunks = chunks;
-    a.tiles = all_tiles;
-    a.cta_chunks = (chunks + (1 << log_s) - 1) >> log_s;
-    best.log_s = log_s;
-    best.clusters = all_tiles < fit[log_s] ? all_tiles : fit[log_s];
-    a.cta_tiles = all_tiles / best.clusters;
-    a.extra = all_tiles % best.clusters;
-    const int cta_most = a.cta_tiles + (a.extra > 0 ? 1 : 0);
-    const bool sums = log_s > 0 || a.cta_chunks * x_chunk > room;   // kept in shared memory
-    const int sum_cap = static_cast<int>(kSumBytes / tile_sum);
-    a.group_tiles = sums && sum_cap < cta_most ? sum_cap : cta_most;
-    // rounds of equal size, at most WARPS tiles
-    const int rounds = (a.group_tiles + C::WARPS - 1) / C::WARPS;
-    a.round_tiles = (a.group_tiles + rounds - 1) / rounds;
-    a.off_sum = slots;
-    a.off_scale = slots + (sums ? a.group_tiles * MATS * args.M * 64 : 0);
-    // X: rows an odd number of 64-byte units apart (bank conflicts), a scale per row and
-    // chunk; pieces of equal size
-    const int fit_x = ((kSmem - a.off_scale - 128) / args.M - 64) / (C::CK * 2 + 4);
-    const int pieces = (a.cta_chunks + fit_x - 1) / fit_x;
-    a.x_chunks = (a.cta_chunks + pieces - 1) / pieces;
-    a.x_stride = (a.x_chunks * (C::CK * 2 / 64) | 1) * 64;
-    a.off_x = (a.off_scale + a.x_chunks * args.M * 4 + 127) / 128 * 128;
-    a.prefetch = pdl_enabled() ? 4 : 0;
-    best.smem = a.off_x + args.M * a.x_stride;
     return true;
   }
 
   static int launch(const GemvPlan& p, cudaStream_t stream) {
-    GemvLaunch l(p.log_s, p.clusters, p.smem, stream);
+    GemvLaunch l(p.log_s, p.clusters, p.threads, p.smem, stream);
     const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kernel, p.a);
     return e == cudaSuccess ? 0 : set_error(4, "matrix-vector launch: %s", cudaGetErrorString(e));
   }
