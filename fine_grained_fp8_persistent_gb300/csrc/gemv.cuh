@@ -23,8 +23,8 @@
 // multiplied by the power's inverse as they are added to the totals.
 //
 // Work split.  One CTA per SM, walking tiles of 16 weight rows in rounds; a warp takes one
-// tile of the round, or, when there are fewer tiles than warps, every KS-th of the tile's
-// 128-byte pieces ("chunks").  X (or as much of it as fits: a "piece") is converted and
+// tile (of one of the two matrices, when gated) of the round, or, when there are fewer
+// tiles than warps, every KS-th of the tile's 128-byte pieces ("chunks").  X (or as much of it as fits: a "piece") is converted and
 // kept in shared memory once per CTA.  Each warp streams its chunks through a ring of its
 // own with cp.async, which goes on across pieces and rounds, so the loop has no barrier,
 // and keeps its sums in registers to the round's end.  The KS shares of a tile are then
@@ -54,12 +54,12 @@ struct GemvKArgs {
   int cta_tiles;     // tiles of 16 weight rows per cluster, one more for the first `extra`
   int extra;
   int round_tiles;   // tiles of one round
-  int ks;            // warps per tile: a CTA has round_tiles * ks warps
+  int ks;            // warps per tile and matrix
   int chunks;        // chunks of the whole reduction
   int cta_chunks;    // chunks of one CTA's share of it (every CTA has at least one)
   int x_chunks;      // chunks of X in shared memory at a time
   int x_stride;      // bytes between rows of X in shared memory
-  int off_slots;     // offsets of the warps' sums [warp][MATS][M][16], of 2^p of each chunk
+  int off_slots;     // offsets of the warps' sums [warp][M][16], of 2^p of each chunk
   int off_scale;     //   and row of X, and of X
   int off_x;
   int prefetch;      // chunks per warp to ask into L2 ahead of the previous kernel's end
@@ -67,15 +67,15 @@ struct GemvKArgs {
 
 // DEEP: one CTA per SM with as many bytes in flight as fit; else half an SM's registers
 // and shared memory.
-template <WType WT, int MATS, int NT, bool DEEP>
+template <WType WT, int NT, bool DEEP>
 struct GemvCfg {
-  static constexpr int WARPS = DEEP ? (MATS == 2 ? 12 : 16) : (MATS == 2 ? 8 : 12);   // at most
+  static constexpr int WARPS = DEEP ? 16 : 12;               // at most
   static constexpr int MIN_CTAS = DEEP ? 1 : 2;              // per SM: bounds the registers
   static constexpr int CK = WT == WType::W16 ? 64 : 256;     // elements of K per chunk (128 bytes of a row)
   static constexpr int WPC = WT == WType::MX ? 2 : 4;        // scale words per row and chunk
   static constexpr int SF_BYTES = WT == WType::W16 ? 0 : WPC * 64;
-  static constexpr int STAGE = MATS * (2048 + SF_BYTES);
-  static constexpr int DEPTH = DEEP && MATS == 1 && NT == 1 ? 5 : 3;   // ring slots of a warp
+  static constexpr int STAGE = 2048 + SF_BYTES;
+  static constexpr int DEPTH = DEEP && NT == 1 ? 5 : 3;   // ring slots of a warp
 };
 
 namespace gemv {
@@ -196,8 +196,8 @@ __device__ __forceinline__ void gemv_store(const GemvKArgs& args, int n, int m, 
 }
 
 template <WType WT, bool BF16, int MATS, int NT, bool DEEP>
-__global__ void __launch_bounds__(32 * GemvCfg<WT, MATS, NT, DEEP>::WARPS, GemvCfg<WT, MATS, NT, DEEP>::MIN_CTAS) gemv_kernel(const GemvKArgs args) {
-  using C = GemvCfg<WT, MATS, NT, DEEP>;
+__global__ void __launch_bounds__(32 * GemvCfg<WT, NT, DEEP>::WARPS, GemvCfg<WT, NT, DEEP>::MIN_CTAS) gemv_kernel(const GemvKArgs args) {
+  using C = GemvCfg<WT, NT, DEEP>;
   using namespace gemv;
   constexpr bool kScaleX = WT != WType::W16 && BF16;   // bf16 X against fp16 weight values
   constexpr bool kMmaBf16 = WT == WType::W16 && BF16;
@@ -211,7 +211,10 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, MATS, NT, DEEP>::WARPS, GemvC
   const int M = args.M, N = args.N, K = args.K, KS = args.ks;
   const int tile0 = static_cast<int>(blockIdx.x) * args.cta_tiles + min(static_cast<int>(blockIdx.x), args.extra);
   const int my_tiles = args.cta_tiles + (static_cast<int>(blockIdx.x) < args.extra ? 1 : 0);
-  const int wt = warp / KS, ks = warp - wt * KS;         // tile of the round and share of it
+  // this warp's tile of the round, matrix and share of it
+  const int wm = warp / KS, ks = warp - wm * KS, wt = wm / MATS;
+  const uint8_t* const weights = static_cast<const uint8_t*>(MATS == 2 && wm % 2 != 0 ? args.W[1] : args.W[0]);
+  const uint32_t* const scale_words = static_cast<const uint32_t*>(MATS == 2 && wm % 2 != 0 ? args.SF[1] : args.SF[0]);
   const int c0 = rank * args.cta_chunks;                 // first chunk of this CTA
   const int nc = min(args.cta_chunks, args.chunks - c0);
   constexpr int ELEM_BITS = WT == WType::W16 ? 16 : 4;
@@ -228,14 +231,9 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, MATS, NT, DEEP>::WARPS, GemvC
     const int row = (tile0 + wt) * 16 + (lane & 15);       // a row per lane, two chunks at a time
     for (int i = lane >> 4; i < args.prefetch && ks + i * KS < nc; i += 2) {
       const int gc = c0 + ks + i * KS;
-#pragma unroll
-      for (int j = 0; j < MATS; ++j) {
-        if (row < N) {
-          prefetch_l2(static_cast<const uint8_t*>(args.W[j]) + static_cast<size_t>(row) * row_bytes + static_cast<size_t>(gc) * 128);
-          if (WT != WType::W16 && (lane & 15) < C::WPC && gc * C::WPC + (lane & 15) < sf_words)
-            prefetch_l2(static_cast<const uint32_t*>(args.SF[j]) + static_cast<size_t>(gc * C::WPC + (lane & 15)) * sf_ld + (tile0 + wt) * 16);
-        }
-      }
+      if (row < N) prefetch_l2(weights + static_cast<size_t>(row) * row_bytes + static_cast<size_t>(gc) * 128);
+      if (WT != WType::W16 && (lane & 15) < C::WPC && gc * C::WPC + (lane & 15) < sf_words)
+        prefetch_l2(scale_words + static_cast<size_t>(gc * C::WPC + (lane & 15)) * sf_ld + (tile0 + wt) * 16);
     }
   }
   ptx::griddep_wait();
@@ -253,8 +251,8 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, MATS, NT, DEEP>::WARPS, GemvC
   int pf_tile = wt, pf_q = ks;                             // tile (of this CTA's) and chunk (of its share) to load next
   int pf_slot = 0, row0 = 0;
   bool pf_rows = false, pf_new = true;
-  const uint8_t* wp[MATS] = {};
-  const uint32_t* sp[MATS] = {};
+  const uint8_t* wp = nullptr;
+  const uint32_t* sp = nullptr;
   if (pf_q >= nc) pf_tile = my_tiles;                      // more shares than chunks: nothing to do
   auto issue = [&]() {
     if (pf_tile < my_tiles) {
@@ -262,50 +260,35 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, MATS, NT, DEEP>::WARPS, GemvC
       if (pf_new) {                                       // a new tile: row pointers
         row0 = (tile0 + pf_tile) * 16;
         pf_rows = row0 + 16 <= N;
-#pragma unroll
-        for (int j = 0; j < MATS; ++j) {
-          wp[j] = static_cast<const uint8_t*>(args.W[j]) + static_cast<size_t>(row0 + cr) * row_bytes + static_cast<size_t>(gc) * 128 + cp * 16;
-          if constexpr (WT != WType::W16)
-            sp[j] = static_cast<const uint32_t*>(args.SF[j]) + static_cast<size_t>(gc * C::WPC + (lane >> 4)) * sf_ld + row0 + (lane & 15);
-        }
+        wp = weights + static_cast<size_t>(row0 + cr) * row_bytes + static_cast<size_t>(gc) * 128 + cp * 16;
+        if constexpr (WT != WType::W16) sp = scale_words + static_cast<size_t>(gc * C::WPC + (lane >> 4)) * sf_ld + row0 + (lane & 15);
         pf_new = false;
       }
       const uint32_t st = ring + static_cast<uint32_t>(pf_slot * C::STAGE);
       if (pf_rows && gc < full_chunks) {
 #pragma unroll
-        for (int j = 0; j < MATS; ++j) {
+        for (int i = 0; i < 4; ++i) cp16_full(st + (i & 1 ? dst_b : dst_a) + 512 * i, wp + i * rows4);
+        if constexpr (WT != WType::W16) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) cp16_full(st + j * 2048 + (i & 1 ? dst_b : dst_a) + 512 * i, wp[j] + i * rows4);
-          if constexpr (WT != WType::W16) {
-#pragma unroll
-            for (int i = 0; i < C::WPC / 2; ++i)
-              cp4_full(st + MATS * 2048 + j * C::SF_BYTES + lane * 4 + 128 * i, sp[j] + static_cast<size_t>(2 * i) * sf_ld);
-          }
+          for (int i = 0; i < C::WPC / 2; ++i) cp4_full(st + 2048 + lane * 4 + 128 * i, sp + static_cast<size_t>(2 * i) * sf_ld);
         }
       } else {                                            // rows past N and columns past K are zero
         const bool in_k = static_cast<size_t>(gc) * 128 + cp * 16 < row_bytes;
 #pragma unroll
-        for (int j = 0; j < MATS; ++j) {
+        for (int i = 0; i < 4; ++i) {
+          const bool ok = in_k && row0 + cr + 4 * i < N;
+          cp16(st + (i & 1 ? dst_b : dst_a) + 512 * i, ok ? wp + i * rows4 : weights, ok);
+        }
+        if constexpr (WT != WType::W16) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool ok = in_k && row0 + cr + 4 * i < N;
-            cp16(st + j * 2048 + (i & 1 ? dst_b : dst_a) + 512 * i, ok ? wp[j] + i * rows4 : static_cast<const uint8_t*>(args.W[j]), ok);
-          }
-          if constexpr (WT != WType::W16) {
-#pragma unroll
-            for (int i = 0; i < C::WPC / 2; ++i) {
-              const bool ok = gc * C::WPC + (lane >> 4) + 2 * i < sf_words && row0 + (lane & 15) < N;
-              cp4(st + MATS * 2048 + j * C::SF_BYTES + lane * 4 + 128 * i,
-                  ok ? sp[j] + static_cast<size_t>(2 * i) * sf_ld : static_cast<const uint32_t*>(args.SF[j]), ok);
-            }
+          for (int i = 0; i < C::WPC / 2; ++i) {
+            const bool ok = gc * C::WPC + (lane >> 4) + 2 * i < sf_words && row0 + (lane & 15) < N;
+            cp4(st + 2048 + lane * 4 + 128 * i, ok ? sp + static_cast<size_t>(2 * i) * sf_ld : scale_words, ok);
           }
         }
       }
-#pragma unroll
-      for (int j = 0; j < MATS; ++j) {
-        wp[j] += 128 * KS;
-        if constexpr (WT != WType::W16) sp[j] += sf_step;
-      }
+      wp += 128 * KS;
+      if constexpr (WT != WType::W16) sp += sf_step;
       pf_q += KS;
       if (pf_q >= nc) {
         pf_q = ks;
@@ -330,13 +313,11 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, MATS, NT, DEEP>::WARPS, GemvC
   for (int n = 0; n < NT; ++n) xl[n] = smem + args.off_x + static_cast<uint32_t>(min(8 * n + g, M - 1) * args.x_stride + t * 16);
 
   for (int round = 0; round < my_tiles; round += args.round_tiles) {
-    float acc[MATS][NT][4];
+    float acc[NT][4];
 #pragma unroll
-    for (int j = 0; j < MATS; ++j)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[j][n][q] = 0.0f;
+      for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
     int q = round + wt < my_tiles ? ks : nc;              // this warp's next chunk
     for (int x0 = 0; x0 < nc; x0 += args.x_chunks) {
       // -------------------------------------------------------- a piece of X
@@ -428,14 +409,12 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, MATS, NT, DEEP>::WARPS, GemvC
 #pragma unroll
             for (int n = 0; n < NT; ++n) lds128(xl[n] + xc + 64 * h, b[n]);
 #pragma unroll
-            for (int j = 0; j < MATS; ++j)
+            for (int i = 0; i < 2; ++i) {
+              uint32_t a[4];
+              ldmatrix_x4(st + (la ^ ((2 * h + i) << 5)), a);
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                uint32_t a[4];
-                ldmatrix_x4(st + j * 2048 + (la ^ ((2 * h + i) << 5)), a);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma16816<kMmaBf16>(acc[j][n], a[0], a[1], a[2], a[3], b[n][2 * i], b[n][2 * i + 1]);
-              }
+              for (int n = 0; n < NT; ++n) mma16816<kMmaBf16>(acc[n], a[0], a[1], a[2], a[3], b[n][2 * i], b[n][2 * i + 1]);
+            }
           }
         } else {
           float xp[NT][2];                                // 2^p of this lane's columns
@@ -446,88 +425,76 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, MATS, NT, DEEP>::WARPS, GemvC
               for (int j = 0; j < 2; ++j) xp[n][j] = xscale[(q - x0) * M + min(8 * n + 2 * t + j, M - 1)];
           }
           // the chunk's sums: of scaled X where X is scaled, else straight into the totals
-          float part_acc[MATS][NT][4];
-          float(&sums)[MATS][NT][4] = kScaleX ? part_acc : acc;
+          float part_acc[NT][4];
+          float(&sums)[NT][4] = kScaleX ? part_acc : acc;
           if constexpr (kScaleX) {
 #pragma unroll
-            for (int j = 0; j < MATS; ++j)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) part_acc[j][n][q] = 0.0f;
+              for (int e = 0; e < 4; ++e) part_acc[n][e] = 0.0f;
           }
-          const uint8_t* scales = smem + so + MATS * 2048;
+          const uint8_t* scales = smem + so + 2048;
           // MXFP4 on scaled X: a scale of 2^65 or more could overflow sums whose product
           // with 2^p is finite; such a chunk multiplies each group by 2^p first
           bool large = false;
           if constexpr (kScaleX && WT == WType::MX) {
-#pragma unroll
-            for (int j = 0; j < MATS; ++j) {
-              const uint32_t w = *reinterpret_cast<const uint32_t*>(scales + j * C::SF_BYTES + lane * 4);
-              large = large || (w & (w << 1) & 0x80808080u) != 0u;
-            }
-            large = __any_sync(0xffffffffu, large);
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(scales + lane * 4);
+            large = __any_sync(0xffffffffu, (w & (w << 1) & 0x80808080u) != 0u);
           }
           auto body = [&](auto large_c) {
             constexpr bool kLarge = decltype(large_c)::value;
 #pragma unroll
             for (int f = 0; f < 2; ++f) {                 // 128 codes of each row
               // scales of rows g and g + 8
-              uint32_t sw[MATS][2][2];
-              [[maybe_unused]] float sf[MATS][2][4];
+              uint32_t sw[2][2];
+              [[maybe_unused]] float sf[2][4];
 #pragma unroll
-              for (int j = 0; j < MATS; ++j)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const uint8_t* p = scales + j * C::SF_BYTES + f * (C::WPC * 32) + (g + 8 * h) * 4;
-                  sw[j][h][0] = *reinterpret_cast<const uint32_t*>(p);
-                  if constexpr (WT == WType::NV) {
-                    sw[j][h][1] = *reinterpret_cast<const uint32_t*>(p + 64);
-                    sw[j][h][0] >>= 8 * (t >> 1);
-                    sw[j][h][1] >>= 8 * (t >> 1);
-                  } else {
-                    e8m0x4(sw[j][h][0], sf[j][h]);
-                  }
+              for (int h = 0; h < 2; ++h) {
+                const uint8_t* p = scales + f * (C::WPC * 32) + (g + 8 * h) * 4;
+                sw[h][0] = *reinterpret_cast<const uint32_t*>(p);
+                if constexpr (WT == WType::NV) {
+                  sw[h][1] = *reinterpret_cast<const uint32_t*>(p + 64);
+                  sw[h][0] >>= 8 * (t >> 1);
+                  sw[h][1] >>= 8 * (t >> 1);
+                } else {
+                  e8m0x4(sw[h][0], sf[h]);
                 }
+              }
 #pragma unroll
               for (int p2 = 0; p2 < 2; ++p2) {            // 64 codes
-                uint32_t a[MATS][4];
-#pragma unroll
-                for (int j = 0; j < MATS; ++j) ldmatrix_x4(st + j * 2048 + (la ^ ((2 * f + p2) << 5)), a[j]);
+                uint32_t a[4];
+                ldmatrix_x4(st + (la ^ ((2 * f + p2) << 5)), a);
 #pragma unroll
                 for (int s2 = 0; s2 < 2; ++s2) {          // 32 codes
                   const int s = 2 * p2 + s2;
                   uint32_t b[NT][4];
 #pragma unroll
                   for (int n = 0; n < NT; ++n) lds128(xl[n] + xc + 256 * f + 64 * s, b[n]);
+                  uint32_t lo[4], hi[4];
+                  e2m1x8(a[2 * s2], lo);
+                  e2m1x8(a[2 * s2 + 1], hi);
+                  if constexpr (WT == WType::NV) {
+                    // lanes t = 0, 1 hold the piece's first group, t = 2, 3 its second
+                    const uint32_t s0 = e4m3_pair(sw[0][p2], 2 * s2), s1 = e4m3_pair(sw[1][p2], 2 * s2);
 #pragma unroll
-                  for (int j = 0; j < MATS; ++j) {
-                    uint32_t lo[4], hi[4];
-                    e2m1x8(a[j][2 * s2], lo);
-                    e2m1x8(a[j][2 * s2 + 1], hi);
-                    if constexpr (WT == WType::NV) {
-                      // lanes t = 0, 1 hold the piece's first group, t = 2, 3 its second
-                      const uint32_t s0 = e4m3_pair(sw[j][0][p2], 2 * s2), s1 = e4m3_pair(sw[j][1][p2], 2 * s2);
-#pragma unroll
-                      for (int q = 0; q < 4; ++q) {
-                        lo[q] = mul2(lo[q], s0);
-                        hi[q] = mul2(hi[q], s1);
-                      }
+                    for (int e = 0; e < 4; ++e) {
+                      lo[e] = mul2(lo[e], s0);
+                      hi[e] = mul2(hi[e], s1);
                     }
+                  }
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                      if constexpr (WT == WType::NV) {
-                        mma16816<false>(sums[j][n], lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
-                        mma16816<false>(sums[j][n], lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
-                      } else {
-                        float p[4];
-                        mma16816_f16_zero(p, lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
-                        mma16816<false>(p, lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
+                  for (int n = 0; n < NT; ++n) {
+                    if constexpr (WT == WType::NV) {
+                      mma16816<false>(sums[n], lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
+                      mma16816<false>(sums[n], lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
+                    } else {
+                      float p[4];
+                      mma16816_f16_zero(p, lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
+                      mma16816<false>(p, lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                          if constexpr (kLarge) acc[j][n][q] = fmaf(p[q] * xp[n][q & 1], sf[j][q >> 1][s], acc[j][n][q]);
-                          else sums[j][n][q] = fmaf(p[q], sf[j][q >> 1][s], sums[j][n][q]);
-                        }
+                      for (int e = 0; e < 4; ++e) {
+                        if constexpr (kLarge) acc[n][e] = fmaf(p[e] * xp[n][e & 1], sf[e >> 1][s], acc[n][e]);
+                        else sums[n][e] = fmaf(p[e], sf[e >> 1][s], sums[n][e]);
                       }
                     }
                   }
@@ -536,11 +503,9 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, MATS, NT, DEEP>::WARPS, GemvC
             }
             if constexpr (kScaleX && !kLarge) {
 #pragma unroll
-              for (int j = 0; j < MATS; ++j)
+              for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                  for (int q = 0; q < 4; ++q) acc[j][n][q] = fmaf(part_acc[j][n][q], xp[n][q & 1], acc[j][n][q]);
+                for (int e = 0; e < 4; ++e) acc[n][e] = fmaf(part_acc[n][e], xp[n][e & 1], acc[n][e]);
             }
           };
           if (kScaleX && WT == WType::MX && large) body(std::true_type{});
@@ -553,23 +518,20 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, MATS, NT, DEEP>::WARPS, GemvC
     // four weight rows of one token per thread: cell = token * 4 + row / 4 of a tile
     float* slots = reinterpret_cast<float*>(smem + args.off_slots);
 #pragma unroll
-    for (int j = 0; j < MATS; ++j)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int col = 8 * n + 2 * t + (e & 1), row = g + 8 * (e >> 1);
-          if (col < M) slots[((warp * MATS + j) * M + col) * 16 + row] = acc[j][n][e];
-        }
+      for (int e = 0; e < 4; ++e) {
+        const int col = 8 * n + 2 * t + (e & 1), row = g + 8 * (e >> 1);
+        if (col < M) slots[(warp * M + col) * 16 + row] = acc[n][e];
+      }
     const int T = min(args.round_tiles, my_tiles - round), cells = 4 * M;
     float4* slots4 = reinterpret_cast<float4*>(slots);
-    if (KS == 1 && S == 1) {                              // a warp's own tile
+    if (MATS == 1 && KS == 1 && S == 1) {                 // a warp's own tile
       __syncwarp();
       if (wt < T)
         for (int cell = lane; cell < cells; cell += 32) {
           float4 v[MATS];
-#pragma unroll
-          for (int j = 0; j < MATS; ++j) v[j] = slots4[(warp * MATS + j) * cells + cell];
+          v[0] = slots4[warp * cells + cell];
           gemv_store<BF16, MATS>(args, (tile0 + round + wt) * 16 + (cell & 3) * 4, cell >> 2, v);
         }
       __syncwarp();
@@ -581,10 +543,10 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, MATS, NT, DEEP>::WARPS, GemvC
       float4 v[MATS];
 #pragma unroll
       for (int j = 0; j < MATS; ++j) {
-        float4& first = slots4[(tile * KS * MATS + j) * cells + cell];
-        v[j] = first;
-        for (int k = 1; k < KS; ++k) add4(v[j], slots4[((tile * KS + k) * MATS + j) * cells + cell]);
-        if (S > 1) first = v[j];
+        float4* first = slots4 + (tile * MATS + j) * KS * cells + cell;
+        v[j] = *first;
+        for (int k = 1; k < KS; ++k) add4(v[j], first[k * cells]);
+        if (S > 1) *first = v[j];
       }
       if (S == 1) gemv_store<BF16, MATS>(args, (tile0 + round + tile) * 16 + (cell & 3) * 4, cell >> 2, v);
     }
@@ -595,7 +557,7 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, MATS, NT, DEEP>::WARPS, GemvC
         float4 v[MATS];
 #pragma unroll
         for (int j = 0; j < MATS; ++j) {
-          const uint32_t at = ptx::smem_u32(slots4 + (tile * KS * MATS + j) * cells + cell);
+          const uint32_t at = ptx::smem_u32(slots4 + (tile * MATS + j) * KS * cells + cell);
           v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           for (int r = 0; r < S; ++r) add4(v[j], ld_cluster_f32x4(map_to_rank(at, static_cast<uint32_t>(r))));
         }
@@ -618,7 +580,7 @@ struct GemvPlan {
 
 template <WType WT, bool BF16, int MATS, int NT, bool DEEP>
 struct GemvLaunch {
-  using C = GemvCfg<WT, MATS, NT, DEEP>;
+  using C = GemvCfg<WT, NT, DEEP>;
   static constexpr int kSmem = 232448;
   static constexpr auto kernel = &gemv_kernel<WT, BF16, MATS, NT, DEEP>;
 
@@ -684,15 +646,16 @@ struct GemvLaunch {
       // tiles per round and warps per tile: all warps busy, as few rounds as can be, and no
       // more shares of a tile than shorten the longest one
       const int tiles = (all_tiles + fit[i] - 1) / fit[i];
-      const int rounds = (tiles + C::WARPS - 1) / C::WARPS;
+      constexpr int kMost = C::WARPS / MATS;              // tiles of a round
+      const int rounds = (tiles + kMost - 1) / kMost;
       const int round_tiles = (tiles + rounds - 1) / rounds;
-      int ks = C::WARPS / round_tiles < per ? C::WARPS / round_tiles : per;
+      int ks = kMost / round_tiles < per ? kMost / round_tiles : per;
       const int longest = (per + ks - 1) / ks;
       ks = (per + longest - 1) / longest;
-      const int warps = round_tiles * ks;
+      const int warps = round_tiles * MATS * ks;
       // shared memory: ring, sums, X (rows an odd number of 64-byte units apart) and scales
       const int slots = warps * C::DEPTH * C::STAGE;
-      const int scale = slots + warps * MATS * args.M * 64;
+      const int scale = slots + warps * args.M * 64;
       const int fit_x = ((kSmem - scale - 128) / args.M - 64) / (C::CK * 2 + 4);
       if (fit_x < 1) continue;
       const int pieces = (per + fit_x - 1) / fit_x;
