@@ -2,9 +2,10 @@
 //
 // Forward:   G = X Wg^T, U = X Wu^T, H = a(G) * U, one launch.
 // Backward:  dG = dH * U * a'(G), dU = dH * a(G) element by element, then
-//            dX = dG Wg + dU Wu and dWg = dG^T X, dWu = dU^T X: three launches.
+//            dX = dG Wg + dU Wu, dWg = dG^T X and dWu = dU^T X in one launch.
 // The products are gated_gemm.cuh's; this file holds the elementwise kernel, the tensor
 // maps, the choice of tile and the launches.
+#include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -67,8 +68,12 @@ struct Launch {
   }
 };
 
+// Time of one tile beside its K blocks (set-up and the part of the epilogue that no other
+// tile's MMAs cover), in K blocks.
+constexpr int kTileCost = 6;
+
 template <GatedOp OP, int ACT, int NCTA, int BN, int STAGES>
-int launch_gemm(const GatedMaps& tm, const GatedGemmArgs& args, cudaStream_t stream) {
+int launch_gemm(const GatedMaps& tm, GatedGemmArgs args, cudaStream_t stream) {
   using C = GatedCfg<OP, NCTA, BN, STAGES>;
   static_assert(C::SMEM_BYTES <= 232448, "shared memory budget");
   auto* fn = &gated_gemm<OP, ACT, NCTA, BN, STAGES>;
@@ -86,11 +91,20 @@ int launch_gemm(const GatedMaps& tm, const GatedGemmArgs& args, cudaStream_t str
     if (e != cudaSuccess || clusters <= 0) return set_error(4, "gated_f16 occupancy: %s", cudaGetErrorString(e));
     max_clusters[dev] = clusters;
   }
-  const long long num_m = static_cast<long long>((args.rows + C::TILE_M - 1) / C::TILE_M) * (OP == GatedOp::GradW ? 2 : 1);
-  const long long tiles = num_m * ((args.cols + C::OUT_N - 1) / C::OUT_N);
-  if (tiles > 0x7F000000LL) return set_error(2, "gated_f16: problem too large");
-  const long long clusters = persistent_clusters(tiles, NCTA, device_sm_count(), max_clusters[dev], sm_cap_enabled());
-  set_last_tile("f16", OP == GatedOp::Forward ? "gated" : OP == GatedOp::GradX ? "grad_x" : "grad_w", NCTA, BN);
+  auto up = [](long long v, long long by) { return (v + by - 1) / by; };
+  const long long n1 = up(C::kFwd ? args.N : args.K, C::OUT_N);
+  const long long tiles1 = up(args.M, C::TILE_M) * n1, tiles2 = C::kFwd ? 0 : 2 * up(args.N, C::TILE_M) * n1;
+  if (tiles1 + tiles2 > 0x7F000000LL) return set_error(2, "gated_f16: problem too large");
+  const long long clusters = persistent_clusters(tiles1 + tiles2, NCTA, device_sm_count(), max_clusters[dev], C::kFwd && sm_cap_enabled());
+  args.long_clusters = 0;
+  args.early_tiles = 0;
+  if (!C::kFwd && tiles1 % clusters != 0) {
+    // the clusters without a last tile of dX do as many tiles of dWg, dWu as take its time
+    const long long cost1 = 2 * up(args.N, 64) + kTileCost, cost2 = up(args.M, 64) + kTileCost;
+    args.long_clusters = static_cast<int>(tiles1 % clusters);
+    const long long early = (clusters - args.long_clusters) * (cost1 / cost2);
+    args.early_tiles = static_cast<int>(early < tiles2 ? early : tiles2);
+  }
   Launch l(static_cast<unsigned>(clusters * NCTA), C::THREADS, C::SMEM_BYTES, NCTA, stream, C::kFwd && pdl_enabled());
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, fn, tm, args);
   return e == cudaSuccess ? 0 : set_error(4, "gated_f16 launch: %s", cudaGetErrorString(e));
@@ -106,14 +120,13 @@ bool output_map(CUtensorMap* m, const void* p, long long rows, long long cols, i
   return encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, p, cols, rows, cols * 2, box_cols, 32, false);
 }
 
-int gemm_args(GatedGemmArgs& g, const GatedArgs& a, int rows, int cols, int reduce) {
+int gemm_args(GatedGemmArgs& g, const GatedArgs& a) {
   std::memset(&g, 0, sizeof(g));
-  g.rows = rows;
-  g.cols = cols;
-  g.nkb = (reduce + 63) / 64;
-  g.a_box_rows = rows >= 128 ? 128 : (rows + 7) / 8 * 8;
+  g.M = a.M;
+  g.N = a.N;
+  g.K = a.K;
+  g.a_box_rows = a.M >= 128 ? 128 : (a.M + 7) / 8 * 8;
   g.bf16 = a.bf16;
-  g.act = a.act;
   g.status = device_status_ptr();
   g.timeout_ns = wait_timeout_ns();
   return g.status ? 0 : 4;
@@ -124,39 +137,37 @@ struct Choice {
   int ncta, bn;
   double t_kb;
 };
-int pick(const Choice* c, int n, long long rows, long long cols_of_bn, int mats, int divide) {
-  // FGF8_FORCE_TILE="<ctas per cluster>x<bn>" selects that tile when it is among the candidates
+// FGF8_FORCE_TILE="<ctas per cluster>x<bn>" selects that tile when it is among the candidates.
+int forced(const Choice* c, int n, int otherwise) {
   if (const char* f = std::getenv("FGF8_FORCE_TILE")) {
     int nc = 0, bn = 0;
     if (std::sscanf(f, "%dx%d", &nc, &bn) == 2)
       for (int i = 0; i < n; ++i)
         if (c[i].ncta == nc && c[i].bn == bn) return i;
   }
+  return otherwise;
+}
+template <int ACT>
+int forward(const GatedArgs& a, const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U, cudaStream_t stream) {
+  static const Choice c[] = {{2, 256, 2.0}, {1, 128, 1.5}, {1, 64, 1.25}, {1, 32, 1.2}};
   int best = 0;
   double cost = -1.0;
-  for (int i = 0; i < n; ++i) {
-    const long long tm = 128LL * c[i].ncta, tn = c[i].bn / divide;
-    const long long tiles = mats * ((rows + tm - 1) / tm) * ((cols_of_bn + tn - 1) / tn);
-    const long long units = device_sm_count() / c[i].ncta;
+  for (int i = 0; i < 4; ++i) {
+    const long long tm = 128LL * c[i].ncta, tn = c[i].bn / 2;
+    const long long tiles = ((a.M + tm - 1) / tm) * ((a.N + tn - 1) / tn), units = device_sm_count() / c[i].ncta;
     const double t = static_cast<double>((tiles + units - 1) / units) * c[i].t_kb;
     if (cost < 0 || t < cost) {
       cost = t;
       best = i;
     }
   }
-  return best;
-}
-
-template <int ACT>
-int forward(const GatedArgs& a, const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U, cudaStream_t stream) {
-  static const Choice c[] = {{2, 256, 2.0}, {1, 128, 1.2}, {1, 64, 0.9}, {1, 32, 0.7}};
-  const Choice& ch = c[pick(c, 4, a.M, a.N, 1, 2)];
+  const Choice& ch = c[forced(c, 4, best)];
   GatedGemmArgs g;
-  if (gemm_args(g, a, a.M, a.N, a.K)) return 4;
+  if (gemm_args(g, a)) return 4;
   g.save = G != nullptr;
   GatedMaps tm;
   std::memset(&tm, 0, sizeof(tm));
-  const int half = ch.bn / 2, cw = half < 32 ? half : 32;
+  const int half = ch.bn / 2, cw = half / 2 < 32 ? half / 2 : 32;   // columns of a staged output chunk
   if (!operand_map(&tm.a[0], a, X, a.M, a.K, g.a_box_rows) || !operand_map(&tm.b[0], a, Wg, a.N, a.K, half) ||
       !operand_map(&tm.b[1], a, Wu, a.N, a.K, half) || !output_map(&tm.d[0], H, a.M, a.N, cw))
     return 4;
@@ -167,33 +178,34 @@ int forward(const GatedArgs& a, const void* X, const void* Wg, const void* Wu, v
   return launch_gemm<GatedOp::Forward, ACT, 1, 32, 10>(tm, g, stream);
 }
 
-int grad_x(const GatedArgs& a, const void* dG, const void* dU, const void* Wg, const void* Wu, void* dX, cudaStream_t stream) {
-  static const Choice c[] = {{2, 256, 2.0}, {1, 128, 1.2}, {1, 64, 0.9}};
-  const Choice& ch = c[pick(c, 3, a.M, a.K, 1, 1)];
+int grads(const GatedArgs& a, const void* dG, const void* dU, const void* X, const void* Wg, const void* Wu, void* dX, void* dWg, void* dWu,
+          cudaStream_t stream) {
+  static const Choice c[] = {{2, 256, 2.0}, {1, 128, 1.5}};
+  double cost = -1.0;
+  int best = 0;
+  for (int i = 0; i < 2; ++i) {
+    const double units = device_sm_count() / c[i].ncta;
+    auto up = [](double v, double by) { return std::ceil(v / by); };
+    const double n1 = up(a.K, c[i].bn), t1 = up(a.M, 128.0 * c[i].ncta) * n1, t2 = 2 * up(a.N, 128.0 * c[i].ncta) * n1;
+    const double c1 = 2 * up(a.N, 64) + kTileCost, c2 = up(a.M, 64) + kTileCost;
+    const double whole = (t1 * c1 + t2 * c2) / units, longest = c1 > whole ? c1 : whole;
+    if (cost < 0 || longest * c[i].t_kb < cost) {
+      cost = longest * c[i].t_kb;
+      best = i;
+    }
+  }
+  best = forced(c, 2, best);
   GatedGemmArgs g;
-  if (gemm_args(g, a, a.M, a.K, a.N)) return 4;
+  if (gemm_args(g, a)) return 4;
   GatedMaps tm;
   std::memset(&tm, 0, sizeof(tm));
   if (!operand_map(&tm.a[0], a, dG, a.M, a.N, g.a_box_rows) || !operand_map(&tm.a[1], a, dU, a.M, a.N, g.a_box_rows) ||
-      !operand_map(&tm.b[0], a, Wg, a.N, a.K, 64) || !operand_map(&tm.b[1], a, Wu, a.N, a.K, 64) || !output_map(&tm.d[0], dX, a.M, a.K, 32))
+      !operand_map(&tm.at[0], a, dG, a.M, a.N, 64) || !operand_map(&tm.at[1], a, dU, a.M, a.N, 64) || !operand_map(&tm.b[0], a, Wg, a.N, a.K, 64) ||
+      !operand_map(&tm.b[1], a, Wu, a.N, a.K, 64) || !operand_map(&tm.b[2], a, X, a.M, a.K, 64) || !output_map(&tm.d[0], dX, a.M, a.K, 32) ||
+      !output_map(&tm.d[1], dWg, a.N, a.K, 32) || !output_map(&tm.d[2], dWu, a.N, a.K, 32))
     return 4;
-  if (ch.ncta == 2) return launch_gemm<GatedOp::GradX, act::kSilu, 2, 256, 6>(tm, g, stream);
-  if (ch.bn == 128) return launch_gemm<GatedOp::GradX, act::kSilu, 1, 128, 6>(tm, g, stream);
-  return launch_gemm<GatedOp::GradX, act::kSilu, 1, 64, 8>(tm, g, stream);
-}
-
-int grad_w(const GatedArgs& a, const void* dG, const void* dU, const void* X, void* dWg, void* dWu, cudaStream_t stream) {
-  static const Choice c[] = {{2, 256, 2.0}, {1, 128, 1.2}};
-  const Choice& ch = c[pick(c, 2, a.N, a.K, 2, 1)];
-  GatedGemmArgs g;
-  if (gemm_args(g, a, a.N, a.K, a.M)) return 4;
-  GatedMaps tm;
-  std::memset(&tm, 0, sizeof(tm));
-  if (!operand_map(&tm.a[0], a, dG, a.M, a.N, 64) || !operand_map(&tm.a[1], a, dU, a.M, a.N, 64) || !operand_map(&tm.b[0], a, X, a.M, a.K, 64) ||
-      !output_map(&tm.d[0], dWg, a.N, a.K, 32) || !output_map(&tm.d[1], dWu, a.N, a.K, 32))
-    return 4;
-  if (ch.ncta == 2) return launch_gemm<GatedOp::GradW, act::kSilu, 2, 256, 6>(tm, g, stream);
-  return launch_gemm<GatedOp::GradW, act::kSilu, 1, 128, 6>(tm, g, stream);
+  if (c[best].ncta == 2) return launch_gemm<GatedOp::Grad, act::kSilu, 2, 256, 6>(tm, g, stream);
+  return launch_gemm<GatedOp::Grad, act::kSilu, 1, 128, 6>(tm, g, stream);
 }
 
 template <int ACT>
@@ -219,8 +231,7 @@ int launch_gated_backward(const GatedArgs& a, const void* dH, const void* X, con
                           const void* G, const void* U, void* dX, void* dWg, void* dWu, void* dG, void* dU,
                           cudaStream_t stream) {
   int r = a.act == act::kSilu ? slopes<act::kSilu>(a, dH, G, U, dG, dU, stream) : slopes<act::kGeluTanh>(a, dH, G, U, dG, dU, stream);
-  if (r == 0) r = grad_x(a, dG, dU, Wg, Wu, dX, stream);
-  if (r == 0) r = grad_w(a, dG, dU, X, dWg, dWu, stream);
+  if (r == 0) r = grads(a, dG, dU, X, Wg, Wu, dX, dWg, dWu, stream);
   return r;
 }
 
