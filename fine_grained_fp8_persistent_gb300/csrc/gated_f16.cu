@@ -72,11 +72,11 @@ struct Launch {
 // tile's MMAs cover), in K blocks.
 constexpr int kTileCost = 6;
 
-template <GatedOp OP, int ACT, int NCTA, int BN, int STAGES>
+template <GatedOp OP, int ACT, int NCTA, int BN, int STAGES, int AROWS = 128>
 int launch_gemm(const GatedMaps& tm, GatedGemmArgs args, cudaStream_t stream) {
-  using C = GatedCfg<OP, NCTA, BN, STAGES>;
+  using C = GatedCfg<OP, NCTA, BN, STAGES, AROWS>;
   static_assert(C::SMEM_BYTES <= 232448, "shared memory budget");
-  auto* fn = &gated_gemm<OP, ACT, NCTA, BN, STAGES>;
+  auto* fn = &gated_gemm<OP, ACT, NCTA, BN, STAGES, AROWS>;
   static int max_clusters[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -175,6 +175,8 @@ int forward(const GatedArgs& a, const void* X, const void* Wg, const void* Wu, v
   if (ch.ncta == 2) return launch_gemm<GatedOp::Forward, ACT, 2, 256, 6>(tm, g, stream);
   if (ch.bn == 128) return launch_gemm<GatedOp::Forward, ACT, 1, 128, 6>(tm, g, stream);
   if (ch.bn == 64) return launch_gemm<GatedOp::Forward, ACT, 1, 64, 8>(tm, g, stream);
+  if (a.M <= 32) return launch_gemm<GatedOp::Forward, ACT, 1, 32, 24, 32>(tm, g, stream);
+  if (a.M <= 64) return launch_gemm<GatedOp::Forward, ACT, 1, 32, 16, 64>(tm, g, stream);
   return launch_gemm<GatedOp::Forward, ACT, 1, 32, 10>(tm, g, stream);
 }
 
