@@ -13,6 +13,7 @@
 #include "activation.cuh"
 #include "gated.h"
 #include "gated_gemm.cuh"
+#include "gated_thin.cuh"
 
 namespace fgf8 {
 namespace {
@@ -72,11 +73,11 @@ struct Launch {
 // tile's MMAs cover), in K blocks.
 constexpr int kTileCost = 6;
 
-template <GatedOp OP, int ACT, int NCTA, int BN, int STAGES, int AROWS = 128>
+template <GatedOp OP, int ACT, int NCTA, int BN, int STAGES>
 int launch_gemm(const GatedMaps& tm, GatedGemmArgs args, cudaStream_t stream) {
-  using C = GatedCfg<OP, NCTA, BN, STAGES, AROWS>;
+  using C = GatedCfg<OP, NCTA, BN, STAGES>;
   static_assert(C::SMEM_BYTES <= 232448, "shared memory budget");
-  auto* fn = &gated_gemm<OP, ACT, NCTA, BN, STAGES, AROWS>;
+  auto* fn = &gated_gemm<OP, ACT, NCTA, BN, STAGES>;
   static int max_clusters[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -105,6 +106,7 @@ int launch_gemm(const GatedMaps& tm, GatedGemmArgs args, cudaStream_t stream) {
     const long long early = (clusters - args.long_clusters) * (cost1 / cost2);
     args.early_tiles = static_cast<int>(early < tiles2 ? early : tiles2);
   }
+  set_last_tile("f16", C::kFwd ? "gated" : "gated_grad", NCTA, BN);
   Launch l(static_cast<unsigned>(clusters * NCTA), C::THREADS, C::SMEM_BYTES, NCTA, stream, C::kFwd && pdl_enabled());
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, fn, tm, args);
   return e == cudaSuccess ? 0 : set_error(4, "gated_f16 launch: %s", cudaGetErrorString(e));
@@ -147,12 +149,89 @@ int forced(const Choice* c, int n, int otherwise) {
   }
   return otherwise;
 }
+// The thin forward pass (gated_thin.cuh): shares S of the reduction per tile of 64 weight
+// rows and its time in units of 128-byte rows through one CTA's copy engine.
+struct ThinPlan {
+  int S, cta_kb;
+  double cost;
+};
+template <int ACT>
+int plan_thin(ThinPlan& p, const GatedArgs& a) {
+  static int fit[64][9] = {};                              // by device and S: clusters that fit
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return set_error(2, "device id %d", dev);
+  if (fit[dev][1] == 0) {
+    auto* fn = &gated_thin<ACT>;
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, thin::kSmemCap);
+    for (int s = 8; e == cudaSuccess && s >= 1; --s) {
+      Launch l(static_cast<unsigned>(device_sm_count() / s * s), thin::kThreads, thin::kSmemCap, s, nullptr, false);
+      int n = 0;
+      e = cudaOccupancyMaxActiveClusters(&n, fn, &l.cfg);
+      if (e == cudaSuccess && n <= 0) e = cudaErrorInvalidConfiguration;
+      if (e == cudaSuccess) fit[dev][s] = n;
+    }
+    if (e != cudaSuccess) {
+      fit[dev][1] = 0;
+      return set_error(4, "gated_f16 occupancy: %s", cudaGetErrorString(e));
+    }
+  }
+  const int tiles = (a.N + thin::kRows - 1) / thin::kRows, nkb = (a.K + 63) / 64, nb = (a.M + 15) / 16 * 16;
+  p.cost = -1.0;
+  for (int s = 1; s <= 8; ++s) {
+    const int per = (nkb + s - 1) / s;
+    if ((s - 1) * per >= nkb) continue;                    // a CTA without work
+    const int waves = (tiles + fit[dev][s] - 1) / fit[dev][s];
+    const double t = waves * (static_cast<double>(per) * (128 + nb) + (s > 1 ? 1500.0 : 500.0));
+    if (p.cost < 0 || t < p.cost) {
+      p.S = s;
+      p.cta_kb = per;
+      p.cost = t;
+    }
+  }
+  return 0;
+}
+
+template <int ACT>
+int launch_thin(const ThinPlan& p, const GatedArgs& a, const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U,
+                cudaStream_t stream) {
+  GatedThinArgs t;
+  std::memset(&t, 0, sizeof(t));
+  t.M = a.M;
+  t.N = a.N;
+  t.K = a.K;
+  t.nb = (a.M + 15) / 16 * 16;
+  const int stage = thin::kABytes + t.nb * 128;
+  const int fit = (thin::kSmemCap - 1024) / stage / thin::kKpu * thin::kKpu;
+  t.stages = fit < thin::kMaxStages ? fit : thin::kMaxStages;
+  t.cta_kb = p.cta_kb;
+  t.bf16 = a.bf16;
+  t.act = a.act;
+  t.out = H;
+  t.keep[0] = G;
+  t.keep[1] = U;
+  t.status = device_status_ptr();
+  t.timeout_ns = wait_timeout_ns();
+  if (!t.status) return 4;
+  CUtensorMap tx, tg, tu;
+  if (!operand_map(&tx, a, X, a.M, a.K, t.nb) || !operand_map(&tg, a, Wg, a.N, a.K, thin::kRows) || !operand_map(&tu, a, Wu, a.N, a.K, thin::kRows))
+    return 4;
+  const int tiles = (a.N + thin::kRows - 1) / thin::kRows;
+  set_last_tile("f16", "gated_thin", p.S, t.nb);
+  Launch l(static_cast<unsigned>(tiles * p.S), thin::kThreads, 1024 + static_cast<size_t>(t.stages) * stage, p.S, stream, pdl_enabled());
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, &gated_thin<ACT>, tx, tg, tu, t);
+  return e == cudaSuccess ? 0 : set_error(4, "gated_f16 launch: %s", cudaGetErrorString(e));
+}
+
 template <int ACT>
 int forward(const GatedArgs& a, const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U, cudaStream_t stream) {
-  static const Choice c[] = {{2, 256, 2.0}, {1, 128, 1.5}, {1, 64, 1.25}, {1, 32, 1.2}};
+  // time of a tile per K block, in 128-byte rows through a CTA's copy engine (1.4 ns): the
+  // rows loaded bound the one-CTA tiles, the MMA the pair (512 tokens at 7168 x 2048, one
+  // wave each: 48 us on 2 x 256, 42 on 1 x 128, 54 for two waves of 1 x 64)
+  static const Choice c[] = {{2, 256, 320.0}, {1, 128, 256.0}, {1, 64, 200.0}};
   int best = 0;
   double cost = -1.0;
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 3; ++i) {
     const long long tm = 128LL * c[i].ncta, tn = c[i].bn / 2;
     const long long tiles = ((a.M + tm - 1) / tm) * ((a.N + tn - 1) / tn), units = device_sm_count() / c[i].ncta;
     const double t = static_cast<double>((tiles + units - 1) / units) * c[i].t_kb;
@@ -161,7 +240,13 @@ int forward(const GatedArgs& a, const void* X, const void* Wg, const void* Wu, v
       best = i;
     }
   }
-  const Choice& ch = c[forced(c, 4, best)];
+  const int kb = (a.K + 63) / 64;
+  if (a.M <= 256 && std::getenv("FGF8_FORCE_TILE") == nullptr) {
+    ThinPlan p;
+    if (int r = plan_thin<ACT>(p, a)) return r;
+    if (p.cost < cost * kb + 500.0) return launch_thin<ACT>(p, a, X, Wg, Wu, H, G, U, stream);
+  }
+  const Choice& ch = c[forced(c, 3, best)];
   GatedGemmArgs g;
   if (gemm_args(g, a)) return 4;
   g.save = G != nullptr;
@@ -174,10 +259,7 @@ int forward(const GatedArgs& a, const void* X, const void* Wg, const void* Wu, v
   if (g.save && (!output_map(&tm.d[1], G, a.M, a.N, cw) || !output_map(&tm.d[2], U, a.M, a.N, cw))) return 4;
   if (ch.ncta == 2) return launch_gemm<GatedOp::Forward, ACT, 2, 256, 6>(tm, g, stream);
   if (ch.bn == 128) return launch_gemm<GatedOp::Forward, ACT, 1, 128, 6>(tm, g, stream);
-  if (ch.bn == 64) return launch_gemm<GatedOp::Forward, ACT, 1, 64, 8>(tm, g, stream);
-  if (a.M <= 32) return launch_gemm<GatedOp::Forward, ACT, 1, 32, 24, 32>(tm, g, stream);
-  if (a.M <= 64) return launch_gemm<GatedOp::Forward, ACT, 1, 32, 16, 64>(tm, g, stream);
-  return launch_gemm<GatedOp::Forward, ACT, 1, 32, 10>(tm, g, stream);
+  return launch_gemm<GatedOp::Forward, ACT, 1, 64, 8>(tm, g, stream);
 }
 
 int grads(const GatedArgs& a, const void* dG, const void* dU, const void* X, const void* Wg, const void* Wu, void* dX, void* dWg, void* dWu,

@@ -23,8 +23,7 @@
 //
 // Roles: warp 0 TMA producer, warp 1 MMA issuer, warps 2-9 epilogue (two per TMEM lane
 // quarter, each with half of the columns), warp 10 relay, which does the MMA issuer's mbarrier waiting and hands over by a named barrier
-// (gemm_persistent.cuh says why).  A pipeline unit is two K blocks of 64
-// (four on thin tiles).  Two
+// (gemm_persistent.cuh says why).  A pipeline unit is two K blocks of 64.  Two
 // accumulator buffers, so the epilogue of a tile overlaps the next tile's MMAs.
 #pragma once
 #include "activation.cuh"
@@ -53,7 +52,7 @@ struct GatedMaps {
   CUtensorMap a[2], b[3], at[2], d[3];
 };
 
-template <GatedOp OP, int NCTA_, int BN_, int STAGES_, int AROWS = 128>
+template <GatedOp OP, int NCTA_, int BN_, int STAGES_>
 struct GatedCfg {
   static constexpr int NCTA = NCTA_, BN = BN_, STAGES = STAGES_;
   static constexpr bool kFwd = OP == GatedOp::Forward;
@@ -65,15 +64,11 @@ struct GatedCfg {
   static_assert(NCTA == 1 || NCTA == 2, "one CTA or a pair");
   static_assert(!kBT || B_LOCAL % 64 == 0, "MN-major B: whole 64-element boxes");
   static_assert(!kFwd || (BN / 2) % 16 == 0, "gate and up halves");
-  // Thin tiles (AROWS < 128, at most that many tokens): a stage holds AROWS rows of X, so
-  // more stages of weights are in flight; the MMA's rows past them read whatever follows
-  // in shared memory (the next stages) and are never stored.
-  static_assert(AROWS == 128 || (kFwd && NCTA == 1), "thin tiles: forward, one CTA");
-  static constexpr int KPU = AROWS < 128 ? 4 : 2;
+  static constexpr int KPU = 2;
   static_assert(STAGES % KPU == 0, "stages per unit");
   static constexpr int UNITS = STAGES / KPU;
   static constexpr int BOX_BYTES = 64 * 128;              // an MN-major box: 64 K rows of 128 bytes
-  static constexpr int A_BYTES = AROWS * 128;
+  static constexpr int A_BYTES = BM * 128;
   static constexpr int B_BYTES = B_LOCAL * 128;
   static constexpr int NACC = 2;
   static constexpr int TMEM_USED = NACC * BN;
@@ -90,7 +85,6 @@ struct GatedCfg {
   static constexpr int EPI_BUFS = 2;                      // staging buffers per epilogue warp
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = STAGES * A_BYTES;
-  static_assert(STAGES * B_BYTES >= (BM - AROWS) * 128, "the rows past the last stage stay in shared memory");
   static constexpr int OFF_EPI = OFF_B + STAGES * B_BYTES;
   static constexpr int OFF_BAR = OFF_EPI + EPI_WARPS * EPI_BUFS * CHUNK_BYTES;
   static constexpr int BAR_FULL = 0, BAR_EMPTY = UNITS, BAR_ACC_FULL = 2 * UNITS;
@@ -109,18 +103,13 @@ __device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t 
 template <int CW>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[CW]) {
   if constexpr (CW == 32) ptx::tmem_ld_32x32b_x32(taddr, r);
-  else if constexpr (CW == 16) ptx::tmem_ld_32x32b_x16(taddr, r);
-  else
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr)
-                 : "memory");
+  else ptx::tmem_ld_32x32b_x16(taddr, r);
 }
 
-template <GatedOp OP, int ACT, int NCTA, int BN, int STAGES, int AROWS = 128>
-__global__ void __launch_bounds__(GatedCfg<OP, NCTA, BN, STAGES, AROWS>::THREADS, 1)
+template <GatedOp OP, int ACT, int NCTA, int BN, int STAGES>
+__global__ void __launch_bounds__(GatedCfg<OP, NCTA, BN, STAGES>::THREADS, 1)
     gated_gemm(const __grid_constant__ GatedMaps tm, const GatedGemmArgs args) {
-  using C = GatedCfg<OP, NCTA, BN, STAGES, AROWS>;
+  using C = GatedCfg<OP, NCTA, BN, STAGES>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = ptx::smem_u32(smem);
