@@ -225,3 +225,18 @@ def test_other_stream_and_graph(fg, dev, M):
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(h0, h2) and all(torch.equal(a, b) for a, b in zip(d0, d2))
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_feed_forward_example(fg, dev, fmt):
+    """The example trains (its loss falls by half at least) and serves in 4 bits: each of three
+    matrices rounds to within a quarter of its groups' steps, about 0.1 of a weight."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "feed_forward.py")
+    spec = importlib.util.spec_from_file_location("feed_forward", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    losses, rel = example.main(["--tokens", "256", "--hidden", "512", "--inter", "1024", "--steps", "12", "--fmt", fmt])
+    assert losses[-1] < 0.5 * losses[0]
+    assert rel < 0.35
