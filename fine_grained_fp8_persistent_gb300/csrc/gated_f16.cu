@@ -264,10 +264,10 @@ int forward(const GatedArgs& a, const void* X, const void* Wg, const void* Wu, v
 
 int grads(const GatedArgs& a, const void* dG, const void* dU, const void* X, const void* Wg, const void* Wu, void* dX, void* dWg, void* dWu,
           cudaStream_t stream) {
-  static const Choice c[] = {{2, 256, 2.0}, {1, 128, 1.5}};
+  static const Choice c[] = {{2, 256, 2.0}, {1, 128, 1.5}, {1, 64, 100.0}};
   double cost = -1.0;
   int best = 0;
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < 3; ++i) {
     const double units = device_sm_count() / c[i].ncta;
     auto up = [](double v, double by) { return std::ceil(v / by); };
     const double n1 = up(a.K, c[i].bn), t1 = up(a.M, 128.0 * c[i].ncta) * n1, t2 = 2 * up(a.N, 128.0 * c[i].ncta) * n1;
@@ -278,7 +278,7 @@ int grads(const GatedArgs& a, const void* dG, const void* dU, const void* X, con
       best = i;
     }
   }
-  best = forced(c, 2, best);
+  best = forced(c, 3, best);
   GatedGemmArgs g;
   if (gemm_args(g, a)) return 4;
   GatedMaps tm;
@@ -289,6 +289,7 @@ int grads(const GatedArgs& a, const void* dG, const void* dU, const void* X, con
       !output_map(&tm.d[1], dWg, a.N, a.K, 32) || !output_map(&tm.d[2], dWu, a.N, a.K, 32))
     return 4;
   if (c[best].ncta == 2) return launch_gemm<GatedOp::Grad, act::kSilu, 2, 256, 6>(tm, g, stream);
+  if (c[best].bn == 64) return launch_gemm<GatedOp::Grad, act::kSilu, 1, 64, 8>(tm, g, stream);
   return launch_gemm<GatedOp::Grad, act::kSilu, 1, 128, 6>(tm, g, stream);
 }
 

@@ -588,20 +588,26 @@ struct GemvLaunch {
 
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  GemvLaunch(int log_s, int clusters, int threads, int smem, cudaStream_t stream) {
+  GemvLaunch(int log_s, int clusters, int threads, int smem, cudaStream_t stream, bool pdl) {
     std::memset(&cfg, 0, sizeof(cfg));
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 1;
-    attr[0].val.clusterDim.y = 1u << log_s;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    // a cluster of one needs no attribute
+    int n = 0;
+    if (log_s > 0) {
+      attr[n].id = cudaLaunchAttributeClusterDimension;
+      attr[n].val.clusterDim.x = 1;
+      attr[n].val.clusterDim.y = 1u << log_s;
+      attr[n++].val.clusterDim.z = 1;
+    }
+    if (pdl) {
+      attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
     cfg.gridDim = dim3(static_cast<unsigned>(clusters), 1u << log_s, 1);
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    cfg.numAttrs = static_cast<unsigned>(n);
   }
 
   // Clusters of 2^log_s CTAs that fit the device at one CTA per SM; null on an error.
@@ -616,10 +622,9 @@ struct GemvLaunch {
     if (fit[dev][0] == 0) {
       cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
       for (int i = 3; e == cudaSuccess && i >= 0; --i) {
-        GemvLaunch l(i, device_sm_count() >> i, 32 * C::WARPS, kSmem, nullptr);
-        l.cfg.numAttrs = 1;
-        int n = 0;
-        e = cudaOccupancyMaxActiveClusters(&n, kernel, &l.cfg);
+        GemvLaunch l(i, device_sm_count() >> i, 32 * C::WARPS, kSmem, nullptr, false);
+        int n = device_sm_count();
+        if (i > 0) e = cudaOccupancyMaxActiveClusters(&n, kernel, &l.cfg);
         if (e == cudaSuccess && n <= 0) e = cudaErrorInvalidConfiguration;
         if (e == cudaSuccess) fit[dev][i] = n;
       }
@@ -689,7 +694,7 @@ struct GemvLaunch {
   }
 
   static int launch(const GemvPlan& p, cudaStream_t stream) {
-    GemvLaunch l(p.log_s, p.clusters, p.threads, p.smem, stream);
+    GemvLaunch l(p.log_s, p.clusters, p.threads, p.smem, stream, pdl_enabled());
     const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kernel, p.a);
     return e == cudaSuccess ? 0 : set_error(4, "matrix-vector launch: %s", cudaGetErrorString(e));
   }
