@@ -134,7 +134,7 @@ int gemm_args(GatedGemmArgs& g, const GatedArgs& a) {
   return g.status ? 0 : 4;
 }
 
-// One tile configuration and its relative time per K block and tile.
+// One tile configuration and its relative time.
 struct Choice {
   int ncta, bn;
   double t_kb;
@@ -264,17 +264,23 @@ int forward(const GatedArgs& a, const void* X, const void* Wg, const void* Wu, v
 
 int grads(const GatedArgs& a, const void* dG, const void* dU, const void* X, const void* Wg, const void* Wu, void* dX, void* dWg, void* dWu,
           cudaStream_t stream) {
-  static const Choice c[] = {{2, 256, 2.0}, {1, 128, 1.5}, {1, 64, 100.0}};
+  // Time of the launch in 128-byte rows through a CTA's copy engine (1.4 ns): the longer of
+  // one dX tile's reduction and an SM's share of all tiles; a tile's stores and set-up
+  // count as `t_kb` further rows.  Measured (us) on 2x256 / 1x128 / 1x64: 17 x 7168 x 2048
+  // 34.8 / 36.7 / 41.1, 67 x 2048 x 1368 21.9 / 19.9 / 17.9, 100 x 2048 x 8192 95 / 85 / 76,
+  // 512 x 7168 x 2048 51 / 74 / 107.
+  static const Choice c[] = {{2, 256, 2300.0}, {1, 128, 1300.0}, {1, 64, 750.0}};
   double cost = -1.0;
   int best = 0;
+  const double a_rows = a.M >= 128 ? 128.0 : (a.M + 7) / 8 * 8;
   for (int i = 0; i < 3; ++i) {
-    const double units = device_sm_count() / c[i].ncta;
     auto up = [](double v, double by) { return std::ceil(v / by); };
+    const double units = device_sm_count() / c[i].ncta, b_rows = c[i].bn / c[i].ncta;
     const double n1 = up(a.K, c[i].bn), t1 = up(a.M, 128.0 * c[i].ncta) * n1, t2 = 2 * up(a.N, 128.0 * c[i].ncta) * n1;
-    const double c1 = 2 * up(a.N, 64) + kTileCost, c2 = up(a.M, 64) + kTileCost;
+    const double c1 = 2 * up(a.N, 64) * (a_rows + b_rows) + c[i].t_kb, c2 = up(a.M, 64) * (128.0 + b_rows) + c[i].t_kb;
     const double whole = (t1 * c1 + t2 * c2) / units, longest = c1 > whole ? c1 : whole;
-    if (cost < 0 || longest * c[i].t_kb < cost) {
-      cost = longest * c[i].t_kb;
+    if (cost < 0 || longest < cost) {
+      cost = longest;
       best = i;
     }
   }

@@ -102,6 +102,16 @@ def gemv64(x, w64):
 def close(got, want, bound, what=""):
     g = got.double()
     assert g.shape == want.shape, (what, g.shape, want.shape)
+    if got.dtype == torch.float16:
+        # past the type's range (what rounds above 65504) the result is infinite; a value whose
+        # bound reaches across the edge may be either
+        edge = 65520.0
+        past = want.abs() - bound >= edge
+        assert torch.equal(g[past], torch.copysign(torch.full_like(want[past], torch.inf), want[past])), what
+        inside = want.abs() + bound < edge
+        g, want, bound = g[inside], want[inside], bound[inside]
+        if not g.numel():
+            return
     assert torch.isfinite(g).all(), f"{what}: non-finite values"
     over = (g - want).abs() - bound
     assert not (over > 0).any(), (f"{what}: {int((over > 0).sum())} of {over.numel()} outside the bound, worst by "

@@ -72,7 +72,7 @@ def test_backward(fg, dev, M, N, K, dtype, act):
 @pytest.mark.parametrize("tile", ["2x256", "1x128", "1x64"])
 @pytest.mark.parametrize("M,N,K", [(20, 40, 72), (300, 520, 200), (640, 1304, 136)])
 def test_every_tile(fg, dev, monkeypatch, M, N, K, tile, dtype):
-    """Each tile shape, whatever the launcher would choose (the backward pass has no 1x64)."""
+    """Each tile shape, whatever the launcher would choose."""
     dh, x, wg, wu, g, u = _grad_inputs(M, N, K, dtype, 11, dev)
     monkeypatch.setenv("FGF8_FORCE_TILE", tile)
     got = fg.gated_f16(x, wg, wu, "silu", save=True)
@@ -80,8 +80,7 @@ def test_every_tile(fg, dev, monkeypatch, M, N, K, tile, dtype):
     for t, w, b, what in zip(got, *ref.forward64(x, wg, wu, "silu"), "hgu"):
         ref.close(t, w, b, what)
     got = fg.gated_f16_backward(dh, x, wg, wu, g, u)
-    if tile != "1x64":
-        assert fg.last_tile() == f"f16 gated_grad {tile}"
+    assert fg.last_tile() == f"f16 gated_grad {tile}"
     for t, w, b, what in zip(got, *ref.backward64(dh, x, wg, wu, g, u, "silu"), ("dx", "dwg", "dwu")):
         ref.close(t, w, b, what)
     assert fg.check_status()[0] == 0

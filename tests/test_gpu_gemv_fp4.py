@@ -98,6 +98,36 @@ def test_every_code_and_scale(fg, dev, oracle, fmt, M):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", [2, 9])
+def test_nan_scales_stay_in_their_rows(fg, dev, oracle, fmt, M):
+    """A NaN scale (E8M0 byte 255, E4M3 0x7F) makes its own weight row's outputs NaN, no others."""
+    N, K = 37, 512
+    wq, sf, w64 = _weights(oracle, N, K, fmt, 12, dev)
+    x = _x(M, K, torch.bfloat16, 13, dev)
+    clean = fg.gemv_fp4(x, wq, sf, fmt)
+    b = sf.cpu().numpy().view(np.uint8).reshape(*sf.shape, 4).copy()
+    b[1, 20, 2] = 255 if fmt == 0 else 0x7F
+    bad = torch.from_numpy(b.view(np.int32).reshape(tuple(sf.shape))).to(dev)
+    y = fg.gemv_fp4(x, wq, bad, fmt)
+    rows = torch.arange(N, device=dev) != 20
+    assert torch.isnan(y[:, 20]).all() and torch.equal(y[:, rows], clean[:, rows])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", [2, 13])
+def test_many_rows(fg, dev, oracle, fmt, M):
+    """More weight rows than one round of tiles holds, plain and gated."""
+    N, K = 45001, 192
+    wq, sf, w64 = _weights(oracle, N, K, fmt, 14, dev)
+    x = _x(M, K, torch.float16, 15, dev)
+    y = fg.gemv_fp4(x, wq, sf, fmt)
+    _check(y, x, w64)
+    h = fg.gated_gemv_fp4(x, wq, sf, wq, sf, fmt)
+    g, dg = ref.gemv64(x, w64)
+    ref.close(h, *ref.gate64(g, dg, g, dg, "silu", x.dtype))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_wide_range_of_x(fg, dev, oracle, fmt):
     """Rows of X that span 2^-100 .. 2^100, one row each, and rows that mix sizes 2^30 apart."""
     M, N, K = 8, 40, 256
