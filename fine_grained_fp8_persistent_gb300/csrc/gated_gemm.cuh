@@ -131,6 +131,9 @@ __global__ void __launch_bounds__(GatedCfg<OP, NCTA, BN, STAGES>::THREADS, 1)
   const int m2 = C::kFwd ? 0 : up(args.N, C::TILE_M), tiles2 = 2 * m2 * n1;
   const int kb1 = up(C::kFwd ? args.K : args.N, 64), kb2 = up(args.M, 64);
 
+  // Tiles run in bands of eight tile columns: a wave of 76 tiles then reads about as many
+  // rows of either operand (bands of 4 to 16 are within 2 % of each other).
+  constexpr int kBand = 8;
   // Tile: output matrix (0 H or dX; 1, 2 dWg, dWu), first row of this CTA's 128, first
   // column, rows and columns of the matrix, K blocks.
   struct Pos { int mat, row, col, rows, nkb; };
@@ -141,16 +144,18 @@ __global__ void __launch_bounds__(GatedCfg<OP, NCTA, BN, STAGES>::THREADS, 1)
   auto tile_at = [&](int i, Pos& p) -> bool {                          // the cluster's i-th tile
     int m, n;
     if (i < mine1) {
-      dense_tile(C0 + i * CN, m1, n1, 16, m, n);
+      dense_tile(C0 + i * CN, m1, n1, kBand, m, n);
       p.mat = 0;
       p.rows = args.M;
       p.nkb = C::kFwd ? kb1 : 2 * kb1;
     } else {
       if (C::kFwd) return false;
       i -= mine1;
-      const int t = i < early ? C0 - args.long_clusters + i * others : args.early_tiles + C0 + (i - early) * CN;
+      // then all take turns, the ones with less to do so far first
+      const int turn = late ? C0 - args.long_clusters : C0 + others;
+      const int t = i < early ? C0 - args.long_clusters + i * others : args.early_tiles + turn + (i - early) * CN;
       if (t >= tiles2) return false;
-      dense_tile(t, 2 * m2, n1, 16, m, n);
+      dense_tile(t, 2 * m2, n1, kBand, m, n);
       p.mat = m >= m2 ? 2 : 1;
       if (p.mat == 2) m -= m2;
       p.rows = args.N;
