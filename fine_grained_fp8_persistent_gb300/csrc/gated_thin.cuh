@@ -9,7 +9,8 @@
 // are weights; here 128 of 192 are.  The copy engine takes about 1.4 ns per row and CTA.)
 // A cluster of S CTAs splits the reduction of a tile; each writes its FP32 sums to shared
 // memory and the cluster adds them through distributed shared memory, in order, with the
-// activation, the product and the store.
+// activation, the product and the store.  Weights from memory, N = 2048, K = 7168 (59 MB,
+// 8.7 us at the copy rate): 15.8 us at 64 tokens, 17.2 at 128, bound by the copy engine.
 //
 // Roles: warp 0 TMA producer, warp 1 MMA issuer, all warps the epilogue (warps 0-3 drain
 // one TMEM lane quarter each).
@@ -25,7 +26,7 @@ struct GatedThinArgs {
   int nb;            // MMA columns: M rounded up to 16
   int stages;        // pipeline stages of a K block (even)
   int cta_kb;        // K blocks of 64 of one CTA's share
-  int bf16, act;
+  int bf16;
   void* out;
   void* keep[2];     // G and U, or null
   uint32_t* status;

@@ -640,8 +640,8 @@ struct GemvLaunch {
   // The layout with the least time by a simple model (ns): the chunks of the busiest SM, X
   // to stage, a cluster's joins.  Measured on a GB300: 40 bytes per ns and SM on half an
   // SM's resources; 48 with the deep rings, which cost 1 us more (the next kernel's CTAs
-  // find no room before this one's exit).  One token at N = K = 7168 in MXFP4 (three tiles
-  // per SM) takes 8.5 us shallow and 9.3 us deep, N = 32768 28.8 and 23.1 us.
+  // find no room before this one's exit).  One token at N = K = 7168 in MXFP4, bf16 X (three
+  // tiles per SM), takes 8.39 us shallow and 8.54 us deep, N = 32768 34.4 and 25.2 us.
   static bool plan(GemvPlan& best, const GemvKArgs& args) {
     const int* fit = max_clusters();
     if (fit == nullptr) return false;

@@ -227,7 +227,8 @@ FGF8_API int gemm_fp4_blockscaled(const void* Aq, const void* SFA, const void* B
  *   G, U : [M][N] (outputs, both or neither may be NULL): the projections rounded
  *          to the same type, which gated_f16_backward reads
  * All of one type, fp16 or bf16 (dtype, an fgf8_dtype); act is an fgf8_act.
- * Requires K % 8 == 0, N % 8 == 0, M >= 0, N, K >= 1.
+ * Requires K % 8 == 0, N % 8 == 0, M >= 0, N, K >= 1, and outputs that overlap no
+ * input.  Always on the static schedule (fgf8_set_scheduler does not apply).
  */
 FGF8_API int gated_f16(const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U, int M, int N,
                        int K, int dtype, int act, void* stream);
@@ -256,7 +257,7 @@ FGF8_API long long fgf8_gated_backward_ws_bytes(int M, int N);
  * generates one token per sequence, whose time is the reading of W.
  *   X  : fp16 or bf16 [M][K] (dtype);  Wq : uint8 [N][K/2];  SF : scale table of N rows
  *   Y  : [M][N], the type of X, rounded to nearest even from FP32 sums
- * X is not quantized.  Requires K % 64 == 0, N, K >= 1, 0 <= M <= 16 (more rows
+ * X is not quantized.  Y overlaps no input.  Requires K % 64 == 0, N, K >= 1, 0 <= M <= 16 (more rows
  * return FGF8_ERR_UNSUPPORTED: quantize_fp4 X and call gemm_fp4_blockscaled).
  */
 FGF8_API int gemv_fp4(const void* X, const void* Wq, const void* SF, void* Y, int M, int N, int K, int fmt,
@@ -298,7 +299,8 @@ FGF8_API int fgf8_check_status(void* stream, unsigned int* raw_bits);
 FGF8_API const char* fgf8_last_error(void);
 
 /* Kernel configuration of the last GEMM this thread launched, as text
- * ("<kind> <schedule> <CTAs per cluster>x<tile width>", e.g. "mxf8 dense 2x224");
+ * ("<kind> <schedule> <CTAs per cluster>x<tile width>", e.g. "mxf8 dense 2x224";
+ * "f16 gated_thin <CTAs of the cluster>x<tokens>" for the gated block of 17 to 256 rows);
  * "" before the first launch.  The pointer stays valid until this thread's next
  * GEMM call. */
 FGF8_API const char* fgf8_last_tile(void);
@@ -316,9 +318,10 @@ FGF8_API int fgf8_selftest_wait_timeout(void* stream);
 
 /* Programmatic dependent launch (on by default; the environment variable
  * FGF8_PDL=0 turns it off at first use).  When on, every kernel but those of
- * gated_f16_backward is launched with programmatic stream serialization: its set-up (barriers, TMEM, descriptor
- * prefetch) overlaps the end of the previous kernel on the stream, and it reads no
- * global data before that kernel has completed.  enable: 1 on, 0 off, anything
+ * gated_f16_backward is launched with programmatic stream serialization: its set-up
+ * (barriers, TMEM, descriptor prefetch) overlaps the end of the previous kernel on
+ * the stream, and it uses no global data before that kernel has completed (the
+ * matrix-vector kernels only prefetch weights into L2).  enable: 1 on, 0 off, anything
  * else leaves it unchanged.  Returns the previous setting. */
 FGF8_API int fgf8_set_pdl(int enable);
 
