@@ -638,15 +638,19 @@ struct GemvLaunch {
   }
 
   // The layout with the least time by a simple model (ns): the chunks of the busiest SM, X
-  // to stage, a cluster's joins.  Measured on a GB300: 40 bytes per ns and SM on half an
-  // SM's resources; 48 with the deep rings, which cost 1 us more (the next kernel's CTAs
-  // find no room before this one's exit).  One token at N = K = 7168 in MXFP4, bf16 X (three
-  // tiles per SM), takes 8.39 us shallow and 8.54 us deep, N = 32768 34.4 and 25.2 us.
+  // to stage, a cluster's joins.  Its constants were searched for the least
+  // loss against the best layout, over device times of both variants with clusters of 1, 2,
+  // 4 and 8, forced in turn (GB300; 32 shapes, up to 7 numbers of tokens, each type): 1.1 %
+  // on average, 19 % at most (0.7 us, 512 rows).  They stand for more than their names (a
+  // rate also holds part of the latency).  Staging runs on all warps and costs latency per
+  // piece, so few warps, many tokens and pieces are what a cluster is for: each of its CTAs
+  // stages its own share of X.  Eight tokens of bf16 at 2048 x 7168 in NVFP4 take 10.8 us
+  // on one CTA per tile and 6.1 us on four; one token in MXFP4 takes 8.39 us shallow and
+  // 8.54 us deep at 7168 x 7168, 34.4 and 25.2 us at 32768 x 7168.
   static bool plan(GemvPlan& best, const GemvKArgs& args) {
     const int* fit = max_clusters();
     if (fit == nullptr) return false;
     const int chunks = (args.K + C::CK - 1) / C::CK, all_tiles = (args.N + 15) / 16;
-    const int x_chunk = (C::CK * 2 + 4) * args.M;          // bytes of X and its scales
     for (int i = 0; i < 4; ++i) {
       const int s = 1 << i, per = (chunks + s - 1) / s;
       if ((s - 1) * per >= chunks) continue;              // a CTA without work
@@ -667,8 +671,13 @@ struct GemvLaunch {
       if (fit_x < 1) continue;
       const int pieces = (per + fit_x - 1) / fit_x;
       const double stagings = pieces > 1 ? pieces * rounds : 1.0;
-      const double ns = static_cast<double>(rounds) * longest * warps * C::STAGE / (DEEP ? 48.0 : 40.0) +
-                        stagings * (per / pieces * static_cast<double>(x_chunk) / 50.0 + 500.0) + (s > 1 ? 2500.0 * rounds : 0.0) + (DEEP ? 1000.0 : 0.0);
+      constexpr double kRate = DEEP ? (WT == WType::W16 ? (NT == 1 ? 67.0 : 54.0) : (NT == 1 ? 42.0 : 32.5))
+                                    : (WT == WType::W16 ? 40.0 : 23.0);      // bytes per ns and SM
+      constexpr double kStage = BF16 && WT != WType::W16 ? 1.2 : 0.43;       // ns per element and warp
+      const double x_elements = static_cast<double>(per) / pieces * C::CK * args.M;
+      double ns = static_cast<double>(rounds) * longest * warps * C::STAGE / kRate +
+                  stagings * (1280.0 + kStage * x_elements / warps) + (DEEP ? 170.0 : 0.0);
+      if (s > 1) ns += 1000.0 + 2040.0 * (rounds - 1) + 8.0 * rounds * round_tiles * args.M + (s == 8 ? 200.0 : 0.0);
       if (best.ns >= 0 && ns >= best.ns) continue;
       best.ns = ns;
       best.log_s = i;
