@@ -128,6 +128,18 @@ def test_many_rows(fg, dev, oracle, fmt, M):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N,K", [(8, 512, 4096), (8, 2048, 7168), (16, 4096, 4096), (7, 333, 7232), (16, 2048, 16384)])
+def test_split_reductions(fg, dev, oracle, M, N, K, dtype, fmt):
+    """Sizes whose reduction a cluster of 2, 4 or 8 CTAs shares, one with an odd last share."""
+    wq, sf, w64 = _weights(oracle, N, K, fmt, 21, dev)
+    x = _x(M, K, dtype, 22, dev)
+    y = fg.gemv_fp4(x, wq, sf, fmt)
+    _check(y, x, w64)
+    assert torch.equal(y, fg.gemv_fp4(x, wq, sf, fmt))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_wide_range_of_x(fg, dev, oracle, fmt):
     """Rows of X that span 2^-100 .. 2^100, one row each, and rows that mix sizes 2^30 apart."""
     M, N, K = 8, 40, 256
