@@ -195,10 +195,11 @@ __global__ void __launch_bounds__(GatedCfg<OP, NCTA, BN, STAGES>::THREADS, 1)
     ptx::tc_fence_before();
   }
   // Forward: nothing above reads global memory, so it overlaps the tail of the previous
-  // kernel.  No kernel here lets the next one start early: with programmatic launches
-  // through the backward pass (elementwise kernel, GradX, GradW, and the next call's
-  // elementwise kernel waiting beside GradW, more CTAs than fit) a queue of calls at
-  // 4096 x 7168 x 2048 stopped for good, outside any wait of these kernels.
+  // kernel.  No kernel here lets the next one start early.  (When the backward pass was
+  // three programmatic launches, a queue of its calls at 4096 x 7168 x 2048 stopped for
+  // good, outside any bounded wait.  Two changes were made together: plain launches, and
+  // the convergence after lane 0's store in the epilogue, without which a split warp could
+  // reach the next tcgen05.ld.  Either may have been what mattered.)
   if constexpr (C::kFwd) ptx::griddep_wait();
   __syncthreads();
   if constexpr (NCTA == 2) cluster_sync_all();

@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(thin::kThreads, 1)
     const uint64_t t0 = ptx::globaltimer();
     while (ptx::globaltimer() - t0 < 200000ull) __nanosleep(1000);
   }
+  __syncwarp();                                             // lanes may have left that wait apart
   ptx::tc_fence_after();
   // accumulator row r (r < 64: G, else U of weight row r - 64) of token m to part[m][r],
   // over the stages

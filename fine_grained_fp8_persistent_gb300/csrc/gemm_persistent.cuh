@@ -77,7 +77,10 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
+// The barrier is a whole-warp (.aligned) instruction: lanes that left a loop or branch at
+// different times meet first.
 __device__ __forceinline__ void cluster_sync_all() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
@@ -130,6 +133,7 @@ __device__ __forceinline__ void tc_commit_mc(uint32_t bar, uint16_t mask) {
 }
 template <int NCTA>
 __device__ __forceinline__ void tc_alloc(uint32_t dst_smem, uint32_t ncols) {
+  __syncwarp();
   if constexpr (NCTA == 2) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
                  "r"(ncols)
@@ -142,6 +146,7 @@ __device__ __forceinline__ void tc_alloc(uint32_t dst_smem, uint32_t ncols) {
 }
 template <int NCTA>
 __device__ __forceinline__ void tc_dealloc(uint32_t taddr, uint32_t ncols) {
+  __syncwarp();
   if constexpr (NCTA == 2)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
                  : "memory");
@@ -1318,6 +1323,7 @@ __global__ void __launch_bounds__(PCfg<KIND, SCHED, NCTA, BN, STAGES, NACC, AROW
             row_ok = false;
           }
         }
+        __syncwarp();
       }
       const size_t row_off = static_cast<size_t>(tl.a_row0 + r) * static_cast<size_t>(N);
       const uint32_t taddr = tmem_base + ((q * 32u) << 16) + static_cast<uint32_t>(acc * BN);
@@ -1352,6 +1358,7 @@ __global__ void __launch_bounds__(PCfg<KIND, SCHED, NCTA, BN, STAGES, NACC, AROW
               }
             }
             fused_group_out(args, PackedBf16{hv}, amax, (tl.n_blk * BN) / 128 + g, grow, row_ok);
+            __syncwarp();
           }
           if (++acc == C::NACC) { acc = 0; acc_phase ^= 1u; }
           continue;
@@ -1399,6 +1406,7 @@ __global__ void __launch_bounds__(PCfg<KIND, SCHED, NCTA, BN, STAGES, NACC, AROW
             ptx::tma_store_2d(&tm_d, buf, x, y);
             ptx::bulk_commit_group();
           }
+          __syncwarp();   // the next TMEM load is a whole-warp instruction
           ++epi_chunks;
         }
         if (++acc == C::NACC) { acc = 0; acc_phase ^= 1u; }
@@ -1417,6 +1425,7 @@ __global__ void __launch_bounds__(PCfg<KIND, SCHED, NCTA, BN, STAGES, NACC, AROW
         }
         if (row_ok)
           store_row32(args.D, row_off, tl.n_blk * BN + 32 * c, N, reinterpret_cast<const float*>(v), bf16);
+        __syncwarp();
       }
       if constexpr (TAIL) {
         uint32_t v[16];
@@ -1466,6 +1475,7 @@ __global__ void __launch_bounds__(PCfg<KIND, SCHED, NCTA, BN, STAGES, NACC, AROW
             row_ok = false;
           }
         }
+        __syncwarp();
       }
       const uint32_t taddr =
           tmem_base + ((q * 32u) << 16) + static_cast<uint32_t>(acc * BN + h * HALF);
@@ -1613,6 +1623,7 @@ __global__ void __launch_bounds__(PCfg<KIND, SCHED, NCTA, BN, STAGES, NACC, AROW
             row_ok = false;
           }
         }
+        __syncwarp();
       }
       const int col0 = tl.n_blk * BN + col_off_h;
 #pragma unroll

@@ -91,8 +91,13 @@ __device__ __forceinline__ void bulk_wait_group() {
 }
 
 // ----------------------------------------------------------------- tcgen05: TMEM
+// The .sync.aligned instructions are undefined for a warp whose lanes have not met again
+// after a branch on the lane or a loop that they leave at different times.  Allocation and
+// release bring the warp together themselves; loads, stores and named barriers stand where
+// pwait or a __syncwarp has done so (in the wrappers too it cost 2 % of the 4-bit GEMM).
 // Allocation is a warp-wide instruction; the base address lands in shared memory.
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
+  __syncwarp();
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
                "r"(ncols)
                : "memory");
@@ -101,6 +106,7 @@ __device__ __forceinline__ void tmem_relinquish() {
   asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  __syncwarp();
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
                : "memory");
 }
