@@ -17,10 +17,12 @@
 // either: lane t's share of a row of X is 16 contiguous bytes.
 //
 // bf16 X is scaled, for each row and chunk of 256 columns, by the power of two that puts
-// the largest finite |x| there into [2^14, 2^15), and rounded to fp16, the type E2M1 decodes
-// to.  Every |x| of at least 2^-31 of that largest one stays exact; smaller ones move by at
-// most 2^-39 of it, below the FP32 accumulation's own rounding.  The chunk's sums are
-// multiplied by the power's inverse as they are added to the totals.
+// the largest finite |x| there into [2^14, 2^15), and converted to fp16, the type E2M1
+// decodes to.  That is exact for every |x| of at least 2^-31 of the largest.  The chunk's
+// sums are multiplied by the power's inverse as they are added to the totals.  Where a row
+// of X holds smaller |x| too (they may be all that its weights leave: code 0 is common),
+// it stays bf16, and a chunk with such a row is multiplied in bf16, where decoded weights
+// are exact as well, at two to three times the instructions.
 //
 // Work split.  One CTA per SM, walking tiles of 16 weight rows in rounds; a warp takes one
 // tile (of one of the two matrices, when gated) of the round, or, when there are fewer
@@ -134,6 +136,11 @@ __device__ __forceinline__ void e8m0x4(uint32_t w, float (&s)[4]) {
   s[1] = __uint_as_float(lo & 0xFFFF0000u);
   s[2] = __uint_as_float(hi << 16);
   s[3] = __uint_as_float(hi & 0xFFFF0000u);
+}
+// An fp16 pair as a bf16 pair, times f; exact for decoded weights and for X scaled to fp16.
+__device__ __forceinline__ uint32_t bf16_pair(uint32_t h, float f) {
+  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return pack_2x16(v.x * f, v.y * f, true);
 }
 // The E4M3 byte `i` of w as an fp16 pair (value, value).
 __device__ __forceinline__ uint32_t e4m3_pair(uint32_t w, int i) {
@@ -303,8 +310,9 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, NT, DEEP>::WARPS, GemvCfg<WT,
   for (int i = 0; i < C::DEPTH - 1; ++i) issue();
 
   const uint32_t xs = sbase + static_cast<uint32_t>(args.off_x);
-  float* xscale = reinterpret_cast<float*>(smem + args.off_scale);   // [chunk][M]
+  float* xscale = reinterpret_cast<float*>(smem + args.off_scale);   // [chunk][M]: the power's inverse, negative: kept in bf16
   int slot = 0;                                           // ring slot of the next chunk
+  [[maybe_unused]] bool wide = false;                     // the piece of X holds rows kept in bf16
 
   // this lane's rows of X (columns of the MMA); columns past M repeat the last row and
   // are never stored
@@ -325,20 +333,46 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, NT, DEEP>::WARPS, GemvCfg<WT,
         if (round > 0 || x0 > 0) __syncthreads();         // the previous piece has been read
         const int xn = min(args.x_chunks, nc - x0);
         const int k0 = (c0 + x0) * C::CK;
+        wide = false;
         // one warp takes 256 columns of a row, 8 per lane (zeros past K)
         const int blocks = (xn * C::CK + 255) / 256;
         // loads in flight per lane: 4, or 8 where 16 rows make the staging long (NVFP4
         // 16 x 32768 x 7168 47.2 -> 46.2 us, MXFP4 48.3 -> 45.3; one token gets 10 % slower)
         constexpr int XL = NT == 2 ? 8 : 4;
+        auto load_x = [&](int m, int v) -> uint4 {        // zeros past K
+          if (k0 + 8 * v >= K) return make_uint4(0u, 0u, 0u, 0u);
+          return __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(args.X) + static_cast<size_t>(m) * K + k0 + 8 * v));
+        };
         for (int it0 = warp; it0 < M * blocks; it0 += XL * W) {
           uint4 w[XL];
 #pragma unroll
           for (int q = 0; q < XL; ++q) {
             const int it = it0 + q * W, m = it / blocks, v = (it - m * blocks) * 32 + lane;
-            w[q] = make_uint4(0u, 0u, 0u, 0u);
-            if (it < M * blocks && k0 + 8 * v < K)
-              w[q] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(args.X) + static_cast<size_t>(m) * K + k0 + 8 * v));
+            w[q] = it < M * blocks ? load_x(m, v) : make_uint4(0u, 0u, 0u, 0u);
           }
+          // 8 columns of row m per lane into shared memory
+          auto put = [&](int m, int v, const uint32_t (&u)[4]) {
+            st_shared_v4(xs + static_cast<uint32_t>(m * args.x_stride + v * 16), u[0], u[1], u[2], u[3]);
+          };
+          // x * 2^sh is exact for |x| of bits `a` and 31 powers of two below; 2^sh is not an
+          // FP32 value above sh = 127 (it reaches 141), where 2^14 of it is applied first;
+          // 2^-sh always is one, a subnormal from sh = 127 on
+          auto put_scaled = [&](int m, int blk, int v, uint32_t (&u)[4], uint32_t a) {
+            const int sh = 141 - (a ? static_cast<int>(a >> 7) : 127);
+            const float f = __uint_as_float(static_cast<uint32_t>(127 + (sh > 127 ? sh - 14 : sh)) << 23);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float lo = __uint_as_float(u[j] << 16), hi = __uint_as_float(u[j] & 0xFFFF0000u);
+              if (sh > 127) {
+                lo *= 16384.0f;
+                hi *= 16384.0f;
+              }
+              u[j] = pack_2x16(lo * f, hi * f, false);
+            }
+            if (lane == 0) xscale[blk * M + m] = sh < 127 ? __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) : __uint_as_float(1u << (149 - sh));
+            put(m, v, u);
+          };
+          bool again = false;
 #pragma unroll
           for (int q = 0; q < XL; ++q) {
             const int it = it0 + q * W;
@@ -352,45 +386,54 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, NT, DEEP>::WARPS, GemvCfg<WT,
 #pragma unroll
                 for (int j = 0; j < 4; ++j) asm volatile("st.shared.b32 [%0], %1;" ::"r"(d + 16 * j), "r"(u[j]) : "memory");
               }
-            } else {
-              if constexpr (kScaleX) {
-                // largest |x| of the 256 columns as bf16 bits; infinities and NaN are left
-                // out of it, in a second look that only rows with them take
-                uint32_t a2 = 0u;
+            } else if constexpr (kScaleX) {
+              // largest and, in this lane, least |x| of the 256 columns as bf16 bits
+              uint32_t a2 = 0u, z2 = 0x7FFF7FFFu;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) a2 = __vmaxu2(a2, u[j] & 0x7FFF7FFFu);
-                uint32_t a = __reduce_max_sync(0xffffffffu, max(a2 & 0xFFFFu, a2 >> 16));
-                if (a >= 0x7F80u) {
-                  a = 0u;
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    const uint32_t lo = u[j] & 0x7FFFu, hi = (u[j] >> 16) & 0x7FFFu;
-                    a = max(a, lo < 0x7F80u ? lo : 0u);
-                    a = max(a, hi < 0x7F80u ? hi : 0u);
-                  }
-                  a = __reduce_max_sync(0xffffffffu, a);
-                }
-                // x * 2^sh is exact; 2^sh is not an FP32 value above sh = 127 (it reaches
-                // 141), where 2^14 of it is applied first; 2^-sh always is one, a subnormal
-                // from sh = 127 on
-                const int sh = 141 - (a ? static_cast<int>(a >> 7) : 127);
-                const float f = __uint_as_float(static_cast<uint32_t>(127 + (sh > 127 ? sh - 14 : sh)) << 23);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  float lo = __uint_as_float(u[j] << 16), hi = __uint_as_float(u[j] & 0xFFFF0000u);
-                  if (sh > 127) {
-                    lo *= 16384.0f;
-                    hi *= 16384.0f;
-                  }
-                  u[j] = pack_2x16(lo * f, hi * f, false);
-                }
-                if (lane == 0) xscale[blk * M + m] = sh < 127 ? __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) : __uint_as_float(1u << (149 - sh));
+              for (int j = 0; j < 4; ++j) {
+                a2 = __vmaxu2(a2, u[j] & 0x7FFF7FFFu);
+                z2 = __vminu2(z2, u[j] & 0x7FFF7FFFu);
               }
-              st_shared_v4(xs + static_cast<uint32_t>(m * args.x_stride + v * 16), u[0], u[1], u[2], u[3]);
+              const uint32_t a = __reduce_max_sync(0xffffffffu, max(a2 & 0xFFFFu, a2 >> 16));
+              again = again || a >= 0x7F80u || static_cast<int>(min(z2 & 0xFFFFu, z2 >> 16)) < static_cast<int>(a & 0x7F80u) - (31 << 7);
+              put_scaled(m, blk, v, u, a);
+            } else {
+              put(m, v, u);
+            }
+          }
+          if constexpr (kScaleX) {
+            // infinities, NaN, zeros or |x| too small for the scale: these rows once more, with
+            // only finite values in the largest and only non-zero ones in the least
+            if (__any_sync(0xffffffffu, again)) {
+#pragma unroll 1
+              for (int it = it0; it < M * blocks && it < it0 + XL * W; it += W) {
+                const int m = it / blocks, blk = it - m * blocks, v = blk * 32 + lane;
+                const uint4 x = load_x(m, v);
+                uint32_t u[4] = {x.x, x.y, x.z, x.w};
+                uint32_t a = 0u, z = 0x7F80u;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const uint32_t e = (u[j / 2] >> (16 * (j & 1))) & 0x7FFFu;
+                  if (e < 0x7F80u && e != 0u) {
+                    a = max(a, e);
+                    z = min(z, e);
+                  }
+                }
+                a = __reduce_max_sync(0xffffffffu, a);
+                z = __reduce_min_sync(0xffffffffu, z);
+                if (static_cast<int>(z) < static_cast<int>(a & 0x7F80u) - (31 << 7)) {
+                  wide = true;
+                  if (lane == 0) xscale[blk * M + m] = -1.0f;
+                  put(m, v, u);
+                } else {
+                  put_scaled(m, blk, v, u, a);
+                }
+              }
             }
           }
         }
-        __syncthreads();
+        if constexpr (kScaleX) wide = __syncthreads_or(wide ? 1 : 0) != 0;
+        else __syncthreads();
       }
 
       // -------------------------------------------------------- this warp's chunks of it
@@ -443,6 +486,70 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, NT, DEEP>::WARPS, GemvCfg<WT,
             const uint32_t w = *reinterpret_cast<const uint32_t*>(scales + lane * 4);
             large = __any_sync(0xffffffffu, (w & (w << 1) & 0x80808080u) != 0u);
           }
+          // The chunk in bf16: X as it was, weights decoded as below and converted.  MXFP4
+          // scales each group's sum; one that overflows (|x| near 2^128) is taken again
+          // from weights times 2^-9.  Rare, so the loop is short rather than fast.
+          [[maybe_unused]] auto bf16_chunk = [&]() {
+            float back[NT];                               // of row 8 n + g of X
+#pragma unroll
+            for (int n = 0; n < NT; ++n) back[n] = xscale[(q - x0) * M + min(8 * n + g, M - 1)];
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {                 // 32 codes of each row
+              uint32_t a[4], lo[4], hi[4];
+              ldmatrix_x4(st + (la ^ static_cast<uint32_t>((i >> 1) << 5)), a);
+              e2m1x8(i & 1 ? a[2] : a[0], lo);
+              e2m1x8(i & 1 ? a[3] : a[1], hi);
+              const uint8_t* w = scales + (i >> 2) * (C::WPC * 32) + g * 4 + (WT == WType::NV ? ((i >> 1) & 1) * 64 : 0);
+              const int at = WT == WType::NV ? 2 * (i & 1) + (t >> 1) : i & 3;
+              const uint32_t w0 = *reinterpret_cast<const uint32_t*>(w) >> (8 * at), w1 = *reinterpret_cast<const uint32_t*>(w + 32) >> (8 * at);
+              [[maybe_unused]] float sf[4], sf1[4];
+              if constexpr (WT == WType::NV) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  lo[e] = mul2(lo[e], e4m3_pair(w0, 0));
+                  hi[e] = mul2(hi[e], e4m3_pair(w1, 0));
+                }
+              } else {
+                e8m0x4(w0, sf);
+                e8m0x4(w1, sf1);
+                sf[1] = sf1[0];
+              }
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                uint32_t b[4];
+                lds128(xl[n] + xc + 64 * i, b);
+                if (back[n] > 0.0f) {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) b[e] = bf16_pair(b[e], back[n]);
+                }
+                auto mma = [&](float (&d)[4], float f) {
+                  uint32_t wl[4], wh[4];
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    wl[e] = bf16_pair(lo[e], f);
+                    wh[e] = bf16_pair(hi[e], f);
+                  }
+                  __syncwarp();
+                  mma16816<true>(d, wl[0], wh[0], wl[1], wh[1], b[0], b[1]);
+                  mma16816<true>(d, wl[2], wh[2], wl[3], wh[3], b[2], b[3]);
+                };
+                if constexpr (WT == WType::NV) {
+                  mma(acc[n], 1.0f);
+                } else {
+                  float p[4] = {}, after = 1.0f;
+                  mma(p, 1.0f);
+                  const bool lost = !(fabsf(p[0]) + fabsf(p[1]) <= 3.0e38f && fabsf(p[2]) + fabsf(p[3]) <= 3.0e38f);
+                  if (__any_sync(0xffffffffu, lost)) {
+                    p[0] = p[1] = p[2] = p[3] = 0.0f;
+                    mma(p, 1.0f / 512.0f);
+                    after = 512.0f;
+                  }
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) acc[n][e] = after == 1.0f ? fmaf(p[e], sf[e >> 1], acc[n][e]) : fmaf(p[e] * sf[e >> 1], after, acc[n][e]);
+                }
+              }
+            }
+          };
           auto body = [&](auto large_c) {
             constexpr bool kLarge = decltype(large_c)::value;
 #pragma unroll
@@ -510,7 +617,17 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, NT, DEEP>::WARPS, GemvCfg<WT,
                 for (int e = 0; e < 4; ++e) acc[n][e] = fmaf(part_acc[n][e], xp[n][e & 1], acc[n][e]);
             }
           };
-          if (kScaleX && WT == WType::MX && large) body(std::true_type{});
+          bool in_bf16 = false;
+          if constexpr (kScaleX) {
+            if (__builtin_expect(wide, 0)) {
+              bool kept = false;
+#pragma unroll
+              for (int n = 0; n < NT; ++n) kept = kept || xp[n][0] < 0.0f || xp[n][1] < 0.0f;
+              in_bf16 = __any_sync(0xffffffffu, kept);
+            }
+          }
+          if (kScaleX && in_bf16) bf16_chunk();
+          else if (kScaleX && WT == WType::MX && large) body(std::true_type{});
           else body(std::false_type{});
         }
       }

@@ -257,7 +257,8 @@ FGF8_API long long fgf8_gated_backward_ws_bytes(int M, int N);
  * generates one token per sequence, whose time is the reading of W.
  *   X  : fp16 or bf16 [M][K] (dtype);  Wq : uint8 [N][K/2];  SF : scale table of N rows
  *   Y  : [M][N], the type of X, rounded to nearest even from FP32 sums
- * X is not quantized.  Y overlaps no input.  Requires K % 64 == 0, N, K >= 1, 0 <= M <= 16 (more rows
+ * X is not quantized: every product is exact, also of x far below the largest |x| of
+ * its row, and the sums are FP32.  Y overlaps no input.  Requires K % 64 == 0, N, K >= 1, 0 <= M <= 16 (more rows
  * return FGF8_ERR_UNSUPPORTED: quantize_fp4 X and call gemm_fp4_blockscaled).
  */
 FGF8_API int gemv_fp4(const void* X, const void* Wq, const void* SF, void* Y, int M, int N, int K, int fmt,
