@@ -9,7 +9,7 @@
 //            and the product lies in 2^-10 .. 2688, so it is exact; the MMA accumulates
 //            over the whole reduction.
 //   MXFP4    the codes in fp16 (exact), one FP32 partial sum per group of 32, then
-//            acc += partial * 2^e: scales reach 2^+-127, which no 16-bit product holds.
+//            acc += partial * 2^e: scales reach 2^+-127, which no fp16 product holds.
 // A 16-byte piece of a weight row holds 32 codes.  ldmatrix hands lane 4 g + t of the warp
 // the 8 codes 8 t .. 8 t + 7 of row g; taken as two K = 16 instructions, instruction i
 // multiplies codes 8 t + 4 i + {0, 1} and {2, 3} of lane t as its k = 2 t + {0, 1} and
@@ -35,7 +35,6 @@
 // shared memory, also in order.
 #pragma once
 #include <cstring>
-#include <type_traits>
 
 #include "activation.cuh"
 #include "gated.h"
@@ -327,6 +326,11 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, NT, DEEP>::WARPS, GemvCfg<WT,
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
     int q = round + wt < my_tiles ? ks : nc;              // this warp's next chunk
+    // MXFP4: bit 7 of the scale bytes that count in the word this lane looks at; in the last
+    // chunk, if it is not a whole one, only of groups before K
+    [[maybe_unused]] const uint32_t look = (tile0 + round + wt) * 16 + (lane & 15) < N ? 0x80808080u : 0u;
+    [[maybe_unused]] const int left = K / SV - ((args.chunks - 1) * C::WPC + (lane >> 4)) * 4;
+    [[maybe_unused]] const uint32_t look_last = left >= 4 ? look : left > 0 ? look >> (8 * (4 - left)) : 0u;
     for (int x0 = 0; x0 < nc; x0 += args.x_chunks) {
       // -------------------------------------------------------- a piece of X
       if (round == 0 || nc > args.x_chunks) {
@@ -479,12 +483,14 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, NT, DEEP>::WARPS, GemvCfg<WT,
               for (int e = 0; e < 4; ++e) part_acc[n][e] = 0.0f;
           }
           const uint8_t* scales = smem + so + 2048;
-          // MXFP4 on scaled X: a scale of 2^65 or more could overflow sums whose product
-          // with 2^p is finite; such a chunk multiplies each group by 2^p first
-          bool large = false;
+          // MXFP4 on scaled X: sums of scaled X times 2^-63 .. 2^64 are plain FP32 values.  A
+          // scale outside of that (E8M0 bits 7 and 6 alike) could overflow or lose digits
+          // before the power's inverse is back, so its chunk is multiplied in bf16.  Rows
+          // past N and groups past K do not count.
+          bool in_bf16 = false;
           if constexpr (kScaleX && WT == WType::MX) {
             const uint32_t w = *reinterpret_cast<const uint32_t*>(scales + lane * 4);
-            large = __any_sync(0xffffffffu, (w & (w << 1) & 0x80808080u) != 0u);
+            in_bf16 = (~(w ^ (w << 1)) & (c0 + q >= full_chunks ? look_last : look)) != 0u;
           }
           // The chunk in bf16: X as it was, weights decoded as below and converted.  MXFP4
           // scales each group's sum; one that overflows (|x| near 2^128) is taken again
@@ -550,8 +556,7 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, NT, DEEP>::WARPS, GemvCfg<WT,
               }
             }
           };
-          auto body = [&](auto large_c) {
-            constexpr bool kLarge = decltype(large_c)::value;
+          auto body = [&]() {
 #pragma unroll
             for (int f = 0; f < 2; ++f) {                 // 128 codes of each row
               // scales of rows g and g + 8
@@ -601,34 +606,28 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, NT, DEEP>::WARPS, GemvCfg<WT,
                       mma16816_f16_zero(p, lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
                       mma16816<false>(p, lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
 #pragma unroll
-                      for (int e = 0; e < 4; ++e) {
-                        if constexpr (kLarge) acc[n][e] = fmaf(p[e] * xp[n][e & 1], sf[e >> 1][s], acc[n][e]);
-                        else sums[n][e] = fmaf(p[e], sf[e >> 1][s], sums[n][e]);
-                      }
+                      for (int e = 0; e < 4; ++e) sums[n][e] = fmaf(p[e], sf[e >> 1][s], sums[n][e]);
                     }
                   }
                 }
               }
             }
-            if constexpr (kScaleX && !kLarge) {
+            if constexpr (kScaleX) {
 #pragma unroll
               for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[n][e] = fmaf(part_acc[n][e], xp[n][e & 1], acc[n][e]);
             }
           };
-          bool in_bf16 = false;
           if constexpr (kScaleX) {
             if (__builtin_expect(wide, 0)) {
-              bool kept = false;
 #pragma unroll
-              for (int n = 0; n < NT; ++n) kept = kept || xp[n][0] < 0.0f || xp[n][1] < 0.0f;
-              in_bf16 = __any_sync(0xffffffffu, kept);
+              for (int n = 0; n < NT; ++n) in_bf16 = in_bf16 || xp[n][0] < 0.0f || xp[n][1] < 0.0f;
             }
+            if (WT == WType::MX || wide) in_bf16 = __any_sync(0xffffffffu, in_bf16);
           }
-          if (kScaleX && in_bf16) bf16_chunk();
-          else if (kScaleX && WT == WType::MX && large) body(std::true_type{});
-          else body(std::false_type{});
+          if (__builtin_expect(kScaleX && in_bf16, 0)) bf16_chunk();
+          else body();
         }
       }
     }

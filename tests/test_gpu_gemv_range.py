@@ -1,5 +1,5 @@
 """GPU tests of the matrix-vector operators on values far apart: small x beside large x that
-meet zero weights.
+meet zero weights, and MXFP4 scales over their whole range.
 
 What is allowed.  Products are exact; sums are FP32, in steps of 16 terms that each may drop
 2^-23 of the magnitudes added so far, and a few joins: gamma(K) sum |x w|.  Nothing else: an x
@@ -104,6 +104,61 @@ def test_x_over_the_whole_range_of_bf16(fg, dev, M, fmt):
     scales = torch.full((N, K // fp4.GROUP[fmt]), 127 if fmt == 0 else 0x38, dtype=torch.uint8, device=dev)
     wq, sf = fp4.pack(codes, scales)
     _check(fg.gemv_fp4(x, wq, sf, fmt), x, fp4.values(codes, scales, fmt))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("M", [1, 5, 8, 16])
+@pytest.mark.parametrize("K", [256, 320, 1088])
+def test_mx_scales_of_any_size_stay_in_their_rows(fg, dev, K, M, dtype):
+    """MXFP4 weight rows and groups whose scales lie anywhere in 2^-127 .. 2^127, side by side,
+    on rows of X of very different sizes."""
+    N = 75
+    gen = torch.Generator(device=dev).manual_seed(K + M)
+    bytes_ = torch.tensor([0, 1, 3, 20, 40, 62, 63, 64, 65, 100, 127, 150, 190, 191, 192, 193, 220, 245, 252, 254], device=dev)
+    own = bytes_[torch.randint(0, len(bytes_), (N, 1), generator=gen, device=dev)]
+    near = (own + torch.randint(-3, 4, (N, K // 32), generator=gen, device=dev)).clamp(0, 254)
+    any_ = bytes_[torch.randint(0, len(bytes_), (N, K // 32), generator=gen, device=dev)]
+    mixed = torch.arange(N, device=dev)[:, None] % 3 == 0          # rows whose groups differ too
+    scales = torch.where(mixed, any_, near).to(torch.uint8)
+    codes = torch.randint(0, 16, (N, K), generator=gen, device=dev, dtype=torch.uint8)
+    wq, sf = fp4.pack(codes, scales)
+    w = fp4.values(codes, scales, 0)
+    sizes = [0, 125, -120, 60, -60, 100, -100, 30] if dtype == torch.bfloat16 else [0, 10, -10, 5]
+    x = torch.randn(M, K, generator=gen, device=dev, dtype=torch.float64)
+    for shift in range(len(sizes)):
+        e = torch.tensor([sizes[(m + shift) % len(sizes)] for m in range(M)], device=dev)
+        xs = torch.ldexp(x, e[:, None]).to(dtype)
+        R, T = ref.unit(dtype)
+        y, err, mags = _sums(xs, w)
+        top = 2.0 ** 126 if dtype == torch.bfloat16 else 2.0 ** 14
+        inside = mags < top
+        if not inside.any():
+            continue
+        b = err + R * (y.abs() + err) + T
+        ref.close(fg.gemv_fp4(xs, wq, sf, 0)[inside], y[inside], b[inside], f"shift {shift}")
+
+
+def test_a_neighbours_large_scale(fg, dev):
+    """Two weight rows of one tile: scale 2^-100 on x of 2^126 gives what it gives whatever the
+    other row's scale; scale 2^-127 on x of about 2^98, beside an x of 2^127 with weight
+    zero, keeps the digits of x."""
+    codes = torch.zeros((16, 256), dtype=torch.uint8, device=dev)
+    scales = torch.full((16, 8), 127, dtype=torch.uint8, device=dev)
+    codes[0, :32] = 7                                  # 6.0
+    scales[0] = 27
+    scales[1] = 200
+    wq, sf = fp4.pack(codes, scales)
+    x = torch.zeros((1, 256), dtype=torch.bfloat16, device=dev)
+    x[0, :32] = 2.0 ** 126
+    assert float(fg.gemv_fp4(x, wq, sf, 0)[0, 0]) == 192 * 2.0 ** 26
+    codes.zero_()
+    codes[2, 1] = 1
+    scales[:] = 127
+    scales[2] = 0
+    wq, sf = fp4.pack(codes, scales)
+    x.zero_()
+    x[0, 0], x[0, 1] = 2.0 ** 127, 255.0 * 2.0 ** 90
+    assert float(fg.gemv_fp4(x, wq, sf, 0)[0, 2]) == 255.0 * 2.0 ** -38
 
 
 @pytest.mark.parametrize("fmt", FMTS)
