@@ -36,8 +36,15 @@ int check_pointers(const char* who, std::initializer_list<const void*> ptrs) {
   return FGF8_OK;
 }
 
-int check_gated(const char* who, int M, int N, int K, int dtype, int act) {
+int check_sizes(const char* who, int M, int N, int K) {
   if (M < 0 || N <= 0 || K <= 0) return fgf8::set_error(FGF8_ERR_INVALID_ARG, "%s: M=%d N=%d K=%d", who, M, N, K);
+  if (M > fgf8::kMaxSize || N > fgf8::kMaxSize || K > fgf8::kMaxSize)
+    return fgf8::set_error(FGF8_ERR_UNSUPPORTED, "%s: M=%d N=%d K=%d: sizes above %d", who, M, N, K, fgf8::kMaxSize);
+  return FGF8_OK;
+}
+
+int check_gated(const char* who, int M, int N, int K, int dtype, int act) {
+  if (int r = check_sizes(who, M, N, K)) return r;
   if (dtype != FGF8_F16 && dtype != FGF8_BF16) return fgf8::set_error(FGF8_ERR_INVALID_ARG, "%s: bad dtype %d", who, dtype);
   if (act != FGF8_ACT_SILU && act != FGF8_ACT_GELU_TANH)
     return fgf8::set_error(FGF8_ERR_INVALID_ARG, "%s: bad activation %d", who, act);
@@ -47,7 +54,7 @@ int check_gated(const char* who, int M, int N, int K, int dtype, int act) {
 }
 
 int check_gemv(const char* who, int M, int N, int K, int fmt, int dtype) {
-  if (M < 0 || N <= 0 || K <= 0) return fgf8::set_error(FGF8_ERR_INVALID_ARG, "%s: M=%d N=%d K=%d", who, M, N, K);
+  if (int r = check_sizes(who, M, N, K)) return r;
   if (fmt != FGF8_FP4_MX && fmt != FGF8_FP4_NV) return fgf8::set_error(FGF8_ERR_INVALID_ARG, "%s: bad format %d", who, fmt);
   if (dtype != FGF8_F16 && dtype != FGF8_BF16) return fgf8::set_error(FGF8_ERR_INVALID_ARG, "%s: bad dtype %d", who, dtype);
   if (K % 64 != 0) return fgf8::set_error(FGF8_ERR_UNSUPPORTED, "%s: K=%d not a multiple of 64", who, K);

@@ -6,6 +6,9 @@
 namespace fgf8 {
 
 constexpr int kGemvMaxRows = 16;   // rows of X the matrix-vector kernels take
+// Largest M, N and K of these operators: the kernels round sizes up to tiles, at most 512
+// rows or columns past the end, in 32-bit integers.
+constexpr int kMaxSize = 0x7FFFFFFF - 1023;
 
 // One gated_f16 / gated_f16_backward call: M tokens, N inner columns, K hidden size.
 struct GatedArgs {

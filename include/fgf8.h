@@ -227,7 +227,7 @@ FGF8_API int gemm_fp4_blockscaled(const void* Aq, const void* SFA, const void* B
  *   G, U : [M][N] (outputs, both or neither may be NULL): the projections rounded
  *          to the same type, which gated_f16_backward reads
  * All of one type, fp16 or bf16 (dtype, an fgf8_dtype); act is an fgf8_act.
- * Requires K % 8 == 0, N % 8 == 0, M >= 0, N, K >= 1, and outputs that overlap no
+ * Requires K % 8 == 0, N % 8 == 0, M >= 0, N, K >= 1, none above 2^31 - 1024, and outputs that overlap no
  * input.  Always on the static schedule (fgf8_set_scheduler does not apply).
  */
 FGF8_API int gated_f16(const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U, int M, int N,
@@ -258,7 +258,8 @@ FGF8_API long long fgf8_gated_backward_ws_bytes(int M, int N);
  *   X  : fp16 or bf16 [M][K] (dtype);  Wq : uint8 [N][K/2];  SF : scale table of N rows
  *   Y  : [M][N], the type of X, rounded to nearest even from FP32 sums
  * X is not quantized: every product is exact, also of x far below the largest |x| of
- * its row, and the sums are FP32.  Y overlaps no input.  Requires K % 64 == 0, N, K >= 1, 0 <= M <= 16 (more rows
+ * its row, and the sums are FP32.  Y overlaps no input.  Requires K % 64 == 0,
+ * N, K >= 1, neither above 2^31 - 1024, 0 <= M <= 16 (more rows
  * return FGF8_ERR_UNSUPPORTED: quantize_fp4 X and call gemm_fp4_blockscaled).
  */
 FGF8_API int gemv_fp4(const void* X, const void* Wq, const void* SF, void* Y, int M, int N, int K, int fmt,
