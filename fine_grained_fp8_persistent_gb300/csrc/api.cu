@@ -5,16 +5,17 @@
 #include <cstdlib>
 #include <cstring>
 #include <initializer_list>
+#include <atomic>
 #include <mutex>
 
 #include <cudaTypedefs.h>
 
 #include "../../include/fgf8.h"
 #include "fgf8_internal.h"
+#include "per_device.h"
 
 namespace {
 
-constexpr int kMaxDevices = 64;
 constexpr int kBlockM = 128;     // rows per tile; the contiguous-layout alignment
 constexpr int kMaxGroups = 1024; // masked scheduler keeps a per-expert prefix in SMEM
 
@@ -22,21 +23,19 @@ constexpr int kMaxGroups = 1024; // masked scheduler keeps a per-expert prefix i
 __device__ uint32_t g_status;
 
 thread_local char g_errbuf[512];
-int g_pdl = -1;   // -1 = not read from the environment yet
-int g_sched = -1;  // tile scheduler; -1 = not read from the environment yet
-int g_smcap = -1;  // wave-preserving SM cap of persistent grids; -1 = not read yet
+std::atomic<int> g_pdl{-1};    // -1 = not read from the environment yet
+std::atomic<int> g_sched{-1};  // tile scheduler; -1 = not read from the environment yet
+std::atomic<int> g_smcap{-1};  // wave-preserving SM cap of persistent grids; -1 = not read yet
 thread_local char g_last_tile[64];
 
 struct DevInfo {
-  bool ready = false;
   int sms = 0;
   int smem_optin = 0;
   uint32_t* status = nullptr;
 };
-DevInfo g_dev[kMaxDevices];
-std::mutex g_dev_mutex;
+fgf8::PerDevice<DevInfo> g_dev;
 
-uint64_t g_timeout_ns = 0;   // 0 = not read from the environment yet
+std::atomic<uint64_t> g_timeout_ns{0};   // 0 = not read from the environment yet
 std::once_flag g_timeout_once;
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
@@ -45,29 +44,34 @@ std::once_flag g_encode_once;
 int current_device(int* dev) {
   const cudaError_t e = cudaGetDevice(dev);
   if (e != cudaSuccess) return fgf8::set_error(FGF8_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
-  if (*dev < 0 || *dev >= kMaxDevices) return fgf8::set_error(FGF8_ERR_UNSUPPORTED, "device id %d", *dev);
+  if (*dev < 0 || *dev >= fgf8::kMaxDevices) return fgf8::set_error(FGF8_ERR_UNSUPPORTED, "device id %d", *dev);
   return FGF8_OK;
 }
 
 const DevInfo* dev_info() {
   int dev = 0;
   if (current_device(&dev) != FGF8_OK) return nullptr;
-  DevInfo& d = g_dev[dev];
-  if (d.ready) return &d;
-  std::lock_guard<std::mutex> lock(g_dev_mutex);
-  if (d.ready) return &d;
-  cudaError_t e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess)
-    e = cudaDeviceGetAttribute(&d.smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-  void* p = nullptr;
-  if (e == cudaSuccess) e = cudaGetSymbolAddress(&p, g_status);
-  if (e != cudaSuccess) {
-    fgf8::set_error(FGF8_ERR_CUDA, "device query: %s", cudaGetErrorString(e));
-    return nullptr;
+  const DevInfo* info = nullptr;
+  g_dev.get(dev, &info, [dev](DevInfo& d) -> int {
+    cudaError_t e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&d.smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    void* p = nullptr;
+    if (e == cudaSuccess) e = cudaGetSymbolAddress(&p, g_status);
+    if (e != cudaSuccess) return fgf8::set_error(FGF8_ERR_CUDA, "device query: %s", cudaGetErrorString(e));
+    d.status = static_cast<uint32_t*>(p);
+    return 0;
+  });
+  return info;
+}
+
+// A switch, read from the environment at its first use unless it was set before.
+int setting(std::atomic<int>& s, int (*from_env)()) {
+  int v = s.load(std::memory_order_relaxed);
+  if (v < 0) {
+    const int env = from_env();
+    if (s.compare_exchange_strong(v, env)) v = env;
   }
-  d.status = static_cast<uint32_t*>(p);
-  d.ready = true;
-  return &d;
+  return v;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -107,27 +111,24 @@ void set_last_tile(const char* kind, const char* sched, int ctas, int bn, const 
 }
 
 bool pdl_enabled() {
-  if (g_pdl < 0) {
+  return setting(g_pdl, [] {
     const char* e = std::getenv("FGF8_PDL");
-    g_pdl = (e != nullptr && e[0] == '0') ? 0 : 1;
-  }
-  return g_pdl != 0;
+    return (e != nullptr && e[0] == '0') ? 0 : 1;
+  }) != 0;
 }
 
 int scheduler_mode() {
-  if (g_sched < 0) {
+  return setting(g_sched, [] {
     const char* e = std::getenv("FGF8_SCHED");
-    g_sched = (e != nullptr && std::strcmp(e, "clc") == 0) ? 1 : 0;
-  }
-  return g_sched;
+    return (e != nullptr && std::strcmp(e, "clc") == 0) ? 1 : 0;
+  });
 }
 
 bool sm_cap_enabled() {
-  if (g_smcap < 0) {
+  return setting(g_smcap, [] {
     const char* e = std::getenv("FGF8_SM_CAP");
-    g_smcap = (e != nullptr && e[0] == '0') ? 0 : 1;
-  }
-  return g_smcap != 0;
+    return (e != nullptr && e[0] == '0') ? 0 : 1;
+  }) != 0;
 }
 
 // "DeepGEMM dissected", section on the SM count (num_min_sms): the fewest SMs that
@@ -175,7 +176,8 @@ uint64_t wait_timeout_ns() {
       const long v = std::strtol(s, nullptr, 10);
       if (v > 0) ms = v;
     }
-    if (g_timeout_ns == 0) g_timeout_ns = static_cast<uint64_t>(ms) * 1000000ull;
+    uint64_t unset = 0;                              // a value set before the first use stays
+    g_timeout_ns.compare_exchange_strong(unset, static_cast<uint64_t>(ms) * 1000000ull);
   });
   return g_timeout_ns;
 }

@@ -14,6 +14,7 @@
 #include "gated.h"
 #include "gated_gemm.cuh"
 #include "gated_thin.cuh"
+#include "per_device.h"
 
 namespace fgf8 {
 namespace {
@@ -79,25 +80,26 @@ int launch_gemm(const GatedMaps& tm, GatedGemmArgs args, cudaStream_t stream) {
   using C = GatedCfg<OP, NCTA, BN, STAGES>;
   static_assert(C::SMEM_BYTES <= 232448, "shared memory budget");
   auto* fn = &gated_gemm<OP, ACT, NCTA, BN, STAGES>;
-  static int max_clusters[64] = {};
+  static PerDevice<int> max_clusters;
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64) return set_error(2, "device id %d", dev);
-  if (max_clusters[dev] == 0) {
+  if (dev < 0 || dev >= kMaxDevices) return set_error(2, "device id %d", dev);
+  const int* fit = nullptr;
+  const int r = max_clusters.get(dev, &fit, [&](int& clusters) {
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
-    int clusters = device_sm_count();
+    clusters = device_sm_count();
     if (e == cudaSuccess && NCTA > 1) {
       Launch probe(static_cast<unsigned>(device_sm_count() / NCTA * NCTA), C::THREADS, C::SMEM_BYTES, NCTA, stream, false);
       e = cudaOccupancyMaxActiveClusters(&clusters, fn, &probe.cfg);
     }
-    if (e != cudaSuccess || clusters <= 0) return set_error(4, "gated_f16 occupancy: %s", cudaGetErrorString(e));
-    max_clusters[dev] = clusters;
-  }
+    return e == cudaSuccess && clusters > 0 ? 0 : set_error(4, "gated_f16 occupancy: %s", cudaGetErrorString(e));
+  });
+  if (r) return r;
   auto up = [](long long v, long long by) { return (v + by - 1) / by; };
   const long long n1 = up(C::kFwd ? args.N : args.K, C::OUT_N);
   const long long tiles1 = up(args.M, C::TILE_M) * n1, tiles2 = C::kFwd ? 0 : 2 * up(args.N, C::TILE_M) * n1;
   if (tiles1 + tiles2 > 0x7F000000LL) return set_error(2, "gated_f16: problem too large");
-  const long long clusters = persistent_clusters(tiles1 + tiles2, NCTA, device_sm_count(), max_clusters[dev], C::kFwd && sm_cap_enabled());
+  const long long clusters = persistent_clusters(tiles1 + tiles2, NCTA, device_sm_count(), *fit, C::kFwd && sm_cap_enabled());
   args.long_clusters = 0;
   args.early_tiles = 0;
   if (!C::kFwd && tiles1 % clusters != 0) {
@@ -158,11 +160,15 @@ struct ThinPlan {
 };
 template <int ACT>
 int plan_thin(ThinPlan& p, const GatedArgs& a) {
-  static int fit[64][9] = {};                              // by device and S: clusters that fit
+  struct Fit {
+    int clusters[9];                                       // by S: clusters that fit
+  };
+  static PerDevice<Fit> fits;
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64) return set_error(2, "device id %d", dev);
-  if (fit[dev][1] == 0) {
+  if (dev < 0 || dev >= kMaxDevices) return set_error(2, "device id %d", dev);
+  const Fit* fit = nullptr;
+  const int r = fits.get(dev, &fit, [](Fit& f) {
     auto* fn = &gated_thin<ACT>;
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, thin::kSmemCap);
     for (int s = 8; e == cudaSuccess && s >= 1; --s) {
@@ -170,19 +176,17 @@ int plan_thin(ThinPlan& p, const GatedArgs& a) {
       int n = 0;
       e = cudaOccupancyMaxActiveClusters(&n, fn, &l.cfg);
       if (e == cudaSuccess && n <= 0) e = cudaErrorInvalidConfiguration;
-      if (e == cudaSuccess) fit[dev][s] = n;
+      f.clusters[s] = n;
     }
-    if (e != cudaSuccess) {
-      fit[dev][1] = 0;
-      return set_error(4, "gated_f16 occupancy: %s", cudaGetErrorString(e));
-    }
-  }
+    return e == cudaSuccess ? 0 : set_error(4, "gated_f16 occupancy: %s", cudaGetErrorString(e));
+  });
+  if (r) return r;
   const int tiles = (a.N + thin::kRows - 1) / thin::kRows, nkb = (a.K + 63) / 64, nb = (a.M + 15) / 16 * 16;
   p.cost = -1.0;
   for (int s = 1; s <= 8; ++s) {
     const int per = (nkb + s - 1) / s;
     if ((s - 1) * per >= nkb) continue;                    // a CTA without work
-    const int waves = (tiles + fit[dev][s] - 1) / fit[dev][s];
+    const int waves = (tiles + fit->clusters[s] - 1) / fit->clusters[s];
     const double t = waves * (static_cast<double>(per) * (128 + nb) + (s > 1 ? 1500.0 : 500.0));
     if (p.cost < 0 || t < p.cost) {
       p.S = s;

@@ -6,6 +6,7 @@
 #include <cstring>
 
 #include "gemm_persistent.cuh"
+#include "per_device.h"
 
 namespace fgf8 {
 
@@ -85,10 +86,10 @@ int launch_persistent(const GemmArgs& a, const TensorMaps& tm, long long tiles, 
   auto* fn = &gemm_persistent<KIND, SCHED, NCTA, BN, STAGES, NACC, AROWS, QOUT>;
   if ((a.dq != nullptr) != QOUT) return set_error(2, "output quantization and kernel disagree");
   constexpr int CL = C::CLUSTER;
-  static int max_clusters[64] = {};
+  static PerDevice<int> max_clusters;
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64) return set_error(2, "device id %d", dev);
+  if (dev < 0 || dev >= kMaxDevices) return set_error(2, "device id %d", dev);
   if (C::SMEM_BYTES > device_max_smem_optin())
     return set_error(2, "tile needs %d bytes of shared memory", C::SMEM_BYTES);
   cudaLaunchConfig_t cfg;
@@ -105,10 +106,10 @@ int launch_persistent(const GemmArgs& a, const TensorMaps& tm, long long tiles, 
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (max_clusters[dev] == 0) {
+  const int* fit = nullptr;
+  const int r = max_clusters.get(dev, &fit, [&](int& clusters) {
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
     if (e != cudaSuccess) return set_error(4, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-    int clusters = 0;
     cfg.gridDim = dim3(CL * (device_sm_count() / CL), 1, 1);
     // the CTAs of a cluster are co-scheduled inside one GPC, so the number of pairs
     // that fit can be below SMs / 2 ("Dissecting NVIDIA Blackwell" (EEPW), section
@@ -117,8 +118,9 @@ int launch_persistent(const GemmArgs& a, const TensorMaps& tm, long long tiles, 
     if (CL == 1) clusters = device_sm_count();
     if (e != cudaSuccess || clusters <= 0)
       return set_error(4, "cudaOccupancyMaxActiveClusters: %s", cudaGetErrorString(e));
-    max_clusters[dev] = clusters;
-  }
+    return 0;
+  });
+  if (r) return r;
   // static schedule: a persistent grid, capped for dense GEMMs by the wave-preserving
   // SM count (grouped layouts only know an upper bound of their tiles here); cluster
   // launch control: one cluster per tile, the kernel cancels the clusters that have
@@ -132,7 +134,7 @@ int launch_persistent(const GemmArgs& a, const TensorMaps& tm, long long tiles, 
     clc_tiles = static_cast<long long>((a.M + 127) / 128) * ((a.N + BN - 1) / BN);
   }
   long long clusters = la.clc ? (clc_tiles > 0 ? clc_tiles : 1)
-                              : persistent_clusters(tiles, CL, device_sm_count(), max_clusters[dev],
+                              : persistent_clusters(tiles, CL, device_sm_count(), *fit,
                                                     SCHED == Sched::Dense && sm_cap_enabled());
   if (clusters * CL > 0x7FFFFFFFLL) return set_error(2, "gemm launch: %lld tiles exceed the grid limit", tiles);
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * CL), 1, 1);

@@ -39,6 +39,7 @@
 #include "activation.cuh"
 #include "gated.h"
 #include "gemm_persistent.cuh"
+#include "per_device.h"
 
 namespace fgf8 {
 
@@ -727,30 +728,30 @@ struct GemvLaunch {
   }
 
   // Clusters of 2^log_s CTAs that fit the device at one CTA per SM; null on an error.
+  struct Fit {
+    int clusters[4];
+  };
   static const int* max_clusters() {
-    static int fit[64][4] = {};
+    static PerDevice<Fit> fits;
     int dev = 0;
     cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64) {
+    if (dev < 0 || dev >= kMaxDevices) {
       set_error(2, "device id %d", dev);
       return nullptr;
     }
-    if (fit[dev][0] == 0) {
+    const Fit* fit = nullptr;
+    fits.get(dev, &fit, [](Fit& f) {
       cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
       for (int i = 3; e == cudaSuccess && i >= 0; --i) {
         GemvLaunch l(i, device_sm_count() >> i, 32 * C::WARPS, kSmem, nullptr, false);
         int n = device_sm_count();
         if (i > 0) e = cudaOccupancyMaxActiveClusters(&n, kernel, &l.cfg);
         if (e == cudaSuccess && n <= 0) e = cudaErrorInvalidConfiguration;
-        if (e == cudaSuccess) fit[dev][i] = n;
+        f.clusters[i] = n;
       }
-      if (e != cudaSuccess) {
-        fit[dev][0] = 0;
-        set_error(4, "matrix-vector set-up: %s", cudaGetErrorString(e));
-        return nullptr;
-      }
-    }
-    return fit[dev];
+      return e == cudaSuccess ? 0 : set_error(4, "matrix-vector set-up: %s", cudaGetErrorString(e));
+    });
+    return fit != nullptr ? fit->clusters : nullptr;
   }
 
   // The layout with the least time by a simple model (ns): the chunks of the busiest SM, X
