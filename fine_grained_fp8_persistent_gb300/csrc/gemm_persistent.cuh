@@ -770,7 +770,7 @@ __global__ void __launch_bounds__(PCfg<KIND, SCHED, NCTA, BN, STAGES, NACC, AROW
       int run = 0;
       for (int g0 = 0; g0 < G; g0 += 32) {
         const int g = g0 + static_cast<int>(lane);
-        int mm = (g < G) ? args.masked_m[g] : 0;
+        int mm = (g < G) ? ptx::ld_global(args.masked_m + g) : 0;
         if (mm < 0 || mm > M) {
           if (leader) atomicOr(args.status, FGF8_DEVERR_INPUT);
           mm = mm < 0 ? 0 : M;
@@ -798,7 +798,7 @@ __global__ void __launch_bounds__(PCfg<KIND, SCHED, NCTA, BN, STAGES, NACC, AROW
       bool ok = nblk <= C::MAX_RUNS;
       for (int b0 = 0; ok && b0 < nblk; b0 += 32) {
         const int b = b0 + static_cast<int>(lane);
-        const int e = b < nblk ? __ldg(args.m_indices + static_cast<size_t>(b) * C::BM) : 0;
+        const int e = b < nblk ? ptx::ld_global(args.m_indices + static_cast<size_t>(b) * C::BM) : 0;
         int up = __shfl_up_sync(0xffffffffu, e, 1);
         if (lane == 0) up = prev;
         const bool start = b < nblk && (b == 0 || e != up);
@@ -889,7 +889,7 @@ __global__ void __launch_bounds__(PCfg<KIND, SCHED, NCTA, BN, STAGES, NACC, AROW
         if (prefix[mid] <= t) lo = mid; else hi = mid - 1;
       }
       g = lo;
-      int mm = __ldg(args.masked_m + g);
+      int mm = ptx::ld_global(args.masked_m + g);
       rows = mm < 0 ? 0 : (mm > M ? M : mm);
       const int mt = (rows + C::TILE_M - 1) / C::TILE_M;
       const int local = t - prefix[g];
@@ -899,7 +899,7 @@ __global__ void __launch_bounds__(PCfg<KIND, SCHED, NCTA, BN, STAGES, NACC, AROW
       dense_tile(t, num_m, num_n, 16, m, n);
       rows = M;
       if constexpr (SCHED == Sched::Contiguous) {
-        g = __ldg(args.m_indices + m * C::TILE_M);
+        g = ptx::ld_global(args.m_indices + m * C::TILE_M);
         if (g < 0 || g >= G) return false;
       }
     }
@@ -1317,7 +1317,7 @@ __global__ void __launch_bounds__(PCfg<KIND, SCHED, NCTA, BN, STAGES, NACC, AROW
       bool row_ok = lane < static_cast<uint32_t>(C::QROWS) && r < tl.row_limit;
       if constexpr (SCHED == Sched::Contiguous) {
         if (row_ok) {
-          const int g = __ldg(args.m_indices + tl.a_row0 + r);
+          const int g = ptx::ld_global(args.m_indices + tl.a_row0 + r);
           if (g != tl.group) {
             if (g >= 0) atomicOr(args.status, FGF8_DEVERR_INPUT);
             row_ok = false;
@@ -1469,7 +1469,7 @@ __global__ void __launch_bounds__(PCfg<KIND, SCHED, NCTA, BN, STAGES, NACC, AROW
       bool row_ok = lane < static_cast<uint32_t>(C::QROWS) && r < tl.row_limit;
       if constexpr (SCHED == Sched::Contiguous) {
         if (row_ok) {
-          const int g = __ldg(args.m_indices + tl.a_row0 + r);
+          const int g = ptx::ld_global(args.m_indices + tl.a_row0 + r);
           if (g != tl.group) {
             if (g >= 0) atomicOr(args.status, FGF8_DEVERR_INPUT);
             row_ok = false;
@@ -1556,8 +1556,8 @@ __global__ void __launch_bounds__(PCfg<KIND, SCHED, NCTA, BN, STAGES, NACC, AROW
 #pragma unroll
         for (int j = 0; j < C::KPU; ++j) {
           const int kb = min(s_kb0 + j, nkb - 1);  // a short tail unit repeats its last K block
-          na[j] = __ldg(s_pa + static_cast<size_t>(kb) * ld_a);
-          nb[j] = __ldg(s_pb + kb);
+          na[j] = ptx::ld_global(s_pa + static_cast<size_t>(kb) * ld_a);
+          nb[j] = ptx::ld_global(s_pb + kb);
         }
         s_kb0 += C::KPU;
         if (s_kb0 >= nkb) {
@@ -1617,7 +1617,7 @@ __global__ void __launch_bounds__(PCfg<KIND, SCHED, NCTA, BN, STAGES, NACC, AROW
       const bool idle = row_off_h + static_cast<int>(q) * C::QROWS >= tl.row_limit;
       if constexpr (SCHED == Sched::Contiguous) {
         if (row_ok) {
-          const int g = __ldg(args.m_indices + tl.a_row0 + r);
+          const int g = ptx::ld_global(args.m_indices + tl.a_row0 + r);
           if (g != tl.group) {
             if (g >= 0) atomicOr(args.status, FGF8_DEVERR_INPUT);
             row_ok = false;

@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, NT, DEEP>::WARPS, GemvCfg<WT,
         constexpr int XL = NT == 2 ? 8 : 4;
         auto load_x = [&](int m, int v) -> uint4 {        // zeros past K
           if (k0 + 8 * v >= K) return make_uint4(0u, 0u, 0u, 0u);
-          return __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(args.X) + static_cast<size_t>(m) * K + k0 + 8 * v));
+          return ptx::ld_global_v4(static_cast<const uint16_t*>(args.X) + static_cast<size_t>(m) * K + k0 + 8 * v);
         };
         for (int it0 = warp; it0 < M * blocks; it0 += XL * W) {
           uint4 w[XL];

@@ -84,8 +84,8 @@ __device__ __forceinline__ void load_1x128(const __nv_bfloat16* __restrict__ X, 
   if (t.active) {
     const uint4* src = reinterpret_cast<const uint4*>(X + static_cast<size_t>(t.m) * K +
                                                       static_cast<size_t>(t.qw) * 512 + 16 * lane);
-    w[0] = __ldg(src);
-    w[1] = __ldg(src + 1);
+    w[0] = ptx::ld_global_v4(src);
+    w[1] = ptx::ld_global_v4(src + 1);
   }
 }
 
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(256, 3) quantize_128x128_kernel(const __nv_bfl
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int n = nb * 128 + 16 * i + rsub;
-    w[i] = n < N ? __ldg(reinterpret_cast<const uint4*>(Wg + static_cast<size_t>(n) * K))
+    w[i] = n < N ? ptx::ld_global_v4(Wg + static_cast<size_t>(n) * K)
                  : make_uint4(0u, 0u, 0u, 0u);
   }
   float amax = 0.0f;

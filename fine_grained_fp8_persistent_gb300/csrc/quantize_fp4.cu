@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(256) quantize_fp4_kernel(const __nv_bfloat16* 
   float amax = 0.0f;
   if (active) {
     const uint4* src = reinterpret_cast<const uint4*>(X + static_cast<size_t>(r) * K + col0);
-    const uint4 w0 = __ldg(src), w1 = __ldg(src + 1);
+    const uint4 w0 = ptx::ld_global_v4(src), w1 = ptx::ld_global_v4(src + 1);
     const uint32_t u[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

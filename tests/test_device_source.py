@@ -70,3 +70,19 @@ def test_matrix_vector_chunks_begin_converged():
     """ldmatrix and mma.sync follow."""
     code = _code(os.path.join(CSRC, "gemv.cuh"))
     assert re.search(r"cp_wait<C::DEPTH - 2>\(\);\s*__syncwarp\(\);\s*issue\(\);", code)
+
+
+def test_kernels_that_start_early_read_coherently():
+    """Under a programmatic launch the kernel before may still write what this one is about to
+    read: the read-only path, whose data nobody may write while the kernel runs, is not for
+    it, nor for anything that the compiler may read above the wait."""
+    checked = 0
+    for path in SOURCES:
+        code = _code(path)
+        assert "ld.global.nc" not in code, os.path.basename(path)
+        if "griddep_wait();" in code:
+            assert "__ldg(" not in code, os.path.basename(path)
+            checked += 1
+    assert checked >= 5
+    ptx = _code(os.path.join(CSRC, "ptx.cuh"))
+    assert ptx.count('asm volatile("ld.global.') == 3
