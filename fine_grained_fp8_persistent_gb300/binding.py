@@ -565,7 +565,8 @@ def sfb_bytes(G: int, N: int, K: int, fmt) -> int:
 
 
 def last_tile() -> str:
-    """Kernel configuration of the last GEMM this thread launched ("mxf8 dense 2x224")."""
+    """Kernel configuration of the last GEMM or matrix-vector product this thread launched
+    ("mxf8 dense 2x224", "nvf4 gemv 1x16 deep r1 p2")."""
     return (_lib.fgf8_last_tile() or b"").decode()
 
 

@@ -26,7 +26,14 @@ thread_local char g_errbuf[512];
 std::atomic<int> g_pdl{-1};    // -1 = not read from the environment yet
 std::atomic<int> g_sched{-1};  // tile scheduler; -1 = not read from the environment yet
 std::atomic<int> g_smcap{-1};  // wave-preserving SM cap of persistent grids; -1 = not read yet
-thread_local char g_last_tile[64];
+// Configuration of the thread's last GEMM or matrix-vector launch; the names are literals.
+struct LastTile {
+  const char *kind = nullptr, *sched = nullptr, *suffix = "";
+  int ctas = 0, bn = 0;
+  int rounds = 0, pieces = 0;   // matrix-vector kernels: 1 and more
+};
+thread_local LastTile g_last;
+thread_local char g_last_tile[96];
 
 struct DevInfo {
   int sms = 0;
@@ -107,7 +114,11 @@ long long align4(long long x) { return (x + 3) / 4 * 4; }
 namespace fgf8 {
 
 void set_last_tile(const char* kind, const char* sched, int ctas, int bn, const char* suffix) {
-  std::snprintf(g_last_tile, sizeof(g_last_tile), "%s %s %dx%d%s", kind, sched, ctas, bn, suffix);
+  g_last = {kind, sched, suffix, ctas, bn, 0, 0};
+}
+
+void set_last_gemv(const char* kind, bool gated, int ctas, int tokens, bool deep, int rounds, int pieces) {
+  g_last = {kind, gated ? "gated_gemv" : "gemv", deep ? "deep" : "shallow", ctas, tokens, rounds, pieces};
 }
 
 bool pdl_enabled() {
@@ -223,7 +234,14 @@ extern "C" {
 
 const char* fgf8_last_error(void) { return g_errbuf; }
 
-const char* fgf8_last_tile(void) { return g_last_tile; }
+// Written out here: a launch only notes the numbers.
+const char* fgf8_last_tile(void) {
+  const LastTile& t = g_last;
+  if (t.kind == nullptr) return "";
+  if (t.rounds == 0) std::snprintf(g_last_tile, sizeof(g_last_tile), "%s %s %dx%d%s", t.kind, t.sched, t.ctas, t.bn, t.suffix);
+  else std::snprintf(g_last_tile, sizeof(g_last_tile), "%s %s %dx%d %s r%d p%d", t.kind, t.sched, t.ctas, t.bn, t.suffix, t.rounds, t.pieces);
+  return g_last_tile;
+}
 
 int fgf8_version(void) { return 100; }
 

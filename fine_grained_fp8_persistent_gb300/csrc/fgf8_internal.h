@@ -72,7 +72,11 @@ long long persistent_clusters(long long tiles, int cluster, int sms, int max_clu
 // Launches the bounded-wait self-test (selftest.cu).
 int launch_wait_selftest(uint32_t* status, uint64_t timeout_ns, cudaStream_t stream);
 // Records the configuration of the GEMM launch this thread makes (fgf8_last_tile).
+// The names are string literals: their text is put together when it is asked for.
 void set_last_tile(const char* kind, const char* sched, int ctas, int bn, const char* suffix = "");
+// The same for a matrix-vector launch: CTAs of the cluster, tokens of the form (8 or 16),
+// ring, rounds of tiles and pieces of X.
+void set_last_gemv(const char* kind, bool gated, int ctas, int tokens, bool deep, int rounds, int pieces);
 int device_sm_count();
 int device_max_smem_optin();
 uint32_t* device_status_ptr();

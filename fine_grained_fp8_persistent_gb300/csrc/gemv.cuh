@@ -694,6 +694,7 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, NT, DEEP>::WARPS, GemvCfg<WT,
 struct GemvPlan {
   double ns;
   int log_s, clusters, threads, smem;
+  int rounds, pieces;   // of the CTA with most tiles
   GemvKArgs a;
 };
 
@@ -799,6 +800,8 @@ struct GemvLaunch {
       if (best.ns >= 0 && ns >= best.ns) continue;
       best.ns = ns;
       best.log_s = i;
+      best.rounds = rounds;
+      best.pieces = pieces;
       best.threads = 32 * warps;
       best.clusters = all_tiles < fit[i] ? all_tiles : fit[i];
       GemvKArgs& a = best.a;
@@ -821,6 +824,7 @@ struct GemvLaunch {
   }
 
   static int launch(const GemvPlan& p, cudaStream_t stream) {
+    set_last_gemv(WT == WType::W16 ? "f16" : WT == WType::MX ? "mxf4" : "nvf4", MATS == 2, 1 << p.log_s, 8 * NT, DEEP, p.rounds, p.pieces);
     GemvLaunch l(p.log_s, p.clusters, p.threads, p.smem, stream, pdl_enabled());
     const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kernel, p.a);
     return e == cudaSuccess ? 0 : set_error(4, "matrix-vector launch: %s", cudaGetErrorString(e));

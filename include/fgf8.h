@@ -300,9 +300,11 @@ FGF8_API int fgf8_check_status(void* stream, unsigned int* raw_bits);
 /* Message for the last non-OK return on this thread ("" if none). */
 FGF8_API const char* fgf8_last_error(void);
 
-/* Kernel configuration of the last GEMM this thread launched, as text
- * ("<kind> <schedule> <CTAs per cluster>x<tile width>", e.g. "mxf8 dense 2x224";
- * "f16 gated_thin <CTAs of the cluster>x<tokens>" for the gated block of 17 to 256 rows);
+/* Kernel configuration of the last GEMM or matrix-vector product this thread launched, as
+ * text ("<kind> <schedule> <CTAs per cluster>x<tile width>", e.g. "mxf8 dense 2x224";
+ * "f16 gated_thin <CTAs of the cluster>x<tokens>" for the gated block of 17 to 256 rows;
+ * "<kind> gemv|gated_gemv <CTAs of the cluster>x<8 or 16 tokens> deep|shallow r<rounds of
+ * tiles> p<pieces of X>" for at most 16 rows, e.g. "nvf4 gemv 1x16 deep r1 p2");
  * "" before the first launch.  The pointer stays valid until this thread's next
  * GEMM call. */
 FGF8_API const char* fgf8_last_tile(void);
