@@ -142,15 +142,16 @@ struct Choice {
   int ncta, bn;
   double t_kb;
 };
-// FGF8_FORCE_TILE="<ctas per cluster>x<bn>" selects that tile when it is among the candidates.
-int forced(const Choice* c, int n, int otherwise) {
+// The candidate that FGF8_FORCE_TILE="<ctas per cluster>x<bn>" names; -1: none of these.
+int forced(const Choice* c, int n) {
   if (const char* f = std::getenv("FGF8_FORCE_TILE")) {
     int nc = 0, bn = 0;
-    if (std::sscanf(f, "%dx%d", &nc, &bn) == 2)
+    char more = 0;                                         // a suffix names a tile of another kernel
+    if (std::sscanf(f, "%dx%d%c", &nc, &bn, &more) == 2)
       for (int i = 0; i < n; ++i)
         if (c[i].ncta == nc && c[i].bn == bn) return i;
   }
-  return otherwise;
+  return -1;
 }
 // The thin forward pass (gated_thin.cuh): shares S of the reduction per tile of 64 weight
 // rows and its time in units of 128-byte rows through one CTA's copy engine.
@@ -244,13 +245,13 @@ int forward(const GatedArgs& a, const void* X, const void* Wg, const void* Wu, v
       best = i;
     }
   }
-  const int kb = (a.K + 63) / 64;
-  if (a.M <= 256 && std::getenv("FGF8_FORCE_TILE") == nullptr) {
+  const int kb = (a.K + 63) / 64, force = forced(c, 3);
+  if (a.M <= 256 && force < 0) {
     ThinPlan p;
     if (int r = plan_thin<ACT>(p, a)) return r;
     if (p.cost < cost * kb + 500.0) return launch_thin<ACT>(p, a, X, Wg, Wu, H, G, U, stream);
   }
-  const Choice& ch = c[forced(c, 3, best)];
+  const Choice& ch = c[force >= 0 ? force : best];
   GatedGemmArgs g;
   if (gemm_args(g, a)) return 4;
   g.save = G != nullptr;
@@ -288,7 +289,8 @@ int grads(const GatedArgs& a, const void* dG, const void* dU, const void* X, con
       best = i;
     }
   }
-  best = forced(c, 3, best);
+  const int force = forced(c, 3);
+  if (force >= 0) best = force;
   GatedGemmArgs g;
   if (gemm_args(g, a)) return 4;
   GatedMaps tm;
