@@ -18,11 +18,18 @@ _EXPORTS = (
 )
 
 
+_NAMES = frozenset(_EXPORTS)
+_binding = None
+
+
 def __getattr__(name):
-    if name in _EXPORTS:
-        from . import binding
-        value = globals()[name] = getattr(binding, name)   # found at once from the next use on
-        return value
+    # looked up in binding at every use, so that what is replaced there is replaced here
+    # (0.4 us; an import statement each time makes it 1 us)
+    global _binding
+    if name in _NAMES:
+        if _binding is None:
+            from . import binding as _binding
+        return getattr(_binding, name)
     raise AttributeError(name)
 
 
