@@ -475,7 +475,8 @@ def gated_f16_backward(dh: torch.Tensor, x: torch.Tensor, wg: torch.Tensor, wu: 
                        u: torch.Tensor, act="silu", dx: torch.Tensor | None = None,
                        dwg: torch.Tensor | None = None, dwu: torch.Tensor | None = None,
                        workspace: torch.Tensor | None = None, stream=None):
-    """Gradients (dX, dWg, dWu) of gated_f16 from dH (M, N) and the G, U it kept.
+    """Gradients (dX, dWg, dWu) of gated_f16 from dH (M, N) and the G, U it kept.  dG and dU
+    are rounded to the operands' type on the way, in fp16 to its range too.
     `workspace` (uint8, gated_backward_ws_bytes(M, N) bytes) is taken from torch when not given."""
     M, K = x.shape
     N = wg.shape[0]

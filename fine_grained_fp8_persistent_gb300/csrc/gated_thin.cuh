@@ -6,11 +6,15 @@
 // through the MMA once, whatever the number of tokens.  (With tokens as M, as for many
 // tokens, the tiles that fill 152 SMs are 16 columns of each weight wide, and every one of
 // them loads all of X: at 64 tokens 96 rows of 128 bytes per K block of 64, of which 32
-// are weights; here 128 of 192 are.  The copy engine takes about 1.4 ns per row and CTA.)
+// are weights; here 128 of 192 are.)
 // A cluster of S CTAs splits the reduction of a tile; each writes its FP32 sums to shared
 // memory and the cluster adds them through distributed shared memory, in order, with the
 // activation, the product and the store.  Weights from memory, N = 2048, K = 7168 (59 MB,
-// 8.7 us at the copy rate): 15.8 us at 64 tokens, 17.2 at 128, bound by the copy engine.
+// 8.7 us at the copy rate): 16.4 us at 64 tokens.  With the weights in L2 the same launch
+// takes 11.5, and its 28 K blocks of 192 rows are 7.5 us of copying at the 1.4 ns per
+// 128-byte row and CTA that wide tiles take, so neither the copy engine nor memory alone
+// bounds it.  128 of 152 SMs work, in one wave, and launch, pipeline fill and the join are
+// not hidden; how the rest divides among them is not established.
 //
 // Roles: warp 0 TMA producer, warp 1 MMA issuer, all warps the epilogue (warps 0-3 drain
 // one TMEM lane quarter each).

@@ -67,8 +67,9 @@ struct GemvKArgs {
   int prefetch;      // chunks per warp to ask into L2 ahead of the previous kernel's end
 };
 
-// DEEP: one CTA per SM with as many bytes in flight as fit; else half an SM's registers
-// and shared memory.
+// DEEP: 16 warps with as many bytes in flight as fit; else 12 warps with rings of three and
+// half an SM's registers, so that the next kernel's CTAs can start beside it where the
+// shared memory that the plan takes for X (up to all of it) leaves them room.
 template <WType WT, int NT, bool DEEP>
 struct GemvCfg {
   static constexpr int WARPS = DEEP ? 16 : 12;               // at most

@@ -238,7 +238,10 @@ FGF8_API int gated_f16(const void* X, const void* Wg, const void* Wu, void* H, v
  *   dG = dH * U * a'(G),  dU = dH * a(G)
  *   dX = dG Wg + dU Wu,   dWg = dG^T X,   dWu = dU^T X
  * dG and dU are computed in FP32 and rounded to the operands' type, the type the
- * tensor cores read; the three products accumulate in FP32 and round once.
+ * tensor cores read; the three products accumulate in FP32 and round once.  In fp16
+ * that also bounds their range: |dG| or |dU| of 65520 and more becomes infinite, and
+ * below 2^-14 they lose digits (scale the loss, as for any fp16 gradient); bf16 has the
+ * range of FP32.
  *   dH, G, U : [M][N];  X, dX : [M][K];  Wg, Wu, dWg, dWu : [N][K]
  *   workspace : fgf8_gated_backward_ws_bytes(M, N) bytes of device memory, holding
  *               dG and dU for the length of the call
