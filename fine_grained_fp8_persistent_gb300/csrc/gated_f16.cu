@@ -20,7 +20,7 @@ namespace fgf8 {
 namespace {
 
 // dG, dU from dH, G, U.  Eight elements (16 bytes) per thread; n8 = M * N / 8.  A stream of
-// three reads and two writes, bound by memory latency: 13.0 us at 4096 x 2048 (84 MB).
+// three reads and two writes, bound by memory latency: 13.5 us at 4096 x 2048 (84 MB).
 template <int ACT, bool BF16>
 __global__ void __launch_bounds__(256) slope_kernel(const uint4* __restrict__ dh, const uint4* __restrict__ g,
                                                     const uint4* __restrict__ u, uint4* __restrict__ dg,
@@ -230,9 +230,10 @@ int launch_thin(const ThinPlan& p, const GatedArgs& a, const void* X, const void
 
 template <int ACT>
 int forward(const GatedArgs& a, const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U, cudaStream_t stream) {
-  // time of a tile per K block, in 128-byte rows through a CTA's copy engine (1.4 ns): the
+  // time of a tile per K block, in 128-byte rows that a CTA copies (1.0 to 1.4 ns): the
   // rows loaded bound the one-CTA tiles, the MMA the pair (512 tokens at 7168 x 2048, one
-  // wave each: 48 us on 2 x 256, 42 on 1 x 128, 54 for two waves of 1 x 64)
+  // wave each: 40 us on 2 x 256, 32 on 1 x 128, 48 for two waves of 1 x 64; 331 tokens at
+  // 1800 x 2744: 18.1, 15.9 and 21.7 us)
   static const Choice c[] = {{2, 256, 320.0}, {1, 128, 256.0}, {1, 64, 200.0}};
   int best = 0;
   double cost = -1.0;
@@ -269,11 +270,11 @@ int forward(const GatedArgs& a, const void* X, const void* Wg, const void* Wu, v
 
 int grads(const GatedArgs& a, const void* dG, const void* dU, const void* X, const void* Wg, const void* Wu, void* dX, void* dWg, void* dWu,
           cudaStream_t stream) {
-  // Time of the launch in 128-byte rows through a CTA's copy engine (1.4 ns): the longer of
+  // Time of the launch in 128-byte rows that a CTA copies (1.0 to 1.4 ns): the longer of
   // one dX tile's reduction and an SM's share of all tiles; a tile's stores and set-up
   // count as `t_kb` further rows.  Measured (us) on 2x256 / 1x128 / 1x64: 17 x 7168 x 2048
-  // 34.8 / 36.7 / 41.1, 67 x 2048 x 1368 21.9 / 19.9 / 17.9, 100 x 2048 x 8192 95 / 85 / 76,
-  // 512 x 7168 x 2048 51 / 74 / 107.
+  // 36.1 / 36.6 / 40.7, 67 x 2048 x 1368 24.3 / 21.3 / 19.2, 100 x 2048 x 8192 95 / 86 / 75,
+  // 512 x 7168 x 2048 52 / 72 / 109, 1000 x 4096 x 4096 92 / 144 / 231.
   static const Choice c[] = {{2, 256, 2300.0}, {1, 128, 1300.0}, {1, 64, 750.0}};
   double cost = -1.0;
   int best = 0;

@@ -29,7 +29,7 @@
 // Measured, bf16, in a burst / back to back under the power cap: 8192 x 7168 x 2048
 // forward 247 / 281 us (1946 / 1712 TFLOP/s, bound by the MMA and by power), 4096 x 4096 x
 // 4096 forward 139 / 161 us, backward 321 / 359 us with the slope kernel.  Sizes of one
-// wave or two take about 1.4 ns per 128-byte row that a CTA copies, whatever the tile.
+// wave or two take 1.0 to 1.4 ns per 128-byte row that a CTA copies, whatever the tile.
 #pragma once
 #include "activation.cuh"
 #include "gated.h"

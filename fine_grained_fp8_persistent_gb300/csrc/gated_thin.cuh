@@ -11,9 +11,9 @@
 // memory and the cluster adds them through distributed shared memory, in order, with the
 // activation, the product and the store.  Weights from memory, N = 2048, K = 7168 (59 MB,
 // 8.7 us at the copy rate): 16.4 us at 64 tokens.  With the weights in L2 the same launch
-// takes 11.5, and its 28 K blocks of 192 rows are 7.5 us of copying at the 1.4 ns per
-// 128-byte row and CTA that wide tiles take, so neither the copy engine nor memory alone
-// bounds it.  128 of 152 SMs work, in one wave, and launch, pipeline fill and the join are
+// takes 12.3, and its 28 K blocks of 192 rows are 5.4 to 7.5 us of copying at the 1.0 to
+// 1.4 ns per 128-byte row and CTA that wide tiles take, so neither the copying nor memory
+// alone bounds it.  128 of 152 SMs work, in one wave, and launch, pipeline fill and the join are
 // not hidden; how the rest divides among them is not established.
 //
 // Roles: warp 0 TMA producer, warp 1 MMA issuer, all warps the epilogue (warps 0-3 drain

@@ -343,7 +343,8 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, NT, DEEP>::WARPS, GemvCfg<WT,
         // one warp takes 256 columns of a row, 8 per lane (zeros past K)
         const int blocks = (xn * C::CK + 255) / 256;
         // loads in flight per lane: 4, or 8 where 16 rows make the staging long (NVFP4
-        // 16 x 32768 x 7168 47.2 -> 46.2 us, MXFP4 48.3 -> 45.3; one token gets 10 % slower)
+        // 16 x 32768 x 7168 47.2 -> 46.2 us, MXFP4 48.3 -> 45.3 when this was taken; one token
+        // gets 10 % slower)
         constexpr int XL = NT == 2 ? 8 : 4;
         auto load_x = [&](int m, int v) -> uint4 {        // zeros past K
           if (k0 + 8 * v >= K) return make_uint4(0u, 0u, 0u, 0u);
@@ -766,7 +767,8 @@ struct GemvLaunch {
   // piece, so few warps, many tokens and pieces are what a cluster is for: each of its CTAs
   // stages its own share of X.  Eight tokens of bf16 at 2048 x 7168 in NVFP4 take 10.8 us
   // on one CTA per tile and 6.1 us on four; one token in MXFP4 takes 8.39 us shallow and
-  // 8.54 us deep at 7168 x 7168, 34.4 and 25.2 us at 32768 x 7168.
+  // 8.54 us deep at 7168 x 7168, 34.4 and 25.2 us at 32768 x 7168.  (Times of that search; what
+  // bf16 X has needed since, for rows and scales far apart, costs 0 to 4 % of either form.)
   static bool plan(GemvPlan& best, const GemvKArgs& args) {
     const int* fit = max_clusters();
     if (fit == nullptr) return false;
