@@ -394,23 +394,27 @@ __global__ void __launch_bounds__(32 * GemvCfg<WT, NT, DEEP>::WARPS, GemvCfg<WT,
                 for (int j = 0; j < 4; ++j) asm volatile("st.shared.b32 [%0], %1;" ::"r"(d + 16 * j), "r"(u[j]) : "memory");
               }
             } else if constexpr (kScaleX) {
-              // largest and, in this lane, least |x| of the 256 columns as bf16 bits
+              // largest and, in this lane, least non-zero |x| of the 256 columns as bf16 bits;
+              // for the least, as 16-bit integers, |x| - 1 - 2^15, where zero is the largest
               uint32_t a2 = 0u, z2 = 0x7FFF7FFFu;
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 a2 = __vmaxu2(a2, u[j] & 0x7FFF7FFFu);
-                z2 = __vminu2(z2, u[j] & 0x7FFF7FFFu);
+                z2 = __vmins2(z2, (u[j] | 0x80008000u) - 0x00010001u);
               }
               const uint32_t a = __reduce_max_sync(0xffffffffu, max(a2 & 0xFFFFu, a2 >> 16));
-              again = again || a >= 0x7F80u || static_cast<int>(min(z2 & 0xFFFFu, z2 >> 16)) < static_cast<int>(a & 0x7F80u) - (31 << 7);
+              // an |x| of bits below `low` would lose digits in fp16
+              const int low = static_cast<int>(a & 0x7F80u) - (31 << 7);
+              const uint32_t limit = __byte_perm(static_cast<uint32_t>(max(low, 1) - 1) | 0x8000u, 0u, 0x1010);
+              again = again || a >= 0x7F80u || __vmins2(z2, limit) != limit;
               put_scaled(m, blk, v, u, a);
             } else {
               put(m, v, u);
             }
           }
           if constexpr (kScaleX) {
-            // infinities, NaN, zeros or |x| too small for the scale: these rows once more, with
-            // only finite values in the largest and only non-zero ones in the least
+            // infinities, NaN or |x| too small for the scale: these rows once more, with only
+            // finite values in the largest
             if (__any_sync(0xffffffffu, again)) {
 #pragma unroll 1
               for (int it = it0; it < M * blocks && it < it0 + XL * W; it += W) {
@@ -768,7 +772,7 @@ struct GemvLaunch {
   // stages its own share of X.  Eight tokens of bf16 at 2048 x 7168 in NVFP4 take 10.8 us
   // on one CTA per tile and 6.1 us on four; one token in MXFP4 takes 8.39 us shallow and
   // 8.54 us deep at 7168 x 7168, 34.4 and 25.2 us at 32768 x 7168.  (Times of that search; what
-  // bf16 X has needed since, for rows and scales far apart, costs 0 to 4 % of either form.)
+  // bf16 X has needed since, for rows and scales far apart, costs 0 to 5 % of either form.)
   static bool plan(GemvPlan& best, const GemvKArgs& args) {
     const int* fit = max_clusters();
     if (fit == nullptr) return false;

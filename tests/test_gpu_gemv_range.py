@@ -162,6 +162,30 @@ def test_a_neighbours_large_scale(fg, dev):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", [1, 7, 16])
+def test_zeros_in_x(fg, dev, M, fmt):
+    """Rows of X that are mostly zero, of either sign, beside large and small ones: zeros say
+    nothing about how far the rest lies apart."""
+    N, K = 50, 1088
+    gen = torch.Generator(device=dev).manual_seed(M + 20)
+    wq, sf, w = fp4.random_matrix(N, K, fmt, 8, dev)
+    x = torch.randn(M, K, generator=gen, device=dev)
+    x = torch.where(torch.rand(M, K, generator=gen, device=dev) < 0.6, torch.copysign(torch.zeros_like(x), x), x)
+    _check(fg.gemv_fp4(x.to(torch.bfloat16), wq, sf, fmt), x.to(torch.bfloat16), w, "zeros")
+    small = x * 2.0 ** -40
+    small[:, 5] = 1.5
+    small[0, 300:] = 0.0
+    codes = wq.clone()
+    codes[:, 2] &= 0x0F                                  # no weight on column 5
+    w[:, 5] = 0.0
+    x = small.to(torch.bfloat16)
+    _check(fg.gemv_fp4(x, codes, sf, fmt), x, w, "small ones")
+    zero = torch.zeros_like(x)
+    zero[:, ::3] = -0.0
+    assert (fg.gemv_fp4(zero, wq, sf, fmt) == 0).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("M", [2, 16])
 def test_non_finite_x_beside_small_x(fg, dev, M, fmt):
     """Infinities and NaN in chunks that also hold x far apart give what the definition gives,
