@@ -308,8 +308,8 @@ FGF8_API const char* fgf8_last_error(void);
  * "f16 gated_thin <CTAs of the cluster>x<tokens>" for the gated block of 17 to 256 rows;
  * "<kind> gemv|gated_gemv <CTAs of the cluster>x<8 or 16 tokens> deep|shallow r<rounds of
  * tiles> p<pieces of X>" for at most 16 rows, e.g. "nvf4 gemv 1x16 deep r1 p2");
- * "" before the first launch.  The pointer stays valid until this thread's next
- * GEMM call. */
+ * "" before the first launch.  The text stays as it is until this thread asks
+ * again. */
 FGF8_API const char* fgf8_last_tile(void);
 
 /*
