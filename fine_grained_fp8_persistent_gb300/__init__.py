@@ -15,6 +15,8 @@ _EXPORTS = (
     "quantize_fp4", "gemm_fp4_blockscaled", "fp4_sf_shape", "FP4_MX", "FP4_NV",
     "gated_f16", "gated_f16_backward", "gated_backward_ws_bytes", "gemv_fp4", "gated_gemv_fp4", "GEMV_MAX_ROWS",
     "ACT_SILU", "ACT_GELU_TANH",
+    "Route", "route_contiguous", "route_masked", "route_rows", "dispatch_f16", "dispatch_fp8", "dispatch_f16_backward",
+    "combine_f16", "combine_f16_backward", "lora_f16",
 )
 
 

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -61,6 +62,15 @@ _SIGS = {
     "gated_f16_backward": ([_P] * 10 + [_I] * 5 + [_P], _I),
     "gemv_fp4": ([_P] * 4 + [_I] * 5 + [_P], _I),
     "gated_gemv_fp4": ([_P] * 6 + [_I] * 6 + [_P], _I),
+    "route_contiguous": ([_P] * 6 + [_I] * 6 + [_P], _I),
+    "route_masked": ([_P] * 4 + [_I] * 5 + [_P], _I),
+    "dispatch_f16": ([_P] * 4 + [_I] * 4 + [_P], _I),
+    "dispatch_fp8": ([_P] * 4 + [_I] * 6 + [_P], _I),
+    "combine_f16": ([_P] * 4 + [_I] * 5 + [_P], _I),
+    "combine_f16_backward": ([_P] * 7 + [_I] * 5 + [_P], _I),
+    "dispatch_f16_backward": ([_P] * 3 + [_I] * 5 + [_P], _I),
+    "lora_f16": ([_P] * 9 + [_I] * 6 + [_LL] * 3 + [_I, _P], _I),
+    "fgf8_route_rows": ([_I] * 4, _LL),
     "fgf8_gated_backward_ws_bytes": ([_I, _I], _LL),
     "fgf8_fp4_sf_bytes": ([_I, _I, _I], _LL),
     "fgf8_mk_alignment_for_contiguous": ([], _I),
@@ -412,18 +422,19 @@ def _empty(shape: tuple, dtype: torch.dtype, like: torch.Tensor, stream) -> torc
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _launch(name: str, stream, tensors: tuple, ints: tuple) -> None:
+def _launch(name: str, stream, tensors: tuple, ints: tuple, strided: tuple = ()) -> None:
     """Run one library entry point on `stream` (None: the current stream of the tensors'
     device): pointers of `tensors`, then `ints`, then the stream.  A matrix-vector kernel
     takes a few microseconds, so this does what _stream, _ptr and _call do without their
-    objects; the raw stream handle and the device come from the calls those make."""
+    objects; the raw stream handle and the device come from the calls those make.
+    `strided`: places of tensors whose layout the caller has checked."""
     device = tensors[0].get_device()
     pointers = []
-    for t in tensors:
+    for i, t in enumerate(tensors):
         if t is None:
             pointers.append(None)
             continue
-        if t.get_device() != device or not t.is_contiguous():
+        if t.get_device() != device or not (t.is_contiguous() or i in strided):
             _ptr(t)                                       # says why, unless the device is another one
             raise ValueError(f"{name}: a tensor is on {t.device}, another one on {tensors[0].device}")
         pointers.append(t.data_ptr())
@@ -541,6 +552,222 @@ def gated_gemv_fp4(x: torch.Tensor, wgq: torch.Tensor, sfg: torch.Tensor, wuq: t
     else:
         _need_like(out, (M, N), x.dtype, "out")
     _launch("gated_gemv_fp4", stream, (x, wgq, sfg, wuq, sfu, out), (M, N, K, f, code, _act(act)))
+    return out
+
+
+# --------------------------------------------------------------------------- rows that choose their own weights
+class Route(NamedTuple):
+    """Rows of the entries (t, j) of a list of group ids, from route_contiguous or route_masked."""
+    rows: torch.Tensor                # int32 (T, k): row of each entry, -1 = none
+    src: torch.Tensor                 # int32 (M,): entry t * k + j of each row, -1 = none
+    m_indices: torch.Tensor | None    # int32 (M,): group of each row, -1 = none; None in the masked layout
+    counts: torch.Tensor              # int32 (G,): entries of each group that have a row (masked_m of the masked layout)
+    starts: torch.Tensor | None       # int32 (G + 1,): first row of each group, end of the last; None in the masked layout
+    align: int                        # rows to which a group is padded (1 in the masked layout)
+    slots: int = 0                    # rows of a group in the masked layout (Mmax), 0 in the contiguous one
+
+
+def route_rows(T: int, k: int, G: int, align: int | None = None) -> int:
+    """Rows of the contiguous layout that hold any split of T * k entries over G groups."""
+    return int(_lib.fgf8_route_rows(int(T), int(k), int(G), mk_alignment_for_contiguous() if align is None else int(align)))
+
+
+def _ids(ids: torch.Tensor) -> tuple[int, int, int]:
+    """(T, k, 1 for int64) of a list of group ids, (T,) or (T, k)."""
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"ids must be int32 or int64, got {ids.dtype}")
+    if ids.dim() not in (1, 2):
+        raise ValueError(f"ids: expected (T,) or (T, k), got {tuple(ids.shape)}")
+    return ids.shape[0], ids.shape[1] if ids.dim() == 2 else 1, 1 if ids.dtype is torch.int64 else 0
+
+
+def _need_i32(t: torch.Tensor, shape: tuple, name: str) -> None:
+    if t.shape != shape or t.dtype is not torch.int32:
+        raise ValueError(f"{name}: expected int32 {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+
+
+def route_contiguous(ids: torch.Tensor, G: int, align: int | None = None, M: int | None = None, stream=None) -> Route:
+    """Places of tokens in the layout of grouped_fp8_contiguous.  ids: int32 or int64 (T, k) or
+    (T,), groups 0 .. G - 1, -1 = none.  Each group is padded to a multiple of `align` rows
+    (default mk_alignment_for_contiguous(), what the grouped product wants; lora_f16 takes
+    any multiple of 16).  M rows, by default route_rows(T, k, G, align), which hold any ids."""
+    T, k, ids64 = _ids(ids)
+    align = mk_alignment_for_contiguous() if align is None else int(align)
+    if M is None:
+        M = max(int(_lib.fgf8_route_rows(T, k, G, align)), 0)
+    i32 = torch.int32
+    rows = _empty((T, k), i32, ids, stream)
+    src, m_indices = _empty((M,), i32, ids, stream), _empty((M,), i32, ids, stream)
+    counts, starts = _empty((max(G, 0),), i32, ids, stream), _empty((max(G, 0) + 1,), i32, ids, stream)
+    _launch("route_contiguous", stream, (ids, rows, src, m_indices, counts, starts), (T, k, G, align, M, ids64))
+    return Route(rows, src, m_indices, counts, starts, align)
+
+
+def route_masked(ids: torch.Tensor, G: int, Mmax: int, stream=None) -> Route:
+    """Places of tokens in the layout of grouped_fp8_masked: group g owns rows g * Mmax and on;
+    counts is its masked_m.  Entries past a group's Mmax rows get none."""
+    T, k, ids64 = _ids(ids)
+    i32 = torch.int32
+    rows = _empty((T, k), i32, ids, stream)
+    src, counts = _empty((max(G, 0) * max(Mmax, 0),), i32, ids, stream), _empty((max(G, 0),), i32, ids, stream)
+    _launch("route_masked", stream, (ids, rows, src, counts), (T, k, G, Mmax, ids64))
+    return Route(rows, src, None, counts, None, 1, Mmax)
+
+
+def _entries(route: Route, T: int) -> tuple[int, int]:
+    """(k, M) of a routing of T tokens."""
+    M, k = route.src.shape[0], route.rows.shape[-1]
+    _need_i32(route.rows, (T, k), "route.rows")
+    _need_i32(route.src, (M,), "route.src")
+    return k, M
+
+
+def dispatch_f16(x: torch.Tensor, route: Route, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Xs (M, K) with Xs[rows[t, j]] = X[t] for fp16/bf16 X (T, K).  In the contiguous layout
+    rows without an entry are zeros, in the masked one they are not written."""
+    T, K = x.shape
+    _dtype16(x, "x")
+    k, M = _entries(route, T)
+    if out is None:
+        out = _empty((M, K), x.dtype, x, stream)
+    else:
+        _need_like(out, (M, K), x.dtype, "out")
+    _launch("dispatch_f16", stream, (x, route.rows, None if route.slots else route.src, out), (T, k, K, M))
+    return out
+
+
+def dispatch_fp8(x: torch.Tensor, route: Route, fmt, xq: torch.Tensor | None = None, sfa: torch.Tensor | None = None,
+                 stream=None):
+    """dispatch_f16 with quantize_1x128 on the way: bf16 X (T, K) -> (E4M3 codes uint8 (M, K),
+    activation scale table), the operands of grouped_fp8_contiguous; of a masked routing codes
+    (G, Mmax, K) and G tables, those of grouped_fp8_masked.  Rows without an entry are not
+    written."""
+    T, K = x.shape
+    if x.dtype is not torch.bfloat16:
+        raise ValueError("x must be bf16")
+    k, M = _entries(route, T)
+    f, slots = _fmt(fmt), route.slots
+    G = M // slots if slots else 1
+    shape, dt = sfa_shape(slots or M, K, f)
+    if xq is None:
+        xq = _empty((G, slots, K) if slots else (M, K), torch.uint8, x, stream)
+    if sfa is None:
+        sfa = _empty((G, *shape) if slots else shape, dt, x, stream)
+    _need(xq, M * K, 1, "xq")
+    _need(sfa, G * shape[0] * shape[1], 4, "sfa")
+    _launch("dispatch_fp8", stream, (x, route.rows, xq, sfa), (T, k, K, M, slots, f))
+    return xq, sfa
+
+
+def _rows_of(ys: torch.Tensor, M: int, dtype: torch.dtype | None, name: str) -> int:
+    """Columns of a (M, N) or, in the masked layout, (G, Mmax, N) operand."""
+    N = ys.shape[-1]
+    if ys.numel() != M * N or (dtype is not None and ys.dtype is not dtype):
+        raise ValueError(f"{name}: expected {M} rows{'' if dtype is None else f' of {dtype}'}, got {ys.dtype} {tuple(ys.shape)}")
+    return N
+
+
+def _need_weights(w: torch.Tensor, shape: tuple, name: str) -> None:
+    if w.shape != shape or w.dtype is not torch.float32:
+        raise ValueError(f"{name}: expected torch.float32 {tuple(shape)}, got {w.dtype} {tuple(w.shape)}")
+
+
+def combine_f16(ys: torch.Tensor, w: torch.Tensor | None, route: Route, out: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """Y (T, N) with Y[t] = sum_j w[t, j] Ys[rows[t, j]] for fp16/bf16 Ys (M, N) and float32
+    w (T, k) (None: all ones), summed in FP32.  Entries without a row add nothing."""
+    code, T = _dtype16(ys, "ys"), route.rows.shape[0]
+    k, M = _entries(route, T)
+    N = _rows_of(ys, M, None, "ys")
+    if w is not None:
+        _need_weights(w, (T, k), "w")
+    if out is None:
+        out = _empty((T, N), ys.dtype, ys, stream)
+    else:
+        _need_like(out, (T, N), ys.dtype, "out")
+    _launch("combine_f16", stream, (ys, w, route.rows, out), (T, k, N, M, code))
+    return out
+
+
+def combine_f16_backward(dy: torch.Tensor, ys: torch.Tensor, w: torch.Tensor, route: Route,
+                         dys: torch.Tensor | None = None, dw: torch.Tensor | None = None, stream=None):
+    """Gradients (dYs (M, N), dw (T, k)) of combine_f16 from dY (T, N).  In the contiguous layout
+    rows of dYs without an entry are zeros, in the masked one they are not written."""
+    T, N = dy.shape
+    code = _dtype16(dy, "dy")
+    k, M = _entries(route, T)
+    if _rows_of(ys, M, dy.dtype, "ys") != N:
+        raise ValueError(f"ys: expected rows of {N}, got {tuple(ys.shape)}")
+    _need_weights(w, (T, k), "w")
+    if dys is None:
+        dys = _empty(ys.shape, ys.dtype, dy, stream)
+    else:
+        _need_like(dys, ys.shape, ys.dtype, "dys")
+    if dw is None:
+        dw = _empty((T, k), torch.float32, dy, stream)
+    else:
+        _need_weights(dw, (T, k), "dw")
+    _launch("combine_f16_backward", stream, (dy, ys, w, route.rows, None if route.slots else route.src, dys, dw), (T, k, N, M, code))
+    return dys, dw
+
+
+def dispatch_f16_backward(dxs: torch.Tensor, route: Route, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradient dX (T, K) of dispatch_f16 (of dispatch_fp8 with the quantization passed straight
+    through) from dXs (M, K): dX[t] = sum_j dXs[rows[t, j]], summed in FP32."""
+    code, T = _dtype16(dxs, "dxs"), route.rows.shape[0]
+    k, M = _entries(route, T)
+    K = _rows_of(dxs, M, None, "dxs")
+    if out is None:
+        out = _empty((T, K), dxs.dtype, dxs, stream)
+    else:
+        _need_like(out, (T, K), dxs.dtype, "out")
+    _launch("dispatch_f16_backward", stream, (dxs, route.rows, out), (T, k, K, M, code))
+    return out
+
+
+def _need_strided(t: torch.Tensor, shape: tuple, dtype: torch.dtype, name: str) -> int:
+    """A 16-bit matrix whose rows are contiguous but may be further apart than they are long
+    (columns of a wider one): elements between rows."""
+    if t.shape != shape or t.dtype is not dtype:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.is_contiguous():
+        return shape[1]
+    if t.stride(1) != 1 or t.stride(0) < shape[1]:
+        raise ValueError(f"{name}: rows must be contiguous and apart, got strides {t.stride()}")
+    return t.stride(0)
+
+
+def lora_f16(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, route: Route, scale: torch.Tensor | None = None,
+             base: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out[t] = base[t] + scale[g] (X[t] A[g]^T) B[g]^T with g the adapter of token t, in one kernel.
+    x (T, K), a (G, r, K), b (G, N, r), base and out (T, N) are fp16/bf16, r a multiple of 8 up to
+    128, scale float32 (G,) (None: ones).  route: route_contiguous(adapter ids (T,), G, align)
+    with align a multiple of 16; one serves every layer of a step.  Tokens without an adapter
+    get base (None: zeros).  out may be base.  Rows of x, base and out may be columns of wider
+    matrices."""
+    T, K = x.shape
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError(f"a and b: expected (G, r, K) and (G, N, r), got {tuple(a.shape)} and {tuple(b.shape)}")
+    G, r, _ = a.shape
+    N = b.shape[1]
+    code, dtype = _dtype16(x, "x"), x.dtype
+    ldx = _need_strided(x, (T, K), dtype, "x")
+    _need_like(a, (G, r, K), dtype, "a")
+    _need_like(b, (G, N, r), dtype, "b")
+    k, M = _entries(route, T)
+    if k != 1 or route.slots:
+        raise ValueError("route: expected a route_contiguous of one adapter per token")
+    if route.align % 16:
+        raise ValueError(f"route: align {route.align} is not a multiple of 16")
+    _need_i32(route.m_indices, (M,), "route.m_indices")
+    if scale is not None:
+        _need_weights(scale, (G,), "scale")
+    if out is None:
+        out = _empty((T, N), dtype, x, stream)
+    ldo = _need_strided(out, (T, N), dtype, "out")
+    ldb = _need_strided(base, (T, N), dtype, "base") if base is not None else 0
+    _launch("lora_f16", stream, (x, a, b, scale, base, route.rows, route.src, route.m_indices, out),
+            (T, K, N, r, G, M, ldx, ldb, ldo, code), strided=(0, 4, 8))
     return out
 
 

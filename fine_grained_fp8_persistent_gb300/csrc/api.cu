@@ -409,7 +409,7 @@ static int check_fp8_common(const char* who, int N, int K, int fmt) {
   return FGF8_OK;
 }
 
-static int dispatch_fp8(fgf8::GemmArgs& a, fgf8::Sched sched, const void* Aq, const void* SFA,
+static int launch_fp8(fgf8::GemmArgs& a, fgf8::Sched sched, const void* Aq, const void* SFA,
                         const void* Bq, const void* SFB, int fmt, void* stream) {
   if (fmt == FGF8_SCALE_UE8M0) {
     a.sfa_ue8m0 = static_cast<const uint32_t*>(SFA);
@@ -433,7 +433,7 @@ int gemm_fp8_blockscaled(const void* Aq, const void* SFA, const void* Bq, const 
   if (int r = check_on_device("gemm_fp8_blockscaled", {Aq, SFA, Bq, SFB, D})) return r;
   fgf8::GemmArgs a;
   if (prepare_args(a, M, N, K, 1, D) != FGF8_OK) return FGF8_ERR_CUDA;
-  return dispatch_fp8(a, fgf8::Sched::Dense, Aq, SFA, Bq, SFB, fmt, stream);
+  return launch_fp8(a, fgf8::Sched::Dense, Aq, SFA, Bq, SFB, fmt, stream);
 }
 
 int gemm_fp8_blockscaled_quant(const void* Aq, const void* SFA, const void* Bq, const void* SFB,
@@ -456,7 +456,7 @@ int gemm_fp8_blockscaled_quant(const void* Aq, const void* SFA, const void* Bq, 
   a.dq = static_cast<uint8_t*>(Dq);
   a.sfd = SFD;
   a.dq_ue8m0 = out_fmt == FGF8_SCALE_UE8M0;
-  return dispatch_fp8(a, fgf8::Sched::Dense, Aq, SFA, Bq, SFB, fmt, stream);
+  return launch_fp8(a, fgf8::Sched::Dense, Aq, SFA, Bq, SFB, fmt, stream);
 }
 
 int gemm_fp4_blockscaled(const void* Aq, const void* SFA, const void* Bq, const void* SFB, void* D, int M,
@@ -498,7 +498,7 @@ int grouped_fp8_contiguous(const void* Aq, const void* SFA, const void* Bq, cons
   fgf8::GemmArgs a;
   if (prepare_args(a, M, N, K, G, D) != FGF8_OK) return FGF8_ERR_CUDA;
   a.m_indices = m_indices;
-  return dispatch_fp8(a, fgf8::Sched::Contiguous, Aq, SFA, Bq, SFB, fmt, stream);
+  return launch_fp8(a, fgf8::Sched::Contiguous, Aq, SFA, Bq, SFB, fmt, stream);
 }
 
 int grouped_fp8_masked(const void* Aq, const void* SFA, const void* Bq, const void* SFB,
@@ -521,7 +521,7 @@ int grouped_fp8_masked(const void* Aq, const void* SFA, const void* Bq, const vo
   fgf8::GemmArgs a;
   if (prepare_args(a, Mmax, N, K, G, D) != FGF8_OK) return FGF8_ERR_CUDA;
   a.masked_m = masked_m;
-  return dispatch_fp8(a, fgf8::Sched::Masked, Aq, SFA, Bq, SFB, fmt, stream);
+  return launch_fp8(a, fgf8::Sched::Masked, Aq, SFA, Bq, SFB, fmt, stream);
 }
 
 }  // extern "C"

@@ -1,40 +1,12 @@
 // api_gated.cu -- the C ABI of the gated feed-forward and 4-bit matrix-vector
 // operators (include/fgf8.h): host-side validation and dispatch.
-#include <initializer_list>
-
 #include "../../include/fgf8.h"
+#include "check.h"
 #include "gated.h"
 
 namespace {
 
-// Every tensor pointer is 16-byte aligned device (or managed) memory of the current
-// device, checked before anything is launched.
-int check_pointers(const char* who, std::initializer_list<const void*> ptrs) {
-  for (const void* p : ptrs) {
-    if (p == nullptr) return fgf8::set_error(FGF8_ERR_INVALID_ARG, "%s: null pointer", who);
-    if ((reinterpret_cast<uintptr_t>(p) & 15u) != 0)
-      return fgf8::set_error(FGF8_ERR_MISALIGNED, "%s: pointers must be 16-byte aligned", who);
-  }
-  int dev = 0;
-  const cudaError_t ed = cudaGetDevice(&dev);
-  if (ed != cudaSuccess) return fgf8::set_error(FGF8_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(ed));
-  int i = 0;
-  for (const void* p : ptrs) {
-    cudaPointerAttributes at;
-    const cudaError_t e = cudaPointerGetAttributes(&at, p);
-    if (e != cudaSuccess) {
-      cudaGetLastError();  // the failed query also sets the runtime's last error; clear it
-      return fgf8::set_error(FGF8_ERR_INVALID_ARG, "%s: pointer %d: %s", who, i, cudaGetErrorString(e));
-    }
-    if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged)
-      return fgf8::set_error(FGF8_ERR_INVALID_ARG, "%s: pointer %d is not device memory", who, i);
-    if (at.type == cudaMemoryTypeDevice && at.device != dev)
-      return fgf8::set_error(FGF8_ERR_INVALID_ARG, "%s: pointer %d is on device %d, the current device is %d", who, i,
-                             at.device, dev);
-    ++i;
-  }
-  return FGF8_OK;
-}
+using fgf8::check_pointers;
 
 int check_sizes(const char* who, int M, int N, int K) {
   if (M < 0 || N <= 0 || K <= 0) return fgf8::set_error(FGF8_ERR_INVALID_ARG, "%s: M=%d N=%d K=%d", who, M, N, K);

@@ -115,5 +115,38 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d, c
          (static_cast<uint32_t>(ptx::cvt_e4m3x2(scaled<UE8M0>(c, g), scaled<UE8M0>(d, g))) << 16);
 }
 
+// Eight bf16 values as FP32.
+__device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(u[i] << 16);
+    f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+}
+
+// Quantize 8 values with the group's scale; returns 8 packed E4M3 bytes.  FP32
+// scales divide (x / s, rounded to nearest, by div_by_scale2 with inv the
+// scale's reciprocal from scale_reciprocal); power-of-two scales multiply
+// by the exact 2^-e (inv).  The format is a template parameter so each kernel
+// carries only its own arithmetic.
+template <bool UE8M0>
+__device__ __forceinline__ uint2 quant8(const float (&f)[8], float s, float inv) {
+  float q[8];
+  if (UE8M0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = f[i] * inv;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) div_by_scale2(f[i], f[i + 1], s, inv, q[i], q[i + 1]);
+  }
+  uint2 r;
+  r.x = static_cast<uint32_t>(ptx::cvt_e4m3x2(q[0], q[1])) |
+        (static_cast<uint32_t>(ptx::cvt_e4m3x2(q[2], q[3])) << 16);
+  r.y = static_cast<uint32_t>(ptx::cvt_e4m3x2(q[4], q[5])) |
+        (static_cast<uint32_t>(ptx::cvt_e4m3x2(q[6], q[7])) << 16);
+  return r;
+}
+
 }  // namespace quant
 }  // namespace fgf8

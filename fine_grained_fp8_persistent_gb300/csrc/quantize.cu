@@ -24,39 +24,9 @@ namespace {
 
 using quant::exp2_neg;
 using quant::kE4M3Max;
+using quant::quant8;
 using quant::ue8m0_exponent;
-
-__device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(u[i] << 16);
-    f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-  }
-}
-
-// Quantize 8 values with the group's scale; returns 8 packed E4M3 bytes.  FP32
-// scales divide (x / s, rounded to nearest, by quant::div_by_scale2 with inv the
-// scale's reciprocal from quant::scale_reciprocal); power-of-two scales multiply
-// by the exact 2^-e (inv).  The format is a template parameter so each kernel
-// carries only its own arithmetic.
-template <bool UE8M0>
-__device__ __forceinline__ uint2 quant8(const float (&f)[8], float s, float inv) {
-  float q[8];
-  if (UE8M0) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = f[i] * inv;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) quant::div_by_scale2(f[i], f[i + 1], s, inv, q[i], q[i + 1]);
-  }
-  uint2 r;
-  r.x = static_cast<uint32_t>(ptx::cvt_e4m3x2(q[0], q[1])) |
-        (static_cast<uint32_t>(ptx::cvt_e4m3x2(q[2], q[3])) << 16);
-  r.y = static_cast<uint32_t>(ptx::cvt_e4m3x2(q[4], q[5])) |
-        (static_cast<uint32_t>(ptx::cvt_e4m3x2(q[6], q[7])) << 16);
-  return r;
-}
+using quant::unpack8;
 
 // One warp per item (row m, group of four 128-wide K blocks).  Lane l covers
 // elements [16 l, 16 l + 16) of the item's 512-element chunk, so lanes 8j..8j+7

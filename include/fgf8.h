@@ -278,6 +278,106 @@ FGF8_API int gemv_fp4(const void* X, const void* Wq, const void* SF, void* Y, in
 FGF8_API int gated_gemv_fp4(const void* X, const void* WgQ, const void* SFg, const void* WuQ, const void* SFu,
                             void* H, int M, int N, int K, int fmt, int dtype, int act, void* stream);
 
+/*
+ * Rows that choose their own weights.  The routing operators give every entry (t, j) of a
+ * list of group ids (the experts of token t, or its adapter) a row of the layouts that the
+ * grouped products read; the others move tokens by it, in 16 bits or quantized to E4M3,
+ * bring them back, and take the gradients of both ways.
+ *   ids  : int32 (ids64 = 0) or int64 (ids64 = 1) [T][k], 0 .. G-1, -1 = no group; the same
+ *          group may stand in a token's list twice
+ *   rows : int32 [T][k], row of each entry, -1 = none
+ *   src  : int32 [M], entry t * k + j of each row, -1 = none
+ * Entries of a group stand in the order of t * k + j, on every run.  An id or a row out of
+ * range sets FGF8_ERR_DEVICE_INPUT and counts as -1.  Two entries may not share a row.
+ *
+ * route_contiguous -- the layout of grouped_fp8_contiguous: groups one behind the other,
+ * each padded to a multiple of `align` rows.
+ *   m_indices : int32 [M], group of each row, -1 = none
+ *   counts    : int32 [G], entries of each group
+ *   starts    : int32 [G + 1], first row of each group, and the row behind the last one
+ * Requires 1 <= G <= 1024, M a multiple of align and at least fgf8_route_rows(T, k, G,
+ * align), so that any ids fit.  T == 0 writes every output.
+ *
+ * route_masked -- the layout of grouped_fp8_masked: group g owns rows g * Mmax and on.
+ *   src      : int32 [G][Mmax]
+ *   masked_m : int32 [G], entries of each group, at most Mmax
+ * Entries of a group past its Mmax rows get none (-1 in rows).  Requires 1 <= G <= 1024,
+ * Mmax >= 1.
+ */
+FGF8_API int route_contiguous(const void* ids, int32_t* rows, int32_t* src, int32_t* m_indices, int32_t* counts,
+                              int32_t* starts, int T, int k, int G, int align, int M, int ids64, void* stream);
+FGF8_API int route_masked(const void* ids, int32_t* rows, int32_t* src, int32_t* masked_m, int T, int k, int G,
+                          int Mmax, int ids64, void* stream);
+
+/* Rows that hold any split of T * k entries over G groups in segments of `align` rows; -1 on
+ * invalid arguments. */
+FGF8_API long long fgf8_route_rows(int T, int k, int G, int align);
+
+/*
+ * dispatch_f16 -- Xs[rows[t][j]] = X[t], 16-bit elements of either type.
+ *   X : [T][K];  Xs : [M][K]
+ *   src : rows without an entry become zeros, so that products over whole segments (weight
+ *         gradients) can read them; NULL: they are not written
+ * Requires K % 8 == 0.
+ *
+ * dispatch_fp8 -- the same with the 1x128 quantization of quantize_1x128 on the way: codes
+ * and scales of a row are the bits that quantize_1x128 gives for that token.
+ *   X : bf16 [T][K];  Xq : uint8 [M][K]
+ *   SFA : activation table for M rows, or, with Mmax > 0 (the masked layout, M = G * Mmax),
+ *         G tables of Mmax rows back to back
+ * Codes and scales of rows without an entry are not written (the grouped products compute
+ * nothing from them).  Requires K % 128 == 0.
+ */
+FGF8_API int dispatch_f16(const void* X, const int32_t* rows, const int32_t* src, void* Xs, int T, int k, int K, int M,
+                          void* stream);
+FGF8_API int dispatch_fp8(const void* X, const int32_t* rows, void* Xq, void* SFA, int T, int k, int K, int M, int Mmax,
+                          int fmt, void* stream);
+
+/*
+ * combine_f16 -- Y[t] = sum_j W[t][j] Ys[rows[t][j]], summed in FP32 in the order of j,
+ * rounded once.  Entries without a row add nothing (W and Ys are not looked at); a token
+ * without any gets zeros.
+ *   Ys : [M][N], Y : [T][N] of one type (dtype);  W : float [T][k], NULL = all ones
+ *
+ * combine_f16_backward -- its gradients:
+ *   dYs[rows[t][j]] = W[t][j] dY[t] (rounded once),  dW[t][j] = <dY[t], Ys[rows[t][j]]>
+ *   dY : [T][N], Ys, dYs : [M][N];  W, dW : float [T][k]; dW of an entry without a row is 0
+ *   src : rows of dYs without an entry become zeros; NULL: they are not written
+ *
+ * dispatch_f16_backward -- the gradient of dispatch_f16: dX[t] = sum_j dXs[rows[t][j]].
+ * It is also that of dispatch_fp8 when the quantization is passed straight through.
+ *   dXs : [M][K], dX : [T][K] of one type (dtype)
+ *
+ * All require N % 8 == 0 (K % 8 == 0), and outputs that overlap no input.
+ */
+FGF8_API int combine_f16(const void* Ys, const float* W, const int32_t* rows, void* Y, int T, int k, int N, int M,
+                         int dtype, void* stream);
+FGF8_API int combine_f16_backward(const void* dY, const void* Ys, const float* W, const int32_t* rows, const int32_t* src,
+                                  void* dYs, float* dW, int T, int k, int N, int M, int dtype, void* stream);
+FGF8_API int dispatch_f16_backward(const void* dXs, const int32_t* rows, void* dX, int T, int k, int K, int M, int dtype,
+                                   void* stream);
+
+/*
+ * lora_f16 -- low-rank adapters of many requests beside a shared projection, in one kernel:
+ *   out[t] = base[t] + scale[g] (X[t] A_g^T) B_g^T,   g the adapter of token t
+ * FP32 sums; X A^T is kept to 16 bits (bf16) or 22 bits (fp16) between the two products, and
+ * out is rounded once.
+ *   X : [T][K], rows ldx elements apart;  A : [G][r][K];  B : [G][N][r]
+ *   scale : float [G], NULL = all ones
+ *   base : [T][N], rows ldb apart, what the shared projection gave; NULL = zeros;
+ *          it may be out itself (with ldb = ldo)
+ *   out : [T][N], rows ldo apart
+ *   rows [T], src [M], m_indices [M] : route_contiguous of the tokens' adapters (k = 1) with
+ *          align a multiple of 16; a routing serves every layer of a step
+ * Tokens without an adapter get base.  X, A, B, base and out are of one type (dtype).
+ * A row that names another adapter than the first of its 16 rows sets
+ * FGF8_ERR_DEVICE_INPUT and is not computed.  Requires K, N, r, ldx, ldb, ldo multiples of
+ * 8, r <= 128, M % 16 == 0, and an out that overlaps no other input than an identical base.
+ */
+FGF8_API int lora_f16(const void* X, const void* A, const void* B, const float* scale, const void* base,
+                      const int32_t* rows, const int32_t* src, const int32_t* m_indices, void* out, int T, int K, int N,
+                      int r, int G, int M, long long ldx, long long ldb, long long ldo, int dtype, void* stream);
+
 /* Bytes of a quantize_fp4 scale table for R rows; -1 on invalid arguments. */
 FGF8_API long long fgf8_fp4_sf_bytes(int R, int K, int fmt);
 
