@@ -32,59 +32,131 @@ __device__ __forceinline__ int load_row(const RowsArgs& a, long long entry) {
   return -1;
 }
 // Rows of up to 32 entries of token t from j0 on, one per lane (-1 past the last).
-__device__ __forceinline__ int load_rows(const RowsArgs& a, int t, int j0, int lane) {
+__device__ __forceinline__ int load_rows(const RowsArgs& a, uint32_t t, int j0, int lane) {
   return j0 + lane < a.k ? load_row(a, static_cast<long long>(t) * a.k + j0 + lane) : -1;
 }
 
-// Rows that no entry owns, of the 32 from r0 on, as a mask.
-__device__ __forceinline__ uint32_t empty_rows(const RowsArgs& a, int r0, int lane) {
-  const bool empty = r0 + lane < a.M && ptx::ld_global(a.src + r0 + lane) < 0;
-  return __ballot_sync(kFull, empty);
-}
+// Items (token t, part p of its row) in flat order, `step` at a time, without a division for
+// each.  T is below 2^31 and a step some thousands, so t does not wrap.
+struct Walk {
+  uint32_t t, p;
+  const uint32_t step_t, step_p, parts;
+  __device__ __forceinline__ Walk(uint32_t first, uint32_t step, uint32_t n)
+      : t(first / n), p(first % n), step_t(step / n), step_p(step % n), parts(n) {}
+  __device__ __forceinline__ void next() {
+    t += step_t;
+    p += step_p;
+    if (p >= parts) {
+      p -= parts;
+      ++t;
+    }
+  }
+};
 
 // ----------------------------------------------------------------- dispatch, 16 bits
-// A warp's item is 2 KB of a token (four 16-byte loads in flight per lane), written to its
-// k rows; behind the tokens, 2 KB of each of 32 rows of the layout that are zeros if no
-// entry owns them.
-constexpr int kPart = 4;                        // 16-byte pieces per lane and item
+// No byte passes through a register: a warp loads a piece of a token (a whole row, or an equal
+// part of at most kMaxPiece bytes) into shared memory with one bulk copy, and lane j stores it
+// to the row of entry j with another.  Each warp has a ring of stages of its own: a stage is
+// loaded again when the stores of the item after it have been issued and its own have read
+// it.  Behind the tokens, each lane looks at one row of the layout and fills it from a piece
+// of zeros if no entry owns it.
+constexpr int kMaxPiece = 8192, kStages = 3, kBulkWarps = 8, kBulkThreads = 32 * kBulkWarps;
 
-__global__ void __launch_bounds__(kThreads) dispatch_f16_kernel(RowsArgs a, const uint4* __restrict__ X,
-                                                                uint4* __restrict__ Xs) {
-  ptx::griddep_wait();                          // everything may come from the previous kernel
+struct BulkArgs {
+  RowsArgs a;
+  long long row_bytes;
+  int pieces, piece;              // parts of a row, and bytes of all of them but the last
+  int zero_rows;                  // rows that a warp looks at together behind the tokens, up to 32
+  uint64_t timeout_ns;
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+
+__global__ void __launch_bounds__(kBulkThreads) dispatch_f16_kernel(BulkArgs args, const uint8_t* __restrict__ X,
+                                                                uint8_t* __restrict__ Xs) {
+  extern __shared__ __align__(128) uint8_t smem[];          // [zeros][warp][stage], args.piece bytes each
+  __shared__ uint64_t bars[kBulkWarps * kStages];
+  __shared__ volatile uint32_t abort_word;
+  const RowsArgs& a = args.a;
+  const int lane = static_cast<int>(threadIdx.x & 31), warp = static_cast<int>(threadIdx.x >> 5);
+  const uint32_t zeros = ptx::smem_u32(smem), ring = zeros + static_cast<uint32_t>(args.piece * (1 + warp * kStages));
+  auto full = [&](int s) { return ptx::smem_u32(&bars[warp * kStages + s]); };
+  if (threadIdx.x == 0) abort_word = 0u;
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) ptx::mbar_init(full(s), 1);
+    ptx::fence_mbar_init();
+  }
+  for (int i = static_cast<int>(threadIdx.x); i < args.piece / 16; i += kBulkThreads)
+    reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
+  ptx::fence_proxy_async_smem();                            // the stores below read it
+  __syncthreads();
+  ptx::griddep_wait();                                      // everything may come from the previous kernel
   ptx::griddep_launch_dependents();
-  const int lane = static_cast<int>(threadIdx.x & 31);
-  const int vecs = a.H / 8, parts = (vecs + 32 * kPart - 1) / (32 * kPart);
-  const long long tokens = static_cast<long long>(a.T) * parts;
-  const long long items = tokens + (a.src != nullptr ? (static_cast<long long>(a.M) + 31) / 32 * parts : 0);
-  const long long step = static_cast<long long>(gridDim.x) * kWarps;
-  for (long long it = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < items; it += step) {
-    if (it < tokens) {
-      const int t = static_cast<int>(it / parts), v0 = static_cast<int>(it % parts) * 32 * kPart + lane;
-      uint4 v[kPart];
-#pragma unroll
-      for (int u = 0; u < kPart; ++u)
-        if (v0 + 32 * u < vecs) v[u] = ptx::ld_global_v4(X + static_cast<size_t>(t) * vecs + v0 + 32 * u);
-      for (int j0 = 0; j0 < a.k; j0 += 32) {
-        const int rows = load_rows(a, t, j0, lane);
-        for (int j = 0; j < 32 && j0 + j < a.k; ++j) {
-          const int row = __shfl_sync(kFull, rows, j);
-          if (row < 0) continue;
-          uint4* out = Xs + static_cast<size_t>(row) * vecs + v0;
-#pragma unroll
-          for (int u = 0; u < kPart; ++u)
-            if (v0 + 32 * u < vecs) st_global_v4(out + 32 * u, v[u]);
-        }
-      }
-    } else {
-      const long long z = it - tokens;
-      const int r0 = static_cast<int>(z / parts) * 32, v0 = static_cast<int>(z % parts) * 32 * kPart + lane;
-      for (uint32_t left = empty_rows(a, r0, lane); left != 0; left &= left - 1) {
-        uint4* out = Xs + static_cast<size_t>(r0 + __ffs(left) - 1) * vecs + v0;
-#pragma unroll
-        for (int u = 0; u < kPart; ++u)
-          if (v0 + 32 * u < vecs) st_global_v4(out + 32 * u, make_uint4(0u, 0u, 0u, 0u));
-      }
+
+  // neighbouring items on different SMs, so that few of them are spread over all
+  const uint32_t T = static_cast<uint32_t>(a.T), first = warp * gridDim.x + blockIdx.x, step = gridDim.x * kBulkWarps;
+  Walk now(first, step, static_cast<uint32_t>(args.pieces)), ahead = now;          // `ahead`: the next item to load
+  auto bytes_of = [&](uint32_t p) {
+    return static_cast<uint32_t>(min(static_cast<long long>(args.piece), args.row_bytes - static_cast<long long>(p) * args.piece));
+  };
+  auto load = [&](int s) {
+    if (ahead.t < T) {
+      ptx::mbar_arrive_expect_tx(full(s), bytes_of(ahead.p));
+      bulk_load(ring + static_cast<uint32_t>(s * args.piece),
+                X + static_cast<size_t>(ahead.t) * args.row_bytes + static_cast<size_t>(ahead.p) * args.piece, bytes_of(ahead.p), full(s));
     }
+    ahead.next();
+  };
+  PairWaitCtl ctl{&abort_word, 0u, a.status, args.timeout_ns, FGF8_DEVERR_ROLE_PRODUCER};
+  if (lane == 0)
+    for (int s = 0; s < kStages - 1; ++s) load(s);
+  int rows = now.t < T ? load_rows(a, now.t, 0, lane) : -1;
+  int stage = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  while (now.t < T) {
+    const uint32_t t = now.t, p = now.p;
+    const int mine = rows;
+    now.next();
+    if (now.t < T) rows = load_rows(a, now.t, 0, lane);
+    ok = pwait(full(stage), phase, ctl);
+    if (!ok) break;
+    const uint32_t src = ring + static_cast<uint32_t>(stage * args.piece);
+    for (int j0 = 0; j0 < a.k; j0 += 32) {
+      const int row = j0 == 0 ? mine : load_rows(a, t, j0, lane);
+      if (row >= 0) bulk_store(Xs + static_cast<size_t>(row) * args.row_bytes + static_cast<size_t>(p) * args.piece, src, bytes_of(p));
+    }
+    ptx::bulk_commit_group();
+    ptx::bulk_wait_group_read<1>();                         // the item before has left its stage
+    __syncwarp();
+    if (lane == 0) load(stage == 0 ? kStages - 1 : stage - 1);
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+  if (ok && a.src != nullptr) {
+    const uint32_t M = static_cast<uint32_t>(a.M), R = static_cast<uint32_t>(args.zero_rows);
+    for (uint32_t r0 = first * R; r0 < M; r0 += step * R) {
+      const uint32_t row = r0 + lane;
+      if (lane < args.zero_rows && row < M && ptx::ld_global(a.src + row) < 0)
+        for (uint32_t p = 0; p < now.parts; ++p)
+          bulk_store(Xs + static_cast<size_t>(row) * args.row_bytes + static_cast<size_t>(p) * args.piece, zeros, bytes_of(p));
+    }
+    ptx::bulk_commit_group();
+  }
+  ptx::bulk_wait_group<0>();
+  // after a wait that ran out, loads may still be under way into this shared memory
+  if (__syncthreads_or(abort_word != 0u ? 1 : 0)) {
+    const uint64_t t0 = ptx::globaltimer();
+    while (ptx::globaltimer() - t0 < 200000ull) __nanosleep(1000);
   }
 }
 
@@ -101,16 +173,16 @@ __global__ void __launch_bounds__(kThreads) dispatch_fp8_kernel(RowsArgs a, cons
   const int per = a.slots > 0 ? a.slots : a.M;             // rows of one scale table
   const size_t ld = (static_cast<size_t>(per) + 3) / 4 * 4;
   const size_t table = ld * (UE8M0 ? kq : nkb);
-  const long long items = static_cast<long long>(a.T) * kq;
-  const long long step = static_cast<long long>(gridDim.x) * kWarps;
-  for (long long it = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < items; it += step) {
-    const int t = static_cast<int>(it / kq), qw = static_cast<int>(it % kq);
-    const int kb = 4 * qw + (lane >> 3);
+  const uint32_t T = static_cast<uint32_t>(a.T);
+  Walk w(blockIdx.x * kWarps + (threadIdx.x >> 5), gridDim.x * kWarps, static_cast<uint32_t>(kq));
+  for (; w.t < T; w.next()) {
+    const int qw = static_cast<int>(w.p), kb = 4 * qw + (lane >> 3);
     const bool active = kb < nkb;
+    const int first_rows = load_rows(a, w.t, 0, lane);
     float f0[8], f1[8];
     float amax = 0.0f;
     if (active) {
-      const uint4* src = X + (static_cast<size_t>(t) * a.H + static_cast<size_t>(qw) * 512 + 16 * lane) / 8;
+      const uint4* src = X + (static_cast<size_t>(w.t) * a.H + static_cast<size_t>(qw) * 512 + 16 * lane) / 8;
       const uint4 w0 = ptx::ld_global_v4(src), w1 = ptx::ld_global_v4(src + 1);
       quant::unpack8(w0, f0);
       quant::unpack8(w1, f1);
@@ -139,12 +211,15 @@ __global__ void __launch_bounds__(kThreads) dispatch_fp8_kernel(RowsArgs a, cons
     const bool scales = UE8M0 ? lane == 0 : (lane & 7) == 0 && active;
     const size_t at = ld * (UE8M0 ? qw : kb);
     for (int j0 = 0; j0 < a.k; j0 += 32) {
-      const int rows = load_rows(a, t, j0, lane);
+      const int rows = j0 == 0 ? first_rows : load_rows(a, w.t, j0, lane);
       for (int j = 0; j < 32 && j0 + j < a.k; ++j) {
         const int row = __shfl_sync(kFull, rows, j);
         if (row < 0) continue;
         if (active) st_global_v4(Xq + (static_cast<size_t>(row) * a.H + static_cast<size_t>(qw) * 512 + 16 * lane) / 16, code);
-        if (scales) SF[static_cast<size_t>(row / per) * table + at + row % per] = word;
+        if (scales) {
+          const int g = a.slots > 0 ? row / a.slots : 0;
+          SF[static_cast<size_t>(g) * table + at + (row - g * a.slots)] = word;
+        }
       }
     }
   }
@@ -165,105 +240,147 @@ __device__ __forceinline__ uint4 pack16(const float (&f)[8], bool bf16) {
   return make_uint4(pack_2x16(f[0], f[1], bf16), pack_2x16(f[2], f[3], bf16), pack_2x16(f[4], f[5], bf16), pack_2x16(f[6], f[7], bf16));
 }
 
-// A warp's item is 512 bytes of a token: 16 bytes per lane of each of its rows, up to
-// kBatch rows in flight, added in FP32 in the order of j.
-constexpr int kBatch = 8;
-
-template <bool BF16, bool WEIGHTED>
-__global__ void __launch_bounds__(kThreads) combine_f16_kernel(RowsArgs a, const uint4* __restrict__ Ys,
+// A warp's item is U * 512 bytes of a token.  A batch of B rows is in flight together, up to
+// eight 16-byte loads per lane, and added in FP32 in the order of j; the next item's rows and
+// weights are loaded ahead of them.  B and U go by k, and the CTAs per SM (24 or 32 warps) by
+// what the registers of B U loads and 8 U sums leave: at 8192 tokens of 7168, k = 8, 32 warps
+// take 167 us and 24 take 179; at 4096 columns, k = 2, U = 2 takes 34.7 us, U = 4 36.2, U = 1 41.2.
+template <bool BF16, bool WEIGHTED, int B, int U>
+__global__ void __launch_bounds__(kThreads, B == 4 ? 3 : 4) combine_f16_kernel(RowsArgs a, const uint4* __restrict__ Ys,
                                                                const float* __restrict__ W, uint4* __restrict__ Y) {
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int lane = static_cast<int>(threadIdx.x & 31);
-  const int vecs = a.H / 8, parts = (vecs + 31) / 32;
-  const long long items = static_cast<long long>(a.T) * parts;
-  const long long step = static_cast<long long>(gridDim.x) * kWarps;
-  for (long long it = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < items; it += step) {
-    const int t = static_cast<int>(it / parts), v = static_cast<int>(it % parts) * 32 + lane;
-    float sum[8] = {};
+  const int vecs = a.H / 8, parts = (vecs + 32 * U - 1) / (32 * U);
+  auto load_weights = [&](uint32_t t, int j0) {
+    return WEIGHTED && j0 + lane < a.k ? ptx::ld_global(W + static_cast<long long>(t) * a.k + j0 + lane) : 1.0f;
+  };
+  const uint32_t T = static_cast<uint32_t>(a.T);
+  Walk next(blockIdx.x * kWarps + (threadIdx.x >> 5), gridDim.x * kWarps, static_cast<uint32_t>(parts));
+  if (next.t >= T) return;
+  int rows = load_rows(a, next.t, 0, lane);
+  float weights = load_weights(next.t, 0);
+  while (next.t < T) {
+    const uint32_t t = next.t;
+    const int v0 = static_cast<int>(next.p) * 32 * U + lane;
+    int mine = rows;
+    float by = weights;
+    next.next();
+    if (next.t < T) {
+      rows = load_rows(a, next.t, 0, lane);
+      weights = load_weights(next.t, 0);
+    }
+    float sum[U][8] = {};
     for (int j0 = 0; j0 < a.k; j0 += 32) {
-      const int rows = load_rows(a, t, j0, lane);
-      float weights = 1.0f;
-      if (WEIGHTED && j0 + lane < a.k) weights = ptx::ld_global(W + static_cast<long long>(t) * a.k + j0 + lane);
+      if (j0 > 0) {
+        mine = load_rows(a, t, j0, lane);
+        by = load_weights(t, j0);
+      }
       const int n = min(32, a.k - j0);
-      for (int j = 0; j < n; j += kBatch) {
-        uint4 y[kBatch];
+      for (int j = 0; j < n; j += B) {
+        uint4 y[B][U];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int row = __shfl_sync(kFull, rows, (j + u) & 31);
-          if (j + u < n && row >= 0 && v < vecs) y[u] = ptx::ld_global_v4(Ys + static_cast<size_t>(row) * vecs + v);
+        for (int b = 0; b < B; ++b) {
+          const int row = __shfl_sync(kFull, mine, (j + b) & 31);   // -1 past the last entry
+          if (row >= 0) {
+            const uint4* p = Ys + static_cast<size_t>(row) * vecs + v0;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+              if (v0 + 32 * u < vecs) y[b][u] = ptx::ld_global_v4(p + 32 * u);
+          }
         }
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int row = __shfl_sync(kFull, rows, (j + u) & 31);
-          const float w = WEIGHTED ? __shfl_sync(kFull, weights, (j + u) & 31) : 1.0f;
-          if (j + u < n && row >= 0) {
-            float f[8];
-            unpack16<BF16>(y[u], f);
+        for (int b = 0; b < B; ++b) {
+          const int row = __shfl_sync(kFull, mine, (j + b) & 31);
+          const float w = WEIGHTED ? __shfl_sync(kFull, by, (j + b) & 31) : 1.0f;
+          if (row >= 0) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] = WEIGHTED ? fmaf(w, f[i], sum[i]) : sum[i] + f[i];
+            for (int u = 0; u < U; ++u) {
+              float f[8];
+              unpack16<BF16>(y[b][u], f);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) sum[u][i] = WEIGHTED ? fmaf(w, f[i], sum[u][i]) : sum[u][i] + f[i];
+            }
           }
         }
       }
     }
-    if (v < vecs) st_global_v4(Y + static_cast<size_t>(t) * vecs + v, pack16(sum, BF16));
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (v0 + 32 * u < vecs) st_global_v4(Y + static_cast<size_t>(t) * vecs + v0 + 32 * u, pack16(sum[u], BF16));
   }
 }
 
 // ----------------------------------------------------------------- gradients of combine
-// A CTA takes a token: its threads walk the row once for every kBatch entries, so dY is read
+// A CTA takes a token, with as many warps as leave each lane about four 16-byte pieces of the
+// row: its threads walk the row once for every B entries, U pieces at a time, so dY is read
 // from HBM once; the dot products are summed over lanes and warps in a fixed order.  Behind
 // the tokens, rows without an entry are zeroed.
-template <bool BF16>
+constexpr int kZeroRows = 4;                    // rows of the layout that a CTA looks at together
+
+template <bool BF16, int B, int U>
 __global__ void __launch_bounds__(kThreads) combine_f16_backward_kernel(RowsArgs a, const uint4* __restrict__ dY,
                                                                         const uint4* __restrict__ Ys, const float* __restrict__ W,
                                                                         uint4* __restrict__ dYs, float* __restrict__ dW) {
-  __shared__ float part[2][kWarps][kBatch];
+  __shared__ float part[2][kWarps][B];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5, warps = static_cast<int>(blockDim.x) >> 5;
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  const int threads = static_cast<int>(blockDim.x), warps = threads >> 5;
   const int vecs = a.H / 8;
   int turn = 0;
   for (int t = static_cast<int>(blockIdx.x); t < a.T; t += static_cast<int>(gridDim.x)) {
-    for (int j0 = 0; j0 < a.k; j0 += kBatch) {
-      int row[kBatch];
-      float w[kBatch], dot[kBatch];
+    for (int j0 = 0; j0 < a.k; j0 += B) {
+      int row[B];
+      float w[B], dot[B];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const long long entry = static_cast<long long>(t) * a.k + j0 + u;
-        row[u] = j0 + u < a.k ? load_row(a, entry) : -1;
-        w[u] = row[u] >= 0 ? ptx::ld_global(W + entry) : 0.0f;
-        dot[u] = 0.0f;
+      for (int b = 0; b < B; ++b) {
+        const long long entry = static_cast<long long>(t) * a.k + j0 + b;
+        row[b] = j0 + b < a.k ? load_row(a, entry) : -1;
+        w[b] = row[b] >= 0 ? ptx::ld_global(W + entry) : 0.0f;
+        dot[b] = 0.0f;
       }
-      for (int v = tid; v < vecs; v += static_cast<int>(blockDim.x)) {
-        float d[8];
-        const uint4 dv = ptx::ld_global_v4(dY + static_cast<size_t>(t) * vecs + v);
-        uint4 y[kBatch];
+      for (int v0 = tid; v0 < vecs; v0 += U * threads) {
+        uint4 dv[U], y[U][B];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-          if (row[u] >= 0) y[u] = ptx::ld_global_v4(Ys + static_cast<size_t>(row[u]) * vecs + v);
-        unpack16<BF16>(dv, d);
+        for (int u = 0; u < U; ++u) {
+          const int v = v0 + u * threads;
+          if (v < vecs) {
+            dv[u] = ptx::ld_global_v4(dY + static_cast<size_t>(t) * vecs + v);
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-          if (row[u] >= 0) {
-            float f[8], g[8];
-            unpack16<BF16>(y[u], f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              dot[u] = fmaf(d[i], f[i], dot[u]);
-              g[i] = w[u] * d[i];
-            }
-            st_global_v4(dYs + static_cast<size_t>(row[u]) * vecs + v, pack16(g, BF16));
+            for (int b = 0; b < B; ++b)
+              if (row[b] >= 0) y[u][b] = ptx::ld_global_v4(Ys + static_cast<size_t>(row[b]) * vecs + v);
           }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int v = v0 + u * threads;
+          if (v < vecs) {
+            float d[8];
+            unpack16<BF16>(dv[u], d);
+#pragma unroll
+            for (int b = 0; b < B; ++b)
+              if (row[b] >= 0) {
+                float f[8], g[8];
+                unpack16<BF16>(y[u][b], f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  dot[b] = fmaf(d[i], f[i], dot[b]);
+                  g[i] = w[b] * d[i];
+                }
+                st_global_v4(dYs + static_cast<size_t>(row[b]) * vecs + v, pack16(g, BF16));
+              }
+          }
+        }
       }
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
+      for (int b = 0; b < B; ++b) {
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) dot[u] += __shfl_xor_sync(kFull, dot[u], off);
-        if (lane == 0) part[turn][warp][u] = dot[u];
+        for (int off = 16; off > 0; off >>= 1) dot[b] += __shfl_xor_sync(kFull, dot[b], off);
+        if (lane == 0) part[turn][warp][b] = dot[b];
       }
       __syncthreads();
-      if (tid < kBatch && j0 + tid < a.k) {
+      if (tid < B && j0 + tid < a.k) {
         float s = 0.0f;
         for (int i = 0; i < warps; ++i) s += part[turn][i][tid];
         dW[static_cast<long long>(t) * a.k + j0 + tid] = s;
@@ -272,24 +389,27 @@ __global__ void __launch_bounds__(kThreads) combine_f16_backward_kernel(RowsArgs
     }
   }
   if (a.src == nullptr) return;
-  const int blocks = static_cast<int>((static_cast<long long>(a.M) + 31) / 32);
-  for (int b = static_cast<int>(blockIdx.x); b < blocks; b += static_cast<int>(gridDim.x))
-    for (uint32_t left = empty_rows(a, 32 * b, lane); left != 0; left &= left - 1) {
-      uint4* out = dYs + static_cast<size_t>(32 * b + __ffs(left) - 1) * vecs;
-      for (int v = tid; v < vecs; v += static_cast<int>(blockDim.x)) st_global_v4(out + v, make_uint4(0u, 0u, 0u, 0u));
+  const int blocks = static_cast<int>((static_cast<long long>(a.M) + kZeroRows - 1) / kZeroRows);
+  for (int b = static_cast<int>(blockIdx.x); b < blocks; b += static_cast<int>(gridDim.x)) {
+    const int r0 = kZeroRows * b;
+    const bool empty = lane < kZeroRows && r0 + lane < a.M && ptx::ld_global(a.src + r0 + lane) < 0;
+    for (uint32_t left = __ballot_sync(kFull, empty); left != 0; left &= left - 1) {
+      uint4* out = dYs + static_cast<size_t>(r0 + __ffs(left) - 1) * vecs;
+      for (int v = tid; v < vecs; v += threads) st_global_v4(out + v, make_uint4(0u, 0u, 0u, 0u));
     }
+  }
 }
 
 // ----------------------------------------------------------------- launches
-// Resident CTAs of a kernel on the current device.
+// Resident CTAs of a kernel on the current device, for a block size.
 template <typename... KArgs>
-int resident(void (*kernel)(KArgs...), PerDevice<int>& cache, int* ctas) {
+int resident(void (*kernel)(KArgs...), PerDevice<int>& cache, int threads, int* ctas) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= kMaxDevices) return set_error(2, "device id %d", dev);
   const int* n = nullptr;
   const int r = cache.get(dev, &n, [&](int& v) {
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kernel, kThreads, 0);
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kernel, threads, 0);
     if (e != cudaSuccess || v <= 0) return set_error(4, "dispatch occupancy: %s", cudaGetErrorString(e));
     v *= device_sm_count();
     return 0;
@@ -299,7 +419,7 @@ int resident(void (*kernel)(KArgs...), PerDevice<int>& cache, int* ctas) {
 }
 
 template <typename... KArgs, typename... Args>
-int launch(void (*kernel)(KArgs...), long long ctas, int threads, cudaStream_t stream, Args... args) {
+int launch(void (*kernel)(KArgs...), long long ctas, int threads, int smem, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cudaLaunchAttribute attr[1];
@@ -307,6 +427,7 @@ int launch(void (*kernel)(KArgs...), long long ctas, int threads, cudaStream_t s
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
   cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
@@ -318,18 +439,81 @@ int launch(void (*kernel)(KArgs...), long long ctas, int threads, cudaStream_t s
 template <typename... KArgs, typename... Args>
 int launch_items(void (*kernel)(KArgs...), PerDevice<int>& cache, long long items, cudaStream_t stream, Args... args) {
   int most = 0;
-  if (const int r = resident(kernel, cache, &most)) return r;
+  if (const int r = resident(kernel, cache, kThreads, &most)) return r;
   const long long ctas = (items + kWarps - 1) / kWarps;
-  return launch(kernel, ctas < most ? ctas : most, kThreads, stream, args...);
+  return launch(kernel, ctas < most ? ctas : most, kThreads, 0, stream, args...);
+}
+
+template <bool BF16, bool WEIGHTED, int B, int U>
+int launch_combine(const RowsArgs& a, const void* Ys, const float* W, void* Y, cudaStream_t stream) {
+  static PerDevice<int> cache;
+  const long long items = static_cast<long long>(a.T) * ((a.H / 8 + 32 * U - 1) / (32 * U));
+  return launch_items(combine_f16_kernel<BF16, WEIGHTED, B, U>, cache, items, stream, a, static_cast<const uint4*>(Ys), W,
+                      static_cast<uint4*>(Y));
+}
+
+template <bool BF16, bool WEIGHTED>
+int combine_by_k(const RowsArgs& a, const void* Ys, const float* W, void* Y, cudaStream_t stream) {
+  if (a.k <= 2) return launch_combine<BF16, WEIGHTED, 2, 2>(a, Ys, W, Y, stream);
+  if (a.k <= 4) return launch_combine<BF16, WEIGHTED, 4, 2>(a, Ys, W, Y, stream);
+  return launch_combine<BF16, WEIGHTED, 8, 1>(a, Ys, W, Y, stream);
+}
+
+template <bool BF16, int B, int U>
+int launch_backward(const RowsArgs& a, const void* dY, const void* Ys, const float* W, void* dYs, float* dW, cudaStream_t stream) {
+  static PerDevice<int> cache[kWarps];
+  // about four pieces per lane, in equal steps
+  const int vecs = a.H / 8, want = (vecs + 127) / 128, most = want < kWarps ? want : kWarps;
+  const int steps = (vecs + 32 * most - 1) / (32 * most), warps = (vecs + 32 * steps - 1) / (32 * steps);
+  auto* fn = combine_f16_backward_kernel<BF16, B, U>;
+  int ctas = 0;
+  if (const int r = resident(fn, cache[warps - 1], 32 * warps, &ctas)) return r;
+  const long long zero = a.src != nullptr ? (static_cast<long long>(a.M) + kZeroRows - 1) / kZeroRows : 0;
+  const long long work = zero > a.T ? zero : a.T;
+  return launch(fn, work < ctas ? work : ctas, 32 * warps, 0, stream, a, static_cast<const uint4*>(dY), static_cast<const uint4*>(Ys), W,
+                static_cast<uint4*>(dYs), dW);
+}
+
+template <bool BF16>
+int backward_by_k(const RowsArgs& a, const void* dY, const void* Ys, const float* W, void* dYs, float* dW, cudaStream_t stream) {
+  if (a.k == 1) return launch_backward<BF16, 1, 4>(a, dY, Ys, W, dYs, dW, stream);
+  if (a.k == 2) return launch_backward<BF16, 2, 2>(a, dY, Ys, W, dYs, dW, stream);
+  if (a.k <= 4) return launch_backward<BF16, 4, 2>(a, dY, Ys, W, dYs, dW, stream);
+  return launch_backward<BF16, 8, 1>(a, dY, Ys, W, dYs, dW, stream);
 }
 
 }  // namespace
 
 int launch_dispatch_f16(const RowsArgs& a, const void* X, void* Xs, cudaStream_t stream) {
-  static PerDevice<int> cache;
-  const long long parts = (a.H / 8 + 32 * kPart - 1) / (32 * kPart);
-  const long long rows = a.T + (a.src != nullptr ? (static_cast<long long>(a.M) + 31) / 32 : 0);
-  return launch_items(dispatch_f16_kernel, cache, rows * parts, stream, a, static_cast<const uint4*>(X), static_cast<uint4*>(Xs));
+  constexpr int kRoom = 230000;                             // of 232448 bytes of shared memory, less the barriers
+  static PerDevice<int> ready;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= kMaxDevices) return set_error(2, "device id %d", dev);
+  const int* set = nullptr;
+  const int r = ready.get(dev, &set, [&](int& v) {
+    v = kRoom;
+    const cudaError_t e = cudaFuncSetAttribute(dispatch_f16_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom);
+    return e == cudaSuccess ? 0 : set_error(4, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  });
+  if (r) return r;
+  BulkArgs b;
+  b.a = a;
+  b.timeout_ns = wait_timeout_ns();
+  const long long row_bytes = 2LL * a.H, pieces = (row_bytes + kMaxPiece - 1) / kMaxPiece;
+  b.row_bytes = row_bytes;
+  b.pieces = static_cast<int>(pieces);
+  b.piece = static_cast<int>(((row_bytes + pieces - 1) / pieces + 15) / 16 * 16);
+  const int smem = b.piece * (1 + kBulkWarps * kStages);
+  const long long per_sm = (kRoom + 2048) / (smem + 2048);
+  const long long most = (per_sm < 4 ? per_sm : 4) * device_sm_count();
+  // few rows are spread over all warps
+  const long long items = a.T * pieces, rows = a.src != nullptr ? a.M : 0;
+  b.zero_rows = 32;
+  while (b.zero_rows > 1 && rows / b.zero_rows < 2 * kBulkWarps * most) b.zero_rows /= 2;
+  const long long blocks = (rows + b.zero_rows - 1) / b.zero_rows, work = items > blocks ? items : blocks;
+  return launch(dispatch_f16_kernel, work < most ? work : most, kBulkThreads, smem, stream, b, static_cast<const uint8_t*>(X),
+                static_cast<uint8_t*>(Xs));
 }
 
 int launch_dispatch_fp8(const RowsArgs& a, const void* X, void* Xq, void* SFA, int fmt, cudaStream_t stream) {
@@ -340,26 +524,13 @@ int launch_dispatch_fp8(const RowsArgs& a, const void* X, void* Xq, void* SFA, i
 }
 
 int launch_combine_f16(const RowsArgs& a, const void* Ys, const float* W, void* Y, int bf16, cudaStream_t stream) {
-  static PerDevice<int> cache[4];
-  const long long items = static_cast<long long>(a.T) * ((a.H / 8 + 31) / 32);
-  auto* fn = W != nullptr ? (bf16 ? combine_f16_kernel<true, true> : combine_f16_kernel<false, true>)
-                          : (bf16 ? combine_f16_kernel<true, false> : combine_f16_kernel<false, false>);
-  return launch_items(fn, cache[(bf16 ? 1 : 0) + (W != nullptr ? 2 : 0)], items, stream, a, static_cast<const uint4*>(Ys), W,
-                      static_cast<uint4*>(Y));
+  if (W != nullptr) return bf16 ? combine_by_k<true, true>(a, Ys, W, Y, stream) : combine_by_k<false, true>(a, Ys, W, Y, stream);
+  return bf16 ? combine_by_k<true, false>(a, Ys, W, Y, stream) : combine_by_k<false, false>(a, Ys, W, Y, stream);
 }
 
 int launch_combine_f16_backward(const RowsArgs& a, const void* dY, const void* Ys, const float* W, void* dYs, float* dW,
                                 int bf16, cudaStream_t stream) {
-  static PerDevice<int> cache[2];
-  auto* fn = bf16 ? combine_f16_backward_kernel<true> : combine_f16_backward_kernel<false>;
-  int most = 0;
-  if (const int r = resident(fn, cache[bf16 ? 1 : 0], &most)) return r;
-  // as few threads as walk the row in the same number of steps
-  const int vecs = a.H / 8, steps = (vecs + kThreads - 1) / kThreads;
-  const int threads = ((vecs + steps - 1) / steps + 31) / 32 * 32;
-  const long long work = a.src != nullptr && (a.M + 31LL) / 32 > a.T ? (a.M + 31LL) / 32 : a.T;
-  return launch(fn, work < most ? work : most, threads, stream, a, static_cast<const uint4*>(dY), static_cast<const uint4*>(Ys), W,
-                static_cast<uint4*>(dYs), dW);
+  return bf16 ? backward_by_k<true>(a, dY, Ys, W, dYs, dW, stream) : backward_by_k<false>(a, dY, Ys, W, dYs, dW, stream);
 }
 
 }  // namespace fgf8

@@ -7,13 +7,15 @@
 //
 // One launch of one cluster.  A CTA takes a run of entries, each of its warps a run of
 // those, so that (CTA, warp, step, lane) is the flat order and the ranks do not depend on
-// timing.  A warp counts its run into its own row of a histogram in shared memory
-// (__match_any_sync: the lanes of one id are counted by one of them, without atomics), the
+// timing.  A warp counts its run into its own row of a histogram in shared memory, the
 // rows are summed over warps, the sums over CTAs through distributed shared memory, and a
-// second walk hands out the rows.  Every CTA scans the groups' counts for itself.  One
-// cluster instead of the whole GPU: the ids of 8192 tokens with 8 experts are 256 KB, and
-// a barrier across a cluster is a hardware barrier, while one across the grid would be a
-// second launch.
+// second walk hands out the rows: the lanes of one id are found by a ballot for each of its
+// bits (__match_any_sync takes longer from some ten thousand entries on).  Every CTA scans the groups' counts for itself.  m_indices
+// follows from the counts alone and is written in row order; src is the only scattered
+// output.  One cluster instead of the whole GPU: the ids of 8192 tokens with 8 experts are
+// 256 KB, and a barrier across a cluster is a hardware barrier, while one across the grid
+// would be a second launch.  Bound by instruction issue on those SMs: 8.6 us at 8192 x 8 ids
+// of 32 groups, 5 % of the dispatch that follows.
 #include <cstring>
 
 #include "gemm_persistent.cuh"
@@ -23,7 +25,12 @@
 namespace fgf8 {
 namespace {
 
-constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kMaxThreads = 1024, kMaxWarps = kMaxThreads / 32;
+constexpr int kMaxCluster = 16;                             // where the device fits so many, else kPortableCluster
+constexpr int kPortableCluster = 8;
+constexpr int kAhead = 4;                                   // steps of ids that a warp loads together
+constexpr int kChunk = 128;                                 // rows of the layout that a warp fills together
+constexpr uint32_t kFull = 0xFFFFFFFFu;
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   uint32_t v;
@@ -34,6 +41,18 @@ __device__ __forceinline__ long long ld_global_s64(const void* p) {
   long long v;
   asm volatile("ld.global.s64 %0, [%1];" : "=l"(v) : "l"(p));
   return v;
+}
+
+// Lanes of the warp with the same id (-1 .. G - 1); `bits` bits of id + 1 hold G.
+__device__ __forceinline__ uint32_t same_id(int id, int bits) {
+  const uint32_t key = static_cast<uint32_t>(id + 1);
+  uint32_t same = kFull;
+  for (int b = 0; b < bits; ++b) {
+    const bool one = (key >> b) & 1u;
+    const uint32_t ones = __ballot_sync(kFull, one);
+    same &= one ? ones : ~ones;
+  }
+  return same;
 }
 
 // The group of entry i, -1 for none and for what is out of range.
@@ -51,49 +70,57 @@ __device__ __forceinline__ int load_id(const RouteArgs& a, int i, int end, bool&
 }
 
 template <bool IDS64>
-__global__ void __launch_bounds__(kThreads, 1) route_kernel(RouteArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, 1) route_kernel(RouteArgs a) {
   extern __shared__ int32_t smem[];
-  const int G = a.G, S = static_cast<int>(gridDim.x);       // the grid is one cluster
-  int32_t* hist = smem;                                     // [warp][G]
-  int32_t* total = hist + kWarps * G;                       // [G] this CTA's counts
+  const int G = a.G, Gs = G | 1;                            // an odd row length: warps read a column without conflicts
+  const int S = static_cast<int>(gridDim.x);                // the grid is one cluster
+  const int threads = static_cast<int>(blockDim.x), W = threads >> 5;
+  int32_t* hist = smem;                                     // [warp][Gs]
+  int32_t* total = hist + W * Gs;                           // [G] this CTA's counts
   int32_t* first = total + G;                               // [G + 1] first row of each group
-  int32_t* count = first + G + 1;                           // [G] counts over all CTAs
-  __shared__ int32_t warp_sum[kWarps];
+  int32_t* base = first + G + 1;                            // [G] row of this CTA's first entry of each group (masked: its rank)
+  int32_t* count = base + G;                                // [G] entries with a row, over all CTAs
+  __shared__ int32_t warp_sum[kMaxWarps];
+  const int bits = 32 - __clz(G), top = 1 << (bits - 1);    // of G, and the highest power of two up to it
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(cluster_rank());
-  for (int i = tid; i < kWarps * G; i += kThreads) hist[i] = 0;
+  for (int i = tid; i < W * Gs; i += threads) hist[i] = 0;
   ptx::griddep_wait();                                      // ids may come from the previous kernel
   ptx::griddep_launch_dependents();
   __syncthreads();
 
   // this warp's run of entries, whole steps of 32
   const long long steps = (static_cast<long long>(a.n) + 31) / 32;
-  const long long per = (steps + S * kWarps - 1) / (S * kWarps);
-  const long long lo = (static_cast<long long>(rank) * kWarps + warp) * per * 32;
+  const long long per = (steps + S * W - 1) / (S * W);
+  const long long lo = (static_cast<long long>(rank) * W + warp) * per * 32;
   const int begin = static_cast<int>(lo < a.n ? lo : a.n);
   const int end = static_cast<int>(lo + per * 32 < a.n ? lo + per * 32 : a.n);
-  int32_t* mine = hist + warp * G;
+  int32_t* mine = hist + warp * Gs;
   bool bad = false;
-  for (int i0 = begin; i0 < end; i0 += 32) {
-    const int id = load_id<IDS64>(a, i0 + lane, end, bad);
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, id);
-    if (id >= 0 && (same & ((1u << lane) - 1u)) == 0) mine[id] += __popc(same);
-    __syncwarp();
+  for (int i0 = begin; i0 < end; i0 += 32 * kAhead) {
+    int id[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) id[u] = load_id<IDS64>(a, i0 + 32 * u + lane, end, bad);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (id[u] >= 0) atomicAdd(mine + id[u], 1);
   }
   if (bad) atomicOr(a.status, FGF8_DEVERR_INPUT);
   __syncthreads();
 
-  // counts of this CTA, and each warp's offset within them
-  for (int g = tid; g < G; g += kThreads) {
-    int32_t sum = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      const int32_t c = hist[w * G + g];
-      hist[w * G + g] = sum;
-      sum += c;
+  // counts of this CTA, and each warp's offset within them: a warp per group, a lane per warp
+  for (int g = warp; g < G; g += W) {
+    const int32_t c = lane < W ? hist[lane * Gs + g] : 0;
+    int32_t scan = c;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int32_t v = __shfl_up_sync(kFull, scan, off);
+      if (lane >= off) scan += v;
     }
-    total[g] = sum;
+    if (lane < W) hist[lane * Gs + g] = scan - c;
+    if (lane == 31) total[g] = scan;
   }
-  cluster_sync_all();
+  if (S > 1) cluster_sync_all(); else __syncthreads();
   int32_t before = 0, all = 0;                              // of group tid: entries of earlier CTAs, of all
   if (tid < G) {
     const uint32_t at = ptx::smem_u32(total + tid);
@@ -102,27 +129,27 @@ __global__ void __launch_bounds__(kThreads, 1) route_kernel(RouteArgs a) {
       if (r < rank) before += c;
       all += c;
     }
-    count[tid] = all;
   }
   // first rows: an exclusive prefix sum of the padded counts, one group per thread
-  const int32_t padded = a.slots > 0 ? 0 : (all + a.align - 1) / a.align * a.align;
-  int32_t scan = padded;
+  const int32_t padded = a.slots > 0 ? a.slots : (all + a.align - 1) / a.align * a.align;
+  const int32_t held = a.slots > 0 && all > a.slots ? a.slots : all;
+  int32_t scan = tid < G ? padded : 0;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const int32_t v = __shfl_up_sync(0xFFFFFFFFu, scan, off);
+    const int32_t v = __shfl_up_sync(kFull, scan, off);
     if (lane >= off) scan += v;
   }
   if (lane == 31) warp_sum[warp] = scan;
   __syncthreads();
-  int32_t start = scan - padded;
-  for (int w = 0; w < warp; ++w) start += warp_sum[w];
-  if (tid < G) first[tid] = a.slots > 0 ? tid * a.slots : start;
-  if (tid == G - 1) first[G] = a.slots > 0 ? G * a.slots : start + padded;
   if (tid < G) {
-    const int32_t base = a.slots > 0 ? before : start + before;
-    for (int w = 0; w < kWarps; ++w) hist[w * G + tid] += base;
+    int32_t start = scan - padded;
+    for (int w = 0; w < warp; ++w) start += warp_sum[w];
+    first[tid] = start;
+    if (tid == G - 1) first[G] = start + padded;
+    base[tid] = a.slots > 0 ? before : start + before;
+    count[tid] = held;
     if (rank == 0) {
-      a.counts[tid] = a.slots > 0 && all > a.slots ? a.slots : all;
+      a.counts[tid] = held;
       if (a.starts != nullptr) {
         a.starts[tid] = start;
         if (tid == G - 1) a.starts[G] = start + padded;
@@ -132,72 +159,99 @@ __global__ void __launch_bounds__(kThreads, 1) route_kernel(RouteArgs a) {
   __syncthreads();
 
   // the entries' rows
-  for (int i0 = begin; i0 < end; i0 += 32) {
+  for (int i0 = begin; i0 < end; i0 += 32 * kAhead) {
+    int id[kAhead];
     bool ignored = false;
-    const int i = i0 + lane, id = load_id<IDS64>(a, i, end, ignored);
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, id);
-    const uint32_t earlier = same & ((1u << lane) - 1u);
-    int32_t row = -1;
-    if (id >= 0) row = mine[id] + __popc(earlier);
-    __syncwarp();
-    if (id >= 0 && earlier == 0) mine[id] += __popc(same);
-    __syncwarp();
-    if (a.slots > 0 && id >= 0) row = row < a.slots ? id * a.slots + row : -1;
-    if (i < end) {
-      a.rows[i] = row;
-      if (row >= 0) {
-        a.src[row] = i;
-        if (a.m_indices != nullptr) a.m_indices[row] = id;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) id[u] = load_id<IDS64>(a, i0 + 32 * u + lane, end, ignored);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (i0 + 32 * u >= end) break;
+      const int i = i0 + 32 * u + lane;
+      const uint32_t same = same_id(id[u], bits), earlier = same & ((1u << lane) - 1u);
+      int32_t row = -1;
+      if (id[u] >= 0) row = base[id[u]] + mine[id[u]] + __popc(earlier);
+      __syncwarp();
+      if (id[u] >= 0 && earlier == 0) mine[id[u]] += __popc(same);
+      __syncwarp();
+      if (a.slots > 0 && id[u] >= 0) row = row < a.slots ? id[u] * a.slots + row : -1;
+      if (i < end) {
+        a.rows[i] = row;
+        if (row >= 0) a.src[row] = i;
       }
     }
   }
-  // rows without an entry: behind each group's, and behind the last group
-  for (int g = rank * kWarps + warp; g <= G; g += S * kWarps) {
-    const int32_t stop = g < G ? first[g + 1] : a.M;
-    const int32_t held = g < G ? (a.slots > 0 && count[g] > a.slots ? a.slots : count[g]) : 0;
-    for (int32_t row = first[g] + held + lane; row < stop; row += 32) {
-      a.src[row] = -1;
-      if (a.m_indices != nullptr) a.m_indices[row] = -1;
+  // m_indices, and src of the rows without an entry, in row order, kChunk rows to a warp
+  for (long long r0 = (static_cast<long long>(warp) * S + rank) * kChunk; r0 < a.M; r0 += static_cast<long long>(S) * W * kChunk) {
+    int g = 0;                                              // the last group that begins at or before r0
+    for (int half = top; half > 0; half >>= 1)
+      if (g + half <= G && first[g + half] <= r0) g += half;
+#pragma unroll
+    for (int u = 0; u < kChunk / 32; ++u) {
+      const int32_t row = static_cast<int32_t>(r0) + 32 * u + lane;
+      if (row >= a.M) break;
+      while (g < G && first[g + 1] <= row) ++g;
+      const bool owned = g < G && row - first[g] < count[g];
+      if (a.m_indices != nullptr) a.m_indices[row] = owned ? g : -1;
+      if (!owned) a.src[row] = -1;
     }
   }
-  cluster_sync_all();                                       // stay until every CTA has read the counts
+  if (S > 1) cluster_sync_all();                            // stay until every CTA has read the counts
 }
 
-constexpr int kMaxCluster = 8;
+size_t smem_bytes(int G, int warps) { return sizeof(int32_t) * (static_cast<size_t>(warps) * (G | 1) + 4 * static_cast<size_t>(G) + 1); }
+
+struct RouteLaunch {
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  RouteLaunch(int ctas, int threads, size_t smem, cudaStream_t stream, bool pdl) {
+    std::memset(&cfg, 0, sizeof(cfg));
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 2 : 1;
+  }
+};
 
 template <bool IDS64>
 int launch(const RouteArgs& a, cudaStream_t stream) {
   auto* fn = &route_kernel<IDS64>;
-  const size_t smem = sizeof(int32_t) * (static_cast<size_t>(kWarps + 3) * a.G + 1);
-  static PerDevice<int> ready;
+  static PerDevice<int> most;                               // CTAs of the largest cluster that the device fits
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= kMaxDevices) return set_error(2, "device id %d", dev);
-  const int* set = nullptr;
-  const int r = ready.get(dev, &set, [&](int& v) {
-    v = static_cast<int>(sizeof(int32_t)) * ((kWarps + 3) * kRouteMaxGroups + 1);
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v);
-    return e == cudaSuccess ? 0 : set_error(4, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  const int* fit = nullptr;
+  const int r = most.get(dev, &fit, [&](int& v) {
+    const size_t smem = smem_bytes(kRouteMaxGroups, kMaxWarps);
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    int clusters = 0;
+    if (e == cudaSuccess) {
+      RouteLaunch l(kMaxCluster, kMaxThreads, smem, nullptr, false);
+      e = cudaOccupancyMaxActiveClusters(&clusters, fn, &l.cfg);
+    }
+    if (e != cudaSuccess) return set_error(4, "route set-up: %s", cudaGetErrorString(e));
+    v = clusters > 0 ? kMaxCluster : kPortableCluster;
+    return 0;
   });
   if (r) return r;
-  cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof(cfg));
-  cudaLaunchAttribute attr[2];
-  // one CTA walks up to four steps per warp alone; past that a cluster shares them
-  const unsigned ctas = a.n <= 4 * kThreads ? 1u : static_cast<unsigned>(kMaxCluster);
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(ctas, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, a);
+  // one CTA where entries and rows are few, else a cluster.  One against eight: 3.1 and 3.8 us at
+  // 1 x 8 ids of 32 groups (1024 rows), 3.3 and 4.1 at 331 x 2 of 8 (1536 rows), 4.6 and 4.0 at
+  // 64 x 8 of 32 (4480 rows).  Eight against sixteen: 15.0 and 9.9 us at 8192 x 8.
+  int threads = a.n < kMaxThreads ? (a.n + 31) / 32 * 32 : kMaxThreads;
+  if (threads < a.G) threads = (a.G + 31) / 32 * 32;
+  if (threads < 256) threads = 256;
+  const int ctas = static_cast<long long>(a.n) + a.M <= 4096 ? 1 : a.n <= 8192 ? kPortableCluster : *fit;
+  RouteLaunch l(ctas, threads, smem_bytes(a.G, threads / 32), stream, pdl_enabled());
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, fn, a);
   return e == cudaSuccess ? 0 : set_error(4, "route launch: %s", cudaGetErrorString(e));
 }
 
