@@ -69,7 +69,7 @@ _SIGS = {
     "combine_f16": ([_P] * 4 + [_I] * 5 + [_P], _I),
     "combine_f16_backward": ([_P] * 7 + [_I] * 5 + [_P], _I),
     "dispatch_f16_backward": ([_P] * 3 + [_I] * 5 + [_P], _I),
-    "lora_f16": ([_P] * 9 + [_I] * 6 + [_LL] * 3 + [_I, _P], _I),
+    "lora_f16": ([_P] * 9 + [_I] * 7 + [_LL] * 3 + [_I, _P], _I),
     "fgf8_route_rows": ([_I] * 4, _LL),
     "fgf8_gated_backward_ws_bytes": ([_I, _I], _LL),
     "fgf8_fp4_sf_bytes": ([_I, _I, _I], _LL),
@@ -742,7 +742,8 @@ def lora_f16(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, route: Route, sc
     """out[t] = base[t] + scale[g] (X[t] A[g]^T) B[g]^T with g the adapter of token t, in one kernel.
     x (T, K), a (G, r, K), b (G, N, r), base and out (T, N) are fp16/bf16, r a multiple of 8 up to
     128, scale float32 (G,) (None: ones).  route: route_contiguous(adapter ids (T,), G, align)
-    with align a multiple of 16; one serves every layer of a step.  Tokens without an adapter
+    with align a multiple of 16 (128 where adapters have some 64 tokens and more each, 16 for
+    fewer); one serves every layer of a step.  Tokens without an adapter
     get base (None: zeros).  out may be base.  Rows of x, base and out may be columns of wider
     matrices."""
     T, K = x.shape
@@ -767,7 +768,7 @@ def lora_f16(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, route: Route, sc
     ldo = _need_strided(out, (T, N), dtype, "out")
     ldb = _need_strided(base, (T, N), dtype, "base") if base is not None else 0
     _launch("lora_f16", stream, (x, a, b, scale, base, route.rows, route.src, route.m_indices, out),
-            (T, K, N, r, G, M, ldx, ldb, ldo, code), strided=(0, 4, 8))
+            (T, K, N, r, G, M, route.align, ldx, ldb, ldo, code), strided=(0, 4, 8))
     return out
 
 

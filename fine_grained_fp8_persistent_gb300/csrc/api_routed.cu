@@ -148,7 +148,7 @@ int combine_f16_backward(const void* dY, const void* Ys, const float* W, const i
 }
 
 int lora_f16(const void* X, const void* A, const void* B, const float* scale, const void* base, const int32_t* rows,
-             const int32_t* src, const int32_t* m_indices, void* out, int T, int K, int N, int r, int G, int M,
+             const int32_t* src, const int32_t* m_indices, void* out, int T, int K, int N, int r, int G, int M, int align,
              long long ldx, long long ldb, long long ldo, int dtype, void* stream) {
   const char* who = "lora_f16";
   if (int e = check_rows(who, T, 1, K, M, 8)) return e;
@@ -156,7 +156,8 @@ int lora_f16(const void* X, const void* A, const void* B, const float* scale, co
   if (int e = check_dtype(who, dtype)) return e;
   if (r < 1 || G < 1) return set_error(FGF8_ERR_INVALID_ARG, "%s: r=%d G=%d", who, r, G);
   if (r % 8 != 0 || r > 128) return set_error(FGF8_ERR_UNSUPPORTED, "%s: rank %d not a multiple of 8 up to 128", who, r);
-  if (M % 16 != 0) return set_error(FGF8_ERR_UNSUPPORTED, "%s: M=%d not a multiple of 16", who, M);
+  if (align < 16 || align % 16 != 0) return set_error(FGF8_ERR_UNSUPPORTED, "%s: align=%d not a multiple of 16", who, align);
+  if (M % align != 0) return set_error(FGF8_ERR_INVALID_ARG, "%s: M=%d not a multiple of align=%d", who, M, align);
   if (ldx < K || ldo < N || (base != nullptr && ldb < N))
     return set_error(FGF8_ERR_INVALID_ARG, "%s: rows of X, base and out are %lld, %lld and %lld apart", who, ldx, ldb, ldo);
   if (ldx % 8 != 0 || ldo % 8 != 0 || (base != nullptr && ldb % 8 != 0))
@@ -166,7 +167,7 @@ int lora_f16(const void* X, const void* A, const void* B, const float* scale, co
   if (int e = check_pointers(who, {X, A, B, when(scale != nullptr, scale, X), when(base != nullptr, base, X), rows,
                                    when(M > 0, src, X), when(M > 0, m_indices, X), out}))
     return e;
-  fgf8::LoraArgs a{X, A, B, scale, base, out, rows, src, m_indices, ldx, ldb, ldo, T, K, N, r, G, M, nullptr};
+  fgf8::LoraArgs a{X, A, B, scale, base, out, rows, src, m_indices, ldx, ldb, ldo, T, K, N, r, G, M, align, nullptr};
   if (int e = status_word(who, &a.status)) return e;
   return fgf8::launch_lora_f16(a, dtype == FGF8_BF16, static_cast<cudaStream_t>(stream));
 }

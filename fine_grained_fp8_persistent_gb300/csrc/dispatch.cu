@@ -79,23 +79,48 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t byt
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
 
+// Rows without an entry, from a piece of zeros in shared memory: a lane looks at one row, a
+// warp at `rows` of them (up to 32; few rows are spread over all warps).
+constexpr int kZeroBytes = 4096;
+
+__device__ __forceinline__ void clear_piece(uint4* zeros) {  // before a __syncthreads
+  for (int i = static_cast<int>(threadIdx.x); i < kZeroBytes / 16; i += static_cast<int>(blockDim.x)) zeros[i] = make_uint4(0u, 0u, 0u, 0u);
+  ptx::fence_proxy_async_smem();
+}
+__device__ __forceinline__ void fill_empty_rows(const RowsArgs& a, uint8_t* out, const uint4* zeros, uint32_t rows, uint32_t first, uint32_t step) {
+  const uint32_t lane = threadIdx.x & 31, M = static_cast<uint32_t>(a.M), src = ptx::smem_u32(zeros);
+  const size_t row_bytes = 2 * static_cast<size_t>(a.H);
+  for (uint32_t r0 = first * rows; r0 < M; r0 += step * rows)
+    if (lane < rows && r0 + lane < M && ptx::ld_global(a.src + r0 + lane) < 0) {
+      uint8_t* row = out + (r0 + lane) * row_bytes;
+      for (size_t b = 0; b < row_bytes; b += kZeroBytes)
+        bulk_store(row + b, src, static_cast<uint32_t>(row_bytes - b < kZeroBytes ? row_bytes - b : kZeroBytes));
+    }
+  ptx::bulk_commit_group();
+}
+// The number for a grid with that many warps.
+inline int zero_rows(const RowsArgs& a, long long warps) {
+  int rows = 32;
+  while (rows > 1 && a.M / rows < 2 * warps) rows /= 2;
+  return rows;
+}
+
 __global__ void __launch_bounds__(kBulkThreads) dispatch_f16_kernel(BulkArgs args, const uint8_t* __restrict__ X,
                                                                 uint8_t* __restrict__ Xs) {
-  extern __shared__ __align__(128) uint8_t smem[];          // [zeros][warp][stage], args.piece bytes each
+  extern __shared__ __align__(128) uint8_t smem[];          // [warp][stage], args.piece bytes each
+  __shared__ __align__(16) uint4 zeros[kZeroBytes / 16];
   __shared__ uint64_t bars[kBulkWarps * kStages];
   __shared__ volatile uint32_t abort_word;
   const RowsArgs& a = args.a;
   const int lane = static_cast<int>(threadIdx.x & 31), warp = static_cast<int>(threadIdx.x >> 5);
-  const uint32_t zeros = ptx::smem_u32(smem), ring = zeros + static_cast<uint32_t>(args.piece * (1 + warp * kStages));
+  const uint32_t ring = ptx::smem_u32(smem) + static_cast<uint32_t>(args.piece * warp * kStages);
   auto full = [&](int s) { return ptx::smem_u32(&bars[warp * kStages + s]); };
   if (threadIdx.x == 0) abort_word = 0u;
   if (lane == 0) {
     for (int s = 0; s < kStages; ++s) ptx::mbar_init(full(s), 1);
     ptx::fence_mbar_init();
   }
-  for (int i = static_cast<int>(threadIdx.x); i < args.piece / 16; i += kBulkThreads)
-    reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
-  ptx::fence_proxy_async_smem();                            // the stores below read it
+  clear_piece(zeros);
   __syncthreads();
   ptx::griddep_wait();                                      // everything may come from the previous kernel
   ptx::griddep_launch_dependents();
@@ -142,16 +167,7 @@ __global__ void __launch_bounds__(kBulkThreads) dispatch_f16_kernel(BulkArgs arg
       phase ^= 1u;
     }
   }
-  if (ok && a.src != nullptr) {
-    const uint32_t M = static_cast<uint32_t>(a.M), R = static_cast<uint32_t>(args.zero_rows);
-    for (uint32_t r0 = first * R; r0 < M; r0 += step * R) {
-      const uint32_t row = r0 + lane;
-      if (lane < args.zero_rows && row < M && ptx::ld_global(a.src + row) < 0)
-        for (uint32_t p = 0; p < now.parts; ++p)
-          bulk_store(Xs + static_cast<size_t>(row) * args.row_bytes + static_cast<size_t>(p) * args.piece, zeros, bytes_of(p));
-    }
-    ptx::bulk_commit_group();
-  }
+  if (ok && a.src != nullptr) fill_empty_rows(a, Xs, zeros, static_cast<uint32_t>(args.zero_rows), first, step);
   ptx::bulk_wait_group<0>();
   // after a wait that ran out, loads may still be under way into this shared memory
   if (__syncthreads_or(abort_word != 0u ? 1 : 0)) {
@@ -316,13 +332,16 @@ __global__ void __launch_bounds__(kThreads, B == 4 ? 3 : 4) combine_f16_kernel(R
 // row: its threads walk the row once for every B entries, U pieces at a time, so dY is read
 // from HBM once; the dot products are summed over lanes and warps in a fixed order.  Behind
 // the tokens, rows without an entry are zeroed.
-constexpr int kZeroRows = 4;                    // rows of the layout that a CTA looks at together
-
 template <bool BF16, int B, int U>
 __global__ void __launch_bounds__(kThreads) combine_f16_backward_kernel(RowsArgs a, const uint4* __restrict__ dY,
                                                                         const uint4* __restrict__ Ys, const float* __restrict__ W,
-                                                                        uint4* __restrict__ dYs, float* __restrict__ dW) {
+                                                                        uint4* __restrict__ dYs, float* __restrict__ dW, int zero_rows) {
   __shared__ float part[2][kWarps][B];
+  __shared__ __align__(16) uint4 zeros[kZeroBytes / 16];
+  if (a.src != nullptr) {
+    clear_piece(zeros);
+    __syncthreads();
+  }
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
@@ -389,15 +408,8 @@ __global__ void __launch_bounds__(kThreads) combine_f16_backward_kernel(RowsArgs
     }
   }
   if (a.src == nullptr) return;
-  const int blocks = static_cast<int>((static_cast<long long>(a.M) + kZeroRows - 1) / kZeroRows);
-  for (int b = static_cast<int>(blockIdx.x); b < blocks; b += static_cast<int>(gridDim.x)) {
-    const int r0 = kZeroRows * b;
-    const bool empty = lane < kZeroRows && r0 + lane < a.M && ptx::ld_global(a.src + r0 + lane) < 0;
-    for (uint32_t left = __ballot_sync(kFull, empty); left != 0; left &= left - 1) {
-      uint4* out = dYs + static_cast<size_t>(r0 + __ffs(left) - 1) * vecs;
-      for (int v = tid; v < vecs; v += threads) st_global_v4(out + v, make_uint4(0u, 0u, 0u, 0u));
-    }
-  }
+  fill_empty_rows(a, reinterpret_cast<uint8_t*>(dYs), zeros, static_cast<uint32_t>(zero_rows), warp * gridDim.x + blockIdx.x, warps * gridDim.x);
+  ptx::bulk_wait_group<0>();
 }
 
 // ----------------------------------------------------------------- launches
@@ -468,10 +480,11 @@ int launch_backward(const RowsArgs& a, const void* dY, const void* Ys, const flo
   auto* fn = combine_f16_backward_kernel<BF16, B, U>;
   int ctas = 0;
   if (const int r = resident(fn, cache[warps - 1], 32 * warps, &ctas)) return r;
-  const long long zero = a.src != nullptr ? (static_cast<long long>(a.M) + kZeroRows - 1) / kZeroRows : 0;
-  const long long work = zero > a.T ? zero : a.T;
+  const int zero = zero_rows(a, static_cast<long long>(ctas) * warps);
+  const long long blocks = a.src != nullptr ? (a.M + static_cast<long long>(zero) * warps - 1) / (zero * warps) : 0;
+  const long long work = blocks > a.T ? blocks : a.T;
   return launch(fn, work < ctas ? work : ctas, 32 * warps, 0, stream, a, static_cast<const uint4*>(dY), static_cast<const uint4*>(Ys), W,
-                static_cast<uint4*>(dYs), dW);
+                static_cast<uint4*>(dYs), dW, zero);
 }
 
 template <bool BF16>
@@ -485,7 +498,7 @@ int backward_by_k(const RowsArgs& a, const void* dY, const void* Ys, const float
 }  // namespace
 
 int launch_dispatch_f16(const RowsArgs& a, const void* X, void* Xs, cudaStream_t stream) {
-  constexpr int kRoom = 230000;                             // of 232448 bytes of shared memory, less the barriers
+  constexpr int kRoom = 226000;                             // of 232448 bytes of shared memory, less what is static
   static PerDevice<int> ready;
   int dev = 0;
   cudaGetDevice(&dev);
@@ -504,14 +517,12 @@ int launch_dispatch_f16(const RowsArgs& a, const void* X, void* Xs, cudaStream_t
   b.row_bytes = row_bytes;
   b.pieces = static_cast<int>(pieces);
   b.piece = static_cast<int>(((row_bytes + pieces - 1) / pieces + 15) / 16 * 16);
-  const int smem = b.piece * (1 + kBulkWarps * kStages);
-  const long long per_sm = (kRoom + 2048) / (smem + 2048);
+  const int smem = b.piece * kBulkWarps * kStages;
+  const long long per_sm = (kRoom + 6000) / (smem + 6000);
   const long long most = (per_sm < 4 ? per_sm : 4) * device_sm_count();
-  // few rows are spread over all warps
-  const long long items = a.T * pieces, rows = a.src != nullptr ? a.M : 0;
-  b.zero_rows = 32;
-  while (b.zero_rows > 1 && rows / b.zero_rows < 2 * kBulkWarps * most) b.zero_rows /= 2;
-  const long long blocks = (rows + b.zero_rows - 1) / b.zero_rows, work = items > blocks ? items : blocks;
+  b.zero_rows = zero_rows(a, kBulkWarps * most);
+  const long long items = a.T * pieces, blocks = a.src != nullptr ? (a.M + b.zero_rows - 1LL) / b.zero_rows : 0;
+  const long long work = items > blocks ? items : blocks;
   return launch(dispatch_f16_kernel, work < most ? work : most, kBulkThreads, smem, stream, b, static_cast<const uint8_t*>(X),
                 static_cast<uint8_t*>(Xs));
 }

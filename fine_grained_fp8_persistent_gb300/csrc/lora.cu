@@ -31,6 +31,7 @@ namespace fgf8 {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
 struct LoraKArgs {
@@ -69,6 +70,72 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   }
   hi = pack_2x16(h[0], h[1], BF16);
   lo = pack_2x16(l[0], l[1], BF16);
+}
+
+// P from the sums over the shares of K: each CTA of the cluster sums every C-th row of `part`
+// over all of them, a warp per row, and hands value, rest and power to all of them.
+template <bool BF16, int RP>
+__device__ __forceinline__ void exchange_rows(const float* part, uint16_t* hi, uint16_t* lo, float* power, int rows, const float* scale_of,
+                                              int scale_rows, int C, int rank) {
+  constexpr int LDP = RP + 4, LDH = RP + 8;
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  for (int row = rank + C * warp; row < rows; row += C * kWarps) {
+    const float scale = scale_of[row / scale_rows];
+    constexpr int PAIRS = (RP + 63) / 64;
+    float2 v[PAIRS];
+    float top = 0.0f;
+#pragma unroll
+    for (int u = 0; u < PAIRS; ++u) {
+      const int col = 2 * (lane + 32 * u);
+      v[u] = make_float2(0.0f, 0.0f);
+      if (col < RP) {
+        const uint32_t at = ptx::smem_u32(part + row * LDP + col);
+        float2 s[kMaxCluster];
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          if (r < C) s[r] = ld_cluster_f32x2(map_to_rank(at, static_cast<uint32_t>(r)));
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          if (r < C) {
+            v[u].x += s[r].x;
+            v[u].y += s[r].y;
+          }
+        v[u].x *= scale;
+        v[u].y *= scale;
+        if (!BF16) top = fmaxf(top, fmaxf(fabsf(v[u].x), fabsf(v[u].y)));
+      }
+    }
+    float up = 1.0f;
+    if (!BF16) {
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+      // the largest goes to [2^14, 2^15): exponents stay where 2^e and 2^-e are normal numbers
+      int e = static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14;
+      e = e < -126 ? -126 : e;
+      if (top == 0.0f || top > 3.4028235e38f) e = 0;
+      up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+      for (int u = 0; u < PAIRS; ++u) {
+        v[u].x *= down;
+        v[u].y *= down;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < PAIRS; ++u) {
+      const int col = 2 * (lane + 32 * u);
+      if (col < RP) {
+        uint32_t h, l;
+        split2<BF16>(v[u].x, v[u].y, h, l);
+        const uint32_t at_h = ptx::smem_u32(hi + row * LDH + col), at_l = ptx::smem_u32(lo + row * LDH + col);
+        for (int r = 0; r < C; ++r) {
+          st_cluster_u32(map_to_rank(at_h, static_cast<uint32_t>(r)), h);
+          st_cluster_u32(map_to_rank(at_l, static_cast<uint32_t>(r)), l);
+        }
+      }
+    }
+    if (lane < C) st_cluster_f32(map_to_rank(ptx::smem_u32(power + row), static_cast<uint32_t>(lane)), up);
+  }
 }
 
 // Rows of tokens without an adapter: base, or zeros.  A warp's item is 2 KB of 32 tokens.
@@ -149,6 +216,17 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_kernel(Lo
   if (__syncthreads_or(g >= 0) == 0) return;                // the same for every CTA of the cluster
   const int t0 = __shfl_sync(kFull, token, q), t1 = __shfl_sync(kFull, token, q + 8);
 
+  // this CTA's part of N, whose rows of B are asked into L2 while A is read
+  const int nblocks = (a.N + 31) / 32;
+  const long long nshare = static_cast<long long>(blockIdx.y) * C + rank, nshares = static_cast<long long>(gridDim.y) * C;
+  const int nb0 = static_cast<int>(nblocks * nshare / nshares), nb1 = static_cast<int>(nblocks * (nshare + 1) / nshares);
+  const uint16_t* bg = static_cast<const uint16_t*>(a.B) + static_cast<size_t>(g < 0 ? 0 : g) * a.N * a.r;
+  if (g >= 0) {
+    const char *from = reinterpret_cast<const char*>(bg + static_cast<size_t>(nb0) * 32 * a.r),
+               *to = reinterpret_cast<const char*>(bg + static_cast<size_t>(min(nb1 * 32, a.N)) * a.r);
+    for (const char* p = from + 128 * (wk * 32 + lane); p < to; p += 128 * 32 * WK) gemv::prefetch_l2(p);
+  }
+
   // ------------------------------------------------------------ X A^T over a share of K
   const int share = rank * WK + wk, shares = C * WK;
   const int kblocks = (a.K + 31) / 32;
@@ -202,59 +280,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_kernel(Lo
   if (C > 1) cluster_sync_all(); else __syncthreads();
 
   // ------------------------------------------------------------ P, a warp per row
-  // each CTA sums every C-th row over the cluster and hands it to all of them
-  for (int row = rank + C * warp; row < WT * 16; row += C * kWarps) {
-    const float scale = tile_scale[row / 16];
-    constexpr int PAIRS = (RP + 63) / 64;
-    float2 v[PAIRS];
-    float top = 0.0f;
-#pragma unroll
-    for (int u = 0; u < PAIRS; ++u) {
-      const int col = 2 * (lane + 32 * u);
-      v[u] = make_float2(0.0f, 0.0f);
-      if (col < RP) {
-        const uint32_t at = ptx::smem_u32(part + row * LDP + col);
-        for (int r = 0; r < C; ++r) {
-          const float2 s = ld_cluster_f32x2(map_to_rank(at, static_cast<uint32_t>(r)));
-          v[u].x += s.x;
-          v[u].y += s.y;
-        }
-        v[u].x *= scale;
-        v[u].y *= scale;
-        if (!BF16) top = fmaxf(top, fmaxf(fabsf(v[u].x), fabsf(v[u].y)));
-      }
-    }
-    float up = 1.0f;
-    if (!BF16) {
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
-      // the largest goes to [2^14, 2^15): exponents stay where 2^e and 2^-e are normal numbers
-      int e = static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14;
-      e = e < -126 ? -126 : e;
-      if (top == 0.0f || top > 3.4028235e38f) e = 0;
-      up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-      for (int u = 0; u < PAIRS; ++u) {
-        v[u].x *= down;
-        v[u].y *= down;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < PAIRS; ++u) {
-      const int col = 2 * (lane + 32 * u);
-      if (col < RP) {
-        uint32_t h, l;
-        split2<BF16>(v[u].x, v[u].y, h, l);
-        const uint32_t at_h = ptx::smem_u32(hi + row * LDH + col), at_l = ptx::smem_u32(lo + row * LDH + col);
-        for (int r = 0; r < C; ++r) {
-          st_cluster_u32(map_to_rank(at_h, static_cast<uint32_t>(r)), h);
-          st_cluster_u32(map_to_rank(at_l, static_cast<uint32_t>(r)), l);
-        }
-      }
-    }
-    if (lane < C) st_cluster_f32(map_to_rank(ptx::smem_u32(power + row), static_cast<uint32_t>(lane)), up);
-  }
+  exchange_rows<BF16, RP>(part, hi, lo, power, WT * 16, tile_scale, 16, C, rank);
   if (C > 1) cluster_sync_all(); else __syncthreads();      // and nothing remote is touched behind this
   if (g < 0) return;
 
@@ -280,10 +306,6 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_kernel(Lo
       }
   }
   const float up0 = power[wt * 16 + q], up1 = power[wt * 16 + q + 8];
-  const int nblocks = (a.N + 31) / 32;
-  const long long nshare = static_cast<long long>(blockIdx.y) * C + rank, nshares = static_cast<long long>(gridDim.y) * C;
-  const int nb0 = static_cast<int>(nblocks * nshare / nshares), nb1 = static_cast<int>(nblocks * (nshare + 1) / nshares);
-  const uint16_t* bg = static_cast<const uint16_t*>(a.B) + static_cast<size_t>(g) * a.N * a.r;
   for (int nb = nb0 + wk; nb < nb1; nb += WK) {
     const int n0 = nb * 32 + 8 * c;                         // this lane's 8 columns of out
     const bool in = n0 < a.N;
@@ -343,78 +365,365 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_kernel(Lo
   }
 }
 
+// ----------------------------------------------------------------- many tokens of an adapter
+// The same two products for blocks of 128 rows with one adapter, in which a byte of A or B
+// serves 128 tokens.  X, A and B go through shared memory by cp.async, kStages blocks deep, so
+// that enough of X and base is on its way without holding registers; four groups of warps
+// take 32 tokens each and read A and B by ldmatrix, two warps of a group halve K, then N.
+// Rows of a stage are 128 bytes in 16-byte pieces, piece p of row i at p ^ (i & 7).
+constexpr int kStages = 3, kWideRows = 128;
+
+template <int RP>
+struct WideCfg {
+  static constexpr int LDP = RP + 4, LDH = RP + 8;
+  static constexpr int KSTAGE = (kWideRows + RP) * 128;     // 64 columns of X and A
+  static constexpr int NB = 64;                             // rows of B in a block
+  static constexpr int LDB = 2 * RP + 16;                   // bytes between them: ldmatrix without conflicts
+  static constexpr int NSTAGE = NB * LDB;
+  static constexpr int PART = kWideRows * LDP * 4;
+  // [part | stages of B], over the stages of X and A, then P
+  static constexpr int OFF_B = PART;
+  static constexpr int FRONT = kStages * KSTAGE > PART + kStages * NSTAGE ? kStages * KSTAGE : PART + kStages * NSTAGE;
+  static constexpr int OFF_HI = FRONT, OFF_LO = OFF_HI + kWideRows * LDH * 2, OFF_POWER = OFF_LO + kWideRows * LDH * 2;
+  static constexpr int SMEM = OFF_POWER + kWideRows * 4;
+};
+
+__device__ __forceinline__ void ldmatrix_x4_at(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3) : "r"(addr) : "memory");
+}
+
+template <bool BF16, int RP>
+__global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_wide_kernel(LoraKArgs args) {
+  using Cf = WideCfg<RP>;
+  constexpr int NB8 = RP / 8;
+  const LoraArgs& a = args.a;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int tokens[kWideRows];
+  __shared__ float block_scale;
+  const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  const int q = lane >> 2, c = lane & 3;
+  const int C = static_cast<int>(gridDim.z), rank = static_cast<int>(blockIdx.z);
+  float* part = reinterpret_cast<float*>(smem);
+  uint16_t *hi = reinterpret_cast<uint16_t*>(smem + Cf::OFF_HI), *lo = reinterpret_cast<uint16_t*>(smem + Cf::OFF_LO);
+  float* power = reinterpret_cast<float*>(smem + Cf::OFF_POWER);
+  const uint32_t base_s = ptx::smem_u32(smem);
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+
+  const int groups = static_cast<int>(gridDim.x) - args.copy;
+  if (static_cast<int>(blockIdx.x) >= groups) {
+    fill_others(a, (static_cast<long long>(blockIdx.x - groups) * C + rank) * kWarps + warp, static_cast<long long>(args.copy) * C * kWarps, lane);
+    return;                                                 // whole clusters
+  }
+  // the block's adapter and tokens
+  const long long row0 = static_cast<long long>(blockIdx.x) * kWideRows;
+  int g = ptx::ld_global(a.m_indices + row0);
+  bool bad = tid == 0 && (g >= a.G);
+  if (g >= a.G) g = -1;
+  if (tid < kWideRows) {
+    const int id = ptx::ld_global(a.m_indices + row0 + tid);
+    int t = ptx::ld_global(a.src + row0 + tid);
+    if (id < 0 || t < 0 || g < 0) {
+      t = -1;
+    } else if (id != g || t >= a.T) {
+      bad = true;
+      t = -1;
+    }
+    tokens[tid] = t;
+  }
+  if (bad) atomicOr(a.status, FGF8_DEVERR_INPUT);
+  if (tid == 0) block_scale = a.scale != nullptr && g >= 0 ? ptx::ld_global(a.scale + g) : 1.0f;
+  __syncthreads();
+  if (g < 0) return;                                        // the same for every CTA of the cluster
+
+  const uint16_t* ag = static_cast<const uint16_t*>(a.A) + static_cast<size_t>(g) * a.r * a.K;
+  const uint16_t* bg = static_cast<const uint16_t*>(a.B) + static_cast<size_t>(g) * a.N * a.r;
+  const int wm = warp & 3, wh = warp >> 2;                  // this warp's 32 tokens, its half of K or N
+
+  // ------------------------------------------------------------ X A^T over a share of K
+  const int ksteps = (a.K + 63) / 64;
+  const int ks0 = static_cast<int>(static_cast<long long>(ksteps) * rank / C), ks1 = static_cast<int>(static_cast<long long>(ksteps) * (rank + 1) / C);
+  const int prow = tid >> 3, pcol = tid & 7;                // the piece that this thread copies of every 32 rows
+  const uint16_t* xrow[kWideRows / 32];
+#pragma unroll
+  for (int i = 0; i < kWideRows / 32; ++i) {
+    const int t = tokens[prow + 32 * i];
+    xrow[i] = t < 0 ? nullptr : static_cast<const uint16_t*>(a.X) + static_cast<size_t>(t) * a.ldx;
+  }
+  auto load_k = [&](int ks, int stage) {
+    const int k = ks * 64 + pcol * 8;
+    const bool in = ks < ks1 && k < a.K;
+    const uint32_t to = base_s + static_cast<uint32_t>(stage * Cf::KSTAGE) + static_cast<uint32_t>(prow * 128 + ((pcol ^ (prow & 7)) << 4));
+    if (ks < ks1) {
+#pragma unroll
+      for (int i = 0; i < kWideRows / 32; ++i) {
+        const bool have = in && xrow[i] != nullptr;
+        gemv::cp16(to + static_cast<uint32_t>(i * 32 * 128), have ? xrow[i] + k : static_cast<const uint16_t*>(a.X), have);
+      }
+#pragma unroll
+      for (int i = 0; i < (RP + 31) / 32; ++i) {
+        const int row = prow + 32 * i;
+        if (row < RP) {
+          const bool have = in && row < a.r;
+          gemv::cp16(to + static_cast<uint32_t>((kWideRows + i * 32) * 128), have ? ag + static_cast<size_t>(row) * a.K + k : ag, have);
+        }
+      }
+    }
+    gemv::cp_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) load_k(ks0 + s, s);
+  float acc[2][NB8][4] = {};
+  int stage = 0;
+  for (int ks = ks0; ks < ks1; ++ks) {
+    gemv::cp_wait<kStages - 2>();
+    __syncthreads();                                        // the stage is there, and everybody is done with the one before
+    load_k(ks + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+    const uint32_t sx = base_s + static_cast<uint32_t>(stage * Cf::KSTAGE), sa = sx + kWideRows * 128;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const int piece = 4 * wh + 2 * kk;                    // the two 16-byte pieces of 16 columns
+      uint32_t xf[2][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int row = 32 * wm + 16 * m + (lane & 15);
+        ldmatrix_x4_at(sx + static_cast<uint32_t>(row * 128 + (((piece + (lane >> 4)) ^ (row & 7)) << 4)), xf[m][0], xf[m][1], xf[m][2], xf[m][3]);
+      }
+#pragma unroll
+      for (int b = 0; b < NB8; b += 2) {
+        const int row = 8 * b + (lane & 7) + ((lane >> 4) << 3);
+        uint32_t w0, w1, w2, w3;
+        ldmatrix_x4_at(sa + static_cast<uint32_t>(row * 128 + (((piece + ((lane >> 3) & 1)) ^ (row & 7)) << 4)), w0, w1, w2, w3);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          gemv::mma16816<BF16>(acc[m][b], xf[m][0], xf[m][1], xf[m][2], xf[m][3], w0, w1);
+          gemv::mma16816<BF16>(acc[m][b + 1], xf[m][0], xf[m][1], xf[m][2], xf[m][3], w2, w3);
+        }
+      }
+    }
+    if (++stage == kStages) stage = 0;
+  }
+  gemv::cp_wait<0>();
+  __syncthreads();
+  // the halves of K meet in shared memory
+#pragma unroll
+  for (int half = 1; half >= 0; --half) {
+    if (wh == half) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int b = 0; b < NB8; ++b)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float2* p = reinterpret_cast<float2*>(part + (32 * wm + 16 * m + 8 * e + q) * Cf::LDP + 8 * b + 2 * c);
+            float2 v = make_float2(acc[m][b][2 * e], acc[m][b][2 * e + 1]);
+            if (half == 0) {
+              const float2 o = *p;
+              v.x += o.x;
+              v.y += o.y;
+            }
+            *p = v;
+          }
+    }
+    __syncthreads();
+  }
+
+  // ------------------------------------------------------------ P B^T over a share of N
+  const int nblocks = (a.N + Cf::NB - 1) / Cf::NB;
+  const int nb0 = static_cast<int>(static_cast<long long>(nblocks) * rank / C), nb1 = static_cast<int>(static_cast<long long>(nblocks) * (rank + 1) / C);
+  // row 8 x + 2 j + e of 32 goes to 8 j + 2 x + e: the eight rows of an MMA side by side, and a
+  // lane's results of four MMAs are eight neighbours
+  auto load_n = [&](int nb, int s) {
+    constexpr int PIECES = RP / 8;                          // of a row
+    if (nb < nb1) {
+#pragma unroll
+      for (int i = tid; i < Cf::NB * PIECES; i += kThreads) {
+        const int row = i / PIECES, piece = i % PIECES, n = nb * Cf::NB + row;
+        const int at = (row & 32) + ((row >> 1) & 3) * 8 + ((row >> 3) & 3) * 2 + (row & 1);
+        const bool have = n < a.N && 8 * piece < a.r;
+        gemv::cp16(base_s + Cf::OFF_B + static_cast<uint32_t>(s * Cf::NSTAGE + at * Cf::LDB + piece * 16),
+                   have ? bg + static_cast<size_t>(n) * a.r + 8 * piece : bg, have);
+      }
+    }
+    gemv::cp_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) load_n(nb0 + s, s);
+  if (C > 1) cluster_sync_all();
+  exchange_rows<BF16, RP>(part, hi, lo, power, kWideRows, &block_scale, kWideRows, C, rank);
+  if (C > 1) cluster_sync_all(); else __syncthreads();      // and nothing remote is touched behind this
+
+  int t[4];                                                 // tokens of rows q, q + 8, q + 16, q + 24 of the 32
+  float up[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    t[i] = tokens[32 * wm + 8 * i + q];
+    up[i] = power[32 * wm + 8 * i + q];
+  }
+  const int off = 32 * wh + 8 * c;                          // this lane's columns of a block
+  uint4 next[4];
+  auto load_base = [&](int nb) {
+    const int n0 = nb * Cf::NB + off;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      next[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (nb < nb1 && a.base != nullptr && n0 < a.N && t[i] >= 0)
+        next[i] = ptx::ld_global_v4(static_cast<const uint16_t*>(a.base) + static_cast<size_t>(t[i]) * a.ldb + n0);
+    }
+  };
+  load_base(nb0);
+  const uint32_t sh = base_s + Cf::OFF_HI + static_cast<uint32_t>((32 * wm + (lane & 15)) * Cf::LDH * 2 + (lane >> 4) * 16);
+  stage = 0;
+  for (int nb = nb0; nb < nb1; ++nb) {
+    gemv::cp_wait<kStages - 2>();
+    __syncthreads();
+    load_n(nb + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+    uint4 base[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) base[i] = next[i];
+    load_base(nb + 1);
+    const uint32_t sb = base_s + Cf::OFF_B + static_cast<uint32_t>(stage * Cf::NSTAGE + (32 * wh + (lane & 7) + ((lane >> 4) << 3)) * Cf::LDB + ((lane >> 3) & 1) * 16);
+    float d[2][4][4] = {};
+#pragma unroll
+    for (int k = 0; k < RP / 16; ++k) {
+      uint32_t bf[4][2];
+      ldmatrix_x4_at(sb + static_cast<uint32_t>(k * 32), bf[0][0], bf[0][1], bf[1][0], bf[1][1]);
+      ldmatrix_x4_at(sb + static_cast<uint32_t>(16 * Cf::LDB + k * 32), bf[2][0], bf[2][1], bf[3][0], bf[3][1]);
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int part_of = 0; part_of < 2; ++part_of) {     // P rounded, and its rest
+          uint32_t pf[4];
+          ldmatrix_x4_at(sh + static_cast<uint32_t>((part_of ? Cf::OFF_LO - Cf::OFF_HI : 0) + m * 16 * Cf::LDH * 2 + k * 32), pf[0], pf[1], pf[2], pf[3]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) gemv::mma16816<BF16>(d[m][j], pf[0], pf[1], pf[2], pf[3], bf[j][0], bf[j][1]);
+        }
+    }
+    const int n0 = nb * Cf::NB + off;
+    if (n0 < a.N) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (t[i] < 0) continue;
+        const uint32_t bw[4] = {base[i].x, base[i].y, base[i].z, base[i].w};
+        uint32_t ow[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          ow[j] = pack_2x16(fmaf(up[i], d[i >> 1][j][2 * (i & 1)], act::to_float(bw[j] & 0xFFFFu, BF16)),
+                            fmaf(up[i], d[i >> 1][j][2 * (i & 1) + 1], act::to_float(bw[j] >> 16, BF16)), BF16);
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + static_cast<size_t>(t[i]) * a.ldo + n0) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+      }
+    }
+    __syncwarp();                                           // whole-warp instructions follow
+    if (++stage == kStages) stage = 0;
+  }
+  gemv::cp_wait<0>();
+}
+
 // Shared memory of a CTA with `tiles` tiles.
 template <int RP>
 constexpr int smem_bytes(int tiles) {
   return kWarps * 16 * (RP + 4) * 4 + 2 * tiles * 16 * (RP + 8) * 2 + tiles * 16 * 4;
 }
 
-template <bool BF16, int RP>
-int launch(LoraKArgs& k, int cluster, int parts, cudaStream_t stream) {
-  auto* fn = &lora_f16_kernel<BF16, RP>;
-  static PerDevice<int> ready;
+struct LoraLaunch {
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  LoraLaunch(long long groups, int parts, int cluster, size_t smem, cudaStream_t stream) {
+    std::memset(&cfg, 0, sizeof(cfg));
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = static_cast<unsigned>(cluster);
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(groups), static_cast<unsigned>(parts), static_cast<unsigned>(cluster));
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  }
+};
+
+// Opens the kernel's shared memory once per device, then launches it.
+template <typename K>
+int launch(K* fn, PerDevice<int>& ready, int most_smem, int smem, const LoraKArgs& k, long long groups, int parts, int cluster, cudaStream_t stream) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= kMaxDevices) return set_error(2, "device id %d", dev);
   const int* set = nullptr;
   const int r = ready.get(dev, &set, [&](int& v) {
-    v = smem_bytes<RP>(kWarps);
+    v = most_smem;
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v);
     return e == cudaSuccess ? 0 : set_error(4, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
   });
   if (r) return r;
-  const long long groups = (k.a.M / 16 + k.tiles - 1) / k.tiles;
-  cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof(cfg));
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = static_cast<unsigned>(cluster);
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(groups + k.copy), static_cast<unsigned>(parts), static_cast<unsigned>(cluster));
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem_bytes<RP>(k.tiles));
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, k);
+  LoraLaunch l(groups + k.copy, parts, cluster, static_cast<size_t>(smem), stream);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, fn, k);
   return e == cudaSuccess ? 0 : set_error(4, "lora_f16 launch: %s", cudaGetErrorString(e));
 }
 
-template <bool BF16>
-int by_rank(LoraKArgs& k, int cluster, int parts, cudaStream_t stream) {
-  if (k.a.r <= 16) return launch<BF16, 16>(k, cluster, parts, stream);
-  if (k.a.r <= 32) return launch<BF16, 32>(k, cluster, parts, stream);
-  if (k.a.r <= 64) return launch<BF16, 64>(k, cluster, parts, stream);
-  return launch<BF16, 128>(k, cluster, parts, stream);
+// Clusters that fill the rows of tokens without an adapter: none in place.
+int copy_clusters(const LoraArgs& a, int cluster) {
+  if (a.base == a.out) return 0;
+  const long long items = (a.T + 31LL) / 32 * ((a.N / 8 + 127) / 128), want = (items + cluster * kWarps - 1) / (cluster * kWarps);
+  const long long most = (2LL * device_sm_count() + cluster - 1) / cluster;
+  return static_cast<int>(want < most ? want : most);
 }
 
-}  // namespace
-
-int launch_lora_f16(const LoraArgs& a, int bf16, cudaStream_t stream) {
+template <bool BF16, int RP>
+int launch_tiles(const LoraArgs& a, cudaStream_t stream) {
+  static PerDevice<int> ready;
   LoraKArgs k;
   k.a = a;
   const long long tiles = a.M / 16, sms = device_sm_count();
   const long long nblocks = (a.N + 31) / 32;
   // a cluster's CTAs split K and N: eight, fewer where there is too little to split
-  int cluster = 8;
+  int cluster = kMaxCluster;
   while (cluster > 1 && (a.K + 31) / 32 < 2 * cluster && nblocks < 2 * cluster) cluster /= 2;
   // tiles share a CTA as soon as there are two CTAs per SM without
   k.tiles = 8;
   while (k.tiles > 1 && (tiles + k.tiles - 1) / k.tiles * cluster < 2 * sms) k.tiles /= 2;
   // few tiles: several clusters per tile, each a part of N
-  long long parts = 1;
-  const long long ctas = (tiles + k.tiles - 1) / k.tiles * cluster;
-  while (parts < 64 && 2 * parts * ctas <= sms && 2 * parts * cluster <= nblocks) parts *= 2;
-  k.copy = 0;
-  if (a.base != a.out) {
-    const long long items = (a.T + 31LL) / 32 * ((a.N / 8 + 127) / 128), want = (items + cluster * kWarps - 1) / (cluster * kWarps);
-    const long long most = (2 * sms + cluster - 1) / cluster;
-    k.copy = static_cast<int>(want < most ? want : most);
-  }
-  return bf16 ? by_rank<true>(k, cluster, static_cast<int>(parts), stream) : by_rank<false>(k, cluster, static_cast<int>(parts), stream);
+  const long long groups = (tiles + k.tiles - 1) / k.tiles;
+  int parts = 1;
+  while (parts < 64 && 2 * parts * groups * cluster <= sms && 2 * parts * cluster <= nblocks) parts *= 2;
+  k.copy = copy_clusters(a, cluster);
+  return launch(&lora_f16_kernel<BF16, RP>, ready, smem_bytes<RP>(kWarps), smem_bytes<RP>(k.tiles), k, groups, parts, cluster, stream);
+}
+
+template <bool BF16, int RP>
+int launch_wide(const LoraArgs& a, cudaStream_t stream) {
+  static PerDevice<int> ready;
+  static_assert(WideCfg<RP>::SMEM <= 232448 - 1024, "shared memory budget");
+  LoraKArgs k;
+  k.a = a;
+  k.tiles = 8;
+  const long long groups = a.M / kWideRows, slots = static_cast<long long>(device_sm_count()) * (RP <= 64 ? 2 : 1);
+  int cluster = kMaxCluster;
+  while (cluster > 1 && (a.K + 63) / 64 < 2 * cluster && (a.N + 63) / 64 < 2 * cluster) cluster /= 2;
+  while (cluster > 1 && groups * cluster / 2 >= 4 * slots) cluster /= 2;
+  k.copy = copy_clusters(a, cluster);
+  return launch(&lora_f16_wide_kernel<BF16, RP>, ready, WideCfg<RP>::SMEM, WideCfg<RP>::SMEM, k, groups, 1, cluster, stream);
+}
+
+template <bool BF16, int RP>
+int by_align(const LoraArgs& a, cudaStream_t stream) {
+  return a.align % kWideRows == 0 ? launch_wide<BF16, RP>(a, stream) : launch_tiles<BF16, RP>(a, stream);
+}
+
+template <bool BF16>
+int by_rank(const LoraArgs& a, cudaStream_t stream) {
+  if (a.r <= 16) return by_align<BF16, 16>(a, stream);
+  if (a.r <= 32) return by_align<BF16, 32>(a, stream);
+  if (a.r <= 64) return by_align<BF16, 64>(a, stream);
+  return by_align<BF16, 128>(a, stream);
+}
+
+}  // namespace
+
+int launch_lora_f16(const LoraArgs& a, int bf16, cudaStream_t stream) {
+  return bf16 ? by_rank<true>(a, stream) : by_rank<false>(a, stream);
 }
 
 }  // namespace fgf8

@@ -54,6 +54,7 @@ struct LoraArgs {
   const int32_t* m_indices; // [M]
   long long ldx, ldb, ldo;
   int T, K, N, r, G, M;
+  int align;                // rows with one adapter, a multiple of 16 that divides M
   uint32_t* status;
 };
 int launch_lora_f16(const LoraArgs& a, int bf16, cudaStream_t stream);

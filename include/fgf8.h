@@ -368,15 +368,17 @@ FGF8_API int dispatch_f16_backward(const void* dXs, const int32_t* rows, void* d
  *          it may be out itself (with ldb = ldo)
  *   out : [T][N], rows ldo apart
  *   rows [T], src [M], m_indices [M] : route_contiguous of the tokens' adapters (k = 1) with
- *          align a multiple of 16; a routing serves every layer of a step
+ *          this align, a multiple of 16: 128 (or a multiple) where adapters have some 64
+ *          tokens and more each, 16 for fewer; a routing serves every layer of a step
  * Tokens without an adapter get base.  X, A, B, base and out are of one type (dtype).
- * A row that names another adapter than the first of its 16 rows sets
+ * A row that names another adapter than the first of its `align` rows sets
  * FGF8_ERR_DEVICE_INPUT and is not computed.  Requires K, N, r, ldx, ldb, ldo multiples of
- * 8, r <= 128, M % 16 == 0, and an out that overlaps no other input than an identical base.
+ * 8, r <= 128, M % align == 0, and an out that overlaps no other input than an identical base.
  */
 FGF8_API int lora_f16(const void* X, const void* A, const void* B, const float* scale, const void* base,
                       const int32_t* rows, const int32_t* src, const int32_t* m_indices, void* out, int T, int K, int N,
-                      int r, int G, int M, long long ldx, long long ldb, long long ldo, int dtype, void* stream);
+                      int r, int G, int M, int align, long long ldx, long long ldb, long long ldo, int dtype,
+                      void* stream);
 
 /* Bytes of a quantize_fp4 scale table for R rows; -1 on invalid arguments. */
 FGF8_API long long fgf8_fp4_sf_bytes(int R, int K, int fmt);

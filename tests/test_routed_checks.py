@@ -113,16 +113,17 @@ def test_combine_refusals(lib):
 
 
 def test_lora_refusals(lib):
-    f = _fn(lib, "lora_f16", 9, 6, 3)
+    f = _fn(lib, "lora_f16", 9, 7, 3)
     ok = [AL] * 4 + [AL] * 5
 
-    def call(T=4, K=64, N=32, r=16, G=2, M=32, ldx=64, ldb=32, ldo=32, dtype=0, ptrs=ok):
-        return f(*ptrs, T, K, N, r, G, M, ldx, ldb, ldo, dtype, None)
+    def call(T=4, K=64, N=32, r=16, G=2, M=32, align=16, ldx=64, ldb=32, ldo=32, dtype=0, ptrs=ok):
+        return f(*ptrs, T, K, N, r, G, M, align, ldx, ldb, ldo, dtype, None)
     assert call(T=-1) == 1 and call(r=0) == 1 and call(G=0) == 1 and call(M=-16) == 1
     assert call(K=60, ldx=64) == 2 and call(N=20) == 2
     assert call(r=12) == 2 and "rank 12" in _err(lib)
     assert call(r=136) == 2
-    assert call(M=40) == 2 and "16" in _err(lib)
+    assert call(align=8) == 2 and "align=8" in _err(lib)
+    assert call(M=40) == 1 and call(M=64, align=128) == 1 and call(align=0) == 2
     assert call(dtype=2) == 1
     assert call(ldx=56) == 1 and "apart" in _err(lib)
     assert call(ldo=24) == 1 and call(ldb=24) == 1
@@ -210,7 +211,7 @@ def test_binding_lora(fg):
     x, a, b = z(T, K), z(G, rank, K), z(G, N, rank)
     r = fg.route_contiguous(z(T, dtype=torch.int32), G, align=16)
     assert fg.lora_f16(x, a, b, r).shape == (T, N)
-    assert fg.calls[-1][2] == (T, K, N, rank, G, 48, 64, 0, 32, 1)
+    assert fg.calls[-1][2] == (T, K, N, rank, G, 48, 16, 64, 0, 32, 1)
     wide = z(T, 3 * N)
     out = wide[:, N:2 * N]
     assert fg.lora_f16(x, a, b, r, base=out, out=out) is out
