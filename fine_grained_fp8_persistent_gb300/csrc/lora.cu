@@ -37,7 +37,6 @@ constexpr uint32_t kFull = 0xFFFFFFFFu;
 struct LoraKArgs {
   LoraArgs a;
   int tiles;       // tiles of a CTA: 1, 2, 4 or 8; its other warps split K and N further
-  int copy;        // clusters behind the tiles' that fill the rows of tokens without an adapter
 };
 
 __device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
@@ -138,27 +137,44 @@ __device__ __forceinline__ void exchange_rows(const float* part, uint16_t* hi, u
   }
 }
 
-// Rows of tokens without an adapter: base, or zeros.  A warp's item is 2 KB of 32 tokens.
-__device__ __forceinline__ void fill_others(const LoraArgs& a, long long worker, long long workers, int lane) {
-  constexpr int kPart = 4;
-  const int vecs = a.N / 8, parts = (vecs + 32 * kPart - 1) / (32 * kPart);
-  const long long items = (static_cast<long long>(a.T) + 31) / 32 * parts;
-  for (long long it = worker; it < items; it += workers) {
-    const int t0 = static_cast<int>(it / parts) * 32, v0 = static_cast<int>(it % parts) * 32 * kPart + lane;
-    const bool other = t0 + lane < a.T && ptx::ld_global(a.rows + t0 + lane) < 0;
-    for (uint32_t left = __ballot_sync(kFull, other); left != 0; left &= left - 1) {
-      const size_t t = static_cast<size_t>(t0 + __ffs(left) - 1);
-      uint4 v[kPart] = {};
+// Rows of tokens without an adapter: base, or zeros.  An item is 2 KB of 32 tokens; every warp
+// of the grid takes its share when its other work is done, and looks at the tokens of its
+// first item as it starts.  In place there is nothing to do.
+struct Others {
+  const LoraArgs& a;
+  const uint32_t worker, workers, parts, items;
+  bool first;
+  static constexpr int kPart = 4;
+
+  __device__ __forceinline__ Others(const LoraArgs& args, uint32_t w, uint32_t n)
+      : a(args), worker(w), workers(n), parts((static_cast<uint32_t>(args.N) / 8 + 32 * kPart - 1) / (32 * kPart)),
+        items(args.base == args.out ? 0u : (static_cast<uint32_t>(args.T) + 31) / 32 * parts) {
+    first = worker < items && look(worker);
+  }
+  // whether this lane's token of an item is one
+  __device__ __forceinline__ bool look(uint32_t it) const {
+    const uint32_t t = it / parts * 32 + (threadIdx.x & 31);
+    return t < static_cast<uint32_t>(a.T) && ptx::ld_global(a.rows + t) < 0;
+  }
+  __device__ __forceinline__ void fill() const {
+    const int lane = static_cast<int>(threadIdx.x & 31), vecs = a.N / 8;
+    for (uint32_t it = worker; it < items; it += workers) {
+      const int v0 = static_cast<int>(it % parts) * 32 * kPart + lane;
+      for (uint32_t left = __ballot_sync(kFull, it == worker ? first : look(it)); left != 0; left &= left - 1) {
+        const size_t t = static_cast<size_t>(it / parts) * 32 + __ffs(left) - 1;
+        uint4 v[kPart] = {};
 #pragma unroll
-      for (int u = 0; u < kPart; ++u)
-        if (a.base != nullptr && v0 + 32 * u < vecs)
-          v[u] = ptx::ld_global_v4(static_cast<const uint16_t*>(a.base) + t * a.ldb + 8 * static_cast<size_t>(v0 + 32 * u));
+        for (int u = 0; u < kPart; ++u)
+          if (a.base != nullptr && v0 + 32 * u < vecs)
+            v[u] = ptx::ld_global_v4(static_cast<const uint16_t*>(a.base) + t * a.ldb + 8 * static_cast<size_t>(v0 + 32 * u));
 #pragma unroll
-      for (int u = 0; u < kPart; ++u)
-        if (v0 + 32 * u < vecs) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + t * a.ldo + 8 * static_cast<size_t>(v0 + 32 * u)) = v[u];
+        for (int u = 0; u < kPart; ++u)
+          if (v0 + 32 * u < vecs) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + t * a.ldo + 8 * static_cast<size_t>(v0 + 32 * u)) = v[u];
+      }
     }
   }
-}
+};
+__device__ __forceinline__ uint32_t cta_of_grid() { return (blockIdx.x * gridDim.y + blockIdx.y) * gridDim.z + blockIdx.z; }
 
 // RP: the rank rounded up to 16, 32, 64 or 128.  Blocks of rank rows past r load nothing.
 template <bool BF16, int RP>
@@ -181,12 +197,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_kernel(Lo
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
 
-  const int groups = static_cast<int>(gridDim.x) - args.copy;
-  if (static_cast<int>(blockIdx.x) >= groups) {
-    if (blockIdx.y == 0)
-      fill_others(a, (static_cast<long long>(blockIdx.x - groups) * C + rank) * kWarps + warp, static_cast<long long>(args.copy) * C * kWarps, lane);
-    return;                                                 // whole clusters
-  }
+  const Others others(a, cta_of_grid() * kWarps + warp, gridDim.x * gridDim.y * gridDim.z * kWarps);
 
   // the tile of this warp: its adapter and tokens
   const int wt = warp % WT, wk = warp / WT;
@@ -213,7 +224,10 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_kernel(Lo
     }
     if (bad) atomicOr(a.status, FGF8_DEVERR_INPUT);
   }
-  if (__syncthreads_or(g >= 0) == 0) return;                // the same for every CTA of the cluster
+  if (__syncthreads_or(g >= 0) == 0) {                      // the same for every CTA of the cluster
+    others.fill();
+    return;
+  }
   const int t0 = __shfl_sync(kFull, token, q), t1 = __shfl_sync(kFull, token, q + 8);
 
   // this CTA's part of N, whose rows of B are asked into L2 while A is read
@@ -282,7 +296,10 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_kernel(Lo
   // ------------------------------------------------------------ P, a warp per row
   exchange_rows<BF16, RP>(part, hi, lo, power, WT * 16, tile_scale, 16, C, rank);
   if (C > 1) cluster_sync_all(); else __syncthreads();      // and nothing remote is touched behind this
-  if (g < 0) return;
+  if (g < 0) {
+    others.fill();
+    return;
+  }
 
   // ------------------------------------------------------------ P B^T over a share of N
   constexpr int KS = RP >= 32 ? RP / 32 : 1;                // steps of 32 rank rows (of 16 when there are no more)
@@ -363,6 +380,8 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_kernel(Lo
       }
     }
   }
+  __syncwarp();
+  others.fill();
 }
 
 // ----------------------------------------------------------------- many tokens of an adapter
@@ -380,10 +399,11 @@ struct WideCfg {
   static constexpr int NB = 64;                             // rows of B in a block
   static constexpr int LDB = 2 * RP + 16;                   // bytes between them: ldmatrix without conflicts
   static constexpr int NSTAGE = NB * LDB;
+  static constexpr int BSTAGE = kWideRows * 2 * NB;         // a block of base
   static constexpr int PART = kWideRows * LDP * 4;
-  // [part | stages of B], over the stages of X and A, then P
-  static constexpr int OFF_B = PART;
-  static constexpr int FRONT = kStages * KSTAGE > PART + kStages * NSTAGE ? kStages * KSTAGE : PART + kStages * NSTAGE;
+  // [part, then stages of base | stages of B], over the stages of X and A; then P
+  static constexpr int OFF_B = PART > kStages * BSTAGE ? PART : kStages * BSTAGE;
+  static constexpr int FRONT = kStages * KSTAGE > OFF_B + kStages * NSTAGE ? kStages * KSTAGE : OFF_B + kStages * NSTAGE;
   static constexpr int OFF_HI = FRONT, OFF_LO = OFF_HI + kWideRows * LDH * 2, OFF_POWER = OFF_LO + kWideRows * LDH * 2;
   static constexpr int SMEM = OFF_POWER + kWideRows * 4;
 };
@@ -410,11 +430,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_wide_kern
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
 
-  const int groups = static_cast<int>(gridDim.x) - args.copy;
-  if (static_cast<int>(blockIdx.x) >= groups) {
-    fill_others(a, (static_cast<long long>(blockIdx.x - groups) * C + rank) * kWarps + warp, static_cast<long long>(args.copy) * C * kWarps, lane);
-    return;                                                 // whole clusters
-  }
+  const Others others(a, cta_of_grid() * kWarps + warp, gridDim.x * gridDim.y * gridDim.z * kWarps);
   // the block's adapter and tokens
   const long long row0 = static_cast<long long>(blockIdx.x) * kWideRows;
   int g = ptx::ld_global(a.m_indices + row0);
@@ -434,7 +450,10 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_wide_kern
   if (bad) atomicOr(a.status, FGF8_DEVERR_INPUT);
   if (tid == 0) block_scale = a.scale != nullptr && g >= 0 ? ptx::ld_global(a.scale + g) : 1.0f;
   __syncthreads();
-  if (g < 0) return;                                        // the same for every CTA of the cluster
+  if (g < 0) {                                              // the same for every CTA of the cluster
+    others.fill();
+    return;
+  }
 
   const uint16_t* ag = static_cast<const uint16_t*>(a.A) + static_cast<size_t>(g) * a.r * a.K;
   const uint16_t* bg = static_cast<const uint16_t*>(a.B) + static_cast<size_t>(g) * a.N * a.r;
@@ -561,27 +580,38 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_wide_kern
     up[i] = power[32 * wm + 8 * i + q];
   }
   const int off = 32 * wh + 8 * c;                          // this lane's columns of a block
-  uint4 next[4];
-  auto load_base = [&](int nb) {
-    const int n0 = nb * Cf::NB + off;
+  // 16-byte piece p of row i of a block of base stands at p ^ turn(i): the pieces that eight
+  // lanes read together are in different banks
+  auto turn = [](int row) { return ((row & 1) << 2) | ((row >> 1) & 3); };
+  int brow[kWideRows / 32];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      next[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (nb < nb1 && a.base != nullptr && n0 < a.N && t[i] >= 0)
-        next[i] = ptx::ld_global_v4(static_cast<const uint16_t*>(a.base) + static_cast<size_t>(t[i]) * a.ldb + n0);
+  for (int i = 0; i < kWideRows / 32; ++i) brow[i] = a.base != nullptr ? tokens[prow + 32 * i] : -1;
+  auto load_base = [&](int nb, int s) {
+    const int n0 = nb * Cf::NB + 8 * pcol;
+    if (nb < nb1) {
+#pragma unroll
+      for (int i = 0; i < kWideRows / 32; ++i) {
+        const bool have = n0 < a.N && brow[i] >= 0;
+        const uint16_t* from = have ? static_cast<const uint16_t*>(a.base) + static_cast<size_t>(brow[i]) * a.ldb + n0 : bg;
+        gemv::cp16(base_s + static_cast<uint32_t>(s * Cf::BSTAGE + (prow + 32 * i) * 128 + ((pcol ^ turn(prow)) << 4)), from, have);
+      }
     }
+    gemv::cp_commit();
   };
-  load_base(nb0);
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) load_base(nb0 + s, s);
   const uint32_t sh = base_s + Cf::OFF_HI + static_cast<uint32_t>((32 * wm + (lane & 15)) * Cf::LDH * 2 + (lane >> 4) * 16);
   stage = 0;
   for (int nb = nb0; nb < nb1; ++nb) {
-    gemv::cp_wait<kStages - 2>();
+    // groups in order: two of B, two of base, then for each block its B and base together
+    if (nb == nb0)
+      gemv::cp_wait<kStages - 2>();
+    else
+      gemv::cp_wait<2 * (kStages - 2)>();
     __syncthreads();
-    load_n(nb + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
-    uint4 base[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) base[i] = next[i];
-    load_base(nb + 1);
+    const int ahead = stage == 0 ? kStages - 1 : stage - 1;
+    load_n(nb + kStages - 1, ahead);
+    load_base(nb + kStages - 1, ahead);
     const uint32_t sb = base_s + Cf::OFF_B + static_cast<uint32_t>(stage * Cf::NSTAGE + (32 * wh + (lane & 7) + ((lane >> 4) << 3)) * Cf::LDB + ((lane >> 3) & 1) * 16);
     float d[2][4][4] = {};
 #pragma unroll
@@ -604,8 +634,9 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_wide_kern
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (t[i] < 0) continue;
-        const uint32_t bw[4] = {base[i].x, base[i].y, base[i].z, base[i].w};
-        uint32_t ow[4];
+        const int row = 32 * wm + 8 * i + q;
+        uint32_t bw[4], ow[4];
+        gemv::lds128(smem + stage * Cf::BSTAGE + row * 128 + (((4 * wh + c) ^ turn(row)) << 4), bw);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           ow[j] = pack_2x16(fmaf(up[i], d[i >> 1][j][2 * (i & 1)], act::to_float(bw[j] & 0xFFFFu, BF16)),
@@ -617,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_wide_kern
     if (++stage == kStages) stage = 0;
   }
   gemv::cp_wait<0>();
+  others.fill();
 }
 
 // Shared memory of a CTA with `tiles` tiles.
@@ -658,17 +690,9 @@ int launch(K* fn, PerDevice<int>& ready, int most_smem, int smem, const LoraKArg
     return e == cudaSuccess ? 0 : set_error(4, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
   });
   if (r) return r;
-  LoraLaunch l(groups + k.copy, parts, cluster, static_cast<size_t>(smem), stream);
+  LoraLaunch l(groups, parts, cluster, static_cast<size_t>(smem), stream);
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, fn, k);
   return e == cudaSuccess ? 0 : set_error(4, "lora_f16 launch: %s", cudaGetErrorString(e));
-}
-
-// Clusters that fill the rows of tokens without an adapter: none in place.
-int copy_clusters(const LoraArgs& a, int cluster) {
-  if (a.base == a.out) return 0;
-  const long long items = (a.T + 31LL) / 32 * ((a.N / 8 + 127) / 128), want = (items + cluster * kWarps - 1) / (cluster * kWarps);
-  const long long most = (2LL * device_sm_count() + cluster - 1) / cluster;
-  return static_cast<int>(want < most ? want : most);
 }
 
 template <bool BF16, int RP>
@@ -688,7 +712,6 @@ int launch_tiles(const LoraArgs& a, cudaStream_t stream) {
   const long long groups = (tiles + k.tiles - 1) / k.tiles;
   int parts = 1;
   while (parts < 64 && 2 * parts * groups * cluster <= sms && 2 * parts * cluster <= nblocks) parts *= 2;
-  k.copy = copy_clusters(a, cluster);
   return launch(&lora_f16_kernel<BF16, RP>, ready, smem_bytes<RP>(kWarps), smem_bytes<RP>(k.tiles), k, groups, parts, cluster, stream);
 }
 
@@ -699,11 +722,19 @@ int launch_wide(const LoraArgs& a, cudaStream_t stream) {
   LoraKArgs k;
   k.a = a;
   k.tiles = 8;
+  // the cluster that takes the least time in waves of what fits the device, each as long as the
+  // share of a CTA and, for the start and the exchange of P, a fortieth of a whole block
   const long long groups = a.M / kWideRows, slots = static_cast<long long>(device_sm_count()) * (RP <= 64 ? 2 : 1);
-  int cluster = kMaxCluster;
-  while (cluster > 1 && (a.K + 63) / 64 < 2 * cluster && (a.N + 63) / 64 < 2 * cluster) cluster /= 2;
-  while (cluster > 1 && groups * cluster / 2 >= 4 * slots) cluster /= 2;
-  k.copy = copy_clusters(a, cluster);
+  int cluster = 1;
+  double best = 0.0;
+  for (int c = 1; c <= kMaxCluster; c *= 2) {
+    if (c > 1 && (a.K + 63) / 64 < 2 * c && (a.N + 63) / 64 < 2 * c) break;
+    const double time = static_cast<double>((groups * c + slots - 1) / slots) * (1.0 / c + 0.025);
+    if (c == 1 || time < best) {
+      best = time;
+      cluster = c;
+    }
+  }
   return launch(&lora_f16_wide_kernel<BF16, RP>, ready, WideCfg<RP>::SMEM, WideCfg<RP>::SMEM, k, groups, 1, cluster, stream);
 }
 
