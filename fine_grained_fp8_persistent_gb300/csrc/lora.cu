@@ -37,6 +37,7 @@ constexpr uint32_t kFull = 0xFFFFFFFFu;
 struct LoraKArgs {
   LoraArgs a;
   int tiles;       // tiles of a CTA: 1, 2, 4 or 8; its other warps split K and N further
+  uint64_t timeout_ns;
 };
 
 __device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
@@ -73,10 +74,11 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
 
 // P from the sums over the shares of K: each CTA of the cluster sums every C-th row of `part`
 // over all of them, a warp per row, and hands value, rest and power to all of them.
-template <bool BF16, int RP>
-__device__ __forceinline__ void exchange_rows(const float* part, uint16_t* hi, uint16_t* lo, float* power, int rows, const float* scale_of,
-                                              int scale_rows, int C, int rank) {
-  constexpr int LDP = RP + 4, LDH = RP + 8;
+// place(row, column, value's address, rest's) says where two columns go.
+template <bool BF16, int RP, typename Place>
+__device__ __forceinline__ void exchange_rows(const float* part, float* power, int rows, const float* scale_of, int scale_rows, int C,
+                                              int rank, Place&& place) {
+  constexpr int LDP = RP + 4;
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   for (int row = rank + C * warp; row < rows; row += C * kWarps) {
     const float scale = scale_of[row / scale_rows];
@@ -124,9 +126,9 @@ __device__ __forceinline__ void exchange_rows(const float* part, uint16_t* hi, u
     for (int u = 0; u < PAIRS; ++u) {
       const int col = 2 * (lane + 32 * u);
       if (col < RP) {
-        uint32_t h, l;
+        uint32_t h, l, at_h, at_l;
         split2<BF16>(v[u].x, v[u].y, h, l);
-        const uint32_t at_h = ptx::smem_u32(hi + row * LDH + col), at_l = ptx::smem_u32(lo + row * LDH + col);
+        place(row, col, at_h, at_l);
         for (int r = 0; r < C; ++r) {
           st_cluster_u32(map_to_rank(at_h, static_cast<uint32_t>(r)), h);
           st_cluster_u32(map_to_rank(at_l, static_cast<uint32_t>(r)), l);
@@ -294,7 +296,10 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_kernel(Lo
   if (C > 1) cluster_sync_all(); else __syncthreads();
 
   // ------------------------------------------------------------ P, a warp per row
-  exchange_rows<BF16, RP>(part, hi, lo, power, WT * 16, tile_scale, 16, C, rank);
+  exchange_rows<BF16, RP>(part, power, WT * 16, tile_scale, 16, C, rank, [&](int row, int col, uint32_t& at_h, uint32_t& at_l) {
+    at_h = ptx::smem_u32(hi + row * LDH + col);
+    at_l = ptx::smem_u32(lo + row * LDH + col);
+  });
   if (C > 1) cluster_sync_all(); else __syncthreads();      // and nothing remote is touched behind this
   if (g < 0) {
     others.fill();
@@ -385,48 +390,68 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_kernel(Lo
 }
 
 // ----------------------------------------------------------------- many tokens of an adapter
-// The same two products for blocks of 128 rows with one adapter, in which a byte of A or B
-// serves 128 tokens.  X, A and B go through shared memory by cp.async, kStages blocks deep, so
-// that enough of X and base is on its way without holding registers; four groups of warps
-// take 32 tokens each and read A and B by ldmatrix, two warps of a group halve K, then N.
-// Rows of a stage are 128 bytes in 16-byte pieces, piece p of row i at p ^ (i & 7).
+// The same two products for blocks of 128 rows with one adapter, on tcgen05: a byte of A or B
+// serves 128 tokens, and the multiplications (2 r of them, with P in two parts 3 r, for each
+// element of X, base and out) are off the warps' hands, which copy and add.
+//   X A^T  [128 x r] in TMEM, K in steps of 64: rows of X (gathered by token) and of A come by
+//          cp.async, kStages deep, into the 128-byte-swizzled K-major layout of the MMA.
+//   P      over the cluster as above, written as two more operands of that layout.
+//   P B^T  [128 x 64] twice in TMEM: while one block of columns is multiplied, the warps add
+//          base to the one before.  A warp copies its 32 rows x 32 columns of base ahead into
+//          shared memory, adds a row per thread there, as TMEM gives it, and stores 64 bytes
+//          of eight rows at a time.  (32 bytes of 32 rows, straight from and to registers:
+//          113 us instead of XX at 8192 tokens, rank 64.)
 constexpr int kStages = 3, kWideRows = 128;
 
 template <int RP>
 struct WideCfg {
-  static constexpr int LDP = RP + 4, LDH = RP + 8;
+  static constexpr int LDP = RP + 4;
   static constexpr int KSTAGE = (kWideRows + RP) * 128;     // 64 columns of X and A
+  static constexpr int KB = (RP + 63) / 64;                 // blocks of 64 rank columns
   static constexpr int NB = 64;                             // rows of B in a block
-  static constexpr int LDB = 2 * RP + 16;                   // bytes between them: ldmatrix without conflicts
-  static constexpr int NSTAGE = NB * LDB;
-  static constexpr int BSTAGE = kWideRows * 2 * NB;         // a block of base
-  static constexpr int PART = kWideRows * LDP * 4;
-  // [part, then stages of base | stages of B], over the stages of X and A; then P
+  static constexpr int NSTAGE = KB * NB * 128;
+  static constexpr int PART = (kWideRows * LDP * 4 + 1023) / 1024 * 1024;
+  static constexpr int BSTAGE = kWideRows * NB * 2;         // a block of base
+  // [part, then stages of base | stages of B], over the stages of X and A; then the two parts of P
   static constexpr int OFF_B = PART > kStages * BSTAGE ? PART : kStages * BSTAGE;
   static constexpr int FRONT = kStages * KSTAGE > OFF_B + kStages * NSTAGE ? kStages * KSTAGE : OFF_B + kStages * NSTAGE;
-  static constexpr int OFF_HI = FRONT, OFF_LO = OFF_HI + kWideRows * LDH * 2, OFF_POWER = OFF_LO + kWideRows * LDH * 2;
-  static constexpr int SMEM = OFF_POWER + kWideRows * 4;
+  static constexpr int PBYTES = KB * kWideRows * 128;
+  static constexpr int OFF_HI = FRONT, OFF_LO = OFF_HI + PBYTES, OFF_POWER = OFF_LO + PBYTES;
+  static constexpr int SMEM = OFF_POWER + kWideRows * 4 + 1024;   // the layout starts on 1024 bytes
+  static constexpr int COL_D = 128;                         // TMEM: X A^T from column 0, two blocks of P B^T from here
+  static constexpr int TMEM = 256;
 };
 
-__device__ __forceinline__ void ldmatrix_x4_at(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3) : "r"(addr) : "memory");
+// Byte of 16-bit column `col` of row `row` in blocks of 64 columns, 128-byte swizzle.
+__device__ __forceinline__ uint32_t swizzled(int rows, int row, int col) {
+  return static_cast<uint32_t>((col >> 6) * rows * 128 + row * 128 + ((((col >> 3) & 7) ^ (row & 7)) << 4) + (col & 7) * 2);
 }
+
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 template <bool BF16, int RP>
 __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_wide_kernel(LoraKArgs args) {
   using Cf = WideCfg<RP>;
-  constexpr int NB8 = RP / 8;
   const LoraArgs& a = args.a;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t raw[];
   __shared__ int tokens[kWideRows];
   __shared__ float block_scale;
+  __shared__ uint64_t bars[kStages + 2];                    // a stage of X and A is read; a block of P B^T is there
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile uint32_t abort_word;
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
-  const int q = lane >> 2, c = lane & 3;
   const int C = static_cast<int>(gridDim.z), rank = static_cast<int>(blockIdx.z);
+  uint8_t* smem = raw + ((1024u - (ptx::smem_u32(raw) & 1023u)) & 1023u);   // the same offset in every CTA
   float* part = reinterpret_cast<float*>(smem);
-  uint16_t *hi = reinterpret_cast<uint16_t*>(smem + Cf::OFF_HI), *lo = reinterpret_cast<uint16_t*>(smem + Cf::OFF_LO);
   float* power = reinterpret_cast<float*>(smem + Cf::OFF_POWER);
   const uint32_t base_s = ptx::smem_u32(smem);
+  auto kbar = [&](int s) { return ptx::smem_u32(&bars[s]); };
+  auto dbar = [&](int d) { return ptx::smem_u32(&bars[kStages + d]); };
+  if (tid == 0) {
+    for (int i = 0; i < kStages + 2; ++i) ptx::mbar_init(ptx::smem_u32(&bars[i]), 1);
+    abort_word = 0u;
+    ptx::fence_mbar_init();
+  }
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
 
@@ -449,15 +474,22 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_wide_kern
   }
   if (bad) atomicOr(a.status, FGF8_DEVERR_INPUT);
   if (tid == 0) block_scale = a.scale != nullptr && g >= 0 ? ptx::ld_global(a.scale + g) : 1.0f;
-  __syncthreads();
   if (g < 0) {                                              // the same for every CTA of the cluster
     others.fill();
     return;
   }
+  if (warp == 1) {
+    tc_alloc<1>(ptx::smem_u32(&tmem_slot), Cf::TMEM);
+    ptx::tc_fence_before();
+  }
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *const_cast<volatile uint32_t*>(&tmem_slot);
+  PairWaitCtl ctl{&abort_word, 0u, a.status, args.timeout_ns, FGF8_DEVERR_ROLE_MMA};
 
   const uint16_t* ag = static_cast<const uint16_t*>(a.A) + static_cast<size_t>(g) * a.r * a.K;
   const uint16_t* bg = static_cast<const uint16_t*>(a.B) + static_cast<size_t>(g) * a.N * a.r;
-  const int wm = warp & 3, wh = warp >> 2;                  // this warp's 32 tokens, its half of K or N
+  constexpr uint32_t kFmt = BF16 ? 1u : 0u;
 
   // ------------------------------------------------------------ X A^T over a share of K
   const int ksteps = (a.K + 63) / 64;
@@ -472,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_wide_kern
   auto load_k = [&](int ks, int stage) {
     const int k = ks * 64 + pcol * 8;
     const bool in = ks < ks1 && k < a.K;
-    const uint32_t to = base_s + static_cast<uint32_t>(stage * Cf::KSTAGE) + static_cast<uint32_t>(prow * 128 + ((pcol ^ (prow & 7)) << 4));
+    const uint32_t to = base_s + static_cast<uint32_t>(stage * Cf::KSTAGE) + swizzled(0, prow, 8 * pcol);
     if (ks < ks1) {
 #pragma unroll
       for (int i = 0; i < kWideRows / 32; ++i) {
@@ -492,163 +524,194 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_wide_kern
   };
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) load_k(ks0 + s, s);
-  float acc[2][NB8][4] = {};
-  int stage = 0;
+  bool ok = true;
+  int stage = 0, last = kStages - 1;                        // this step's stage and the one before it
+  uint32_t phase = 0;                                       // of the stage before
   for (int ks = ks0; ks < ks1; ++ks) {
     gemv::cp_wait<kStages - 2>();
-    __syncthreads();                                        // the stage is there, and everybody is done with the one before
-    load_k(ks + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
-    const uint32_t sx = base_s + static_cast<uint32_t>(stage * Cf::KSTAGE), sa = sx + kWideRows * 128;
+    ptx::fence_proxy_async_smem();
+    __syncthreads();                                        // the stage is there
+    if (warp == 0) {
+      if (lane == 0 && ok) {
+        const uint32_t s = base_s + static_cast<uint32_t>(stage * Cf::KSTAGE);
+        const uint64_t xd = smem_desc_sw128(s), ad = smem_desc_sw128(s + kWideRows * 128);
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      const int piece = 4 * wh + 2 * kk;                    // the two 16-byte pieces of 16 columns
-      uint32_t xf[2][4];
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const int row = 32 * wm + 16 * m + (lane & 15);
-        ldmatrix_x4_at(sx + static_cast<uint32_t>(row * 128 + (((piece + (lane >> 4)) ^ (row & 7)) << 4)), xf[m][0], xf[m][1], xf[m][2], xf[m][3]);
+        for (int k = 0; k < 4; ++k)
+          ptx::mma_f16(tmem, xd + 2 * k, ad + 2 * k, idesc_dense(kFmt, kFmt, RP, 128), ks > ks0 || k > 0 ? 1u : 0u);
+        ptx::mma_commit(kbar(stage));
       }
-#pragma unroll
-      for (int b = 0; b < NB8; b += 2) {
-        const int row = 8 * b + (lane & 7) + ((lane >> 4) << 3);
-        uint32_t w0, w1, w2, w3;
-        ldmatrix_x4_at(sa + static_cast<uint32_t>(row * 128 + (((piece + ((lane >> 3) & 1)) ^ (row & 7)) << 4)), w0, w1, w2, w3);
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          gemv::mma16816<BF16>(acc[m][b], xf[m][0], xf[m][1], xf[m][2], xf[m][3], w0, w1);
-          gemv::mma16816<BF16>(acc[m][b + 1], xf[m][0], xf[m][1], xf[m][2], xf[m][3], w2, w3);
-        }
-      }
+      __syncwarp();
     }
+    if (ks > ks0 && ok) ok = pwait(kbar(last), phase, ctl); // the stage before has been read
+    load_k(ks + kStages - 1, last);
+    if (ks > ks0 && last == kStages - 1) phase ^= 1u;
+    last = stage;
     if (++stage == kStages) stage = 0;
   }
   gemv::cp_wait<0>();
+  if (ks1 > ks0 && ok) ok = pwait(kbar(last), phase, ctl);
   __syncthreads();
-  // the halves of K meet in shared memory
+  ptx::tc_fence_after();
+  const int row = 32 * (warp & 3) + lane, half = warp >> 2; // this thread's row, and half of the columns
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+  if (RP >= 32 || half == 0) {
+    constexpr int COLS = RP >= 32 ? RP / 2 : 16, STEP = COLS < 32 ? COLS : 32;
 #pragma unroll
-  for (int half = 1; half >= 0; --half) {
-    if (wh == half) {
+    for (int c = 0; c < COLS; c += STEP) {
+      uint32_t v[STEP];
+      tmem_ld_chunk(lanes + static_cast<uint32_t>(half * COLS + c), v);
+      ptx::tmem_wait_ld();
+      ptx::reg_fence(v);
+      float4* to = reinterpret_cast<float4*>(part + row * Cf::LDP + half * COLS + c);
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int b = 0; b < NB8; ++b)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float2* p = reinterpret_cast<float2*>(part + (32 * wm + 16 * m + 8 * e + q) * Cf::LDP + 8 * b + 2 * c);
-            float2 v = make_float2(acc[m][b][2 * e], acc[m][b][2 * e + 1]);
-            if (half == 0) {
-              const float2 o = *p;
-              v.x += o.x;
-              v.y += o.y;
-            }
-            *p = v;
-          }
+      for (int i = 0; i < STEP / 4; ++i)
+        to[i] = ks1 > ks0 ? make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]))
+                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
-    __syncthreads();
   }
+  __syncthreads();
 
   // ------------------------------------------------------------ P B^T over a share of N
   const int nblocks = (a.N + Cf::NB - 1) / Cf::NB;
   const int nb0 = static_cast<int>(static_cast<long long>(nblocks) * rank / C), nb1 = static_cast<int>(static_cast<long long>(nblocks) * (rank + 1) / C);
-  // row 8 x + 2 j + e of 32 goes to 8 j + 2 x + e: the eight rows of an MMA side by side, and a
-  // lane's results of four MMAs are eight neighbours
   auto load_n = [&](int nb, int s) {
     constexpr int PIECES = RP / 8;                          // of a row
     if (nb < nb1) {
 #pragma unroll
       for (int i = tid; i < Cf::NB * PIECES; i += kThreads) {
-        const int row = i / PIECES, piece = i % PIECES, n = nb * Cf::NB + row;
-        const int at = (row & 32) + ((row >> 1) & 3) * 8 + ((row >> 3) & 3) * 2 + (row & 1);
+        const int brow = i / PIECES, piece = i % PIECES, n = nb * Cf::NB + brow;
         const bool have = n < a.N && 8 * piece < a.r;
-        gemv::cp16(base_s + Cf::OFF_B + static_cast<uint32_t>(s * Cf::NSTAGE + at * Cf::LDB + piece * 16),
+        gemv::cp16(base_s + Cf::OFF_B + static_cast<uint32_t>(s * Cf::NSTAGE) + swizzled(Cf::NB, brow, 8 * piece),
                    have ? bg + static_cast<size_t>(n) * a.r + 8 * piece : bg, have);
       }
     }
-    gemv::cp_commit();
   };
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) load_n(nb0 + s, s);
+  for (int s = 0; s < kStages - 1; ++s) {
+    load_n(nb0 + s, s);
+    gemv::cp_commit();
+  }
   if (C > 1) cluster_sync_all();
-  exchange_rows<BF16, RP>(part, hi, lo, power, kWideRows, &block_scale, kWideRows, C, rank);
+  exchange_rows<BF16, RP>(part, power, kWideRows, &block_scale, kWideRows, C, rank, [&](int prow_of, int col, uint32_t& at_h, uint32_t& at_l) {
+    at_h = base_s + Cf::OFF_HI + swizzled(kWideRows, prow_of, col);
+    at_l = at_h + Cf::PBYTES;
+  });
+  fence_proxy_async_all();                                  // the MMAs of every CTA read what was written
   if (C > 1) cluster_sync_all(); else __syncthreads();      // and nothing remote is touched behind this
+  fence_proxy_async_all();
 
-  int t[4];                                                 // tokens of rows q, q + 8, q + 16, q + 24 of the 32
-  float up[4];
+  const float up = power[row];
+  // base of this warp's rows and half of a block's columns: 16-byte piece p of row i stands at
+  // p ^ turn(i), in different banks both for eight rows and for four pieces of two rows
+  auto turn = [](int i) { return ((i & 1) << 2) | ((i >> 1) & 3); };
+  const int piece = 4 * half + (lane & 3);                  // what this lane copies and stores of rows 8 i + lane / 4
+  int token[4];
+  uint32_t at[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    t[i] = tokens[32 * wm + 8 * i + q];
-    up[i] = power[32 * wm + 8 * i + q];
+    const int r = 32 * (warp & 3) + 8 * i + (lane >> 2);
+    token[i] = tokens[r];
+    at[i] = static_cast<uint32_t>(r * 128 + ((piece ^ turn(r)) << 4));
   }
-  const int off = 32 * wh + 8 * c;                          // this lane's columns of a block
-  // 16-byte piece p of row i of a block of base stands at p ^ turn(i): the pieces that eight
-  // lanes read together are in different banks
-  auto turn = [](int row) { return ((row & 1) << 2) | ((row >> 1) & 3); };
-  int brow[kWideRows / 32];
-#pragma unroll
-  for (int i = 0; i < kWideRows / 32; ++i) brow[i] = a.base != nullptr ? tokens[prow + 32 * i] : -1;
   auto load_base = [&](int nb, int s) {
-    const int n0 = nb * Cf::NB + 8 * pcol;
+    const int n = nb * Cf::NB + 8 * piece;
     if (nb < nb1) {
 #pragma unroll
-      for (int i = 0; i < kWideRows / 32; ++i) {
-        const bool have = n0 < a.N && brow[i] >= 0;
-        const uint16_t* from = have ? static_cast<const uint16_t*>(a.base) + static_cast<size_t>(brow[i]) * a.ldb + n0 : bg;
-        gemv::cp16(base_s + static_cast<uint32_t>(s * Cf::BSTAGE + (prow + 32 * i) * 128 + ((pcol ^ turn(prow)) << 4)), from, have);
+      for (int i = 0; i < 4; ++i) {
+        const bool have = a.base != nullptr && token[i] >= 0 && n < a.N;
+        const uint16_t* from = have ? static_cast<const uint16_t*>(a.base) + static_cast<size_t>(token[i]) * a.ldb + n : bg;
+        gemv::cp16(base_s + static_cast<uint32_t>(s * Cf::BSTAGE) + at[i], from, have);
       }
     }
-    gemv::cp_commit();
+  };
+  auto finish = [&](int nb, int d, uint32_t phase_d, int s) {   // block nb from accumulator d and its stage
+    if (ok) ok = pwait(dbar(d), phase_d, ctl);
+    ptx::tc_fence_after();
+    uint32_t v[32];
+    tmem_ld_chunk(lanes + static_cast<uint32_t>(Cf::COL_D + Cf::NB * d + 32 * half), v);
+    ptx::tmem_wait_ld();
+    ptx::reg_fence(v);
+    ptx::tc_fence_before();
+    uint8_t* mine = smem + s * Cf::BSTAGE;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint8_t* p = mine + row * 128 + (((4 * half + i) ^ turn(row)) << 4);
+      uint32_t b[4], o[4];
+      gemv::lds128(p, b);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        o[j] = pack_2x16(fmaf(up, __uint_as_float(v[8 * i + 2 * j]), act::to_float(b[j] & 0xFFFFu, BF16)),
+                         fmaf(up, __uint_as_float(v[8 * i + 2 * j + 1]), act::to_float(b[j] >> 16, BF16)), BF16);
+      *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    __syncwarp();
+    const int n = nb * Cf::NB + 8 * piece;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (token[i] >= 0 && n < a.N && ok) {
+        uint32_t o[4];
+        gemv::lds128(mine + at[i], o);
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + static_cast<size_t>(token[i]) * a.ldo + n) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    __syncwarp();                                           // the stage is free, and whole-warp instructions follow
   };
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) load_base(nb0 + s, s);
-  const uint32_t sh = base_s + Cf::OFF_HI + static_cast<uint32_t>((32 * wm + (lane & 15)) * Cf::LDH * 2 + (lane >> 4) * 16);
+  for (int s = 0; s < kStages - 1; ++s) {
+    load_base(nb0 + s, s);
+    gemv::cp_commit();
+  }
   stage = 0;
-  for (int nb = nb0; nb < nb1; ++nb) {
-    // groups in order: two of B, two of base, then for each block its B and base together
+  for (int nb = nb0; nb <= nb1; ++nb) {                     // one more round, which only finishes the last block
+    // groups of copies in order: two of B, two of base, then for each block its B and base
+    // together.  Block nb needs its B, and base of the block before.
     if (nb == nb0)
-      gemv::cp_wait<kStages - 2>();
+      gemv::cp_wait<2 * (kStages - 1) - 1>();
+    else if (nb == nb0 + 1)
+      gemv::cp_wait<kStages - 1>();
     else
-      gemv::cp_wait<2 * (kStages - 2)>();
-    __syncthreads();
-    const int ahead = stage == 0 ? kStages - 1 : stage - 1;
-    load_n(nb + kStages - 1, ahead);
-    load_base(nb + kStages - 1, ahead);
-    const uint32_t sb = base_s + Cf::OFF_B + static_cast<uint32_t>(stage * Cf::NSTAGE + (32 * wh + (lane & 7) + ((lane >> 4) << 3)) * Cf::LDB + ((lane >> 3) & 1) * 16);
-    float d[2][4][4] = {};
+      gemv::cp_wait<kStages - 2>();
+    const int d = (nb - nb0) & 1, before = stage == 0 ? kStages - 1 : stage - 1;
+    if (nb < nb1) {
+      ptx::fence_proxy_async_smem();
+      __syncthreads();
+      if (warp == 0) {
+        if (lane == 0 && ok) {
+          ptx::tc_fence_after();
+          const uint32_t s = base_s + Cf::OFF_B + static_cast<uint32_t>(stage * Cf::NSTAGE);
+          const uint32_t to = tmem + static_cast<uint32_t>(Cf::COL_D + Cf::NB * d);
 #pragma unroll
-    for (int k = 0; k < RP / 16; ++k) {
-      uint32_t bf[4][2];
-      ldmatrix_x4_at(sb + static_cast<uint32_t>(k * 32), bf[0][0], bf[0][1], bf[1][0], bf[1][1]);
-      ldmatrix_x4_at(sb + static_cast<uint32_t>(16 * Cf::LDB + k * 32), bf[2][0], bf[2][1], bf[3][0], bf[3][1]);
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int part_of = 0; part_of < 2; ++part_of) {     // P rounded, and its rest
-          uint32_t pf[4];
-          ldmatrix_x4_at(sh + static_cast<uint32_t>((part_of ? Cf::OFF_LO - Cf::OFF_HI : 0) + m * 16 * Cf::LDH * 2 + k * 32), pf[0], pf[1], pf[2], pf[3]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) gemv::mma16816<BF16>(d[m][j], pf[0], pf[1], pf[2], pf[3], bf[j][0], bf[j][1]);
+          for (int k = 0; k < RP / 16; ++k) {
+            const uint64_t bd = smem_desc_sw128(s + static_cast<uint32_t>((k >> 2) * Cf::NB * 128)) + 2 * (k & 3);
+            const uint32_t p = base_s + Cf::OFF_HI + static_cast<uint32_t>((k >> 2) * kWideRows * 128);
+            ptx::mma_f16(to, smem_desc_sw128(p) + 2 * (k & 3), bd, idesc_dense(kFmt, kFmt, Cf::NB, 128), k > 0 ? 1u : 0u);
+            ptx::mma_f16(to, smem_desc_sw128(p + Cf::PBYTES) + 2 * (k & 3), bd, idesc_dense(kFmt, kFmt, Cf::NB, 128), 1u);
+          }
+          ptx::mma_commit(dbar(d));
         }
-    }
-    const int n0 = nb * Cf::NB + off;
-    if (n0 < a.N) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (t[i] < 0) continue;
-        const int row = 32 * wm + 8 * i + q;
-        uint32_t bw[4], ow[4];
-        gemv::lds128(smem + stage * Cf::BSTAGE + row * 128 + (((4 * wh + c) ^ turn(row)) << 4), bw);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          ow[j] = pack_2x16(fmaf(up[i], d[i >> 1][j][2 * (i & 1)], act::to_float(bw[j] & 0xFFFFu, BF16)),
-                            fmaf(up[i], d[i >> 1][j][2 * (i & 1) + 1], act::to_float(bw[j] >> 16, BF16)), BF16);
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + static_cast<size_t>(t[i]) * a.ldo + n0) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+        __syncwarp();
       }
+    } else {
+      __syncwarp();                                         // this warp's copies of base are there
     }
-    __syncwarp();                                           // whole-warp instructions follow
+    if (nb > nb0) finish(nb - 1, d ^ 1, static_cast<uint32_t>((nb - 1 - nb0) >> 1) & 1u, before);
+    load_n(nb + kStages - 1, before);
+    load_base(nb + kStages - 1, before);
+    gemv::cp_commit();
     if (++stage == kStages) stage = 0;
   }
   gemv::cp_wait<0>();
+  __syncwarp();
   others.fill();
+  // every MMA has completed, unless a wait ran out: then they get a while before shared memory
+  // and TMEM are given back
+  if (__syncthreads_or(abort_word != 0u ? 1 : 0)) {
+    const uint64_t since = ptx::globaltimer();
+    while (ptx::globaltimer() - since < 200000ull) __nanosleep(1000);
+  }
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    tc_dealloc<1>(tmem, Cf::TMEM);
+  }
 }
 
 // Shared memory of a CTA with `tiles` tiles.
@@ -700,6 +763,7 @@ int launch_tiles(const LoraArgs& a, cudaStream_t stream) {
   static PerDevice<int> ready;
   LoraKArgs k;
   k.a = a;
+  k.timeout_ns = 0;                                         // this form waits for no barrier
   const long long tiles = a.M / 16, sms = device_sm_count();
   const long long nblocks = (a.N + 31) / 32;
   // a cluster's CTAs split K and N: eight, fewer where there is too little to split
@@ -722,6 +786,7 @@ int launch_wide(const LoraArgs& a, cudaStream_t stream) {
   LoraKArgs k;
   k.a = a;
   k.tiles = 8;
+  k.timeout_ns = wait_timeout_ns();
   // the cluster that takes the least time in waves of what fits the device, each as long as the
   // share of a CTA and, for the start and the exchange of P, a fortieth of a whole block
   const long long groups = a.M / kWideRows, slots = static_cast<long long>(device_sm_count()) * (RP <= 64 ? 2 : 1);
