@@ -150,7 +150,7 @@ struct Others {
 
   __device__ __forceinline__ Others(const LoraArgs& args, uint32_t w, uint32_t n)
       : a(args), worker(w), workers(n), parts((static_cast<uint32_t>(args.N) / 8 + 32 * kPart - 1) / (32 * kPart)),
-        items(args.base == args.out ? 0u : (static_cast<uint32_t>(args.T) + 31) / 32 * parts) {
+        items(args.base == args.out || n == 0u ? 0u : (static_cast<uint32_t>(args.T) + 31) / 32 * parts) {
     first = worker < items && look(worker);
   }
   // whether this lane's token of an item is one
@@ -392,26 +392,31 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_kernel(Lo
 // ----------------------------------------------------------------- many tokens of an adapter
 // The same two products for blocks of 128 rows with one adapter, on tcgen05: a byte of A or B
 // serves 128 tokens, and the multiplications (2 r of them, with P in two parts 3 r, for each
-// element of X, base and out) are off the warps' hands, which copy and add.
-//   X A^T  [128 x r] in TMEM, K in steps of 64: rows of X (gathered by token) and of A come by
-//          cp.async, kStages deep, into the 128-byte-swizzled K-major layout of the MMA.
-//   P      over the cluster as above, written as two more operands of that layout.
-//   P B^T  [128 x 64] twice in TMEM: while one block of columns is multiplied, the warps add
-//          base to the one before.  A warp copies its 32 rows x 32 columns of base ahead into
-//          shared memory, adds a row per thread there, as TMEM gives it, and stores 64 bytes
-//          of eight rows at a time.  (32 bytes of 32 rows, straight from and to registers:
-//          113 us instead of XX at 8192 tokens, rank 64.)
-constexpr int kStages = 3, kWideRows = 128;
+// element of X, base and out) are off the warps' hands.
+//   X A^T  [128 x r] in TMEM, K in steps of 64 through a ring of kStages: the tokens' rows of X
+//          by cp.async from four warps, a tile of A by TMA.  (TMA's tile::gather4 takes some 80
+//          cycles for four rows of 128 bytes: 137 us for the calls below, whatever the rank.)
+//   P      over the cluster as above, written as two more operands.
+//   P B^T  [128 x 64] twice in TMEM, through another ring in its place: B and the tokens' rows
+//          of base by cp.async.  Four warps add base to the even blocks and four to the odd ones,
+//          a row per thread as TMEM gives it, put the sums where base stood, and store 128 bytes
+//          of four rows at a time.
+// All operands are K-major with 128-byte swizzle, rows of 64 columns.  Warps that copy, multiply
+// and add wait for one another on mbarriers only: with a block-wide barrier for each step the
+// same work took 86 us, and a third of that went to threads whose proxy fence waited for their
+// own copies.  8192 tokens of 8 adapters, 7168 x 7168: 66 us at rank 16, 73 at 64 (5.1 TB/s),
+// 100 at 128, where one CTA fills the SM; the bytes alone take 54 to 57.
+constexpr int kStages = 3, kWideRows = 128, kCopyWarps = 4;
+constexpr int kWideThreads = kThreads + 32 * kCopyWarps + 32;   // sums and adding, copies, MMAs
 
 template <int RP>
 struct WideCfg {
   static constexpr int LDP = RP + 4;
-  static constexpr int KSTAGE = (kWideRows + RP) * 128;     // 64 columns of X and A
+  static constexpr int XBYTES = kWideRows * 128, KSTAGE = XBYTES + RP * 128;   // 64 columns of X and of A
   static constexpr int KB = (RP + 63) / 64;                 // blocks of 64 rank columns
   static constexpr int NB = 64;                             // rows of B in a block
-  static constexpr int NSTAGE = KB * NB * 128;
+  static constexpr int NSTAGE = KB * NB * 128, BSTAGE = kWideRows * NB * 2;    // a block of B, of base
   static constexpr int PART = (kWideRows * LDP * 4 + 1023) / 1024 * 1024;
-  static constexpr int BSTAGE = kWideRows * NB * 2;         // a block of base
   // [part, then stages of base | stages of B], over the stages of X and A; then the two parts of P
   static constexpr int OFF_B = PART > kStages * BSTAGE ? PART : kStages * BSTAGE;
   static constexpr int FRONT = kStages * KSTAGE > OFF_B + kStages * NSTAGE ? kStages * KSTAGE : OFF_B + kStages * NSTAGE;
@@ -426,17 +431,26 @@ struct WideCfg {
 __device__ __forceinline__ uint32_t swizzled(int rows, int row, int col) {
   return static_cast<uint32_t>((col >> 6) * rows * 128 + row * 128 + ((((col >> 3) & 7) ^ (row & 7)) << 4) + (col & 7) * 2);
 }
-
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+// 16 bytes of a row into shared memory, zeros where there are none; the row's next bytes are
+// asked into L2 with them.
+__device__ __forceinline__ void cp16_row(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// This thread's arrival on a barrier, when all its cp.async so far have come.
+__device__ __forceinline__ void cp_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 
 template <bool BF16, int RP>
-__global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_wide_kernel(LoraKArgs args) {
+__global__ void __launch_bounds__(kWideThreads, RP <= 64 ? 2 : 1) lora_f16_wide_kernel(const __grid_constant__ CUtensorMap map_a,
+                                                                                       const __grid_constant__ LoraKArgs args) {
   using Cf = WideCfg<RP>;
   const LoraArgs& a = args.a;
   extern __shared__ __align__(128) uint8_t raw[];
-  __shared__ int tokens[kWideRows];
+  __shared__ int tokens[kWideRows];                         // -1 where a row has none
   __shared__ float block_scale;
-  __shared__ uint64_t bars[kStages + 2];                    // a stage of X and A is read; a block of P B^T is there
+  __shared__ uint64_t bars[4 * kStages + 5];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t abort_word;
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
@@ -445,17 +459,34 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_wide_kern
   float* part = reinterpret_cast<float*>(smem);
   float* power = reinterpret_cast<float*>(smem + Cf::OFF_POWER);
   const uint32_t base_s = ptx::smem_u32(smem);
-  auto kbar = [&](int s) { return ptx::smem_u32(&bars[s]); };
-  auto dbar = [&](int d) { return ptx::smem_u32(&bars[kStages + d]); };
+  auto bar = [&](int i) { return ptx::smem_u32(&bars[i]); };
+  auto kfull = [&](int s) { return bar(s); };               // a stage of X and A has come, has been read
+  auto kfree = [&](int s) { return bar(kStages + s); };
+  auto nfull = [&](int s) { return bar(2 * kStages + s); }; // a stage of B and base
+  auto nfree = [&](int s) { return bar(3 * kStages + s); };
+  auto dfull = [&](int d) { return bar(4 * kStages + d); }; // a block of P B^T is in TMEM, has been taken out
+  auto dfree = [&](int d) { return bar(4 * kStages + 2 + d); };
+  const uint32_t kdone = bar(4 * kStages + 4);              // X A^T is in TMEM
   if (tid == 0) {
-    for (int i = 0; i < kStages + 2; ++i) ptx::mbar_init(ptx::smem_u32(&bars[i]), 1);
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(kfull(s), 1 + 32 * kCopyWarps);
+      ptx::mbar_init(kfree(s), 1);
+      ptx::mbar_init(nfull(s), 32 * kCopyWarps);
+      ptx::mbar_init(nfree(s), 1 + kWarps / 2);
+    }
+    for (int d = 0; d < 2; ++d) {
+      ptx::mbar_init(dfull(d), 1);
+      ptx::mbar_init(dfree(d), kWarps / 2);
+    }
+    ptx::mbar_init(kdone, 1);
     abort_word = 0u;
     ptx::fence_mbar_init();
   }
+  if (warp == kWarps && lane == 0) ptx::prefetch_tmap(&map_a);
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
 
-  const Others others(a, cta_of_grid() * kWarps + warp, gridDim.x * gridDim.y * gridDim.z * kWarps);
+  const Others others(a, cta_of_grid() * kWarps + warp, warp < kWarps ? gridDim.x * gridDim.y * gridDim.z * kWarps : 0u);
   // the block's adapter and tokens
   const long long row0 = static_cast<long long>(blockIdx.x) * kWideRows;
   int g = ptx::ld_global(a.m_indices + row0);
@@ -478,237 +509,237 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_wide_kern
     others.fill();
     return;
   }
-  if (warp == 1) {
+  if (warp == kWarps + kCopyWarps) {
     tc_alloc<1>(ptx::smem_u32(&tmem_slot), Cf::TMEM);
     ptx::tc_fence_before();
   }
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *const_cast<volatile uint32_t*>(&tmem_slot);
-  PairWaitCtl ctl{&abort_word, 0u, a.status, args.timeout_ns, FGF8_DEVERR_ROLE_MMA};
-
-  const uint16_t* ag = static_cast<const uint16_t*>(a.A) + static_cast<size_t>(g) * a.r * a.K;
-  const uint16_t* bg = static_cast<const uint16_t*>(a.B) + static_cast<size_t>(g) * a.N * a.r;
+  PairWaitCtl ctl{&abort_word, 0u, a.status, args.timeout_ns, 0u};
   constexpr uint32_t kFmt = BF16 ? 1u : 0u;
 
-  // ------------------------------------------------------------ X A^T over a share of K
-  const int ksteps = (a.K + 63) / 64;
+  const int ksteps = (a.K + 63) / 64, nblocks = (a.N + Cf::NB - 1) / Cf::NB;
   const int ks0 = static_cast<int>(static_cast<long long>(ksteps) * rank / C), ks1 = static_cast<int>(static_cast<long long>(ksteps) * (rank + 1) / C);
-  const int prow = tid >> 3, pcol = tid & 7;                // the piece that this thread copies of every 32 rows
-  const uint16_t* xrow[kWideRows / 32];
+  const int nb0 = static_cast<int>(static_cast<long long>(nblocks) * rank / C), nb1 = static_cast<int>(static_cast<long long>(nblocks) * (rank + 1) / C);
+  // stage and parity of the i-th use of a ring
+  struct Ring {
+    int s = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+      if (++s == kStages) s = 0, phase ^= 1u;
+    }
+  };
+
+  if (warp >= kWarps && warp < kWarps + kCopyWarps) {
+    // ---------------------------------------------------------- copies
+    ctl.role_bit = FGF8_DEVERR_ROLE_PRODUCER;
+    constexpr int kRows = 4 * kCopyWarps;                   // copied together: 8 pieces of a row by 8 lanes
+    const int me = tid - kThreads, prow = me >> 3, pcol = me & 7;
+    const bool first = me == 0;                             // who also asks for the tiles of A
+    const uint16_t* from[kWideRows / kRows];                // this lane's pieces of its rows, at column 0
+    int bytes[kWideRows / kRows];                           // 16, or 0 for a row without a token
+    auto rows_of = [&](const void* matrix, long long ld) {
 #pragma unroll
-  for (int i = 0; i < kWideRows / 32; ++i) {
-    const int t = tokens[prow + 32 * i];
-    xrow[i] = t < 0 ? nullptr : static_cast<const uint16_t*>(a.X) + static_cast<size_t>(t) * a.ldx;
-  }
-  auto load_k = [&](int ks, int stage) {
-    const int k = ks * 64 + pcol * 8;
-    const bool in = ks < ks1 && k < a.K;
-    const uint32_t to = base_s + static_cast<uint32_t>(stage * Cf::KSTAGE) + swizzled(0, prow, 8 * pcol);
-    if (ks < ks1) {
-#pragma unroll
-      for (int i = 0; i < kWideRows / 32; ++i) {
-        const bool have = in && xrow[i] != nullptr;
-        gemv::cp16(to + static_cast<uint32_t>(i * 32 * 128), have ? xrow[i] + k : static_cast<const uint16_t*>(a.X), have);
+      for (int i = 0; i < kWideRows / kRows; ++i) {
+        const int t = tokens[prow + kRows * i];
+        bytes[i] = t >= 0 ? 16 : 0;
+        from[i] = static_cast<const uint16_t*>(matrix) + (t >= 0 ? static_cast<long long>(t) * ld : 0) + 8 * pcol;
       }
+    };
+    // 64 columns from `col` on
+    auto copy_rows = [&](uint32_t to, int col, int cols) {
+      const uint32_t at = to + swizzled(0, prow, 8 * pcol);
+      const bool in = col + 8 * pcol < cols;
 #pragma unroll
-      for (int i = 0; i < (RP + 31) / 32; ++i) {
-        const int row = prow + 32 * i;
-        if (row < RP) {
-          const bool have = in && row < a.r;
-          gemv::cp16(to + static_cast<uint32_t>((kWideRows + i * 32) * 128), have ? ag + static_cast<size_t>(row) * a.K + k : ag, have);
-        }
+      for (int i = 0; i < kWideRows / kRows; ++i)
+        cp16_row(at + static_cast<uint32_t>(i * kRows * 128), in ? from[i] + col : from[i], in ? bytes[i] : 0);
+    };
+    rows_of(a.X, a.ldx);
+    bool ok = true;
+    Ring r;
+    for (int ks = ks0; ks < ks1; ++ks) {
+      ok = pwait(kfree(r.s), r.phase ^ 1u, ctl);
+      if (!ok) break;
+      const uint32_t to = base_s + static_cast<uint32_t>(r.s * Cf::KSTAGE);
+      if (first) {
+        ptx::mbar_arrive_expect_tx(kfull(r.s), static_cast<uint32_t>(a.r * 128));
+        ptx::tma_load_2d(to + Cf::XBYTES, &map_a, kfull(r.s), ks * 64, g * a.r);
       }
+      copy_rows(to, ks * 64, a.K);
+      cp_arrive(kfull(r.s));
+      r.next();
+    }
+    // shared memory changes hands: B's stages when X A^T is done, base's when P has been exchanged
+    if (ok && ks1 > ks0) ok = pwait(kdone, 0u, ctl);
+    const uint16_t* bg = static_cast<const uint16_t*>(a.B) + static_cast<size_t>(g) * a.N * a.r;
+    auto load_b = [&](int nb, int s) {
+      constexpr int PIECES = RP / 8;                        // of a row
+#pragma unroll
+      for (int i = 0; i < Cf::NB * PIECES / (32 * kCopyWarps); ++i) {
+        const int at = me + 32 * kCopyWarps * i, brow = at / PIECES, piece = at % PIECES, n = nb * Cf::NB + brow;
+        const bool have = n < a.N && 8 * piece < a.r;
+        gemv::cp16(base_s + static_cast<uint32_t>(Cf::OFF_B + s * Cf::NSTAGE) + swizzled(Cf::NB, brow, 8 * piece),
+                   have ? bg + static_cast<size_t>(n) * a.r + 8 * piece : bg, have);
+      }
+    };
+    for (int s = 0; ok && s < kStages && nb0 + s < nb1; ++s) load_b(nb0 + s, s);
+    rows_of(a.base, a.ldb);
+    __syncwarp();
+    cluster_sync_all();
+    cluster_sync_all();
+    Ring n;
+    for (int nb = nb0; ok && nb < nb1; ++nb) {
+      if (nb >= nb0 + kStages) {
+        ok = pwait(nfree(n.s), n.phase ^ 1u, ctl);
+        if (!ok) break;
+        load_b(nb, n.s);
+      }
+      if (a.base != nullptr) copy_rows(base_s + static_cast<uint32_t>(n.s * Cf::BSTAGE), nb * Cf::NB, a.N);
+      cp_arrive(nfull(n.s));
+      n.next();
     }
     gemv::cp_commit();
-  };
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) load_k(ks0 + s, s);
-  bool ok = true;
-  int stage = 0, last = kStages - 1;                        // this step's stage and the one before it
-  uint32_t phase = 0;                                       // of the stage before
-  for (int ks = ks0; ks < ks1; ++ks) {
-    gemv::cp_wait<kStages - 2>();
-    ptx::fence_proxy_async_smem();
-    __syncthreads();                                        // the stage is there
-    if (warp == 0) {
-      if (lane == 0 && ok) {
-        const uint32_t s = base_s + static_cast<uint32_t>(stage * Cf::KSTAGE);
-        const uint64_t xd = smem_desc_sw128(s), ad = smem_desc_sw128(s + kWideRows * 128);
+    gemv::cp_wait<0>();
+    __syncwarp();
+  } else if (warp == kWarps + kCopyWarps) {
+    // ---------------------------------------------------------- MMAs
+    ctl.role_bit = FGF8_DEVERR_ROLE_MMA;
+    bool ok = true;
+    Ring r;
+    for (int ks = ks0; ks < ks1; ++ks) {
+      ok = pwait(kfull(r.s), r.phase, ctl);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      if (lane == 0) {
+        // the copies are for the tensor core; here, because a thread that fences waits for all
+        // its own copies under way
+        ptx::fence_proxy_async_smem();
+        const uint32_t s = base_s + static_cast<uint32_t>(r.s * Cf::KSTAGE);
+        const uint64_t xd = smem_desc_sw128(s), ad = smem_desc_sw128(s + Cf::XBYTES);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           ptx::mma_f16(tmem, xd + 2 * k, ad + 2 * k, idesc_dense(kFmt, kFmt, RP, 128), ks > ks0 || k > 0 ? 1u : 0u);
-        ptx::mma_commit(kbar(stage));
+        ptx::mma_commit(kfree(r.s));
+        if (ks + 1 == ks1) ptx::mma_commit(kdone);
       }
       __syncwarp();
+      r.next();
     }
-    if (ks > ks0 && ok) ok = pwait(kbar(last), phase, ctl); // the stage before has been read
-    load_k(ks + kStages - 1, last);
-    if (ks > ks0 && last == kStages - 1) phase ^= 1u;
-    last = stage;
-    if (++stage == kStages) stage = 0;
-  }
-  gemv::cp_wait<0>();
-  if (ks1 > ks0 && ok) ok = pwait(kbar(last), phase, ctl);
-  __syncthreads();
-  ptx::tc_fence_after();
-  const int row = 32 * (warp & 3) + lane, half = warp >> 2; // this thread's row, and half of the columns
-  const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-  if (RP >= 32 || half == 0) {
-    constexpr int COLS = RP >= 32 ? RP / 2 : 16, STEP = COLS < 32 ? COLS : 32;
+    cluster_sync_all();
+    cluster_sync_all();
+    fence_proxy_async_all();                                // P is read by the tensor core
+    Ring n;
+    for (int nb = nb0; ok && nb < nb1; ++nb) {
+      const int d = (nb - nb0) & 1;
+      ok = pwait(nfull(n.s), n.phase, ctl) && (nb < nb0 + 2 || pwait(dfree(d), (static_cast<uint32_t>(nb - nb0 - 2) >> 1) & 1u, ctl));
+      if (!ok) break;
+      ptx::tc_fence_after();
+      if (lane == 0) {
+        ptx::fence_proxy_async_smem();
+        const uint32_t s = base_s + Cf::OFF_B + static_cast<uint32_t>(n.s * Cf::NSTAGE);
+        const uint32_t to = tmem + static_cast<uint32_t>(Cf::COL_D + Cf::NB * d);
 #pragma unroll
-    for (int c = 0; c < COLS; c += STEP) {
-      uint32_t v[STEP];
-      tmem_ld_chunk(lanes + static_cast<uint32_t>(half * COLS + c), v);
-      ptx::tmem_wait_ld();
-      ptx::reg_fence(v);
-      float4* to = reinterpret_cast<float4*>(part + row * Cf::LDP + half * COLS + c);
-#pragma unroll
-      for (int i = 0; i < STEP / 4; ++i)
-        to[i] = ks1 > ks0 ? make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]))
-                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    }
-  }
-  __syncthreads();
-
-  // ------------------------------------------------------------ P B^T over a share of N
-  const int nblocks = (a.N + Cf::NB - 1) / Cf::NB;
-  const int nb0 = static_cast<int>(static_cast<long long>(nblocks) * rank / C), nb1 = static_cast<int>(static_cast<long long>(nblocks) * (rank + 1) / C);
-  auto load_n = [&](int nb, int s) {
-    constexpr int PIECES = RP / 8;                          // of a row
-    if (nb < nb1) {
-#pragma unroll
-      for (int i = tid; i < Cf::NB * PIECES; i += kThreads) {
-        const int brow = i / PIECES, piece = i % PIECES, n = nb * Cf::NB + brow;
-        const bool have = n < a.N && 8 * piece < a.r;
-        gemv::cp16(base_s + Cf::OFF_B + static_cast<uint32_t>(s * Cf::NSTAGE) + swizzled(Cf::NB, brow, 8 * piece),
-                   have ? bg + static_cast<size_t>(n) * a.r + 8 * piece : bg, have);
+        for (int k = 0; k < RP / 16; ++k) {
+          const uint64_t bd = smem_desc_sw128(s + static_cast<uint32_t>((k >> 2) * Cf::NB * 128)) + 2 * (k & 3);
+          const uint32_t p = base_s + Cf::OFF_HI + static_cast<uint32_t>((k >> 2) * kWideRows * 128);
+          ptx::mma_f16(to, smem_desc_sw128(p) + 2 * (k & 3), bd, idesc_dense(kFmt, kFmt, Cf::NB, 128), k > 0 ? 1u : 0u);
+          ptx::mma_f16(to, smem_desc_sw128(p + Cf::PBYTES) + 2 * (k & 3), bd, idesc_dense(kFmt, kFmt, Cf::NB, 128), 1u);
+        }
+        ptx::mma_commit(nfree(n.s));
+        ptx::mma_commit(dfull(d));
       }
+      __syncwarp();
+      n.next();
     }
-  };
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) {
-    load_n(nb0 + s, s);
-    gemv::cp_commit();
-  }
-  if (C > 1) cluster_sync_all();
-  exchange_rows<BF16, RP>(part, power, kWideRows, &block_scale, kWideRows, C, rank, [&](int prow_of, int col, uint32_t& at_h, uint32_t& at_l) {
-    at_h = base_s + Cf::OFF_HI + swizzled(kWideRows, prow_of, col);
-    at_l = at_h + Cf::PBYTES;
-  });
-  fence_proxy_async_all();                                  // the MMAs of every CTA read what was written
-  if (C > 1) cluster_sync_all(); else __syncthreads();      // and nothing remote is touched behind this
-  fence_proxy_async_all();
-
-  const float up = power[row];
-  // base of this warp's rows and half of a block's columns: 16-byte piece p of row i stands at
-  // p ^ turn(i), in different banks both for eight rows and for four pieces of two rows
-  auto turn = [](int i) { return ((i & 1) << 2) | ((i >> 1) & 3); };
-  const int piece = 4 * half + (lane & 3);                  // what this lane copies and stores of rows 8 i + lane / 4
-  int token[4];
-  uint32_t at[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 32 * (warp & 3) + 8 * i + (lane >> 2);
-    token[i] = tokens[r];
-    at[i] = static_cast<uint32_t>(r * 128 + ((piece ^ turn(r)) << 4));
-  }
-  auto load_base = [&](int nb, int s) {
-    const int n = nb * Cf::NB + 8 * piece;
-    if (nb < nb1) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool have = a.base != nullptr && token[i] >= 0 && n < a.N;
-        const uint16_t* from = have ? static_cast<const uint16_t*>(a.base) + static_cast<size_t>(token[i]) * a.ldb + n : bg;
-        gemv::cp16(base_s + static_cast<uint32_t>(s * Cf::BSTAGE) + at[i], from, have);
-      }
-    }
-  };
-  auto finish = [&](int nb, int d, uint32_t phase_d, int s) {   // block nb from accumulator d and its stage
-    if (ok) ok = pwait(dbar(d), phase_d, ctl);
+  } else {
+    // ---------------------------------------------------------- sums, exchange, adding
+    ctl.role_bit = FGF8_DEVERR_ROLE_EPILOGUE;
+    const int row = 32 * (warp & 3) + lane, half = warp >> 2;   // this thread's row, and half of the columns
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    bool ok = ks1 == ks0 || pwait(kdone, 0u, ctl);
     ptx::tc_fence_after();
-    uint32_t v[32];
-    tmem_ld_chunk(lanes + static_cast<uint32_t>(Cf::COL_D + Cf::NB * d + 32 * half), v);
-    ptx::tmem_wait_ld();
-    ptx::reg_fence(v);
-    ptx::tc_fence_before();
-    uint8_t* mine = smem + s * Cf::BSTAGE;
+    if (RP >= 32 || half == 0) {
+      constexpr int COLS = RP >= 32 ? RP / 2 : 16, STEP = COLS < 32 ? COLS : 32;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint8_t* p = mine + row * 128 + (((4 * half + i) ^ turn(row)) << 4);
-      uint32_t b[4], o[4];
-      gemv::lds128(p, b);
+      for (int c = 0; c < COLS; c += STEP) {
+        uint32_t v[STEP];
+        tmem_ld_chunk(lanes + static_cast<uint32_t>(half * COLS + c), v);
+        ptx::tmem_wait_ld();
+        ptx::reg_fence(v);
+        float4* to = reinterpret_cast<float4*>(part + row * Cf::LDP + half * COLS + c);
+        // rank columns past r hold what the stage's last rows happened to be
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        o[j] = pack_2x16(fmaf(up, __uint_as_float(v[8 * i + 2 * j]), act::to_float(b[j] & 0xFFFFu, BF16)),
-                         fmaf(up, __uint_as_float(v[8 * i + 2 * j + 1]), act::to_float(b[j] >> 16, BF16)), BF16);
-      *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int i = 0; i < STEP / 4; ++i)
+          to[i] = ks1 > ks0 && half * COLS + c + 4 * i < a.r
+                      ? make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]))
+                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+    }
+    cluster_sync_all();
+    exchange_rows<BF16, RP>(part, power, kWideRows, &block_scale, kWideRows, C, rank, [&](int r, int col, uint32_t& at_h, uint32_t& at_l) {
+      at_h = base_s + Cf::OFF_HI + swizzled(kWideRows, r, col);
+      at_l = at_h + Cf::PBYTES;
+    });
+    fence_proxy_async_all();                                // the MMAs of every CTA read P; copies overwrite the sums
+    cluster_sync_all();                                     // and nothing remote is touched behind this
+    const float up = power[row];
+    // four warps take the even blocks, four the odd ones
+    int token[8];                                           // of rows 4 i + lane / 8, of which this lane stores 16 bytes
+#pragma unroll
+    for (int i = 0; i < 8; ++i) token[i] = tokens[32 * (warp & 3) + 4 * i + (lane >> 3)];
+    Ring n;
+    if (half == 1) n.next();
+    for (int nb = nb0 + half; ok && nb < nb1; nb += 2) {
+      const int d = half;
+      ok = pwait(dfull(d), (static_cast<uint32_t>(nb - nb0) >> 1) & 1u, ctl) && pwait(nfull(n.s), n.phase, ctl);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      uint8_t* mine = smem + n.s * Cf::BSTAGE;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t v[32];
+        tmem_ld_chunk(lanes + static_cast<uint32_t>(Cf::COL_D + Cf::NB * d + 32 * c), v);
+        ptx::tmem_wait_ld();
+        ptx::reg_fence(v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint8_t* p = mine + swizzled(0, row, 32 * c + 8 * i);
+          uint32_t b[4] = {0u, 0u, 0u, 0u}, o[4];
+          if (a.base != nullptr) gemv::lds128(p, b);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            o[j] = pack_2x16(fmaf(up, __uint_as_float(v[8 * i + 2 * j]), act::to_float(b[j] & 0xFFFFu, BF16)),
+                             fmaf(up, __uint_as_float(v[8 * i + 2 * j + 1]), act::to_float(b[j] >> 16, BF16)), BF16);
+          *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(dfree(d));
+      const int col = nb * Cf::NB + 8 * (lane & 7);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (token[i] >= 0 && col < a.N) {
+          uint32_t o[4];
+          gemv::lds128(mine + swizzled(0, 32 * (warp & 3) + 4 * i + (lane >> 3), 8 * (lane & 7)), o);
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + static_cast<size_t>(token[i]) * a.ldo + col) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(nfree(n.s));
+      n.next();
+      n.next();
     }
     __syncwarp();
-    const int n = nb * Cf::NB + 8 * piece;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (token[i] >= 0 && n < a.N && ok) {
-        uint32_t o[4];
-        gemv::lds128(mine + at[i], o);
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + static_cast<size_t>(token[i]) * a.ldo + n) = make_uint4(o[0], o[1], o[2], o[3]);
-      }
-    __syncwarp();                                           // the stage is free, and whole-warp instructions follow
-  };
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) {
-    load_base(nb0 + s, s);
-    gemv::cp_commit();
+    others.fill();
   }
-  stage = 0;
-  for (int nb = nb0; nb <= nb1; ++nb) {                     // one more round, which only finishes the last block
-    // groups of copies in order: two of B, two of base, then for each block its B and base
-    // together.  Block nb needs its B, and base of the block before.
-    if (nb == nb0)
-      gemv::cp_wait<2 * (kStages - 1) - 1>();
-    else if (nb == nb0 + 1)
-      gemv::cp_wait<kStages - 1>();
-    else
-      gemv::cp_wait<kStages - 2>();
-    const int d = (nb - nb0) & 1, before = stage == 0 ? kStages - 1 : stage - 1;
-    if (nb < nb1) {
-      ptx::fence_proxy_async_smem();
-      __syncthreads();
-      if (warp == 0) {
-        if (lane == 0 && ok) {
-          ptx::tc_fence_after();
-          const uint32_t s = base_s + Cf::OFF_B + static_cast<uint32_t>(stage * Cf::NSTAGE);
-          const uint32_t to = tmem + static_cast<uint32_t>(Cf::COL_D + Cf::NB * d);
-#pragma unroll
-          for (int k = 0; k < RP / 16; ++k) {
-            const uint64_t bd = smem_desc_sw128(s + static_cast<uint32_t>((k >> 2) * Cf::NB * 128)) + 2 * (k & 3);
-            const uint32_t p = base_s + Cf::OFF_HI + static_cast<uint32_t>((k >> 2) * kWideRows * 128);
-            ptx::mma_f16(to, smem_desc_sw128(p) + 2 * (k & 3), bd, idesc_dense(kFmt, kFmt, Cf::NB, 128), k > 0 ? 1u : 0u);
-            ptx::mma_f16(to, smem_desc_sw128(p + Cf::PBYTES) + 2 * (k & 3), bd, idesc_dense(kFmt, kFmt, Cf::NB, 128), 1u);
-          }
-          ptx::mma_commit(dbar(d));
-        }
-        __syncwarp();
-      }
-    } else {
-      __syncwarp();                                         // this warp's copies of base are there
-    }
-    if (nb > nb0) finish(nb - 1, d ^ 1, static_cast<uint32_t>((nb - 1 - nb0) >> 1) & 1u, before);
-    load_n(nb + kStages - 1, before);
-    load_base(nb + kStages - 1, before);
-    gemv::cp_commit();
-    if (++stage == kStages) stage = 0;
-  }
-  gemv::cp_wait<0>();
-  __syncwarp();
-  others.fill();
-  // every MMA has completed, unless a wait ran out: then they get a while before shared memory
-  // and TMEM are given back
+  // everything asked for has come and has been read, unless a wait ran out: then it gets a while
+  // before shared memory and TMEM are given back
   if (__syncthreads_or(abort_word != 0u ? 1 : 0)) {
     const uint64_t since = ptx::globaltimer();
     while (ptx::globaltimer() - since < 200000ull) __nanosleep(1000);
   }
-  if (warp == 1) {
+  if (warp == kWarps + kCopyWarps) {
     ptx::tc_fence_after();
     tc_dealloc<1>(tmem, Cf::TMEM);
   }
@@ -723,7 +754,7 @@ constexpr int smem_bytes(int tiles) {
 struct LoraLaunch {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  LoraLaunch(long long groups, int parts, int cluster, size_t smem, cudaStream_t stream) {
+  LoraLaunch(long long groups, int parts, int cluster, int threads, int smem, cudaStream_t stream, bool pdl) {
     std::memset(&cfg, 0, sizeof(cfg));
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 1;
@@ -732,35 +763,39 @@ struct LoraLaunch {
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(groups), static_cast<unsigned>(parts), static_cast<unsigned>(cluster));
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    cfg.numAttrs = pdl ? 2 : 1;
   }
 };
 
-// Opens the kernel's shared memory once per device, then launches it.
+// Clusters of 1, 2, 4 and 8 CTAs that run on the device together.
+struct Fit {
+  int clusters[4];
+};
 template <typename K>
-int launch(K* fn, PerDevice<int>& ready, int most_smem, int smem, const LoraKArgs& k, long long groups, int parts, int cluster, cudaStream_t stream) {
+int find_fit(K* fn, PerDevice<Fit>& fits, int threads, int most_smem, int smem, const Fit** out) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= kMaxDevices) return set_error(2, "device id %d", dev);
-  const int* set = nullptr;
-  const int r = ready.get(dev, &set, [&](int& v) {
-    v = most_smem;
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v);
-    return e == cudaSuccess ? 0 : set_error(4, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  return fits.get(dev, out, [&](Fit& f) {
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem);
+    for (int i = 0; e == cudaSuccess && i < 4; ++i) {
+      LoraLaunch l(device_sm_count(), 1, 1 << i, threads, smem, nullptr, false);
+      e = cudaOccupancyMaxActiveClusters(&f.clusters[i], fn, &l.cfg);
+      if (e == cudaSuccess && f.clusters[i] <= 0) e = cudaErrorInvalidConfiguration;
+    }
+    return e == cudaSuccess ? 0 : set_error(4, "lora_f16 set-up: %s", cudaGetErrorString(e));
   });
-  if (r) return r;
-  LoraLaunch l(groups, parts, cluster, static_cast<size_t>(smem), stream);
-  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, fn, k);
-  return e == cudaSuccess ? 0 : set_error(4, "lora_f16 launch: %s", cudaGetErrorString(e));
 }
 
 template <bool BF16, int RP>
 int launch_tiles(const LoraArgs& a, cudaStream_t stream) {
-  static PerDevice<int> ready;
+  static PerDevice<Fit> fits;
+  const Fit* fit = nullptr;
+  if (const int r = find_fit(&lora_f16_kernel<BF16, RP>, fits, kThreads, smem_bytes<RP>(kWarps), smem_bytes<RP>(1), &fit)) return r;
   LoraKArgs k;
   k.a = a;
   k.timeout_ns = 0;                                         // this form waits for no barrier
@@ -776,36 +811,56 @@ int launch_tiles(const LoraArgs& a, cudaStream_t stream) {
   const long long groups = (tiles + k.tiles - 1) / k.tiles;
   int parts = 1;
   while (parts < 64 && 2 * parts * groups * cluster <= sms && 2 * parts * cluster <= nblocks) parts *= 2;
-  return launch(&lora_f16_kernel<BF16, RP>, ready, smem_bytes<RP>(kWarps), smem_bytes<RP>(k.tiles), k, groups, parts, cluster, stream);
+  LoraLaunch l(groups, parts, cluster, kThreads, smem_bytes<RP>(k.tiles), stream, pdl_enabled());
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, &lora_f16_kernel<BF16, RP>, k);
+  return e == cudaSuccess ? 0 : set_error(4, "lora_f16 launch: %s", cudaGetErrorString(e));
 }
 
 template <bool BF16, int RP>
 int launch_wide(const LoraArgs& a, cudaStream_t stream) {
-  static PerDevice<int> ready;
-  static_assert(WideCfg<RP>::SMEM <= 232448 - 1024, "shared memory budget");
+  using Cf = WideCfg<RP>;
+  static_assert(Cf::SMEM <= 232448 - 2048, "shared memory budget");
+  static PerDevice<Fit> fits;
+  const Fit* fit = nullptr;
+  if (const int r = find_fit(&lora_f16_wide_kernel<BF16, RP>, fits, kWideThreads, Cf::SMEM, Cf::SMEM, &fit)) return r;
   LoraKArgs k;
   k.a = a;
   k.tiles = 8;
   k.timeout_ns = wait_timeout_ns();
-  // the cluster that takes the least time in waves of what fits the device, each as long as the
-  // share of a CTA and, for the start and the exchange of P, a fortieth of a whole block
-  const long long groups = a.M / kWideRows, slots = static_cast<long long>(device_sm_count()) * (RP <= 64 ? 2 : 1);
+  // The cluster whose CTAs take the least time, in units of a whole block alone on an SM: each
+  // takes its share and 0.08 for the start and the exchange of P, 1.28 times as long where two
+  // are on an SM (up to rank 64; the occupancy query counts one CTA per SM for a kernel with
+  // tensor memory).  At 7168 x 7168, rank 64, clusters of 1, 2, 4 and 8: 153, 91, 73 and 84 us
+  // for 71 blocks, 155, 94, 114 and 107 for 76, which do not fit the device as fours.
+  constexpr int kPerSm = RP <= 64 ? 2 : 1;
+  constexpr double kShared = RP <= 64 ? 1.28 : 1.0;
+  const long long groups = a.M / kWideRows;
   int cluster = 1;
   double best = 0.0;
-  for (int c = 1; c <= kMaxCluster; c *= 2) {
+  for (int i = 0; i < 4; ++i) {
+    const int c = 1 << i;
     if (c > 1 && (a.K + 63) / 64 < 2 * c && (a.N + 63) / 64 < 2 * c) break;
-    const double time = static_cast<double>((groups * c + slots - 1) / slots) * (1.0 / c + 0.025);
+    const long long alone = fit->clusters[i], waves = groups / (kPerSm * alone), rest = groups % (kPerSm * alone);
+    const double time = (1.0 / c + 0.08) * (static_cast<double>(waves) * kShared + (rest == 0 ? 0.0 : rest <= alone ? 1.0 : kShared));
     if (c == 1 || time < best) {
       best = time;
       cluster = c;
     }
   }
-  return launch(&lora_f16_wide_kernel<BF16, RP>, ready, WideCfg<RP>::SMEM, WideCfg<RP>::SMEM, k, groups, 1, cluster, stream);
+  const CUtensorMapDataType dt = BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUtensorMap m;
+  const uint64_t K = static_cast<uint64_t>(a.K);
+  if (!encode_tmap_2d(&m, dt, a.A, K, static_cast<uint64_t>(a.G) * a.r, 2 * K, 64, static_cast<uint32_t>(a.r), true)) return 4;
+  LoraLaunch l(groups, 1, cluster, kWideThreads, Cf::SMEM, stream, pdl_enabled());
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, &lora_f16_wide_kernel<BF16, RP>, m, k);
+  return e == cudaSuccess ? 0 : set_error(4, "lora_f16 launch: %s", cudaGetErrorString(e));
 }
 
 template <bool BF16, int RP>
 int by_align(const LoraArgs& a, cudaStream_t stream) {
-  return a.align % kWideRows == 0 ? launch_wide<BF16, RP>(a, stream) : launch_tiles<BF16, RP>(a, stream);
+  // the copy engine counts the rows of all adapters' A in 32 bits
+  const long long rows = static_cast<long long>(a.G) * a.r;
+  return a.align % kWideRows == 0 && rows <= kRouteMaxSize ? launch_wide<BF16, RP>(a, stream) : launch_tiles<BF16, RP>(a, stream);
 }
 
 template <bool BF16>
