@@ -2,21 +2,21 @@
 //   out[t] = base[t] + s_g (X[t] A_g^T) B_g^T,   g the adapter of token t,
 // A_g (r, K), B_g (N, r) with r up to 128, tokens grouped by adapter in tiles of 16 rows.
 //
-// One launch.  A cluster takes a run of tiles.  First its CTAs split K: a warp multiplies
-// the 16 tokens of a tile with the adapter's rows over its share of K, the shares' sums meet
-// in distributed shared memory, and P = s X A^T goes to every CTA of the cluster.  Then the
-// CTAs split N.  P never leaves the chip, X and base are read once, out is written once.
-// With few tiles, several clusters take the same tiles and each its part of N; they all
-// compute P, from A that then comes from L2.
+// One launch, in two forms: tiles of 16 rows (below) and, where the rows of an adapter come in
+// blocks of 128, those (further down).  A cluster takes a tile or block.  First its CTAs split
+// K: X A^T over a share of K, whose sums meet in distributed shared memory.  Then they split
+// N.  P = s X A^T never leaves the chip, X and base are read once, out is written once.
 //
-// The products run on mma.sync m16n8k16 with tokens as M: the call is bound by the reading
-// and writing of X, base and out (for one token by that of A and B), not by the r = 16 .. 128
-// multiplications that each of those elements meets.  Operands come from global memory
-// straight into the registers of the MMA: the order of the reduction is free, so lane
-// 4 q + c takes the elements 8 c .. 8 c + 7 of a row as its k indices of two instructions,
-// which is one 16-byte load and 64 contiguous bytes of each row.  In the second product the
-// columns of B are permuted in the same way so that a lane's results are 8 neighbours of a
-// token's row.
+// Tiles of 16 are for few tokens per adapter, where the adapter's own bytes and the latency of
+// a chain of dependent steps are the time: ids, X and A, sums, B, out.  Warps multiply on
+// mma.sync m16n8k16 with tokens as M, operands straight from global memory into the registers
+// of the MMA: the order of the reduction is free, so lane 4 q + c takes the elements
+// 8 c .. 8 c + 7 of a row as its k indices of two instructions, which is one 16-byte load and
+// 64 contiguous bytes of each row.  In the second product the columns of B are permuted in the
+// same way so that a lane's results are 8 neighbours of a token's row.  While A is read, the
+// CTA's part of B is asked into L2, and its first blocks come while the sums meet.  Where SMs
+// are left, several clusters take the same tile and each its part of N; they all compute P,
+// from A that then comes from L2.
 //
 // P is the left operand of the second product, in 16 bits.  It is split into a rounded value
 // and the rounded rest, two instructions instead of one, so that it keeps 16 (bf16) or 22
@@ -36,7 +36,6 @@ constexpr uint32_t kFull = 0xFFFFFFFFu;
 
 struct LoraKArgs {
   LoraArgs a;
-  int tiles;       // tiles of a CTA: 1, 2, 4 or 8; its other warps split K and N further
   uint64_t timeout_ns;
 };
 
@@ -72,25 +71,27 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   lo = pack_2x16(l[0], l[1], BF16);
 }
 
-// P from the sums over the shares of K: each CTA of the cluster sums every C-th row of `part`
-// over all of them, a warp per row, and hands value, rest and power to all of them.
-// place(row, column, value's address, rest's) says where two columns go.
+// P from the sums over the shares of K, as value, rest and power.  With `all` every CTA of the
+// cluster sums all rows over `part` of all CTAs and keeps them; otherwise it sums every C-th row
+// and hands it to all of them.  place(row, column, value's address, rest's) says where two
+// columns go.  A row is summed by as many lanes as it has pairs of columns, up to 32.
 template <bool BF16, int RP, typename Place>
-__device__ __forceinline__ void exchange_rows(const float* part, float* power, int rows, const float* scale_of, int scale_rows, int C,
-                                              int rank, Place&& place) {
-  constexpr int LDP = RP + 4;
-  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
-  for (int row = rank + C * warp; row < rows; row += C * kWarps) {
-    const float scale = scale_of[row / scale_rows];
-    constexpr int PAIRS = (RP + 63) / 64;
+__device__ __forceinline__ void exchange_rows(const float* part, float* power, int rows, const float* scale_at, int C, int rank,
+                                              bool all, Place&& place) {
+  constexpr int LDP = RP + 4, LANES = RP >= 64 ? 32 : RP / 2, PAIRS = RP / 2 / LANES, TOGETHER = 32 / LANES;
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31), at_lane = lane % LANES;
+  const int first = all ? 0 : rank, step = all ? 1 : C;
+  const float scale = *scale_at;
+  for (int i = warp * TOGETHER; first + step * i < rows; i += kWarps * TOGETHER) {
+    const int row = first + step * (i + lane / LANES);
+    const bool in = row < rows;
     float2 v[PAIRS];
     float top = 0.0f;
 #pragma unroll
     for (int u = 0; u < PAIRS; ++u) {
-      const int col = 2 * (lane + 32 * u);
       v[u] = make_float2(0.0f, 0.0f);
-      if (col < RP) {
-        const uint32_t at = ptx::smem_u32(part + row * LDP + col);
+      if (in) {
+        const uint32_t at = ptx::smem_u32(part + row * LDP + 2 * (at_lane + LANES * u));
         float2 s[kMaxCluster];
 #pragma unroll
         for (int r = 0; r < kMaxCluster; ++r)
@@ -108,8 +109,9 @@ __device__ __forceinline__ void exchange_rows(const float* part, float* power, i
     }
     float up = 1.0f;
     if (!BF16) {
+      __syncwarp();
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+      for (int off = LANES / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
       // the largest goes to [2^14, 2^15): exponents stay where 2^e and 2^-e are normal numbers
       int e = static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14;
       e = e < -126 ? -126 : e;
@@ -122,21 +124,32 @@ __device__ __forceinline__ void exchange_rows(const float* part, float* power, i
         v[u].y *= down;
       }
     }
+    if (!in) continue;
+    const int to0 = all ? rank : 0, to1 = all ? rank + 1 : C;
 #pragma unroll
     for (int u = 0; u < PAIRS; ++u) {
-      const int col = 2 * (lane + 32 * u);
-      if (col < RP) {
-        uint32_t h, l, at_h, at_l;
-        split2<BF16>(v[u].x, v[u].y, h, l);
-        place(row, col, at_h, at_l);
-        for (int r = 0; r < C; ++r) {
-          st_cluster_u32(map_to_rank(at_h, static_cast<uint32_t>(r)), h);
-          st_cluster_u32(map_to_rank(at_l, static_cast<uint32_t>(r)), l);
-        }
+      uint32_t h, l, at_h, at_l;
+      split2<BF16>(v[u].x, v[u].y, h, l);
+      place(row, 2 * (at_lane + LANES * u), at_h, at_l);
+      for (int r = to0; r < to1; ++r) {
+        st_cluster_u32(map_to_rank(at_h, static_cast<uint32_t>(r)), h);
+        st_cluster_u32(map_to_rank(at_l, static_cast<uint32_t>(r)), l);
       }
     }
-    if (lane < C) st_cluster_f32(map_to_rank(ptx::smem_u32(power + row), static_cast<uint32_t>(lane)), up);
+    if (at_lane == 0)
+      for (int r = to0; r < to1; ++r) st_cluster_f32(map_to_rank(ptx::smem_u32(power + row), static_cast<uint32_t>(r)), up);
   }
+  __syncwarp();
+}
+
+// The two halves of a cluster barrier (whole-warp instructions).
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Rows of tokens without an adapter: base, or zeros.  An item is 2 KB of 32 tokens; every warp
@@ -182,51 +195,46 @@ __device__ __forceinline__ uint32_t cta_of_grid() { return (blockIdx.x * gridDim
 template <bool BF16, int RP>
 __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_kernel(LoraKArgs args) {
   constexpr int NB = RP / 8;                                // blocks of 8 rank rows
-  constexpr int UNROLL = RP <= 16 ? 4 : RP <= 32 ? 3 : RP <= 64 ? 2 : 1;
+  constexpr int UNROLL = RP <= 32 ? 4 : RP <= 64 ? 2 : 1;    // steps of 32 columns of K in flight
   constexpr int LDP = RP + 4;                               // floats of a row of sums in shared memory
   constexpr int LDH = RP + 8;                               // 16-bit values of a row of P
   const LoraArgs& a = args.a;
   extern __shared__ __align__(16) uint8_t smem[];
-  const int WT = args.tiles, WK = kWarps / WT;
-  float* part = reinterpret_cast<float*>(smem);             // [WK][16 WT][LDP] sums over a share of K
-  uint16_t* hi = reinterpret_cast<uint16_t*>(part + kWarps * 16 * LDP);  // [16 WT][LDH]
-  uint16_t* lo = hi + WT * 16 * LDH;
-  float* power = reinterpret_cast<float*>(lo + WT * 16 * LDH);           // [16 WT] what a row of P is to be multiplied by
+  float* part = reinterpret_cast<float*>(smem);             // [warp][16][LDP] sums over a share of K
+  uint16_t* hi = reinterpret_cast<uint16_t*>(part + kWarps * 16 * LDP);  // [16][LDH]
+  uint16_t* lo = hi + 16 * LDH;
+  float* power = reinterpret_cast<float*>(lo + 16 * LDH);   // [16] what a row of P is to be multiplied by
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const int q = lane >> 2, c = lane & 3;
   const int C = static_cast<int>(gridDim.z), rank = static_cast<int>(blockIdx.z);      // the cluster is (1, 1, C)
-  __shared__ float tile_scale[kWarps];
+  __shared__ float tile_scale;
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
 
   const Others others(a, cta_of_grid() * kWarps + warp, gridDim.x * gridDim.y * gridDim.z * kWarps);
 
-  // the tile of this warp: its adapter and tokens
-  const int wt = warp % WT, wk = warp / WT;
-  const long long row0 = (static_cast<long long>(blockIdx.x) * WT + wt) * 16;
-  int g = -1, token = -1;
-  if (row0 < a.M) {                                         // M is a multiple of 16
-    int id = -1;
-    if (lane < 16) {
-      id = ptx::ld_global(a.m_indices + row0 + lane);
-      token = ptx::ld_global(a.src + row0 + lane);
-    }
-    g = __shfl_sync(kFull, id, 0);
-    // rows of another adapter, adapters and tokens out of range are reported and left alone
-    bool bad = false;
-    if (g >= a.G) {
-      bad = lane == 0;
-      g = -1;
-    }
-    if (id < 0 || token < 0 || g < 0) {
-      token = -1;
-    } else if (id != g || token >= a.T) {
-      bad = true;
-      token = -1;
-    }
-    if (bad) atomicOr(a.status, FGF8_DEVERR_INPUT);
+  // the tile's adapter and tokens
+  const long long row0 = static_cast<long long>(blockIdx.x) * 16;
+  int id = -1, token = -1;
+  if (lane < 16) {
+    id = ptx::ld_global(a.m_indices + row0 + lane);
+    token = ptx::ld_global(a.src + row0 + lane);
   }
-  if (__syncthreads_or(g >= 0) == 0) {                      // the same for every CTA of the cluster
+  int g = __shfl_sync(kFull, id, 0);
+  // rows of another adapter, adapters and tokens out of range are reported and left alone
+  bool bad = false;
+  if (g >= a.G) {
+    bad = lane == 0;
+    g = -1;
+  }
+  if (id < 0 || token < 0 || g < 0) {
+    token = -1;
+  } else if (id != g || token >= a.T) {
+    bad = true;
+    token = -1;
+  }
+  if (bad) atomicOr(a.status, FGF8_DEVERR_INPUT);
+  if (g < 0) {                                              // the same for every warp of the cluster
     others.fill();
     return;
   }
@@ -236,48 +244,46 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_kernel(Lo
   const int nblocks = (a.N + 31) / 32;
   const long long nshare = static_cast<long long>(blockIdx.y) * C + rank, nshares = static_cast<long long>(gridDim.y) * C;
   const int nb0 = static_cast<int>(nblocks * nshare / nshares), nb1 = static_cast<int>(nblocks * (nshare + 1) / nshares);
-  const uint16_t* bg = static_cast<const uint16_t*>(a.B) + static_cast<size_t>(g < 0 ? 0 : g) * a.N * a.r;
-  if (g >= 0) {
+  const uint16_t* bg = static_cast<const uint16_t*>(a.B) + static_cast<size_t>(g) * a.N * a.r;
+  {
     const char *from = reinterpret_cast<const char*>(bg + static_cast<size_t>(nb0) * 32 * a.r),
                *to = reinterpret_cast<const char*>(bg + static_cast<size_t>(min(nb1 * 32, a.N)) * a.r);
-    for (const char* p = from + 128 * (wk * 32 + lane); p < to; p += 128 * 32 * WK) gemv::prefetch_l2(p);
+    for (const char* p = from + 128 * tid; p < to; p += 128 * kThreads) gemv::prefetch_l2(p);
   }
 
   // ------------------------------------------------------------ X A^T over a share of K
-  const int share = rank * WK + wk, shares = C * WK;
+  const int share = rank * kWarps + warp, shares = C * kWarps;
   const int kblocks = (a.K + 31) / 32;
   const int kb0 = static_cast<int>(static_cast<long long>(kblocks) * share / shares);
   const int kb1 = static_cast<int>(static_cast<long long>(kblocks) * (share + 1) / shares);
   float acc[NB][4] = {};
-  if (g >= 0) {
-    const uint16_t* x0 = static_cast<const uint16_t*>(a.X) + static_cast<size_t>(t0 < 0 ? 0 : t0) * a.ldx;
-    const uint16_t* x1 = static_cast<const uint16_t*>(a.X) + static_cast<size_t>(t1 < 0 ? 0 : t1) * a.ldx;
-    const uint16_t* w = static_cast<const uint16_t*>(a.A) + (static_cast<size_t>(g) * a.r + q) * a.K;
-    for (int kb = kb0; kb < kb1; kb += UNROLL) {
-      uint4 xv[UNROLL][2], wv[UNROLL][NB];
+  const uint16_t* x0 = static_cast<const uint16_t*>(a.X) + static_cast<size_t>(t0 < 0 ? 0 : t0) * a.ldx;
+  const uint16_t* x1 = static_cast<const uint16_t*>(a.X) + static_cast<size_t>(t1 < 0 ? 0 : t1) * a.ldx;
+  const uint16_t* w = static_cast<const uint16_t*>(a.A) + (static_cast<size_t>(g) * a.r + q) * a.K;
+  for (int kb = kb0; kb < kb1; kb += UNROLL) {
+    uint4 xv[UNROLL][2], wv[UNROLL][NB];
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
-        const int k = (kb + u) * 32 + 8 * c;
-        const bool in = kb + u < kb1 && k < a.K;
-        xv[u][0] = in && t0 >= 0 ? ptx::ld_global_v4(x0 + k) : make_uint4(0u, 0u, 0u, 0u);
-        xv[u][1] = in && t1 >= 0 ? ptx::ld_global_v4(x1 + k) : make_uint4(0u, 0u, 0u, 0u);
+    for (int u = 0; u < UNROLL; ++u) {
+      const int k = (kb + u) * 32 + 8 * c;
+      const bool in = kb + u < kb1 && k < a.K;
+      xv[u][0] = in && t0 >= 0 ? ptx::ld_global_v4(x0 + k) : make_uint4(0u, 0u, 0u, 0u);
+      xv[u][1] = in && t1 >= 0 ? ptx::ld_global_v4(x1 + k) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-          wv[u][b] = in && 8 * b < a.r ? ptx::ld_global_v4(w + static_cast<size_t>(8 * b) * a.K + k) : make_uint4(0u, 0u, 0u, 0u);
-      }
-      __syncwarp();                                         // the instructions below are whole-warp ones
-#pragma unroll
-      for (int u = 0; u < UNROLL; ++u)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          gemv::mma16816<BF16>(acc[b], xv[u][0].x, xv[u][1].x, xv[u][0].y, xv[u][1].y, wv[u][b].x, wv[u][b].y);
-          gemv::mma16816<BF16>(acc[b], xv[u][0].z, xv[u][1].z, xv[u][0].w, xv[u][1].w, wv[u][b].z, wv[u][b].w);
-        }
+      for (int b = 0; b < NB; ++b)
+        wv[u][b] = in && 8 * b < a.r ? ptx::ld_global_v4(w + static_cast<size_t>(8 * b) * a.K + k) : make_uint4(0u, 0u, 0u, 0u);
     }
+    __syncwarp();                                         // the instructions below are whole-warp ones
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        gemv::mma16816<BF16>(acc[b], xv[u][0].x, xv[u][1].x, xv[u][0].y, xv[u][1].y, wv[u][b].x, wv[u][b].y);
+        gemv::mma16816<BF16>(acc[b], xv[u][0].z, xv[u][1].z, xv[u][0].w, xv[u][1].w, wv[u][b].z, wv[u][b].w);
+      }
   }
-  if (wk == 0 && lane == 0) tile_scale[wt] = a.scale != nullptr && g >= 0 ? ptx::ld_global(a.scale + g) : 1.0f;
+  if (tid == 0) tile_scale = a.scale != nullptr ? ptx::ld_global(a.scale + g) : 1.0f;
   {
-    float* p = part + (wk * WT + wt) * 16 * LDP;
+    float* p = part + warp * 16 * LDP;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       *reinterpret_cast<float2*>(p + q * LDP + 8 * b + 2 * c) = make_float2(acc[b][0], acc[b][1]);
@@ -285,32 +291,66 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_kernel(Lo
     }
   }
   __syncthreads();
-  if (WK > 1) {
-    for (int i = tid; i < WT * 16 * RP; i += kThreads) {
-      const int at = i / RP * LDP + i % RP;
-      float s = part[at];
-      for (int k = 1; k < WK; ++k) s += part[k * WT * 16 * LDP + at];
-      part[at] = s;
-    }
+  for (int i = tid; i < 16 * RP; i += kThreads) {
+    const int at = i / RP * LDP + i % RP;
+    float sum = part[at];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) sum += part[w * 16 * LDP + at];
+    part[at] = sum;
   }
-  if (C > 1) cluster_sync_all(); else __syncthreads();
 
-  // ------------------------------------------------------------ P, a warp per row
-  exchange_rows<BF16, RP>(part, power, WT * 16, tile_scale, 16, C, rank, [&](int row, int col, uint32_t& at_h, uint32_t& at_l) {
+  // a block of 32 columns of out: what it adds to and B's rows for it, at this lane's columns
+  constexpr int KS = RP >= 32 ? RP / 32 : 1;                // steps of 32 rank rows (of 16 when there are no more)
+  struct Block {
+    uint4 base[2];
+    uint4 b[4][KS];
+  };
+  auto load_block = [&](int nb, Block& v) {
+    const int n0 = nb * 32 + 8 * c;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int t = half ? t1 : t0;
+      v.base[half] = make_uint4(0u, 0u, 0u, 0u);
+      if (a.base != nullptr && nb < nb1 && n0 < a.N && t >= 0)
+        v.base[half] = ptx::ld_global_v4(static_cast<const uint16_t*>(a.base) + static_cast<size_t>(t) * a.ldb + n0);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = nb * 32 + 8 * (q >> 1) + 2 * j + (q & 1);
+      const uint16_t* bn = bg + static_cast<size_t>(n) * a.r;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        v.b[j][s] = make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (RP >= 32) {
+          if (nb < nb1 && n < a.N && 32 * s + 8 * c < a.r) v.b[j][s] = ptx::ld_global_v4(bn + 32 * s + 8 * c);
+        } else {
+          if (nb < nb1 && n < a.N && 4 * c < a.r) {
+            const uint2 w = ld_global_v2(bn + 4 * c);
+            v.b[j][s].x = w.x;
+            v.b[j][s].y = w.y;
+          }
+        }
+      }
+    }
+  };
+  // the first block, and where registers allow the second, come while P is exchanged
+  constexpr bool kTwo = RP <= 32;
+  Block even, odd;
+  load_block(nb0 + warp, even);
+  if (kTwo) load_block(nb0 + warp + kWarps, odd);
+  // every CTA sums all rows, and they meet once
+  if (C > 1) cluster_sync_all(); else __syncthreads();
+  exchange_rows<BF16, RP>(part, power, 16, &tile_scale, C, rank, true, [&](int row, int col, uint32_t& at_h, uint32_t& at_l) {
     at_h = ptx::smem_u32(hi + row * LDH + col);
     at_l = ptx::smem_u32(lo + row * LDH + col);
   });
-  if (C > 1) cluster_sync_all(); else __syncthreads();      // and nothing remote is touched behind this
-  if (g < 0) {
-    others.fill();
-    return;
-  }
+  cluster_arrive();                                         // behind this nothing remote is touched
+  __syncthreads();
 
   // ------------------------------------------------------------ P B^T over a share of N
-  constexpr int KS = RP >= 32 ? RP / 32 : 1;                // steps of 32 rank rows (of 16 when there are no more)
   uint32_t ph[KS][8], pl[KS][8];                            // [row q: 4 words][row q + 8: 4 words]
   {
-    const uint16_t *h0 = hi + (wt * 16 + q) * LDH, *l0 = lo + (wt * 16 + q) * LDH;
+    const uint16_t *h0 = hi + q * LDH, *l0 = lo + q * LDH;
 #pragma unroll
     for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -327,66 +367,54 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_kernel(Lo
         }
       }
   }
-  const float up0 = power[wt * 16 + q], up1 = power[wt * 16 + q + 8];
-  for (int nb = nb0 + wk; nb < nb1; nb += WK) {
-    const int n0 = nb * 32 + 8 * c;                         // this lane's 8 columns of out
-    const bool in = n0 < a.N;
-    uint4 base0 = make_uint4(0u, 0u, 0u, 0u), base1 = base0;
-    if (a.base != nullptr && in) {
-      const uint16_t* b = static_cast<const uint16_t*>(a.base);
-      if (t0 >= 0) base0 = ptx::ld_global_v4(b + static_cast<size_t>(t0) * a.ldb + n0);
-      if (t1 >= 0) base1 = ptx::ld_global_v4(b + static_cast<size_t>(t1) * a.ldb + n0);
-    }
+  const float up0 = power[q], up1 = power[q + 8];
+  auto finish = [&](int nb, const Block& v) {
+    __syncwarp();                                           // the instructions below are whole-warp ones
     float d[4][4] = {};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = nb * 32 + 8 * (q >> 1) + 2 * j + (q & 1);
-      const uint16_t* bn = bg + static_cast<size_t>(n < a.N ? n : 0) * a.r;
-      uint4 bv[KS];
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        bv[s] = make_uint4(0u, 0u, 0u, 0u);
+        gemv::mma16816<BF16>(d[j], ph[s][0], ph[s][4], ph[s][1], ph[s][5], v.b[j][s].x, v.b[j][s].y);
+        gemv::mma16816<BF16>(d[j], pl[s][0], pl[s][4], pl[s][1], pl[s][5], v.b[j][s].x, v.b[j][s].y);
         if constexpr (RP >= 32) {
-          if (n < a.N && 32 * s + 8 * c < a.r) bv[s] = ptx::ld_global_v4(bn + 32 * s + 8 * c);
-        } else {
-          if (n < a.N && 4 * c < a.r) {
-            const uint2 v = ld_global_v2(bn + 4 * c);
-            bv[s].x = v.x;
-            bv[s].y = v.y;
-          }
+          gemv::mma16816<BF16>(d[j], ph[s][2], ph[s][6], ph[s][3], ph[s][7], v.b[j][s].z, v.b[j][s].w);
+          gemv::mma16816<BF16>(d[j], pl[s][2], pl[s][6], pl[s][3], pl[s][7], v.b[j][s].z, v.b[j][s].w);
         }
       }
-      __syncwarp();
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        gemv::mma16816<BF16>(d[j], ph[s][0], ph[s][4], ph[s][1], ph[s][5], bv[s].x, bv[s].y);
-        gemv::mma16816<BF16>(d[j], pl[s][0], pl[s][4], pl[s][1], pl[s][5], bv[s].x, bv[s].y);
-        if constexpr (RP >= 32) {
-          gemv::mma16816<BF16>(d[j], ph[s][2], ph[s][6], ph[s][3], ph[s][7], bv[s].z, bv[s].w);
-          gemv::mma16816<BF16>(d[j], pl[s][2], pl[s][6], pl[s][3], pl[s][7], bv[s].z, bv[s].w);
-        }
-      }
-    }
-    if (in) {
-      uint16_t* o = static_cast<uint16_t*>(a.out);
+    const int n0 = nb * 32 + 8 * c;                         // this lane's 8 columns of out
+    if (n0 < a.N) {
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int t = half ? t1 : t0;
         if (t < 0) continue;
         const float up = half ? up1 : up0;
-        const uint4& b = half ? base1 : base0;
-        const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+        const uint32_t bw[4] = {v.base[half].x, v.base[half].y, v.base[half].z, v.base[half].w};
         uint32_t ow[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           ow[j] = pack_2x16(fmaf(up, d[j][2 * half], act::to_float(bw[j] & 0xFFFFu, BF16)),
                             fmaf(up, d[j][2 * half + 1], act::to_float(bw[j] >> 16, BF16)), BF16);
-        *reinterpret_cast<uint4*>(o + static_cast<size_t>(t) * a.ldo + n0) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + static_cast<size_t>(t) * a.ldo + n0) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
       }
+    }
+  };
+  if constexpr (kTwo) {
+    for (int nb = nb0 + warp; nb < nb1; nb += 2 * kWarps) {
+      finish(nb, even);
+      load_block(nb + 2 * kWarps, even);
+      if (nb + kWarps < nb1) finish(nb + kWarps, odd);
+      load_block(nb + 3 * kWarps, odd);
+    }
+  } else {
+    for (int nb = nb0 + warp; nb < nb1; nb += kWarps) {
+      finish(nb, even);
+      load_block(nb + kWarps, even);
     }
   }
   __syncwarp();
   others.fill();
+  cluster_wait();                                           // a CTA stays until all have read its sums
 }
 
 // ----------------------------------------------------------------- many tokens of an adapter
@@ -677,7 +705,7 @@ __global__ void __launch_bounds__(kWideThreads, RP <= 64 ? 2 : 1) lora_f16_wide_
       }
     }
     cluster_sync_all();
-    exchange_rows<BF16, RP>(part, power, kWideRows, &block_scale, kWideRows, C, rank, [&](int r, int col, uint32_t& at_h, uint32_t& at_l) {
+    exchange_rows<BF16, RP>(part, power, kWideRows, &block_scale, C, rank, false, [&](int r, int col, uint32_t& at_h, uint32_t& at_l) {
       at_h = base_s + Cf::OFF_HI + swizzled(kWideRows, r, col);
       at_l = at_h + Cf::PBYTES;
     });
@@ -745,11 +773,9 @@ __global__ void __launch_bounds__(kWideThreads, RP <= 64 ? 2 : 1) lora_f16_wide_
   }
 }
 
-// Shared memory of a CTA with `tiles` tiles.
+// Shared memory of a CTA with one tile.
 template <int RP>
-constexpr int smem_bytes(int tiles) {
-  return kWarps * 16 * (RP + 4) * 4 + 2 * tiles * 16 * (RP + 8) * 2 + tiles * 16 * 4;
-}
+constexpr int kTileSmem = kWarps * 16 * (RP + 4) * 4 + 2 * 16 * (RP + 8) * 2 + 16 * 4;
 
 struct LoraLaunch {
   cudaLaunchConfig_t cfg;
@@ -776,12 +802,12 @@ struct Fit {
   int clusters[4];
 };
 template <typename K>
-int find_fit(K* fn, PerDevice<Fit>& fits, int threads, int most_smem, int smem, const Fit** out) {
+int find_fit(K* fn, PerDevice<Fit>& fits, int threads, int smem, const Fit** out) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= kMaxDevices) return set_error(2, "device id %d", dev);
   return fits.get(dev, out, [&](Fit& f) {
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem);
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     for (int i = 0; e == cudaSuccess && i < 4; ++i) {
       LoraLaunch l(device_sm_count(), 1, 1 << i, threads, smem, nullptr, false);
       e = cudaOccupancyMaxActiveClusters(&f.clusters[i], fn, &l.cfg);
@@ -793,26 +819,23 @@ int find_fit(K* fn, PerDevice<Fit>& fits, int threads, int most_smem, int smem, 
 
 template <bool BF16, int RP>
 int launch_tiles(const LoraArgs& a, cudaStream_t stream) {
+  auto* fn = &lora_f16_kernel<BF16, RP>;
   static PerDevice<Fit> fits;
   const Fit* fit = nullptr;
-  if (const int r = find_fit(&lora_f16_kernel<BF16, RP>, fits, kThreads, smem_bytes<RP>(kWarps), smem_bytes<RP>(1), &fit)) return r;
+  if (const int r = find_fit(fn, fits, kThreads, kTileSmem<RP>, &fit)) return r;
+  // A cluster's CTAs split K and N: eight, unless a warp's share of K falls below 32 columns or
+  // the tiles' CTAs are a third more than run together (some tiles are empty).  Clusters that
+  // share a tile's N, and each compute P, help up to 64 CTAs with 4 KB of B each.  Over 15
+  // shapes of 1 to 2000 tokens this is at most 7 % slower than the best of all splits.
+  const long long tiles = a.M / 16, slots = (RP <= 64 ? 2LL : 1LL) * device_sm_count(), bytes = 2LL * a.N * a.r;
+  int cluster = kMaxCluster, parts = 1;
+  while (cluster > 1 && (256 * cluster > a.K || 3 * tiles * cluster > 4 * slots)) cluster /= 2;
+  while (2 * parts * cluster <= (a.N + 31) / 32 && 2 * parts * cluster * tiles <= 64 && bytes / (2 * parts * cluster) >= 4096) parts *= 2;
   LoraKArgs k;
   k.a = a;
-  k.timeout_ns = 0;                                         // this form waits for no barrier
-  const long long tiles = a.M / 16, sms = device_sm_count();
-  const long long nblocks = (a.N + 31) / 32;
-  // a cluster's CTAs split K and N: eight, fewer where there is too little to split
-  int cluster = kMaxCluster;
-  while (cluster > 1 && (a.K + 31) / 32 < 2 * cluster && nblocks < 2 * cluster) cluster /= 2;
-  // tiles share a CTA as soon as there are two CTAs per SM without
-  k.tiles = 8;
-  while (k.tiles > 1 && (tiles + k.tiles - 1) / k.tiles * cluster < 2 * sms) k.tiles /= 2;
-  // few tiles: several clusters per tile, each a part of N
-  const long long groups = (tiles + k.tiles - 1) / k.tiles;
-  int parts = 1;
-  while (parts < 64 && 2 * parts * groups * cluster <= sms && 2 * parts * cluster <= nblocks) parts *= 2;
-  LoraLaunch l(groups, parts, cluster, kThreads, smem_bytes<RP>(k.tiles), stream, pdl_enabled());
-  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, &lora_f16_kernel<BF16, RP>, k);
+  k.timeout_ns = 0;                                         // this form waits on no mbarrier
+  LoraLaunch l(tiles, parts, cluster, kThreads, kTileSmem<RP>, stream, pdl_enabled());
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, fn, k);
   return e == cudaSuccess ? 0 : set_error(4, "lora_f16 launch: %s", cudaGetErrorString(e));
 }
 
@@ -822,10 +845,9 @@ int launch_wide(const LoraArgs& a, cudaStream_t stream) {
   static_assert(Cf::SMEM <= 232448 - 2048, "shared memory budget");
   static PerDevice<Fit> fits;
   const Fit* fit = nullptr;
-  if (const int r = find_fit(&lora_f16_wide_kernel<BF16, RP>, fits, kWideThreads, Cf::SMEM, Cf::SMEM, &fit)) return r;
+  if (const int r = find_fit(&lora_f16_wide_kernel<BF16, RP>, fits, kWideThreads, Cf::SMEM, &fit)) return r;
   LoraKArgs k;
   k.a = a;
-  k.tiles = 8;
   k.timeout_ns = wait_timeout_ns();
   // The cluster whose CTAs take the least time, in units of a whole block alone on an SM: each
   // takes its share and 0.08 for the start and the exchange of P, 1.28 times as long where two
