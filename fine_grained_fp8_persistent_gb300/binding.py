@@ -594,10 +594,9 @@ def route_contiguous(ids: torch.Tensor, G: int, align: int | None = None, M: int
     T, k, ids64 = _ids(ids)
     align = mk_alignment_for_contiguous() if align is None else int(align)
     if M is None:
-        M = max(int(_lib.fgf8_route_rows(T, k, G, align)), 0)
+        M = _lib.fgf8_route_rows(T, k, G, align)
     i32 = torch.int32
-    rows = _empty((T, k), i32, ids, stream)
-    src, m_indices = _empty((M,), i32, ids, stream), _empty((M,), i32, ids, stream)
+    rows, src, m_indices = _empty((T, k), i32, ids, stream), _empty((max(M, 0),), i32, ids, stream), _empty((max(M, 0),), i32, ids, stream)
     counts, starts = _empty((max(G, 0),), i32, ids, stream), _empty((max(G, 0) + 1,), i32, ids, stream)
     _launch("route_contiguous", stream, (ids, rows, src, m_indices, counts, starts), (T, k, G, align, M, ids64))
     return Route(rows, src, m_indices, counts, starts, align)
@@ -616,10 +615,13 @@ def route_masked(ids: torch.Tensor, G: int, Mmax: int, stream=None) -> Route:
 
 def _entries(route: Route, T: int) -> tuple[int, int]:
     """(k, M) of a routing of T tokens."""
-    M, k = route.src.shape[0], route.rows.shape[-1]
-    _need_i32(route.rows, (T, k), "route.rows")
-    _need_i32(route.src, (M,), "route.src")
-    return k, M
+    rows, src = route.rows, route.src
+    shape, i32 = rows.shape, torch.int32
+    if len(shape) != 2 or shape[0] != T or rows.dtype is not i32:
+        _need_i32(rows, (T, shape[-1] if shape else 1), "route.rows")
+    if src.dim() != 1 or src.dtype is not i32:
+        _need_i32(src, (src.numel(),), "route.src")
+    return shape[1], src.shape[0]
 
 
 def dispatch_f16(x: torch.Tensor, route: Route, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
