@@ -435,7 +435,8 @@ def _launch(name: str, stream, tensors: tuple, ints: tuple, strided: tuple = ())
             pointers.append(None)
             continue
         if t.get_device() != device or not (t.is_contiguous() or i in strided):
-            _ptr(t)                                       # says why, unless the device is another one
+            if i not in strided:
+                _ptr(t)                                   # says why, unless the device is another one
             raise ValueError(f"{name}: a tensor is on {t.device}, another one on {tensors[0].device}")
         pointers.append(t.data_ptr())
     if device < 0:

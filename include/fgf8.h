@@ -326,7 +326,7 @@ FGF8_API long long fgf8_route_rows(int T, int k, int G, int align);
  *   SFA : activation table for M rows, or, with Mmax > 0 (the masked layout, M = G * Mmax),
  *         G tables of Mmax rows back to back
  * Codes and scales of rows without an entry are not written (the grouped products compute
- * nothing from them).  Requires K % 128 == 0.
+ * nothing from them).  Requires K % 128 == 0.  Outputs of both overlap no input.
  */
 FGF8_API int dispatch_f16(const void* X, const int32_t* rows, const int32_t* src, void* Xs, int T, int k, int K, int M,
                           void* stream);

@@ -152,6 +152,73 @@ def test_bad_rows_are_reported(fg, dev):
     assert fg.check_status()[0] == 0
 
 
+def test_bad_rows_in_wide_blocks_are_reported(fg, dev):
+    """The same where rows come in blocks of 128."""
+    T, G, K, N, r = 300, 3, 64, 40, 16
+    x, a, b, base, scale, ids = _inputs(T, G, K, N, r, torch.bfloat16, dev, absent=0.0, skew=0.0)
+    route = fg.route_contiguous(ids, G, 128)
+    want = fg.lora_f16(x, a, b, route, base=base)
+    other = torch.nonzero(route.m_indices >= 0).view(-1)[5:6]      # a row that is not the first of its block
+    token = int(route.src[other])
+    for field, value in (("m_indices", (int(ids[token]) + 1) % G), ("m_indices", G), ("src", T), ("src", 2 ** 31 - 1)):
+        t = getattr(route, field).clone()
+        t[other] = value
+        out = base.clone()
+        fg.lora_f16(x, a, b, route._replace(**{field: t}), base=out, out=out)
+        assert fg.check_status()[0] == fg.ERR_DEVICE_INPUT
+        keep = torch.arange(T, device=dev) != token
+        assert torch.equal(out[keep], want[keep]) and torch.equal(out[token], base[token])
+    m = route.m_indices.clone()
+    m[:128] = G + 5                                         # a whole block
+    out = base.clone()
+    fg.lora_f16(x, a, b, route._replace(m_indices=m), base=out, out=out)
+    assert fg.check_status()[0] == fg.ERR_DEVICE_INPUT
+    # tiles of 16 that claim to be blocks of 128: rows of other adapters than the first's are left alone
+    mixed = fg.route_contiguous(ids, G, 16, M=384)._replace(align=128)
+    out = base.clone()
+    fg.lora_f16(x, a, b, mixed, base=out, out=out)
+    assert fg.check_status()[0] == fg.ERR_DEVICE_INPUT
+    first = mixed.m_indices.view(-1, 128)[:, 0].repeat_interleave(128)
+    right = torch.zeros(T, dtype=torch.bool, device=dev)
+    own = (mixed.src >= 0) & (mixed.m_indices == first)
+    right[mixed.src[own].long()] = True
+    assert 0 < int(right.sum()) < T and torch.equal(out[right], want[right]) and torch.equal(out[~right], base[~right])
+    assert fg.check_status()[0] == 0
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_wide_blocks_with_few_tokens(fg, dev, dtype):
+    """Blocks of 128 rows of which most are empty, some of them whole blocks, ragged K and N."""
+    for T, G, K, N, r in [(3, 5, 200, 136, 24), (130, 2, 72, 1000, 128), (257, 40, 328, 72, 56)]:
+        x, a, b, base, scale, ids = _inputs(T, G, K, N, r, dtype, dev)
+        route = fg.route_contiguous(ids, G, 256)
+        out = fg.lora_f16(x, a, b, route, scale=scale, base=base)
+        gated_reference.close(out, *ref.lora64(x, a, b, ids, scale, base))
+    assert fg.check_status()[0] == 0
+
+
+@pytest.mark.parametrize("align", [16, 128])
+def test_queue_of_dependent_calls(fg, dev, align):
+    """Calls that each read what the one before wrote, with and without programmatic launches."""
+    T, G, K, r = 260, 3, 256, 32
+    x, a, b, _, _, ids = _inputs(T, G, K, K, r, torch.bfloat16, dev)
+    before = fg.set_pdl(False)
+    try:
+        outs = []
+        for pdl in (False, True, True):
+            fg.set_pdl(pdl)
+            y = x.clone()
+            for _ in range(40):
+                route = fg.route_contiguous(ids, G, align)
+                z = fg.lora_f16(y, a, b, route, base=y)
+                y = fg.lora_f16(z, a, b, route, base=x)
+            outs.append(y)
+        assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    finally:
+        fg.set_pdl(before)
+    assert fg.check_status()[0] == 0
+
+
 def test_streams_and_graphs(fg, dev):
     """On another stream than the current one; captured once and replayed on other inputs, two
     graphs side by side."""

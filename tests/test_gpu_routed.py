@@ -446,6 +446,19 @@ def test_streams_and_graphs(fg, dev):
     assert fg.check_status()[0] == 0
 
 
+def test_long_list_in_a_graph(fg, dev):
+    """A routing on a cluster of 16 CTAs, captured and replayed on other ids."""
+    T, k, G = 9000, 4, 40
+    ids = ref.random_ids(T, k, G, 1).to(dev)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = fg.route_contiguous(ids, G)
+    ids.copy_(ref.random_ids(T, k, G, 2, 0.2, 0.1))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(held[:5], fg.route_contiguous(ids, G)[:5]))
+
+
 def test_queue_of_dependent_calls(fg, dev):
     """Calls that each read what the one before wrote, with and without programmatic launches."""
     T, k, G, H = 500, 2, 8, 512
