@@ -71,75 +71,94 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   lo = pack_2x16(l[0], l[1], BF16);
 }
 
-// P from the sums over the shares of K, as value, rest and power.  With `all` every CTA of the
+// P from the sums over the shares of K, as value, rest and power.  With ALL every CTA of the
 // cluster sums all rows over `part` of all CTAs and keeps them; otherwise it sums every C-th row
 // and hands it to all of them.  place(row, column, value's address, rest's) says where two
 // columns go.  A row is summed by as many lanes as it has pairs of columns, up to 32.
-template <bool BF16, int RP, typename Place>
+template <bool BF16, int RP, bool ALL, typename Place>
 __device__ __forceinline__ void exchange_rows(const float* part, float* power, int rows, const float* scale_at, int C, int rank,
-                                              bool all, Place&& place) {
+                                              Place&& place) {
   constexpr int LDP = RP + 4, LANES = RP >= 64 ? 32 : RP / 2, PAIRS = RP / 2 / LANES, TOGETHER = 32 / LANES;
+  constexpr int ROWS = ALL || RP == 16 ? 1 : RP == 128 ? 2 : 4;   // rows of a lane whose loads are in flight together
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31), at_lane = lane % LANES;
-  const int first = all ? 0 : rank, step = all ? 1 : C;
+  const int first = ALL ? 0 : rank, step = ALL ? 1 : C;
   const float scale = *scale_at;
-  for (int i = warp * TOGETHER; first + step * i < rows; i += kWarps * TOGETHER) {
-    const int row = first + step * (i + lane / LANES);
-    const bool in = row < rows;
-    float2 v[PAIRS];
-    float top = 0.0f;
+  for (int i = warp * TOGETHER; first + step * i < rows; i += kWarps * TOGETHER * ROWS) {
+    float2 v[ROWS][PAIRS];
+    int row[ROWS];
 #pragma unroll
-    for (int u = 0; u < PAIRS; ++u) {
-      v[u] = make_float2(0.0f, 0.0f);
-      if (in) {
-        const uint32_t at = ptx::smem_u32(part + row * LDP + 2 * (at_lane + LANES * u));
-        float2 s[kMaxCluster];
+    for (int m = 0; m < ROWS; ++m) {
+      row[m] = first + step * (i + m * kWarps * TOGETHER + lane / LANES);
+      if (row[m] >= rows) row[m] = -1;
 #pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r)
-          if (r < C) s[r] = ld_cluster_f32x2(map_to_rank(at, static_cast<uint32_t>(r)));
-#pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r)
-          if (r < C) {
-            v[u].x += s[r].x;
-            v[u].y += s[r].y;
-          }
-        v[u].x *= scale;
-        v[u].y *= scale;
-        if (!BF16) top = fmaxf(top, fmaxf(fabsf(v[u].x), fabsf(v[u].y)));
-      }
+      for (int u = 0; u < PAIRS; ++u) v[m][u] = make_float2(0.0f, 0.0f);
     }
-    float up = 1.0f;
-    if (!BF16) {
-      __syncwarp();
+    // over the cluster in its order, two CTAs at a time
+    for (int r = 0; r < C; r += 2) {
+      float2 s[2][ROWS][PAIRS];
 #pragma unroll
-      for (int off = LANES / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
-      // the largest goes to [2^14, 2^15): exponents stay where 2^e and 2^-e are normal numbers
-      int e = static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14;
-      e = e < -126 ? -126 : e;
-      if (top == 0.0f || top > 3.4028235e38f) e = 0;
-      up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int m = 0; m < ROWS; ++m)
+#pragma unroll
+          for (int u = 0; u < PAIRS; ++u) {
+            s[h][m][u] = make_float2(0.0f, 0.0f);
+            if (row[m] >= 0 && r + h < C)
+              s[h][m][u] = ld_cluster_f32x2(map_to_rank(ptx::smem_u32(part + row[m] * LDP + 2 * (at_lane + LANES * u)), static_cast<uint32_t>(r + h)));
+          }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int m = 0; m < ROWS; ++m)
+#pragma unroll
+          for (int u = 0; u < PAIRS; ++u) {
+            v[m][u].x += s[h][m][u].x;
+            v[m][u].y += s[h][m][u].y;
+          }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int m = 0; m < ROWS; ++m) {
+      float top = 0.0f, up = 1.0f;
 #pragma unroll
       for (int u = 0; u < PAIRS; ++u) {
-        v[u].x *= down;
-        v[u].y *= down;
+        v[m][u].x *= scale;
+        v[m][u].y *= scale;
+        if (!BF16) top = fmaxf(top, fmaxf(fabsf(v[m][u].x), fabsf(v[m][u].y)));
       }
-    }
-    if (!in) continue;
-    const int to0 = all ? rank : 0, to1 = all ? rank + 1 : C;
+      if (!BF16) {
 #pragma unroll
-    for (int u = 0; u < PAIRS; ++u) {
-      uint32_t h, l, at_h, at_l;
-      split2<BF16>(v[u].x, v[u].y, h, l);
-      place(row, 2 * (at_lane + LANES * u), at_h, at_l);
-      for (int r = to0; r < to1; ++r) {
-        st_cluster_u32(map_to_rank(at_h, static_cast<uint32_t>(r)), h);
-        st_cluster_u32(map_to_rank(at_l, static_cast<uint32_t>(r)), l);
+        for (int off = LANES / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+        // the largest goes to [2^14, 2^15): exponents stay where 2^e and 2^-e are normal numbers
+        int e = static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14;
+        e = e < -126 ? -126 : e;
+        if (top == 0.0f || top > 3.4028235e38f) e = 0;
+        up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+        for (int u = 0; u < PAIRS; ++u) {
+          v[m][u].x *= down;
+          v[m][u].y *= down;
+        }
       }
+      if (row[m] >= 0) {
+        const int to0 = ALL ? rank : 0, to1 = ALL ? rank + 1 : C;
+#pragma unroll
+        for (int u = 0; u < PAIRS; ++u) {
+          uint32_t h, l, at_h, at_l;
+          split2<BF16>(v[m][u].x, v[m][u].y, h, l);
+          place(row[m], 2 * (at_lane + LANES * u), at_h, at_l);
+          for (int r = to0; r < to1; ++r) {
+            st_cluster_u32(map_to_rank(at_h, static_cast<uint32_t>(r)), h);
+            st_cluster_u32(map_to_rank(at_l, static_cast<uint32_t>(r)), l);
+          }
+        }
+        if (at_lane == 0)
+          for (int r = to0; r < to1; ++r) st_cluster_f32(map_to_rank(ptx::smem_u32(power + row[m]), static_cast<uint32_t>(r)), up);
+      }
+      __syncwarp();
     }
-    if (at_lane == 0)
-      for (int r = to0; r < to1; ++r) st_cluster_f32(map_to_rank(ptx::smem_u32(power + row), static_cast<uint32_t>(r)), up);
   }
-  __syncwarp();
 }
 
 // The two halves of a cluster barrier (whole-warp instructions).
@@ -340,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_kernel(Lo
   if (kTwo) load_block(nb0 + warp + kWarps, odd);
   // every CTA sums all rows, and they meet once
   if (C > 1) cluster_sync_all(); else __syncthreads();
-  exchange_rows<BF16, RP>(part, power, 16, &tile_scale, C, rank, true, [&](int row, int col, uint32_t& at_h, uint32_t& at_l) {
+  exchange_rows<BF16, RP, true>(part, power, 16, &tile_scale, C, rank, [&](int row, int col, uint32_t& at_h, uint32_t& at_l) {
     at_h = ptx::smem_u32(hi + row * LDH + col);
     at_l = ptx::smem_u32(lo + row * LDH + col);
   });
@@ -705,7 +724,7 @@ __global__ void __launch_bounds__(kWideThreads, RP <= 64 ? 2 : 1) lora_f16_wide_
       }
     }
     cluster_sync_all();
-    exchange_rows<BF16, RP>(part, power, kWideRows, &block_scale, C, rank, false, [&](int r, int col, uint32_t& at_h, uint32_t& at_l) {
+    exchange_rows<BF16, RP, false>(part, power, kWideRows, &block_scale, C, rank, [&](int r, int col, uint32_t& at_h, uint32_t& at_l) {
       at_h = base_s + Cf::OFF_HI + swizzled(kWideRows, r, col);
       at_l = at_h + Cf::PBYTES;
     });
