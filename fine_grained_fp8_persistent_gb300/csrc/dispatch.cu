@@ -179,34 +179,46 @@ __global__ void __launch_bounds__(kBulkThreads) dispatch_f16_kernel(BulkArgs arg
 // ----------------------------------------------------------------- dispatch, E4M3
 // A warp's item is 512 elements of a token, quantized as quantize_1x128 does it (lanes
 // 8 i .. 8 i + 7 hold K block i, 16 elements each), codes and scales written to its k rows.
-template <bool UE8M0>
-__global__ void __launch_bounds__(kThreads) dispatch_fp8_kernel(RowsArgs a, const uint4* __restrict__ X,
+template <bool UE8M0, bool MASKED>
+__global__ void __launch_bounds__(kThreads, 4) dispatch_fp8_kernel(RowsArgs a, const uint4* __restrict__ X,
                                                                 uint4* __restrict__ Xq, uint32_t* __restrict__ SF) {
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int lane = static_cast<int>(threadIdx.x & 31);
   const int nkb = a.H / 128, kq = (nkb + 3) / 4;
-  const int per = a.slots > 0 ? a.slots : a.M;             // rows of one scale table
+  const int per = MASKED ? a.slots : a.M;                  // rows of one scale table
   const size_t ld = (static_cast<size_t>(per) + 3) / 4 * 4;
   const size_t table = ld * (UE8M0 ? kq : nkb);
   const uint32_t T = static_cast<uint32_t>(a.T);
   Walk w(blockIdx.x * kWarps + (threadIdx.x >> 5), gridDim.x * kWarps, static_cast<uint32_t>(kq));
-  for (; w.t < T; w.next()) {
+  uint4 next0, next1;                                      // the next item's elements and rows
+  int next_rows = -1;
+  auto load = [&]() {
+    if (4 * static_cast<int>(w.p) + (lane >> 3) < nkb) {
+      const uint4* src = X + (static_cast<size_t>(w.t) * a.H + static_cast<size_t>(w.p) * 512 + 16 * lane) / 8;
+      next0 = ptx::ld_global_v4(src);
+      next1 = ptx::ld_global_v4(src + 1);
+    }
+    next_rows = load_rows(a, w.t, 0, lane);
+  };
+  if (w.t < T) load();
+  while (w.t < T) {
+    const uint32_t t = w.t;
     const int qw = static_cast<int>(w.p), kb = 4 * qw + (lane >> 3);
     const bool active = kb < nkb;
-    const int first_rows = load_rows(a, w.t, 0, lane);
+    const int first_rows = next_rows;
     float f0[8], f1[8];
     float amax = 0.0f;
     if (active) {
-      const uint4* src = X + (static_cast<size_t>(w.t) * a.H + static_cast<size_t>(qw) * 512 + 16 * lane) / 8;
-      const uint4 w0 = ptx::ld_global_v4(src), w1 = ptx::ld_global_v4(src + 1);
-      quant::unpack8(w0, f0);
-      quant::unpack8(w1, f1);
+      quant::unpack8(next0, f0);
+      quant::unpack8(next1, f1);
 #pragma unroll
       for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(f0[i]), fabsf(f1[i])));
     }
 #pragma unroll
     for (int off = 4; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, off));
+    w.next();
+    if (w.t < T) load();
     float s = 1.0f, inv = 1.0f;
     uint32_t word = 0;                                     // what this lane writes to the scale table
     if (UE8M0) {
@@ -227,15 +239,18 @@ __global__ void __launch_bounds__(kThreads) dispatch_fp8_kernel(RowsArgs a, cons
     const bool scales = UE8M0 ? lane == 0 : (lane & 7) == 0 && active;
     const size_t at = ld * (UE8M0 ? qw : kb);
     for (int j0 = 0; j0 < a.k; j0 += 32) {
-      const int rows = j0 == 0 ? first_rows : load_rows(a, w.t, j0, lane);
+      const int rows = j0 == 0 ? first_rows : load_rows(a, t, j0, lane);
+      // in the masked layout each lane finds its row's place in the scale tables, so that the
+      // division is not made for every row by every lane
+      unsigned long long place = 0;
+      if (MASKED && rows >= 0) place = rows / per * static_cast<unsigned long long>(table) + static_cast<unsigned>(rows % per);
+      __syncwarp();
       for (int j = 0; j < 32 && j0 + j < a.k; ++j) {
         const int row = __shfl_sync(kFull, rows, j);
+        const unsigned long long to = MASKED ? __shfl_sync(kFull, place, j) : static_cast<unsigned long long>(row);
         if (row < 0) continue;
         if (active) st_global_v4(Xq + (static_cast<size_t>(row) * a.H + static_cast<size_t>(qw) * 512 + 16 * lane) / 16, code);
-        if (scales) {
-          const int g = a.slots > 0 ? row / a.slots : 0;
-          SF[static_cast<size_t>(g) * table + at + (row - g * a.slots)] = word;
-        }
+        if (scales) SF[to + at] = word;
       }
     }
   }
@@ -528,9 +543,12 @@ int launch_dispatch_f16(const RowsArgs& a, const void* X, void* Xs, cudaStream_t
 }
 
 int launch_dispatch_fp8(const RowsArgs& a, const void* X, void* Xq, void* SFA, int fmt, cudaStream_t stream) {
-  static PerDevice<int> cache[2];
+  static PerDevice<int> cache[4];
   const long long items = static_cast<long long>(a.T) * ((a.H / 128 + 3) / 4);
-  return launch_items(fmt ? dispatch_fp8_kernel<true> : dispatch_fp8_kernel<false>, cache[fmt ? 1 : 0], items, stream, a,
+  const bool masked = a.slots > 0;
+  auto* fn = fmt ? (masked ? dispatch_fp8_kernel<true, true> : dispatch_fp8_kernel<true, false>)
+                 : (masked ? dispatch_fp8_kernel<false, true> : dispatch_fp8_kernel<false, false>);
+  return launch_items(fn, cache[(fmt ? 1 : 0) + (masked ? 2 : 0)], items, stream, a,
                       static_cast<const uint4*>(X), static_cast<uint4*>(Xq), static_cast<uint32_t*>(SFA));
 }
 
