@@ -745,8 +745,8 @@ def lora_f16(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, route: Route, sc
     """out[t] = base[t] + scale[g] (X[t] A[g]^T) B[g]^T with g the adapter of token t, in one kernel.
     x (T, K), a (G, r, K), b (G, N, r), base and out (T, N) are fp16/bf16, r a multiple of 8 up to
     128, scale float32 (G,) (None: ones).  route: route_contiguous(adapter ids (T,), G, align)
-    with align a multiple of 16 (128 where adapters have some 64 tokens and more each, 16 for
-    fewer); one serves every layer of a step.  Tokens without an adapter
+    with align a multiple of 16 (a multiple of 128 lets the call take blocks of 128 rows, which
+    pays from some thousand tokens on); one serves every layer of a step.  Tokens without an adapter
     get base (None: zeros).  out may be base.  Rows of x, base and out may be columns of wider
     matrices."""
     T, K = x.shape
@@ -797,8 +797,8 @@ def sfb_bytes(G: int, N: int, K: int, fmt) -> int:
 
 
 def last_tile() -> str:
-    """Kernel configuration of the last GEMM or matrix-vector product this thread launched
-    ("mxf8 dense 2x224", "nvf4 gemv 1x16 deep r1 p2")."""
+    """Kernel configuration of the last GEMM, matrix-vector product or lora_f16 this thread launched
+    ("mxf8 dense 2x224", "nvf4 gemv 1x16 deep r1 p2", "f16 lora 4x128")."""
     return (_lib.fgf8_last_tile() or b"").decode()
 
 

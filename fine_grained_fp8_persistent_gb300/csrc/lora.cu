@@ -22,6 +22,7 @@
 // and the rounded rest, two instructions instead of one, so that it keeps 16 (bf16) or 22
 // (fp16) bits and the only rounding to the operands' type is that of out.  In fp16 each row
 // of P is first scaled by a power of two, so that no sum over K leaves the type's range.
+#include <cstdlib>
 #include <cstring>
 
 #include "gemv.cuh"
@@ -792,6 +793,13 @@ __global__ void __launch_bounds__(kWideThreads, RP <= 64 ? 2 : 1) lora_f16_wide_
   }
 }
 
+// Tiles of 16 rows with a token in them: all of them in segments of 16 rows; in longer ones, which
+// end in empty tiles, at most a partly filled one for each adapter.
+long long used_tiles(const LoraArgs& a) {
+  const long long most = a.M / 16, est = a.T / 16 + (a.T < a.G ? a.T : a.G) + 1;
+  return est < most ? est : most;
+}
+
 // Shared memory of a CTA with one tile.
 template <int RP>
 constexpr int kTileSmem = kWarps * 16 * (RP + 4) * 4 + 2 * 16 * (RP + 8) * 2 + 16 * 4;
@@ -846,14 +854,15 @@ int launch_tiles(const LoraArgs& a, cudaStream_t stream) {
   // the tiles' CTAs are a third more than run together (some tiles are empty).  Clusters that
   // share a tile's N, and each compute P, help up to 64 CTAs with 4 KB of B each.  Over 15
   // shapes of 1 to 2000 tokens this is at most 7 % slower than the best of all splits.
-  const long long tiles = a.M / 16, slots = (RP <= 64 ? 2LL : 1LL) * device_sm_count(), bytes = 2LL * a.N * a.r;
+  const long long tiles = used_tiles(a), slots = (RP <= 64 ? 2LL : 1LL) * device_sm_count(), bytes = 2LL * a.N * a.r;
   int cluster = kMaxCluster, parts = 1;
   while (cluster > 1 && (256 * cluster > a.K || 3 * tiles * cluster > 4 * slots)) cluster /= 2;
   while (2 * parts * cluster <= (a.N + 31) / 32 && 2 * parts * cluster * tiles <= 64 && bytes / (2 * parts * cluster) >= 4096) parts *= 2;
   LoraKArgs k;
   k.a = a;
   k.timeout_ns = 0;                                         // this form waits on no mbarrier
-  LoraLaunch l(tiles, parts, cluster, kThreads, kTileSmem<RP>, stream, pdl_enabled());
+  set_last_tile("f16", "lora", cluster, 16);
+  LoraLaunch l(a.M / 16, parts, cluster, kThreads, kTileSmem<RP>, stream, pdl_enabled());
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, fn, k);
   return e == cudaSuccess ? 0 : set_error(4, "lora_f16 launch: %s", cudaGetErrorString(e));
 }
@@ -892,24 +901,43 @@ int launch_wide(const LoraArgs& a, cudaStream_t stream) {
   CUtensorMap m;
   const uint64_t K = static_cast<uint64_t>(a.K);
   if (!encode_tmap_2d(&m, dt, a.A, K, static_cast<uint64_t>(a.G) * a.r, 2 * K, 64, static_cast<uint32_t>(a.r), true)) return 4;
+  set_last_tile("f16", "lora", cluster, kWideRows);
   LoraLaunch l(groups, 1, cluster, kWideThreads, Cf::SMEM, stream, pdl_enabled());
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, &lora_f16_wide_kernel<BF16, RP>, m, k);
   return e == cudaSuccess ? 0 : set_error(4, "lora_f16 launch: %s", cudaGetErrorString(e));
 }
 
-template <bool BF16, int RP>
-int by_align(const LoraArgs& a, cudaStream_t stream) {
+// Blocks of 128 rows or tiles of 16, by the time each takes, in us.  Tiles: 5 and the bytes that
+// leave L2, at 8.2 TB/s: X, base and out once, A and B once for every 16 tokens.  Blocks: 17 for
+// the start, the exchange and the filling of the rings, and the bytes from memory at 6.3 TB/s, a
+// third less where one CTA fills an SM.  Against times of both forms at 48 shapes (4 to 8192
+// tokens of 4 to 64 adapters, rank 16 to 128) the choice is at most 14 % slower than the better
+// one; 4096 tokens of 32 adapters, 4096 x 4096: 26 and 33 us at rank 16, 49 and 41 at 64.
+// FGF8_FORCE_TILE=1x16 or 1x128 takes a form where the rows allow it.
+bool wide_form(const LoraArgs& a) {
   // the copy engine counts the rows of all adapters' A in 32 bits
-  const long long rows = static_cast<long long>(a.G) * a.r;
-  return a.align % kWideRows == 0 && rows <= kRouteMaxSize ? launch_wide<BF16, RP>(a, stream) : launch_tiles<BF16, RP>(a, stream);
+  if (a.align % kWideRows != 0 || static_cast<long long>(a.G) * a.r > kRouteMaxSize) return false;
+  if (const char* f = std::getenv("FGF8_FORCE_TILE")) {
+    if (std::strcmp(f, "1x16") == 0) return false;
+    if (std::strcmp(f, "1x128") == 0) return true;
+  }
+  const double rows = 2.0 * a.T * (static_cast<double>(a.K) + 2.0 * a.N), adapter = 2.0 * a.r * (static_cast<double>(a.K) + a.N);
+  const double tiles = 5.0 + (rows + used_tiles(a) * adapter) / 8.2e6;
+  const double blocks = 17.0 + (rows + (a.T < a.G ? a.T : a.G) * adapter) / (a.r <= 64 ? 6.3e6 : 4.3e6);
+  return blocks < tiles;
+}
+
+template <bool BF16, int RP>
+int by_form(const LoraArgs& a, cudaStream_t stream) {
+  return wide_form(a) ? launch_wide<BF16, RP>(a, stream) : launch_tiles<BF16, RP>(a, stream);
 }
 
 template <bool BF16>
 int by_rank(const LoraArgs& a, cudaStream_t stream) {
-  if (a.r <= 16) return by_align<BF16, 16>(a, stream);
-  if (a.r <= 32) return by_align<BF16, 32>(a, stream);
-  if (a.r <= 64) return by_align<BF16, 64>(a, stream);
-  return by_align<BF16, 128>(a, stream);
+  if (a.r <= 16) return by_form<BF16, 16>(a, stream);
+  if (a.r <= 32) return by_form<BF16, 32>(a, stream);
+  if (a.r <= 64) return by_form<BF16, 64>(a, stream);
+  return by_form<BF16, 128>(a, stream);
 }
 
 }  // namespace

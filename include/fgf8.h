@@ -368,8 +368,9 @@ FGF8_API int dispatch_f16_backward(const void* dXs, const int32_t* rows, void* d
  *          it may be out itself (with ldb = ldo)
  *   out : [T][N], rows ldo apart
  *   rows [T], src [M], m_indices [M] : route_contiguous of the tokens' adapters (k = 1) with
- *          this align, a multiple of 16: 128 (or a multiple) where adapters have some 64
- *          tokens and more each, 16 for fewer; a routing serves every layer of a step
+ *          this align, a multiple of 16; with a multiple of 128 the call can take blocks of
+ *          128 rows, which pays from some thousand tokens on; a routing serves every layer of
+ *          a step
  * Tokens without an adapter get base.  X, A, B, base and out are of one type (dtype).
  * A row that names another adapter than the first of its `align` rows sets
  * FGF8_ERR_DEVICE_INPUT and is not computed.  Requires K, N, r, ldx, ldb, ldo multiples of
@@ -405,11 +406,12 @@ FGF8_API int fgf8_check_status(void* stream, unsigned int* raw_bits);
 /* Message for the last non-OK return on this thread ("" if none). */
 FGF8_API const char* fgf8_last_error(void);
 
-/* Kernel configuration of the last GEMM or matrix-vector product this thread launched, as
+/* Kernel configuration of the last GEMM, matrix-vector product or lora_f16 this thread launched, as
  * text ("<kind> <schedule> <CTAs per cluster>x<tile width>", e.g. "mxf8 dense 2x224";
  * "f16 gated_thin <CTAs of the cluster>x<tokens>" for the gated block of 17 to 256 rows;
  * "<kind> gemv|gated_gemv <CTAs of the cluster>x<8 or 16 tokens> deep|shallow r<rounds of
- * tiles> p<pieces of X>" for at most 16 rows, e.g. "nvf4 gemv 1x16 deep r1 p2");
+ * tiles> p<pieces of X>" for at most 16 rows, e.g. "nvf4 gemv 1x16 deep r1 p2";
+ * "f16 lora <CTAs of the cluster>x<16 or 128 rows>");
  * "" before the first launch.  The text stays as it is until this thread asks
  * again. */
 FGF8_API const char* fgf8_last_tile(void);

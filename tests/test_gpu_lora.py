@@ -37,13 +37,19 @@ def _inputs(T, G, K, N, r, dtype, dev, absent=0.15, seed=0, skew=0.3):
     return *(t.to(dtype).to(dev) for t in (x, a, b, base)), scale, ids
 
 
-@pytest.mark.parametrize("align", [16, 128])
+# rows of the routing and the form: tiles of 16 in segments of 16 and of 128 rows, blocks of 128
+FORMS = [(16, 16), (128, 16), (128, 128)]
+
+
+@pytest.mark.parametrize("align,rows", FORMS)
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("T,G,K,N,r", SHAPES)
-def test_lora(fg, dev, T, G, K, N, r, dtype, align):
+def test_lora(fg, dev, monkeypatch, T, G, K, N, r, dtype, align, rows):
     x, a, b, base, scale, ids = _inputs(T, G, K, N, r, dtype, dev)
     route = fg.route_contiguous(ids, G, align)
+    monkeypatch.setenv("FGF8_FORCE_TILE", f"1x{rows}")
     out = fg.lora_f16(x, a, b, route, scale=scale, base=base)
+    assert fg.last_tile().startswith("f16 lora ") and fg.last_tile().endswith(f"x{rows}")
     gated_reference.close(out, *ref.lora64(x, a, b, ids, scale, base))
     again = base.clone()
     assert fg.lora_f16(x, a, b, route, scale=scale, base=again, out=again) is again
@@ -55,10 +61,23 @@ def test_lora(fg, dev, T, G, K, N, r, dtype, align):
     assert fg.check_status()[0] == 0
 
 
+# 9000 tokens read adapters 567 times in tiles, in us: rank 32 21 against 26 in blocks, rank 64 30
+# against 26
+@pytest.mark.parametrize("T,r,form", [(100, 32, 16), (9000, 32, 16), (9000, 64, 128)])
+def test_form_by_size(fg, dev, T, r, form):
+    """Few tokens go in tiles whatever their segments, many of a large rank in blocks."""
+    x, a, b, base, scale, ids = _inputs(T, 4, 1024, 1024, r, torch.bfloat16, dev)
+    out = fg.lora_f16(x, a, b, fg.route_contiguous(ids, 4, 128), scale=scale, base=base)
+    assert fg.last_tile().endswith(f"x{form}")
+    gated_reference.close(out, *ref.lora64(x, a, b, ids, scale, base))
+
+
+@pytest.mark.parametrize("align,rows", FORMS)
 @pytest.mark.parametrize("dtype", TYPES)
-def test_no_token_has_an_adapter(fg, dev, dtype):
+def test_no_token_has_an_adapter(fg, dev, monkeypatch, dtype, align, rows):
+    monkeypatch.setenv("FGF8_FORCE_TILE", f"1x{rows}")
     x, a, b, base, scale, ids = _inputs(40, 3, 64, 136, 16, dtype, dev)
-    route = fg.route_contiguous(torch.full_like(ids, -1), 3, 16)
+    route = fg.route_contiguous(torch.full_like(ids, -1), 3, align)
     assert torch.equal(fg.lora_f16(x, a, b, route, base=base), base)
     assert not fg.lora_f16(x, a, b, route).any()
 
@@ -69,13 +88,15 @@ def test_no_tokens(fg, dev):
     assert fg.lora_f16(x[:0], a, b, route, base=base[:0]).shape == (0, 136)
 
 
+@pytest.mark.parametrize("align,rows", FORMS)
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("T", [3, 700])
-def test_rows_of_wider_matrices(fg, dev, T, dtype):
+def test_rows_of_wider_matrices(fg, dev, monkeypatch, T, dtype, align, rows):
     """x, base and out as columns of wider matrices; what stands beside out is left as it was."""
+    monkeypatch.setenv("FGF8_FORCE_TILE", f"1x{rows}")
     G, K, N, r = 4, 136, 72, 16
     x, a, b, base, scale, ids = _inputs(T, G, K, N, r, dtype, dev)
-    route = fg.route_contiguous(ids, G, 16)
+    route = fg.route_contiguous(ids, G, align)
     want = fg.lora_f16(x, a, b, route, scale=scale, base=base)
     wx = torch.full((T, 3 * K), float("nan"), dtype=dtype, device=dev)
     wx[:, K:2 * K] = x
@@ -87,8 +108,9 @@ def test_rows_of_wider_matrices(fg, dev, T, dtype):
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("align,rows", FORMS)
 @pytest.mark.parametrize("dtype", TYPES)
-def test_large_and_small_values(fg, dev, dtype):
+def test_large_and_small_values(fg, dev, monkeypatch, dtype, align, rows):
     """X A^T far above fp16's range beside B far below one, and a token whose own values are tiny:
     the rows of P keep their digits."""
     T, G, K, N, r = 20, 2, 256, 64, 16
@@ -98,18 +120,21 @@ def test_large_and_small_values(fg, dev, dtype):
     a *= 64.0
     b *= 2.0 ** -9
     scale = scale * 64.0
-    route = fg.route_contiguous(ids, G, 16)
+    monkeypatch.setenv("FGF8_FORCE_TILE", f"1x{rows}")
+    route = fg.route_contiguous(ids, G, align)
     out = fg.lora_f16(x, a, b, route, scale=scale)
     p = torch.einsum("tk,trk->tr", x.double(), a[ids.long()].double()) * scale[ids.long()].double().unsqueeze(1)
     assert p.abs().max() > 70000
     gated_reference.close(out, *ref.lora64(x, a, b, ids, scale, None))
 
 
+@pytest.mark.parametrize("align,rows", FORMS)
 @pytest.mark.parametrize("dtype", TYPES)
-def test_infinities_and_nans_stay_in_their_tokens(fg, dev, dtype):
+def test_infinities_and_nans_stay_in_their_tokens(fg, dev, monkeypatch, dtype, align, rows):
+    monkeypatch.setenv("FGF8_FORCE_TILE", f"1x{rows}")
     T, G, K, N, r = 40, 3, 136, 72, 16
     x, a, b, base, scale, ids = _inputs(T, G, K, N, r, dtype, dev, absent=0.0)
-    route = fg.route_contiguous(ids, G, 16)
+    route = fg.route_contiguous(ids, G, align)
     want = fg.lora_f16(x, a, b, route, base=base)
     x2, base2 = x.clone(), base.clone()
     x2[7, 3] = float("nan")
@@ -152,8 +177,9 @@ def test_bad_rows_are_reported(fg, dev):
     assert fg.check_status()[0] == 0
 
 
-def test_bad_rows_in_wide_blocks_are_reported(fg, dev):
+def test_bad_rows_in_wide_blocks_are_reported(fg, dev, monkeypatch):
     """The same where rows come in blocks of 128."""
+    monkeypatch.setenv("FGF8_FORCE_TILE", "1x128")
     T, G, K, N, r = 300, 3, 64, 40, 16
     x, a, b, base, scale, ids = _inputs(T, G, K, N, r, torch.bfloat16, dev, absent=0.0, skew=0.0)
     route = fg.route_contiguous(ids, G, 128)
@@ -187,8 +213,9 @@ def test_bad_rows_in_wide_blocks_are_reported(fg, dev):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-def test_wide_blocks_with_few_tokens(fg, dev, dtype):
+def test_wide_blocks_with_few_tokens(fg, dev, monkeypatch, dtype):
     """Blocks of 128 rows of which most are empty, some of them whole blocks, ragged K and N."""
+    monkeypatch.setenv("FGF8_FORCE_TILE", "1x128")
     for T, G, K, N, r in [(3, 5, 200, 136, 24), (130, 2, 72, 1000, 128), (257, 40, 328, 72, 56)]:
         x, a, b, base, scale, ids = _inputs(T, G, K, N, r, dtype, dev)
         route = fg.route_contiguous(ids, G, 256)
@@ -197,9 +224,10 @@ def test_wide_blocks_with_few_tokens(fg, dev, dtype):
     assert fg.check_status()[0] == 0
 
 
-@pytest.mark.parametrize("align", [16, 128])
-def test_queue_of_dependent_calls(fg, dev, align):
+@pytest.mark.parametrize("align,rows", FORMS)
+def test_queue_of_dependent_calls(fg, dev, monkeypatch, align, rows):
     """Calls that each read what the one before wrote, with and without programmatic launches."""
+    monkeypatch.setenv("FGF8_FORCE_TILE", f"1x{rows}")
     T, G, K, r = 260, 3, 256, 32
     x, a, b, _, _, ids = _inputs(T, G, K, K, r, torch.bfloat16, dev)
     before = fg.set_pdl(False)
@@ -219,12 +247,14 @@ def test_queue_of_dependent_calls(fg, dev, align):
     assert fg.check_status()[0] == 0
 
 
-def test_streams_and_graphs(fg, dev):
+@pytest.mark.parametrize("align,rows", FORMS)
+def test_streams_and_graphs(fg, dev, monkeypatch, align, rows):
     """On another stream than the current one; captured once and replayed on other inputs, two
     graphs side by side."""
+    monkeypatch.setenv("FGF8_FORCE_TILE", f"1x{rows}")
     T, G, K, N, r = 50, 6, 264, 328, 32
     x, a, b, base, scale, ids = _inputs(T, G, K, N, r, torch.bfloat16, dev)
-    route = fg.route_contiguous(ids, G, 16)
+    route = fg.route_contiguous(ids, G, align)
     want = fg.lora_f16(x, a, b, route, scale=scale, base=base)
     side = torch.cuda.Stream(dev)
     side.wait_stream(torch.cuda.current_stream())
@@ -235,7 +265,7 @@ def test_streams_and_graphs(fg, dev):
     for _ in range(2):
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            rt = fg.route_contiguous(ids, G, 16)
+            rt = fg.route_contiguous(ids, G, align)
             y = fg.lora_f16(x, a, b, rt, scale=scale, base=base)
             outs.append(fg.lora_f16(x, a, b, rt, scale=scale, base=y, out=y))
         graphs.append(g)
@@ -247,7 +277,7 @@ def test_streams_and_graphs(fg, dev):
         with torch.cuda.stream(s):
             g.replay()
     torch.cuda.synchronize()
-    rt = fg.route_contiguous(ids, G, 16)
+    rt = fg.route_contiguous(ids, G, align)
     y = fg.lora_f16(x, a, b, rt, scale=scale, base=base)
     want = fg.lora_f16(x, a, b, rt, scale=scale, base=y)
     assert all(torch.equal(o, want) for o in outs)
