@@ -163,9 +163,10 @@ int lora_f16(const void* X, const void* A, const void* B, const float* scale, co
   if (ldx % 8 != 0 || ldo % 8 != 0 || (base != nullptr && ldb % 8 != 0))
     return set_error(FGF8_ERR_MISALIGNED, "%s: row distances must be multiples of 8", who);
   if (base == out && ldb != ldo) return set_error(FGF8_ERR_INVALID_ARG, "%s: base is out with another row distance", who);
-  if (T == 0 || (M == 0 && base == out)) return FGF8_OK;
-  if (int e = check_pointers(who, {X, A, B, when(scale != nullptr, scale, X), when(base != nullptr, base, X), rows,
-                                   when(M > 0, src, X), when(M > 0, m_indices, X), out}))
+  if (T == 0) return FGF8_OK;
+  if (M == 0) return set_error(FGF8_ERR_INVALID_ARG, "%s: no rows for T=%d tokens", who, T);
+  if (int e = check_pointers(who, {X, A, B, when(scale != nullptr, scale, X), when(base != nullptr, base, X), rows, src,
+                                   m_indices, out}))
     return e;
   fgf8::LoraArgs a{X, A, B, scale, base, out, rows, src, m_indices, ldx, ldb, ldo, T, K, N, r, G, M, align, nullptr};
   if (int e = status_word(who, &a.status)) return e;

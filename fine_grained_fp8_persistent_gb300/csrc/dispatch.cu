@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads) combine_f16_backward_kernel(RowsArgs
   const int threads = static_cast<int>(blockDim.x), warps = threads >> 5;
   const int vecs = a.H / 8;
   int turn = 0;
-  for (int t = static_cast<int>(blockIdx.x); t < a.T; t += static_cast<int>(gridDim.x)) {
+  for (uint32_t t = blockIdx.x; t < static_cast<uint32_t>(a.T); t += gridDim.x) {
     for (int j0 = 0; j0 < a.k; j0 += B) {
       int row[B];
       float w[B], dot[B];

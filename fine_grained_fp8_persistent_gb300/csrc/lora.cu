@@ -242,17 +242,9 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_kernel(Lo
   }
   int g = __shfl_sync(kFull, id, 0);
   // rows of another adapter, adapters and tokens out of range are reported and left alone
-  bool bad = false;
-  if (g >= a.G) {
-    bad = lane == 0;
-    g = -1;
-  }
-  if (id < 0 || token < 0 || g < 0) {
-    token = -1;
-  } else if (id != g || token >= a.T) {
-    bad = true;
-    token = -1;
-  }
+  bool bad = id >= a.G || (id >= 0 && token >= 0 && (id != g || token >= a.T));
+  if (g >= a.G) g = -1;
+  if (bad || id < 0 || token < 0) token = -1;
   if (bad) atomicOr(a.status, FGF8_DEVERR_INPUT);
   if (g < 0) {                                              // the same for every warp of the cluster
     others.fill();
@@ -538,20 +530,13 @@ __global__ void __launch_bounds__(kWideThreads, RP <= 64 ? 2 : 1) lora_f16_wide_
   // the block's adapter and tokens
   const long long row0 = static_cast<long long>(blockIdx.x) * kWideRows;
   int g = ptx::ld_global(a.m_indices + row0);
-  bool bad = tid == 0 && (g >= a.G);
-  if (g >= a.G) g = -1;
   if (tid < kWideRows) {
-    const int id = ptx::ld_global(a.m_indices + row0 + tid);
-    int t = ptx::ld_global(a.src + row0 + tid);
-    if (id < 0 || t < 0 || g < 0) {
-      t = -1;
-    } else if (id != g || t >= a.T) {
-      bad = true;
-      t = -1;
-    }
-    tokens[tid] = t;
+    const int id = ptx::ld_global(a.m_indices + row0 + tid), t = ptx::ld_global(a.src + row0 + tid);
+    const bool bad = id >= a.G || (id >= 0 && t >= 0 && (id != g || t >= a.T));
+    tokens[tid] = bad || id < 0 ? -1 : t;                   // t is -1 where there is none
+    if (bad) atomicOr(a.status, FGF8_DEVERR_INPUT);
   }
-  if (bad) atomicOr(a.status, FGF8_DEVERR_INPUT);
+  if (g >= a.G) g = -1;
   if (tid == 0) block_scale = a.scale != nullptr && g >= 0 ? ptx::ld_global(a.scale + g) : 1.0f;
   if (g < 0) {                                              // the same for every CTA of the cluster
     others.fill();

@@ -288,7 +288,8 @@ FGF8_API int gated_gemv_fp4(const void* X, const void* WgQ, const void* SFg, con
  *   rows : int32 [T][k], row of each entry, -1 = none
  *   src  : int32 [M], entry t * k + j of each row, -1 = none
  * Entries of a group stand in the order of t * k + j, on every run.  An id or a row out of
- * range sets FGF8_ERR_DEVICE_INPUT and counts as -1.  Two entries may not share a row.
+ * range sets FGF8_ERR_DEVICE_INPUT and counts as -1.  Two entries may not share a row, and
+ * outputs overlap no input.
  *
  * route_contiguous -- the layout of grouped_fp8_contiguous: groups one behind the other,
  * each padded to a multiple of `align` rows.
@@ -372,9 +373,11 @@ FGF8_API int dispatch_f16_backward(const void* dXs, const int32_t* rows, void* d
  *          128 rows, which pays from some thousand tokens on; a routing serves every layer of
  *          a step
  * Tokens without an adapter get base.  X, A, B, base and out are of one type (dtype).
- * A row that names another adapter than the first of its `align` rows sets
+ * The rows of a tile of 16, or of a block of 128 where the call takes those, have one adapter:
+ * a row that names another one than the first, or one out of range, sets
  * FGF8_ERR_DEVICE_INPUT and is not computed.  Requires K, N, r, ldx, ldb, ldo multiples of
- * 8, r <= 128, M % align == 0, and an out that overlaps no other input than an identical base.
+ * 8, r <= 128, M % align == 0, M > 0 where there are tokens, and an out that overlaps no other
+ * input than an identical base.
  */
 FGF8_API int lora_f16(const void* X, const void* A, const void* B, const float* scale, const void* base,
                       const int32_t* rows, const int32_t* src, const int32_t* m_indices, void* out, int T, int K, int N,

@@ -212,6 +212,24 @@ def test_bad_rows_in_wide_blocks_are_reported(fg, dev, monkeypatch):
     assert fg.check_status()[0] == 0
 
 
+@pytest.mark.parametrize("align,rows", FORMS)
+def test_row_behind_an_empty_first_row_is_reported(fg, dev, monkeypatch, align, rows):
+    """A tile or block whose first row has no adapter has none: a row of it that names one is not
+    computed, and not passed over in silence."""
+    monkeypatch.setenv("FGF8_FORCE_TILE", f"1x{rows}")
+    T, G, K, N, r = 40, 2, 64, 40, 16
+    x, a, b, base, scale, ids = _inputs(T, G, K, N, r, torch.bfloat16, dev, absent=0.0, skew=0.0)
+    route = fg.route_contiguous(ids, G, align)
+    m = route.m_indices.clone()
+    m[0] = -1
+    out = base.clone()
+    fg.lora_f16(x, a, b, route._replace(m_indices=m), base=out, out=out)
+    assert fg.check_status()[0] == fg.ERR_DEVICE_INPUT
+    held = route.src[:rows][m[:rows] >= 0].long()
+    assert held.numel() > 0 and torch.equal(out[held], base[held])
+    assert fg.check_status()[0] == 0
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_wide_blocks_with_few_tokens(fg, dev, monkeypatch, dtype):
     """Blocks of 128 rows of which most are empty, some of them whole blocks, ragged K and N."""

@@ -134,6 +134,14 @@ def test_lora_refusals(lib):
     assert call(ptrs=[None] * 9, T=0) == 0
 
 
+def test_lora_without_rows(lib):
+    """Tokens need rows, even when none has an adapter and out is another matrix than base."""
+    f = _fn(lib, "lora_f16", 9, 7, 3)
+    for out, ldo in ((AL, 32), (P(0x20000), 40)):
+        assert f(*[AL] * 8, out, 4, 64, 32, 16, 2, 0, 16, 64, 32, ldo, 0, None) == 1 and "no rows" in _err(lib)
+    assert f(*[AL] * 9, 0, 64, 32, 16, 2, 0, 16, 64, 32, 32, 0, None) == 0
+
+
 # ----------------------------------------------------------------- the binding
 @pytest.fixture()
 def fg(monkeypatch):
