@@ -84,6 +84,15 @@ __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
+// The two halves of a cluster barrier.
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 // Arrive on a barrier of any CTA of the cluster.  The default (release, CTA
 // scope) form is enough: what the waiting side reads next is either TMEM written
 // by tcgen05 ops this thread has already waited on (tcgen05.wait + fence pair) or

@@ -162,16 +162,6 @@ __device__ __forceinline__ void exchange_rows(const float* part, float* power, i
   }
 }
 
-// The two halves of a cluster barrier (whole-warp instructions).
-__device__ __forceinline__ void cluster_arrive() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  __syncwarp();
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // Rows of tokens without an adapter: base, or zeros.  An item is 2 KB of 32 tokens; every warp
 // of the grid takes its share when its other work is done, and looks at the tokens of its
 // first item as it starts.  In place there is nothing to do.

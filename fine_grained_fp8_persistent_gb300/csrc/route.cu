@@ -5,17 +5,19 @@
 //   contiguous: row(i) = starts(id) + rank(i), starts = prefix sum of the counts rounded up
 //   masked:     row(i) = slots id + rank(i), or none where rank(i) >= slots
 //
-// One launch of one cluster.  A CTA takes a run of entries, each of its warps a run of
-// those, so that (CTA, warp, step, lane) is the flat order and the ranks do not depend on
-// timing.  A warp counts its run into its own row of a histogram in shared memory, the
-// rows are summed over warps, the sums over CTAs through distributed shared memory, and a
-// second walk hands out the rows: the lanes of one id are found by a ballot for each of its
-// bits (__match_any_sync takes longer from some ten thousand entries on).  Every CTA scans the groups' counts for itself.  m_indices
-// follows from the counts alone and is written in row order; src is the only scattered
-// output.  One cluster instead of the whole GPU: the ids of 8192 tokens with 8 experts are
-// 256 KB, and a barrier across a cluster is a hardware barrier, while one across the grid
-// would be a second launch.  Bound by instruction issue on those SMs: 8.6 us at 8192 x 8 ids
-// of 32 groups, 5 % of the dispatch that follows.
+// One launch of a few clusters, each of which counts all entries, so that they do not wait for
+// one another, and places its share of them.  In a cluster a CTA takes a run of entries, each
+// of its warps a run of those, so that (CTA, warp, step, lane) is the flat order and the ranks
+// do not depend on timing.  A warp counts its run into its own row of a histogram in shared
+// memory, the rows are summed over warps, the sums over CTAs through distributed shared memory,
+// and a second walk hands out the rows of this cluster's warps: the lanes of one id are found
+// by a ballot for each of its bits (__match_any_sync takes longer from some ten thousand entries
+// on).  Every CTA scans the groups' counts for itself.  m_indices follows from the counts alone
+// and is written in row order; src is the only scattered output.  Clusters instead of the whole
+// GPU at once: the ids of 8192 tokens with 8 experts are 256 KB, and a barrier across a cluster
+// is a hardware barrier, while one across the grid would be a second launch.  Bound by
+// the chain of steps (ids, counts, barrier, sums, rows) and by instruction issue: 7.2 us at
+// 8192 x 8 ids of 32 groups, 4 % of the dispatch that follows; one cluster for all takes 8.2.
 #include <cstring>
 
 #include "gemm_persistent.cuh"
@@ -69,14 +71,17 @@ __device__ __forceinline__ int load_id(const RouteArgs& a, int i, int end, bool&
   return -1;
 }
 
+// Two CTAs to an SM: in 32 registers a thread, where the next kernel's CTAs can stand beside
+// them and wait.  In 64 the route of 8192 x 8 ids and the dispatch_f16 behind it take 205 us
+// together, 201 in 32.
 template <bool IDS64>
-__global__ void __launch_bounds__(kMaxThreads, 1) route_kernel(RouteArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, 2) route_kernel(RouteArgs a, int S) {
   extern __shared__ int32_t smem[];
-  const int G = a.G, Gs = G | 1;                            // an odd row length: warps read a column without conflicts
-  const int S = static_cast<int>(gridDim.x);                // the grid is one cluster
+  const int G = a.G;
+  const int cluster = static_cast<int>(blockIdx.x) / S, clusters = static_cast<int>(gridDim.x) / S;   // S CTAs each
   const int threads = static_cast<int>(blockDim.x), W = threads >> 5;
-  int32_t* hist = smem;                                     // [warp][Gs]
-  int32_t* total = hist + W * Gs;                           // [G] this CTA's counts
+  int32_t* hist = smem;                                     // [warp][G]
+  int32_t* total = hist + W * G;                            // [G] this CTA's counts
   int32_t* first = total + G;                               // [G + 1] first row of each group
   int32_t* base = first + G + 1;                            // [G] row of this CTA's first entry of each group (masked: its rank)
   int32_t* count = base + G;                                // [G] entries with a row, over all CTAs
@@ -84,7 +89,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) route_kernel(RouteArgs a) {
   const int bits = 32 - __clz(G), top = 1 << (bits - 1);    // of G, and the highest power of two up to it
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(cluster_rank());
-  for (int i = tid; i < W * Gs; i += threads) hist[i] = 0;
+  for (int i = tid; i < W * G; i += threads) hist[i] = 0;
   ptx::griddep_wait();                                      // ids may come from the previous kernel
   ptx::griddep_launch_dependents();
   __syncthreads();
@@ -95,10 +100,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) route_kernel(RouteArgs a) {
   const long long lo = (static_cast<long long>(rank) * W + warp) * per * 32;
   const int begin = static_cast<int>(lo < a.n ? lo : a.n);
   const int end = static_cast<int>(lo + per * 32 < a.n ? lo + per * 32 : a.n);
-  int32_t* mine = hist + warp * Gs;
+  int32_t* mine = hist + warp * G;
   bool bad = false;
+  int id[kAhead];
   for (int i0 = begin; i0 < end; i0 += 32 * kAhead) {
-    int id[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) id[u] = load_id<IDS64>(a, i0 + 32 * u + lane, end, bad);
 #pragma unroll
@@ -108,28 +113,38 @@ __global__ void __launch_bounds__(kMaxThreads, 1) route_kernel(RouteArgs a) {
   if (bad) atomicOr(a.status, FGF8_DEVERR_INPUT);
   __syncthreads();
 
-  // counts of this CTA, and each warp's offset within them: a warp per group, a lane per warp
-  for (int g = warp; g < G; g += W) {
-    const int32_t c = lane < W ? hist[lane * Gs + g] : 0;
-    int32_t scan = c;
+  // counts of this CTA, and each warp's offset within them: a thread per group
+  if (tid < G) {
+    int32_t sum = 0;
+    for (int w = 0; w < W; w += 8) {
+      int32_t c[8];
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int32_t v = __shfl_up_sync(kFull, scan, off);
-      if (lane >= off) scan += v;
+      for (int u = 0; u < 8; ++u) c[u] = w + u < W ? hist[(w + u) * G + tid] : 0;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (w + u < W) hist[(w + u) * G + tid] = sum;
+        sum += c[u];
+      }
     }
-    if (lane < W) hist[lane * Gs + g] = scan - c;
-    if (lane == 31) total[g] = scan;
+    total[tid] = sum;
   }
   if (S > 1) cluster_sync_all(); else __syncthreads();
   int32_t before = 0, all = 0;                              // of group tid: entries of earlier CTAs, of all
   if (tid < G) {
     const uint32_t at = ptx::smem_u32(total + tid);
-    for (int r = 0; r < S; ++r) {
-      const int32_t c = static_cast<int32_t>(ld_cluster_u32(map_to_rank(at, static_cast<uint32_t>(r))));
-      if (r < rank) before += c;
-      all += c;
+    for (int r = 0; r < S; r += kPortableCluster) {
+      uint32_t c[kPortableCluster] = {};                    // in flight together
+#pragma unroll
+      for (int u = 0; u < kPortableCluster; ++u)
+        if (r + u < S) c[u] = ld_cluster_u32(map_to_rank(at, static_cast<uint32_t>(r + u)));
+#pragma unroll
+      for (int u = 0; u < kPortableCluster; ++u) {
+        if (r + u < rank) before += static_cast<int32_t>(c[u]);
+        all += static_cast<int32_t>(c[u]);
+      }
     }
   }
+  if (S > 1) cluster_arrive();                              // behind this nothing remote is read
   // first rows: an exclusive prefix sum of the padded counts, one group per thread
   const int32_t padded = a.slots > 0 ? a.slots : (all + a.align - 1) / a.align * a.align;
   const int32_t held = a.slots > 0 && all > a.slots ? a.slots : all;
@@ -148,7 +163,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) route_kernel(RouteArgs a) {
     if (tid == G - 1) first[G] = start + padded;
     base[tid] = a.slots > 0 ? before : start + before;
     count[tid] = held;
-    if (rank == 0) {
+    if (blockIdx.x == 0) {
       a.counts[tid] = held;
       if (a.starts != nullptr) {
         a.starts[tid] = start;
@@ -158,12 +173,13 @@ __global__ void __launch_bounds__(kMaxThreads, 1) route_kernel(RouteArgs a) {
   }
   __syncthreads();
 
-  // the entries' rows
-  for (int i0 = begin; i0 < end; i0 += 32 * kAhead) {
-    int id[kAhead];
+  // the rows of the entries that fall to this cluster
+  for (int i0 = warp % clusters == cluster ? begin : end; i0 < end; i0 += 32 * kAhead) {
     bool ignored = false;
+    if (per > kAhead) {                                     // else the registers still hold them
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) id[u] = load_id<IDS64>(a, i0 + 32 * u + lane, end, ignored);
+      for (int u = 0; u < kAhead; ++u) id[u] = load_id<IDS64>(a, i0 + 32 * u + lane, end, ignored);
+    }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       if (i0 + 32 * u >= end) break;
@@ -182,7 +198,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) route_kernel(RouteArgs a) {
     }
   }
   // m_indices, and src of the rows without an entry, in row order, kChunk rows to a warp
-  for (long long r0 = (static_cast<long long>(warp) * S + rank) * kChunk; r0 < a.M; r0 += static_cast<long long>(S) * W * kChunk) {
+  const long long ctas = gridDim.x;
+  for (long long r0 = (warp * ctas + blockIdx.x) * kChunk; r0 < a.M; r0 += ctas * W * kChunk) {
     int g = 0;                                              // the last group that begins at or before r0
     for (int half = top; half > 0; half >>= 1)
       if (g + half <= G && first[g + half] <= r0) g += half;
@@ -196,15 +213,15 @@ __global__ void __launch_bounds__(kMaxThreads, 1) route_kernel(RouteArgs a) {
       if (!owned) a.src[row] = -1;
     }
   }
-  if (S > 1) cluster_sync_all();                            // stay until every CTA has read the counts
+  if (S > 1) cluster_wait();                                // stay until every CTA has read the counts
 }
 
-size_t smem_bytes(int G, int warps) { return sizeof(int32_t) * (static_cast<size_t>(warps) * (G | 1) + 4 * static_cast<size_t>(G) + 1); }
+size_t smem_bytes(int G, int warps) { return sizeof(int32_t) * (static_cast<size_t>(warps) * G + 4 * static_cast<size_t>(G) + 1); }
 
 struct RouteLaunch {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  RouteLaunch(int ctas, int threads, size_t smem, cudaStream_t stream, bool pdl) {
+  RouteLaunch(int ctas, int clusters, int threads, size_t smem, cudaStream_t stream, bool pdl) {
     std::memset(&cfg, 0, sizeof(cfg));
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
@@ -212,7 +229,7 @@ struct RouteLaunch {
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas * clusters), 1, 1);
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -221,37 +238,46 @@ struct RouteLaunch {
   }
 };
 
+// The largest cluster that the device fits, and how many of kMaxCluster CTAs side by side.
+struct Fit {
+  int ctas, clusters;
+};
+
 template <bool IDS64>
 int launch(const RouteArgs& a, cudaStream_t stream) {
   auto* fn = &route_kernel<IDS64>;
-  static PerDevice<int> most;                               // CTAs of the largest cluster that the device fits
+  static PerDevice<Fit> fits;
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= kMaxDevices) return set_error(2, "device id %d", dev);
-  const int* fit = nullptr;
-  const int r = most.get(dev, &fit, [&](int& v) {
+  const Fit* fit = nullptr;
+  const int r = fits.get(dev, &fit, [&](Fit& f) {
     const size_t smem = smem_bytes(kRouteMaxGroups, kMaxWarps);
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     int clusters = 0;
     if (e == cudaSuccess) {
-      RouteLaunch l(kMaxCluster, kMaxThreads, smem, nullptr, false);
+      RouteLaunch l(kMaxCluster, 1, kMaxThreads, smem, nullptr, false);
       e = cudaOccupancyMaxActiveClusters(&clusters, fn, &l.cfg);
     }
     if (e != cudaSuccess) return set_error(4, "route set-up: %s", cudaGetErrorString(e));
-    v = clusters > 0 ? kMaxCluster : kPortableCluster;
+    f.ctas = clusters > 0 ? kMaxCluster : kPortableCluster;
+    f.clusters = clusters;
     return 0;
   });
   if (r) return r;
-  // one CTA where entries and rows are few, else a cluster.  One against eight: 3.1 and 3.8 us at
-  // 1 x 8 ids of 32 groups (1024 rows), 3.3 and 4.1 at 331 x 2 of 8 (1536 rows), 4.6 and 4.0 at
-  // 64 x 8 of 32 (4480 rows).  Eight against sixteen: 15.0 and 9.9 us at 8192 x 8.
-  int threads = a.n < kMaxThreads ? (a.n + 31) / 32 * 32 : kMaxThreads;
-  if (threads < a.G) threads = (a.G + 31) / 32 * 32;
-  if (threads < 256) threads = 256;
-  const int ctas = static_cast<long long>(a.n) + a.M <= 4096 ? 1 : a.n <= 8192 ? kPortableCluster : *fit;
-  RouteLaunch l(ctas, threads, smem_bytes(a.G, threads / 32), stream, pdl_enabled());
-  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, fn, a);
+  // CTAs that share the counting, and groups of them.  One CTA (sixteen times where there are more
+  // rows than it fills at once), eight eight times and sixteen four times, in us: 3.3, 3.5 and 3.9
+  // at 64 x 8 ids of 32 groups, 5.2, 3.7 and 4.9 at 512 x 8, 5.0 and 4.9 (the last two) at
+  // 2048 x 8, 8.8 and 7.1 at 8192 x 8, 26.8 and 21.1 at 32768 x 8 of 256.  Eight times sixteen
+  // CTAs are more than fit side by side: 11.7 at 8192 x 8.
+  const int ctas = a.n <= 512 ? 1 : a.n <= 16384 ? kPortableCluster : fit->ctas;
+  const int clusters = ctas == 1 ? (static_cast<long long>(a.n) + a.M <= 4096 ? 1 : 16) : ctas == kMaxCluster ? (fit->clusters < 4 ? fit->clusters : 4) : 8;
+  // a thread for each entry of a CTA, and for each group
+  const long long least = a.G > 256 ? a.G : 256, each = (static_cast<long long>(a.n) + ctas - 1) / ctas, want = each > least ? each : least;
+  const int threads = want < kMaxThreads ? static_cast<int>((want + 31) / 32 * 32) : kMaxThreads;
+  RouteLaunch l(ctas, clusters, threads, smem_bytes(a.G, threads / 32), stream, pdl_enabled());
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, fn, a, ctas);
   return e == cudaSuccess ? 0 : set_error(4, "route launch: %s", cudaGetErrorString(e));
 }
 
