@@ -447,14 +447,28 @@ struct WideCfg {
   static constexpr int NB = 64;                             // rows of B in a block
   static constexpr int NSTAGE = KB * NB * 128, BSTAGE = kWideRows * NB * 2;    // a block of B, of base
   static constexpr int PART = (kWideRows * LDP * 4 + 1023) / 1024 * 1024;
-  // [part, then stages of base | stages of B], over the stages of X and A; then the two parts of P
-  static constexpr int OFF_B = PART > kStages * BSTAGE ? PART : kStages * BSTAGE;
-  static constexpr int FRONT = kStages * KSTAGE > OFF_B + kStages * NSTAGE ? kStages * KSTAGE : OFF_B + kStages * NSTAGE;
+  // stages of base, the sums over the later ones of them, stages of B, the two parts of P; the
+  // stages of X and A lie over all of it
+  static constexpr int EARLY = RP == 64 ? 1 : 2;            // stages of base before the sums
+  static constexpr int OFF_PART = EARLY * BSTAGE;
+  static constexpr int OFF_B = OFF_PART + PART > kStages * BSTAGE ? OFF_PART + PART : kStages * BSTAGE;
   static constexpr int PBYTES = KB * kWideRows * 128;
-  static constexpr int OFF_HI = FRONT, OFF_LO = OFF_HI + PBYTES, OFF_POWER = OFF_LO + PBYTES;
+  static constexpr int OFF_HI = OFF_B + kStages * NSTAGE, OFF_LO = OFF_HI + PBYTES, OFF_POWER = OFF_LO + PBYTES;
+  static constexpr int KSTAGES = OFF_POWER / KSTAGE;
   static constexpr int SMEM = OFF_POWER + kWideRows * 4 + 1024;   // the layout starts on 1024 bytes
+  static_assert(KSTAGES >= 3 && SMEM <= (RP <= 64 ? 112 : 224) * 1024, "shared memory of one or two CTAs");
   static constexpr int COL_D = 128;                         // TMEM: X A^T from column 0, two blocks of P B^T from here
   static constexpr int TMEM = 256;
+};
+
+// Stage and parity of the uses of a ring, one after the other.
+template <int STAGES>
+struct Ring {
+  int s = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == STAGES) s = 0, phase ^= 1u;
+  }
 };
 
 // Byte of 16-bit column `col` of row `row` in blocks of 64 columns, 128-byte swizzle.
@@ -480,27 +494,30 @@ __global__ void __launch_bounds__(kWideThreads, RP <= 64 ? 2 : 1) lora_f16_wide_
   extern __shared__ __align__(128) uint8_t raw[];
   __shared__ int tokens[kWideRows];                         // -1 where a row has none
   __shared__ float block_scale;
-  __shared__ uint64_t bars[4 * kStages + 5];
+  __shared__ uint64_t bars[2 * Cf::KSTAGES + 2 * kStages + 5];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t abort_word;
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const int C = static_cast<int>(gridDim.z), rank = static_cast<int>(blockIdx.z);
   uint8_t* smem = raw + ((1024u - (ptx::smem_u32(raw) & 1023u)) & 1023u);   // the same offset in every CTA
-  float* part = reinterpret_cast<float*>(smem);
+  float* part = reinterpret_cast<float*>(smem + Cf::OFF_PART);
   float* power = reinterpret_cast<float*>(smem + Cf::OFF_POWER);
   const uint32_t base_s = ptx::smem_u32(smem);
   auto bar = [&](int i) { return ptx::smem_u32(&bars[i]); };
+  constexpr int NBARS = 2 * Cf::KSTAGES, DBARS = NBARS + 2 * kStages;
   auto kfull = [&](int s) { return bar(s); };               // a stage of X and A has come, has been read
-  auto kfree = [&](int s) { return bar(kStages + s); };
-  auto nfull = [&](int s) { return bar(2 * kStages + s); }; // a stage of B and base
-  auto nfree = [&](int s) { return bar(3 * kStages + s); };
-  auto dfull = [&](int d) { return bar(4 * kStages + d); }; // a block of P B^T is in TMEM, has been taken out
-  auto dfree = [&](int d) { return bar(4 * kStages + 2 + d); };
-  const uint32_t kdone = bar(4 * kStages + 4);              // X A^T is in TMEM
+  auto kfree = [&](int s) { return bar(Cf::KSTAGES + s); };
+  auto nfull = [&](int s) { return bar(NBARS + s); };       // a stage of B and base
+  auto nfree = [&](int s) { return bar(NBARS + kStages + s); };
+  auto dfull = [&](int d) { return bar(DBARS + d); };       // a block of P B^T is in TMEM, has been taken out
+  auto dfree = [&](int d) { return bar(DBARS + 2 + d); };
+  const uint32_t kdone = bar(DBARS + 4);                    // X A^T is in TMEM
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < Cf::KSTAGES; ++s) {
       ptx::mbar_init(kfull(s), 1 + 32 * kCopyWarps);
       ptx::mbar_init(kfree(s), 1);
+    }
+    for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(nfull(s), 32 * kCopyWarps);
       ptx::mbar_init(nfree(s), 1 + kWarps / 2);
     }
@@ -545,15 +562,6 @@ __global__ void __launch_bounds__(kWideThreads, RP <= 64 ? 2 : 1) lora_f16_wide_
   const int ksteps = (a.K + 63) / 64, nblocks = (a.N + Cf::NB - 1) / Cf::NB;
   const int ks0 = static_cast<int>(static_cast<long long>(ksteps) * rank / C), ks1 = static_cast<int>(static_cast<long long>(ksteps) * (rank + 1) / C);
   const int nb0 = static_cast<int>(static_cast<long long>(nblocks) * rank / C), nb1 = static_cast<int>(static_cast<long long>(nblocks) * (rank + 1) / C);
-  // stage and parity of the i-th use of a ring
-  struct Ring {
-    int s = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next() {
-      if (++s == kStages) s = 0, phase ^= 1u;
-    }
-  };
-
   if (warp >= kWarps && warp < kWarps + kCopyWarps) {
     // ---------------------------------------------------------- copies
     ctl.role_bit = FGF8_DEVERR_ROLE_PRODUCER;
@@ -580,7 +588,7 @@ __global__ void __launch_bounds__(kWideThreads, RP <= 64 ? 2 : 1) lora_f16_wide_
     };
     rows_of(a.X, a.ldx);
     bool ok = true;
-    Ring r;
+    Ring<Cf::KSTAGES> r;
     for (int ks = ks0; ks < ks1; ++ks) {
       ok = pwait(kfree(r.s), r.phase ^ 1u, ctl);
       if (!ok) break;
@@ -608,19 +616,24 @@ __global__ void __launch_bounds__(kWideThreads, RP <= 64 ? 2 : 1) lora_f16_wide_
     };
     for (int s = 0; ok && s < kStages && nb0 + s < nb1; ++s) load_b(nb0 + s, s);
     rows_of(a.base, a.ldb);
+    Ring<kStages> n;
+    auto load_base = [&](int nb) {
+      if (a.base != nullptr) copy_rows(base_s + static_cast<uint32_t>(n.s * Cf::BSTAGE), nb * Cf::NB, a.N);
+      cp_arrive(nfull(n.s));
+      n.next();
+    };
+    int nb = nb0;
+    for (; ok && nb < nb1 && nb < nb0 + Cf::EARLY; ++nb) load_base(nb);
     __syncwarp();
     cluster_sync_all();
     cluster_sync_all();
-    Ring n;
-    for (int nb = nb0; ok && nb < nb1; ++nb) {
+    for (; ok && nb < nb1; ++nb) {
       if (nb >= nb0 + kStages) {
         ok = pwait(nfree(n.s), n.phase ^ 1u, ctl);
         if (!ok) break;
         load_b(nb, n.s);
       }
-      if (a.base != nullptr) copy_rows(base_s + static_cast<uint32_t>(n.s * Cf::BSTAGE), nb * Cf::NB, a.N);
-      cp_arrive(nfull(n.s));
-      n.next();
+      load_base(nb);
     }
     gemv::cp_commit();
     gemv::cp_wait<0>();
@@ -629,7 +642,7 @@ __global__ void __launch_bounds__(kWideThreads, RP <= 64 ? 2 : 1) lora_f16_wide_
     // ---------------------------------------------------------- MMAs
     ctl.role_bit = FGF8_DEVERR_ROLE_MMA;
     bool ok = true;
-    Ring r;
+    Ring<Cf::KSTAGES> r;
     for (int ks = ks0; ks < ks1; ++ks) {
       ok = pwait(kfull(r.s), r.phase, ctl);
       if (!ok) break;
@@ -652,7 +665,7 @@ __global__ void __launch_bounds__(kWideThreads, RP <= 64 ? 2 : 1) lora_f16_wide_
     cluster_sync_all();
     cluster_sync_all();
     fence_proxy_async_all();                                // P is read by the tensor core
-    Ring n;
+    Ring<kStages> n;
     for (int nb = nb0; ok && nb < nb1; ++nb) {
       const int d = (nb - nb0) & 1;
       ok = pwait(nfull(n.s), n.phase, ctl) && (nb < nb0 + 2 || pwait(dfree(d), (static_cast<uint32_t>(nb - nb0 - 2) >> 1) & 1u, ctl));
@@ -711,7 +724,7 @@ __global__ void __launch_bounds__(kWideThreads, RP <= 64 ? 2 : 1) lora_f16_wide_
     int token[8];                                           // of rows 4 i + lane / 8, of which this lane stores 16 bytes
 #pragma unroll
     for (int i = 0; i < 8; ++i) token[i] = tokens[32 * (warp & 3) + 4 * i + (lane >> 3)];
-    Ring n;
+    Ring<kStages> n;
     if (half == 1) n.next();
     for (int nb = nb0 + half; ok && nb < nb1; nb += 2) {
       const int d = half;
