@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_kernel(Lo
 // The same two products for blocks of 128 rows with one adapter, on tcgen05: a byte of A or B
 // serves 128 tokens, and the multiplications (2 r of them, with P in two parts 3 r, for each
 // element of X, base and out) are off the warps' hands.
-//   X A^T  [128 x r] in TMEM, K in steps of 64 through a ring of kStages: the tokens' rows of X
+//   X A^T  [128 x r] in TMEM, K in steps of 64 through a ring of KSTAGES: the tokens' rows of X
 //          by cp.async from four warps, a tile of A by TMA.  (TMA's tile::gather4 takes some 80
 //          cycles for four rows of 128 bytes: 137 us for the calls below, whatever the rank.)
 //   P      over the cluster as above, written as two more operands.
@@ -434,8 +434,10 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_kernel(Lo
 // All operands are K-major with 128-byte swizzle, rows of 64 columns.  Warps that copy, multiply
 // and add wait for one another on mbarriers only: with a block-wide barrier for each step the
 // same work took 86 us, and a third of that went to threads whose proxy fence waited for their
-// own copies.  8192 tokens of 8 adapters, 7168 x 7168: 66 us at rank 16, 73 at 64 (5.1 TB/s),
-// 100 at 128, where one CTA fills the SM; the bytes alone take 54 to 57.
+// own copies.  8192 tokens of 8 adapters, 7168 x 7168: 64 us at rank 16, 72 at 64 (5.1 TB/s),
+// 95 at 128, where one CTA fills the SM; the bytes alone take 54 to 57.  At rank 64 X A^T is done
+// after 28 us and P after 34, and the rest streams at 7 TB/s.  No gain from columns dealt to the
+// cluster's CTAs in turn, nor from asking base into L2 while P is exchanged.
 constexpr int kStages = 3, kWideRows = 128, kCopyWarps = 4;
 constexpr int kWideThreads = kThreads + 32 * kCopyWarps + 32;   // sums and adding, copies, MMAs
 
