@@ -164,28 +164,34 @@ __device__ __forceinline__ void exchange_rows(const float* part, float* power, i
 
 // Rows of tokens without an adapter: base, or zeros.  An item is 2 KB of 32 tokens; every warp
 // of the grid takes its share when its other work is done, and looks at the tokens of its
-// first item as it starts.  In place there is nothing to do.
+// first item as it starts.  A row out of range is reported and counts as none.  In place the
+// tokens are looked at for that alone.
 struct Others {
   const LoraArgs& a;
+  const bool in_place;
   const uint32_t worker, workers, parts, items;
   bool first;
   static constexpr int kPart = 4;
 
   __device__ __forceinline__ Others(const LoraArgs& args, uint32_t w, uint32_t n)
-      : a(args), worker(w), workers(n), parts((static_cast<uint32_t>(args.N) / 8 + 32 * kPart - 1) / (32 * kPart)),
-        items(args.base == args.out || n == 0u ? 0u : (static_cast<uint32_t>(args.T) + 31) / 32 * parts) {
+      : a(args), in_place(args.base == args.out), worker(w), workers(n),
+        parts(in_place ? 1u : (static_cast<uint32_t>(args.N) / 8 + 32 * kPart - 1) / (32 * kPart)),
+        items(n == 0u ? 0u : (static_cast<uint32_t>(args.T) + 31) / 32 * parts) {
     first = worker < items && look(worker);
   }
   // whether this lane's token of an item is one
   __device__ __forceinline__ bool look(uint32_t it) const {
     const uint32_t t = it / parts * 32 + (threadIdx.x & 31);
-    return t < static_cast<uint32_t>(a.T) && ptx::ld_global(a.rows + t) < 0;
+    if (t >= static_cast<uint32_t>(a.T)) return false;
+    const int row = ptx::ld_global(a.rows + t);
+    if (row < -1 || row >= a.M) atomicOr(a.status, FGF8_DEVERR_INPUT);
+    return row < 0 || row >= a.M;
   }
   __device__ __forceinline__ void fill() const {
     const int lane = static_cast<int>(threadIdx.x & 31), vecs = a.N / 8;
     for (uint32_t it = worker; it < items; it += workers) {
       const int v0 = static_cast<int>(it % parts) * 32 * kPart + lane;
-      for (uint32_t left = __ballot_sync(kFull, it == worker ? first : look(it)); left != 0; left &= left - 1) {
+      for (uint32_t left = __ballot_sync(kFull, (it == worker ? first : look(it)) && !in_place); left != 0; left &= left - 1) {
         const size_t t = static_cast<size_t>(it / parts) * 32 + __ffs(left) - 1;
         uint4 v[kPart] = {};
 #pragma unroll
@@ -232,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_kernel(Lo
   }
   int g = __shfl_sync(kFull, id, 0);
   // rows of another adapter, adapters and tokens out of range are reported and left alone
-  bool bad = id >= a.G || (id >= 0 && token >= 0 && (id != g || token >= a.T));
+  bool bad = id < -1 || token < -1 || id >= a.G || (id >= 0 && token >= 0 && (id != g || token >= a.T));
   if (g >= a.G) g = -1;
   if (bad || id < 0 || token < 0) token = -1;
   if (bad) atomicOr(a.status, FGF8_DEVERR_INPUT);
@@ -541,7 +547,7 @@ __global__ void __launch_bounds__(kWideThreads, RP <= 64 ? 2 : 1) lora_f16_wide_
   int g = ptx::ld_global(a.m_indices + row0);
   if (tid < kWideRows) {
     const int id = ptx::ld_global(a.m_indices + row0 + tid), t = ptx::ld_global(a.src + row0 + tid);
-    const bool bad = id >= a.G || (id >= 0 && t >= 0 && (id != g || t >= a.T));
+    const bool bad = id < -1 || t < -1 || id >= a.G || (id >= 0 && t >= 0 && (id != g || t >= a.T));
     tokens[tid] = bad || id < 0 ? -1 : t;                   // t is -1 where there is none
     if (bad) atomicOr(a.status, FGF8_DEVERR_INPUT);
   }

@@ -372,10 +372,11 @@ FGF8_API int dispatch_f16_backward(const void* dXs, const int32_t* rows, void* d
  *          this align, a multiple of 16; with a multiple of 128 the call can take blocks of
  *          128 rows, which pays from some thousand tokens on; a routing serves every layer of
  *          a step
- * Tokens without an adapter get base.  X, A, B, base and out are of one type (dtype).
+ * Tokens without an adapter get base, and so do those whose row is out of range, which sets
+ * FGF8_ERR_DEVICE_INPUT, in place too.  X, A, B, base and out are of one type (dtype).
  * The rows of a tile of 16, or of a block of 128 where the call takes those, have one adapter:
- * a row that names another one than the first, or one out of range, sets
- * FGF8_ERR_DEVICE_INPUT and is not computed.  Requires K, N, r, ldx, ldb, ldo multiples of
+ * a row that names another one than the first, or an adapter or a token out of range (below
+ * -1 as well), sets FGF8_ERR_DEVICE_INPUT and is not computed.  Requires K, N, r, ldx, ldb, ldo multiples of
  * 8, r <= 128, M % align == 0, M > 0 where there are tokens, and an out that overlaps no other
  * input than an identical base.
  */
