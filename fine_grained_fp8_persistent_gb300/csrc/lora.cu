@@ -75,10 +75,12 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
 // P from the sums over the shares of K, as value, rest and power.  With ALL every CTA of the
 // cluster sums all rows over `part` of all CTAs and keeps them; otherwise it sums every C-th row
 // and hands it to all of them.  place(row, column, value's address, rest's) says where two
-// columns go.  A row is summed by as many lanes as it has pairs of columns, up to 32.
+// columns go.  A row is summed by as many lanes as it has pairs of columns, up to 32.  Columns
+// from the rank on do not exist: they are zeros here, whatever stands in `part` (an infinity of X
+// by nothing is NaN there) and whatever the scale is.
 template <bool BF16, int RP, bool ALL, typename Place>
-__device__ __forceinline__ void exchange_rows(const float* part, float* power, int rows, const float* scale_at, int C, int rank,
-                                              Place&& place) {
+__device__ __forceinline__ void exchange_rows(const float* part, float* power, int rows, int columns, const float* scale_at, int C,
+                                              int rank, Place&& place) {
   constexpr int LDP = RP + 4, LANES = RP >= 64 ? 32 : RP / 2, PAIRS = RP / 2 / LANES, TOGETHER = 32 / LANES;
   constexpr int ROWS = ALL || RP == 16 ? 1 : RP == 128 ? 2 : 4;   // rows of a lane whose loads are in flight together
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31), at_lane = lane % LANES;
@@ -123,8 +125,12 @@ __device__ __forceinline__ void exchange_rows(const float* part, float* power, i
       float top = 0.0f, up = 1.0f;
 #pragma unroll
       for (int u = 0; u < PAIRS; ++u) {
-        v[m][u].x *= scale;
-        v[m][u].y *= scale;
+        if (2 * (at_lane + LANES * u) < columns) {
+          v[m][u].x *= scale;
+          v[m][u].y *= scale;
+        } else {
+          v[m][u] = make_float2(0.0f, 0.0f);
+        }
         if (!BF16) top = fmaxf(top, fmaxf(fabsf(v[m][u].x), fabsf(v[m][u].y)));
       }
       if (!BF16) {
@@ -348,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_f16_kernel(Lo
   if (kTwo) load_block(nb0 + warp + kWarps, odd);
   // every CTA sums all rows, and they meet once
   if (C > 1) cluster_sync_all(); else __syncthreads();
-  exchange_rows<BF16, RP, true>(part, power, 16, &tile_scale, C, rank, [&](int row, int col, uint32_t& at_h, uint32_t& at_l) {
+  exchange_rows<BF16, RP, true>(part, power, 16, a.r, &tile_scale, C, rank, [&](int row, int col, uint32_t& at_h, uint32_t& at_l) {
     at_h = ptx::smem_u32(hi + row * LDH + col);
     at_l = ptx::smem_u32(lo + row * LDH + col);
   });
@@ -712,16 +718,16 @@ __global__ void __launch_bounds__(kWideThreads, RP <= 64 ? 2 : 1) lora_f16_wide_
         ptx::tmem_wait_ld();
         ptx::reg_fence(v);
         float4* to = reinterpret_cast<float4*>(part + row * Cf::LDP + half * COLS + c);
-        // rank columns past r hold what the stage's last rows happened to be
+        // rank columns from r on hold what the stage's last rows happened to be
 #pragma unroll
         for (int i = 0; i < STEP / 4; ++i)
-          to[i] = ks1 > ks0 && half * COLS + c + 4 * i < a.r
+          to[i] = ks1 > ks0
                       ? make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]))
                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
     }
     cluster_sync_all();
-    exchange_rows<BF16, RP, false>(part, power, kWideRows, &block_scale, C, rank, [&](int r, int col, uint32_t& at_h, uint32_t& at_l) {
+    exchange_rows<BF16, RP, false>(part, power, kWideRows, a.r, &block_scale, C, rank, [&](int r, int col, uint32_t& at_h, uint32_t& at_l) {
       at_h = base_s + Cf::OFF_HI + swizzled(kWideRows, r, col);
       at_l = at_h + Cf::PBYTES;
     });

@@ -1,4 +1,5 @@
-"""GPU tests of lora_f16 at its edges: routings that name rows, adapters and tokens out of range."""
+"""GPU tests of lora_f16 at its edges: routings that name rows, adapters and tokens out of range,
+and infinite values."""
 import pytest
 import torch
 
@@ -80,4 +81,61 @@ def test_negative_adapters_and_tokens_are_reported(fg, dev, monkeypatch, align, 
     out = base.clone()
     fg.lora_f16(x, a, b, route._replace(m_indices=m), base=out, out=out)
     assert fg.check_status()[0] == fg.ERR_DEVICE_INPUT
+    assert fg.check_status()[0] == 0
+
+
+# ----------------------------------------------------------------- infinities
+def _lora_ieee(x, a, b, ids, scale, base):
+    """The definition term by term in 64 bits, infinities and NaN as IEEE arithmetic has them."""
+    x, a, b, base, ids = x.double().cpu(), a.double().cpu(), b.double().cpu(), base.double().cpu(), ids.long().cpu()
+    p = (x.unsqueeze(1) * a[ids]).sum(-1)
+    if scale is not None:
+        p = p * scale.double().cpu()[ids].unsqueeze(1)
+    return base + (p.unsqueeze(1) * b[ids]).sum(-1)
+
+
+def _same_kinds(out, want, bound_of):
+    """NaN and infinities where the definition has them, the rest within its bound."""
+    got = out.double().cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(want)), f"NaN: {int(torch.isnan(got).sum())}, the definition {int(torch.isnan(want).sum())}"
+    inf = torch.isinf(want)
+    assert torch.equal(got[inf], want[inf])
+    fine = torch.isfinite(want)
+    value, bound = (t.cpu()[fine] for t in bound_of)
+    assert ((got[fine] - value).abs() <= bound).all()
+
+
+# ranks that are not their padded size: columns of P from r on do not exist
+@pytest.mark.parametrize("align,rows", FORMS)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("r", [8, 16, 24, 40, 72])
+def test_infinite_x_or_scale(fg, dev, monkeypatch, r, dtype, align, rows):
+    """A token with an infinity, and an adapter with an infinite scale, give the infinities of the
+    definition: every term of a column has one sign."""
+    monkeypatch.setenv("FGF8_FORCE_TILE", f"1x{rows}")
+    T, G, K, N = 24, 2, 136, 72
+    x, a, b, base, ids = _inputs(T, G, K, N, r, dtype, dev)
+    route = fg.route_contiguous(ids, G, align)
+    t = 11
+    g = int(ids[t])
+    scale = torch.tensor([0.75, 0.75], device=dev)
+    columns = torch.where(torch.arange(N, device=dev) % 3 == 0, -1.0, 1.0).to(dtype)
+    b[g] = (b[g].abs() + 2.0 ** -10) * torch.sign(a[g, :, 5]) * columns.unsqueeze(1)
+    a[g, :, 5] += torch.sign(a[g, :, 5]) * 2.0 ** -10
+    bounds = ref.lora64(x, a, b, ids, scale, base)          # of the tokens that stay finite
+    far = x.clone()
+    far[t, 5] = float("inf")
+    want = _lora_ieee(far, a, b, ids, scale, base)
+    assert torch.isinf(want[t]).all() and torch.isfinite(want[torch.arange(T) != t]).all()
+    _same_kinds(fg.lora_f16(far, a, b, route, scale=scale, base=base), want, bounds)
+    # P of one sign per rank row: all tokens of the adapter see sgn(A) K times
+    x[ids == g] = x[ids == g].abs() + 0.5
+    a[g] = a[g].abs() + 2.0 ** -10
+    b[g] = (b[g].abs() + 2.0 ** -10) * columns.unsqueeze(1)
+    scale[g] = float("inf")
+    want = _lora_ieee(x, a, b, ids, scale, base)
+    mine = (ids == g).cpu()
+    assert torch.isinf(want[mine]).all() and torch.isfinite(want[~mine]).all()
+    bounds = ref.lora64(x, a, b, torch.where(ids == g, -1, ids), torch.ones_like(scale) * 0.75, base)
+    _same_kinds(fg.lora_f16(x, a, b, route, scale=scale, base=base), want, bounds)
     assert fg.check_status()[0] == 0
