@@ -363,6 +363,9 @@ FGF8_API int dispatch_f16_backward(const void* dXs, const int32_t* rows, void* d
  *   out[t] = base[t] + scale[g] (X[t] A_g^T) B_g^T,   g the adapter of token t
  * FP32 sums; X A^T is kept to 16 bits (bf16) or 22 bits (fp16) between the two products, and
  * out is rounded once.
+ * Infinities and NaN give what the formula gives, but for an infinity of B beside an element of
+ * X A^T too small for what is kept of it, which gives NaN: one below 2^-133 (bf16), or below
+ * 2^-39 of its token's largest (fp16).
  *   X : [T][K], rows ldx elements apart;  A : [G][r][K];  B : [G][N][r]
  *   scale : float [G], NULL = all ones
  *   base : [T][N], rows ldb apart, what the shared projection gave; NULL = zeros;

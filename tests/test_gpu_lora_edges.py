@@ -139,3 +139,54 @@ def test_infinite_x_or_scale(fg, dev, monkeypatch, r, dtype, align, rows):
     bounds = ref.lora64(x, a, b, torch.where(ids == g, -1, ids), torch.ones_like(scale) * 0.75, base)
     _same_kinds(fg.lora_f16(x, a, b, route, scale=scale, base=base), want, bounds)
     assert fg.check_status()[0] == 0
+
+
+@pytest.mark.parametrize("align,rows", FORMS)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("r", [8, 24, 64, 128])
+def test_infinite_weights(fg, dev, monkeypatch, r, dtype, align, rows):
+    """Infinities in B meet each element of P once, whatever parts P is kept in: an exact one has no
+    rest, others have one of the other sign.  An infinity in A makes one element of a row of P
+    infinite and leaves its others what they are."""
+    monkeypatch.setenv("FGF8_FORCE_TILE", f"1x{rows}")
+    T, G, K, N = 40, 2, 136, 136
+    x, a, b, base, ids = _inputs(T, G, K, N, r, dtype, dev)
+    ids[:20], ids[20:] = 0, 1
+    route = fg.route_contiguous(ids, G, align)
+    # exact P, among them zeros: tokens 0 .. 3 are one column of A times small whole numbers
+    x[:4] = 0.0
+    x[:4, 0] = torch.tensor([1.0, -2.0, 3.0, 0.0]).to(dtype).to(dev)
+    bounds = ref.lora64(x, a, b, ids, None, base)
+    far = b.clone()
+    far[0, 7, 3], far[0, 100, 0], far[1, 64, r - 1] = float("inf"), float("-inf"), float("inf")
+    want = _lora_ieee(x, a, far, ids, None, base)
+    assert int(torch.isinf(want).sum()) == 20 + 2 * 19 and torch.isnan(want[3, 7]) and torch.isnan(want[3, 100])
+    _same_kinds(fg.lora_f16(x, a, far, route, base=base), want, bounds)
+    # one infinite element of P beside large ones of the other sign
+    wide = a.clone()
+    wide[1] *= -1024.0
+    wide[1, 2, 9] = float("inf")
+    x[20:] = x[20:].abs() * 1024.0 + 1.0
+    b[1] = b[1].abs() + 2.0 ** -10
+    want = _lora_ieee(x, wide, b, ids, None, base)
+    assert torch.isinf(want[20:]).all() and torch.isfinite(want[:20]).all()
+    _same_kinds(fg.lora_f16(x, wide, b, route, base=base), want, bounds)
+    assert fg.check_status()[0] == 0
+
+
+def test_infinite_weights_in_place_and_without_a_base(fg, dev, monkeypatch):
+    T, G, K, N, r = 200, 3, 264, 200, 32
+    for dtype in TYPES:
+        x, a, b, base, ids = _inputs(T, G, K, N, r, dtype, dev)
+        b[1, 13, 4] = float("inf")
+        b[2, 190, 31] = float("nan")
+        zero = torch.zeros_like(base)
+        for align, rows in FORMS:
+            monkeypatch.setenv("FGF8_FORCE_TILE", f"1x{rows}")
+            route = fg.route_contiguous(ids, G, align)
+            finite = torch.nan_to_num(b, nan=0.0, posinf=0.0)
+            out = base.clone()
+            fg.lora_f16(x, a, b, route, base=out, out=out)
+            _same_kinds(out, _lora_ieee(x, a, b, ids, None, base), ref.lora64(x, a, finite, ids, None, base))
+            _same_kinds(fg.lora_f16(x, a, b, route), _lora_ieee(x, a, b, ids, None, zero), ref.lora64(x, a, finite, ids, None, zero))
+    assert fg.check_status()[0] == 0
