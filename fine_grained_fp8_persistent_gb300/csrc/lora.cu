@@ -863,11 +863,15 @@ int launch_tiles(const LoraArgs& a, cudaStream_t stream) {
   // A cluster's CTAs split K and N: eight, unless a warp's share of K falls below 32 columns or
   // the tiles' CTAs are a third more than run together (some tiles are empty).  Clusters that
   // share a tile's N, and each compute P, help up to 64 CTAs with 4 KB of B each.  Over 15
-  // shapes of 1 to 2000 tokens this is at most 7 % slower than the best of all splits.
+  // shapes of 1 to 2000 tokens this is at most 7 % slower than the best of all splits.  Empty
+  // tiles have CTAs too, so a layout of more than kMostCtas with these splits goes without: launching
+  // them is the time there, and their warps are counted in 32 bits.
   const long long tiles = used_tiles(a), slots = (RP <= 64 ? 2LL : 1LL) * device_sm_count(), bytes = 2LL * a.N * a.r;
   int cluster = kMaxCluster, parts = 1;
   while (cluster > 1 && (256 * cluster > a.K || 3 * tiles * cluster > 4 * slots)) cluster /= 2;
   while (2 * parts * cluster <= (a.N + 31) / 32 && 2 * parts * cluster * tiles <= 64 && bytes / (2 * parts * cluster) >= 4096) parts *= 2;
+  constexpr long long kMostCtas = 1 << 24;
+  if (a.M / 16 * parts > kMostCtas / cluster) cluster = parts = 1;
   LoraKArgs k;
   k.a = a;
   k.timeout_ns = 0;                                         // this form waits on no mbarrier

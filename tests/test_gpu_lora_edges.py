@@ -1,8 +1,9 @@
 """GPU tests of lora_f16 at its edges: routings that name rows, adapters and tokens out of range,
-and infinite values."""
+infinite values, layouts far larger than their tokens."""
 import pytest
 import torch
 
+import gated_reference
 import routed_reference as ref
 
 pytestmark = pytest.mark.gpu
@@ -189,4 +190,19 @@ def test_infinite_weights_in_place_and_without_a_base(fg, dev, monkeypatch):
             fg.lora_f16(x, a, b, route, base=out, out=out)
             _same_kinds(out, _lora_ieee(x, a, b, ids, None, base), ref.lora64(x, a, finite, ids, None, base))
             _same_kinds(fg.lora_f16(x, a, b, route), _lora_ieee(x, a, b, ids, None, zero), ref.lora64(x, a, finite, ids, None, zero))
+    assert fg.check_status()[0] == 0
+
+
+# ----------------------------------------------------------------- large layouts
+def test_a_layout_far_larger_than_its_tokens(fg, dev, monkeypatch):
+    """2^28 rows for two tokens: 2^24 tiles, whose warps would not be counted in 32 bits if each tile
+    had the 32 CTAs of a call with two."""
+    monkeypatch.setenv("FGF8_FORCE_TILE", "1x16")
+    T, G, K, N, r = 2, 1, 2048, 8192, 16
+    x, a, b, base, ids = _inputs(T, G, K, N, r, torch.bfloat16, dev)
+    ids[1] = -1
+    route = fg.route_contiguous(ids, G, 16, M=1 << 28)
+    out = fg.lora_f16(x, a, b, route, base=base, out=torch.full_like(base, 3.0))
+    gated_reference.close(out, *ref.lora64(x, a, b, ids, None, base))
+    assert torch.equal(out[1], base[1])
     assert fg.check_status()[0] == 0
