@@ -145,8 +145,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) route_kernel(RouteArgs a, int 
     }
   }
   if (S > 1) cluster_arrive();                              // behind this nothing remote is read
-  // first rows: an exclusive prefix sum of the padded counts, one group per thread
-  const int32_t padded = a.slots > 0 ? a.slots : (all + a.align - 1) / a.align * a.align;
+  // first rows: an exclusive prefix sum of the padded counts, one group per thread.  A padded
+  // count fits the M rows; a count plus a segment need not fit 32 bits.
+  const int32_t padded = a.slots > 0 ? a.slots : (all / a.align + (all % a.align != 0 ? 1 : 0)) * a.align;
   const int32_t held = a.slots > 0 && all > a.slots ? a.slots : all;
   int32_t scan = tid < G ? padded : 0;
 #pragma unroll

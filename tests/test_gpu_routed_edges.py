@@ -72,3 +72,20 @@ def test_infinities_and_nans_as_quantize_has_them(fg, dev, fmt):
     own = torch.nonzero(src >= 0).view(-1)
     assert torch.equal(xq[own], codes[src[own] // k])
     assert torch.equal(sfa[:, own].view(torch.int32), table[:, src[own] // k].view(torch.int32))
+
+
+# ----------------------------------------------------------------- routing
+def test_segments_of_two_thousand_million_rows(fg, dev):
+    """One group whose entries and segment together pass 2^31: its padded size does not."""
+    n, M = 2000, 0x7FFFFFFF - 1023
+    ids = torch.zeros(n, dtype=torch.int32, device=dev)
+    ids[7] = -1
+    r = fg.route_contiguous(ids, 1, align=M)
+    assert fg.route_rows(n, 1, 1, M) == M == r.src.shape[0]
+    assert r.starts.tolist() == [0, M] and r.counts.tolist() == [n - 1]
+    at = torch.nonzero(ids == 0).view(-1).int()
+    assert torch.equal(r.rows.view(-1)[at.long()], torch.arange(n - 1, device=dev, dtype=torch.int32)) and int(r.rows[7, 0]) == -1
+    assert torch.equal(r.src[: n - 1], at) and not r.m_indices[: n - 1].any()
+    for t in (r.src, r.m_indices):
+        for piece in t[n - 1:].split(1 << 28):
+            assert (piece == -1).all()
