@@ -192,6 +192,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2) route_kernel(RouteArgs a, int 
       if (id[u] >= 0 && earlier == 0) mine[id[u]] += __popc(same);
       __syncwarp();
       if (a.slots > 0 && id[u] >= 0) row = row < a.slots ? id[u] * a.slots + row : -1;
+      // ids that changed since they were counted (they must not) may leave the layout
+      if (row >= a.M) row = -1;
       if (i < end) {
         a.rows[i] = row;
         if (row >= 0) a.src[row] = i;

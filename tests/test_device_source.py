@@ -86,3 +86,14 @@ def test_kernels_that_start_early_read_coherently():
     assert checked >= 5
     ptx = _code(os.path.join(CSRC, "ptx.cuh"))
     assert ptx.count('asm volatile("ld.global.') == 3
+
+
+def test_rows_of_ids_read_twice_are_held_to_the_layout():
+    """The routing reads ids a second time to place them.  If they change in between, which a run
+    cannot show at will, counts and places disagree: a row goes through a look at M before it is
+    stored to, and is not negative there."""
+    code = _code(os.path.join(CSRC, "route.cu"))
+    store = re.search(r"if \(row >= 0\) a\.src\[row\] = i;", code)
+    assert store and code.count("a.src[row] = i") == 1
+    look = code.rfind("if (row >= a.M) row = -1;", 0, store.start())
+    assert look > 0 and not re.search(r"\brow = (?!-1;)", code[look + 1:store.start()].replace("a.rows[i] = row", ""))
