@@ -553,7 +553,6 @@ __global__ void __launch_bounds__(kWideThreads, RP <= 64 ? 2 : 1) lora_f16_wide_
   }
   if (warp == kWarps && lane == 0) ptx::prefetch_tmap(&map_a);
   ptx::griddep_wait();
-  ptx::griddep_launch_dependents();
 
   const Others others(a, cta_of_grid() * kWarps + warp, warp < kWarps ? gridDim.x * gridDim.y * gridDim.z * kWarps : 0u);
   // the block's adapter and tokens
@@ -576,6 +575,9 @@ __global__ void __launch_bounds__(kWideThreads, RP <= 64 ? 2 : 1) lora_f16_wide_
     ptx::tc_fence_before();
   }
   __syncthreads();
+  // Not before this CTA holds its tensor memory: the next kernel's CTAs take theirs before they
+  // wait for this grid, and one that fitted beside this CTA would hold what it waits for.
+  ptx::griddep_launch_dependents();
   ptx::tc_fence_after();
   const uint32_t tmem = *const_cast<volatile uint32_t*>(&tmem_slot);
   PairWaitCtl ctl{&abort_word, 0u, a.status, args.timeout_ns, 0u};

@@ -97,3 +97,16 @@ def test_rows_of_ids_read_twice_are_held_to_the_layout():
     assert store and code.count("a.src[row] = i") == 1
     look = code.rfind("if (row >= a.M) row = -1;", 0, store.start())
     assert look > 0 and not re.search(r"\brow = (?!-1;)", code[look + 1:store.start()].replace("a.rows[i] = row", ""))
+
+
+def test_tensor_memory_is_taken_before_the_next_kernel_may_start():
+    """A kernel that lets the next one start and only then takes tensor memory may find that the
+    next one's CTAs hold it while they wait for this kernel's end."""
+    checked = 0
+    for path in SOURCES:
+        for body in re.split(r"\b__global__\b", _code(path))[1:]:
+            takes, starts = re.search(r"\btc_alloc<", body), body.find("griddep_launch_dependents();")
+            if takes and starts >= 0:
+                assert takes.start() < starts, os.path.basename(path)
+                checked += 1
+    assert checked >= 2
