@@ -568,9 +568,17 @@ class Route(NamedTuple):
     slots: int = 0                    # rows of a group in the masked layout (Mmax), 0 in the contiguous one
 
 
+# Sizes are C ints: ctypes would cut a longer one down to its low half.  They are looked at or-ed,
+# because a call takes a few microseconds.
+_MOST = 0x7FFFFFFF
+
+
 def route_rows(T: int, k: int, G: int, align: int | None = None) -> int:
     """Rows of the contiguous layout that hold any split of T * k entries over G groups."""
-    return int(_lib.fgf8_route_rows(int(T), int(k), int(G), mk_alignment_for_contiguous() if align is None else int(align)))
+    sizes = int(T), int(k), int(G), mk_alignment_for_contiguous() if align is None else int(align)
+    if max(map(abs, sizes)) > _MOST:
+        raise ValueError(f"route_rows: sizes past 32 bits in {sizes}")
+    return int(_lib.fgf8_route_rows(*sizes))
 
 
 def _ids(ids: torch.Tensor) -> tuple[int, int, int]:
@@ -594,6 +602,8 @@ def route_contiguous(ids: torch.Tensor, G: int, align: int | None = None, M: int
     any multiple of 16).  M rows, by default route_rows(T, k, G, align), which hold any ids."""
     T, k, ids64 = _ids(ids)
     align = mk_alignment_for_contiguous() if align is None else int(align)
+    if T | k | abs(G) | abs(align) | abs(M or 0) > _MOST:
+        raise ValueError(f"route_contiguous: sizes past 32 bits in T={T} k={k} G={G} align={align} M={M}")
     if M is None:
         M = _lib.fgf8_route_rows(T, k, G, align)
     i32 = torch.int32
@@ -607,6 +617,8 @@ def route_masked(ids: torch.Tensor, G: int, Mmax: int, stream=None) -> Route:
     """Places of tokens in the layout of grouped_fp8_masked: group g owns rows g * Mmax and on;
     counts is its masked_m.  Entries past a group's Mmax rows get none."""
     T, k, ids64 = _ids(ids)
+    if T | k | abs(G) | abs(Mmax) > _MOST:
+        raise ValueError(f"route_masked: sizes past 32 bits in T={T} k={k} G={G} Mmax={Mmax}")
     i32 = torch.int32
     rows = _empty((T, k), i32, ids, stream)
     src, counts = _empty((max(G, 0) * max(Mmax, 0),), i32, ids, stream), _empty((max(G, 0),), i32, ids, stream)
@@ -614,15 +626,18 @@ def route_masked(ids: torch.Tensor, G: int, Mmax: int, stream=None) -> Route:
     return Route(rows, src, None, counts, None, 1, Mmax)
 
 
-def _entries(route: Route, T: int) -> tuple[int, int]:
-    """(k, M) of a routing of T tokens."""
+def _entries(route: Route, T: int, sizes: int) -> tuple[int, int]:
+    """(k, M) of a routing of T tokens.  `sizes`: the call's other sizes, or-ed."""
     rows, src = route.rows, route.src
     shape, i32 = rows.shape, torch.int32
     if len(shape) != 2 or shape[0] != T or rows.dtype is not i32:
         _need_i32(rows, (T, shape[-1] if shape else 1), "route.rows")
     if src.dim() != 1 or src.dtype is not i32:
         _need_i32(src, (src.numel(),), "route.src")
-    return shape[1], src.shape[0]
+    k, M = shape[1], src.shape[0]
+    if T | k | M | sizes > _MOST:
+        raise ValueError(f"sizes past 32 bits: {T} tokens, {k} entries each, {M} rows, or the rows' own")
+    return k, M
 
 
 def dispatch_f16(x: torch.Tensor, route: Route, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -630,7 +645,7 @@ def dispatch_f16(x: torch.Tensor, route: Route, out: torch.Tensor | None = None,
     rows without an entry are zeros, in the masked one they are not written."""
     T, K = x.shape
     _dtype16(x, "x")
-    k, M = _entries(route, T)
+    k, M = _entries(route, T, K)
     if out is None:
         out = _empty((M, K), x.dtype, x, stream)
     else:
@@ -648,7 +663,7 @@ def dispatch_fp8(x: torch.Tensor, route: Route, fmt, xq: torch.Tensor | None = N
     T, K = x.shape
     if x.dtype is not torch.bfloat16:
         raise ValueError("x must be bf16")
-    k, M = _entries(route, T)
+    k, M = _entries(route, T, K)
     f, slots = _fmt(fmt), route.slots
     G = M // slots if slots else 1
     shape, dt = sfa_shape(slots or M, K, f)
@@ -680,7 +695,7 @@ def combine_f16(ys: torch.Tensor, w: torch.Tensor | None, route: Route, out: tor
     """Y (T, N) with Y[t] = sum_j w[t, j] Ys[rows[t, j]] for fp16/bf16 Ys (M, N) and float32
     w (T, k) (None: all ones), summed in FP32.  Entries without a row add nothing."""
     code, T = _dtype16(ys, "ys"), route.rows.shape[0]
-    k, M = _entries(route, T)
+    k, M = _entries(route, T, ys.shape[-1])
     N = _rows_of(ys, M, None, "ys")
     if w is not None:
         _need_weights(w, (T, k), "w")
@@ -698,7 +713,7 @@ def combine_f16_backward(dy: torch.Tensor, ys: torch.Tensor, w: torch.Tensor, ro
     rows of dYs without an entry are zeros, in the masked one they are not written."""
     T, N = dy.shape
     code = _dtype16(dy, "dy")
-    k, M = _entries(route, T)
+    k, M = _entries(route, T, N)
     if _rows_of(ys, M, dy.dtype, "ys") != N:
         raise ValueError(f"ys: expected rows of {N}, got {tuple(ys.shape)}")
     _need_weights(w, (T, k), "w")
@@ -718,7 +733,7 @@ def dispatch_f16_backward(dxs: torch.Tensor, route: Route, out: torch.Tensor | N
     """Gradient dX (T, K) of dispatch_f16 (of dispatch_fp8 with the quantization passed straight
     through) from dXs (M, K): dX[t] = sum_j dXs[rows[t, j]], summed in FP32."""
     code, T = _dtype16(dxs, "dxs"), route.rows.shape[0]
-    k, M = _entries(route, T)
+    k, M = _entries(route, T, dxs.shape[-1])
     K = _rows_of(dxs, M, None, "dxs")
     if out is None:
         out = _empty((T, K), dxs.dtype, dxs, stream)
@@ -758,7 +773,7 @@ def lora_f16(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, route: Route, sc
     ldx = _need_strided(x, (T, K), dtype, "x")
     _need_like(a, (G, r, K), dtype, "a")
     _need_like(b, (G, N, r), dtype, "b")
-    k, M = _entries(route, T)
+    k, M = _entries(route, T, K | N | G | r)
     if k != 1 or route.slots:
         raise ValueError("route: expected a route_contiguous of one adapter per token")
     if route.align % 16:
