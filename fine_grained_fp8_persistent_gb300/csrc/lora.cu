@@ -836,32 +836,20 @@ struct LoraLaunch {
   }
 };
 
-// Clusters of 1, 2, 4 and 8 CTAs that run on the device together.
-struct Fit {
-  int clusters[4];
-};
-template <typename K>
-int find_fit(K* fn, PerDevice<Fit>& fits, int threads, int smem, const Fit** out) {
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= kMaxDevices) return set_error(2, "device id %d", dev);
-  return fits.get(dev, out, [&](Fit& f) {
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    for (int i = 0; e == cudaSuccess && i < 4; ++i) {
-      LoraLaunch l(device_sm_count(), 1, 1 << i, threads, smem, nullptr, false);
-      e = cudaOccupancyMaxActiveClusters(&f.clusters[i], fn, &l.cfg);
-      if (e == cudaSuccess && f.clusters[i] <= 0) e = cudaErrorInvalidConfiguration;
-    }
-    return e == cudaSuccess ? 0 : set_error(4, "lora_f16 set-up: %s", cudaGetErrorString(e));
-  });
-}
-
 template <bool BF16, int RP>
 int launch_tiles(const LoraArgs& a, cudaStream_t stream) {
   auto* fn = &lora_f16_kernel<BF16, RP>;
-  static PerDevice<Fit> fits;
-  const Fit* fit = nullptr;
-  if (const int r = find_fit(fn, fits, kThreads, kTileSmem<RP>, &fit)) return r;
+  static PerDevice<int> ready;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= kMaxDevices) return set_error(2, "device id %d", dev);
+  const int* set = nullptr;
+  const int r = ready.get(dev, &set, [&](int& v) {
+    v = kTileSmem<RP>;
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v);
+    return e == cudaSuccess ? 0 : set_error(4, "lora_f16 set-up: %s", cudaGetErrorString(e));
+  });
+  if (r) return r;
   // A cluster's CTAs split K and N: eight, unless a warp's share of K falls below 32 columns or
   // the tiles' CTAs are a third more than run together (some tiles are empty).  Clusters that
   // share a tile's N, and each compute P, help up to 64 CTAs with 4 KB of B each.  Over 15
@@ -881,6 +869,26 @@ int launch_tiles(const LoraArgs& a, cudaStream_t stream) {
   LoraLaunch l(a.M / 16, parts, cluster, kThreads, kTileSmem<RP>, stream, pdl_enabled());
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, fn, k);
   return e == cudaSuccess ? 0 : set_error(4, "lora_f16 launch: %s", cudaGetErrorString(e));
+}
+
+// Clusters of 1, 2, 4 and 8 CTAs that run on the device together.
+struct Fit {
+  int clusters[4];
+};
+template <typename K>
+int find_fit(K* fn, PerDevice<Fit>& fits, int threads, int smem, const Fit** out) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= kMaxDevices) return set_error(2, "device id %d", dev);
+  return fits.get(dev, out, [&](Fit& f) {
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    for (int i = 0; e == cudaSuccess && i < 4; ++i) {
+      LoraLaunch l(device_sm_count(), 1, 1 << i, threads, smem, nullptr, false);
+      e = cudaOccupancyMaxActiveClusters(&f.clusters[i], fn, &l.cfg);
+      if (e == cudaSuccess && f.clusters[i] <= 0) e = cudaErrorInvalidConfiguration;
+    }
+    return e == cudaSuccess ? 0 : set_error(4, "lora_f16 set-up: %s", cudaGetErrorString(e));
+  });
 }
 
 template <bool BF16, int RP>
