@@ -31,8 +31,8 @@ def _same(route, want, what=""):
 
 
 # ----------------------------------------------------------------- routing
-# no tokens, one, lists on both sides of the one-CTA form (4096 entries), more groups than
-# entries, every group of 1024, ids that fill no step of 32
+# no tokens, one, lists of each form (test_gpu_routed_edges.py stands on their borders), more groups
+# than entries, every group of 1024, ids that fill no step of 32
 ROUTES = [(0, 1, 4), (1, 1, 1), (1, 8, 8), (5, 3, 7), (33, 2, 5), (1000, 1, 1), (4096, 1, 64), (4097, 1, 3), (512, 8, 256),
           (513, 8, 256), (700, 9, 1000), (20000, 4, 1024), (3, 40, 6)]
 

@@ -89,3 +89,31 @@ def test_segments_of_two_thousand_million_rows(fg, dev):
     for t in (r.src, r.m_indices):
         for piece in t[n - 1:].split(1 << 28):
             assert (piece == -1).all()
+
+
+# Lists of up to 512 entries take one CTA (sixteen times where entries and rows are more than
+# 4096), up to 16384 eight of them in a cluster, longer ones sixteen.
+@pytest.mark.parametrize("n", [1, 5, 511, 512, 513, 3000, 16383, 16384, 16385])
+@pytest.mark.parametrize("G,align", [(7, 1), (32, 128), (1000, 16)])
+def test_lists_at_the_borders_of_the_forms(fg, dev, n, G, align):
+    ids = ref.random_ids(n, 1, G, n + G, 0.1, 0.2)
+    M = fg.route_rows(n, 1, G, align)
+    for rows in (M, M + (4096 + align - 1) // align * align):
+        r = fg.route_contiguous(ids.to(dev), G, align, M=rows)
+        for got, want, name in zip(r[:5], ref.route(ids.numpy(), G, align, rows), r._fields):
+            assert np.array_equal(got.cpu().numpy(), want), (rows, name)
+    assert fg.check_status()[0] == 0
+
+
+@pytest.mark.parametrize("T,k,G,Mmax", [(64, 8, 32, 256), (1, 8, 32, 256), (3, 1, 32, 256), (63, 8, 5, 1000), (64, 8, 32, 3)])
+def test_few_entries_for_many_slots(fg, dev, T, k, G, Mmax):
+    """A decode step: few entries, which sixteen CTAs count and place, some with fewer warps' shares
+    than there are CTAs."""
+    for absent in (0.0, 0.3, 1.0):
+        ids = ref.random_ids(T, k, G, T + k, absent, 0.1)
+        for given in (ids, ids.long()):
+            r = fg.route_masked(given.to(dev), G, Mmax)
+            want = ref.route(ids.numpy(), G, 1, G * Mmax, Mmax)
+            for got, w, name in ((r.rows, want[0], "rows"), (r.src, want[1], "src"), (r.counts, want[3], "counts")):
+                assert np.array_equal(got.cpu().numpy(), w), name
+    assert fg.check_status()[0] == 0
