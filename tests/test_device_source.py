@@ -110,3 +110,14 @@ def test_tensor_memory_is_taken_before_the_next_kernel_may_start():
                 assert takes.start() < starts, os.path.basename(path)
                 checked += 1
     assert checked >= 2
+
+
+def test_halves_of_the_cluster_barrier_converge_first():
+    """Both follow loops that lanes leave at different times, as the whole barrier does."""
+    seen = set()
+    for path in SOURCES:
+        for name, body in _functions(_code(path)):
+            if name in ("cluster_arrive", "cluster_wait"):
+                assert body.lstrip().startswith("__syncwarp();"), f"{os.path.basename(path)}: {name}"
+                seen.add(name)
+    assert len(seen) == 2
