@@ -33,3 +33,10 @@ def test_recorded_traffic_is_for_a_hash_of_the_right_form():
     assert len(sha) == 16 and int(sha, 16) >= 0
     assert set(b.NCU_TRAFFIC) == {"src_sha", "bytes_per_launch"}
     assert b.NCU_TRAFFIC["bytes_per_launch"] > 140_000_000     # at least the algorithmic 140.7 MB
+
+
+def test_recorded_traffic_is_of_these_sources():
+    """Else the bench prints no traffic: a change of the GEMM's sources takes a new capture with it,
+    by the command in profiles/gemm_mxf8_dense_4096x7168x7168.md."""
+    b = _bench()
+    assert b.NCU_TRAFFIC["src_sha"] == b._src_sha()
