@@ -853,7 +853,8 @@ int launch_tiles(const LoraArgs& a, cudaStream_t stream) {
   // A cluster's CTAs split K and N: eight, unless a warp's share of K falls below 32 columns or
   // the tiles' CTAs are a third more than run together (some tiles are empty).  Clusters that
   // share a tile's N, and each compute P, help up to 64 CTAs with 4 KB of B each.  Over 15
-  // shapes of 1 to 2000 tokens this is at most 7 % slower than the best of all splits.  Empty
+  // shapes of 1 to 2000 tokens this is within 4 % of the best of all splits at eleven and at most
+  // 15 % slower (7.8 us for 6.8, 24 tokens of 32 adapters, 2048 x 8192).  Empty
   // tiles have CTAs too, so a layout of more than kMostCtas with these splits goes without: launching
   // them is the time there, and their warps are counted in 32 bits.
   const long long tiles = used_tiles(a), slots = (RP <= 64 ? 2LL : 1LL) * device_sm_count(), bytes = 2LL * a.N * a.r;
@@ -934,9 +935,11 @@ int launch_wide(const LoraArgs& a, cudaStream_t stream) {
 // Blocks of 128 rows or tiles of 16, by the time each takes, in us.  Tiles: 5 and the bytes that
 // leave L2, at 8.2 TB/s: X, base and out once, A and B once for every 16 tokens.  Blocks: 17 for
 // the start, the exchange and the filling of the rings, and the bytes from memory at 6.3 TB/s, a
-// third less where one CTA fills an SM.  Against times of both forms at 48 shapes (4 to 8192
-// tokens of 4 to 64 adapters, rank 16 to 128) the choice is at most 14 % slower than the better
-// one; 4096 tokens of 32 adapters, 4096 x 4096: 26 and 33 us at rank 16, 49 and 41 at 64.
+// third less where one CTA fills an SM.  Against times of both forms at 108 shapes (4 to 8192
+// tokens of 4 and 32 adapters, 1024 x 1024 to 7168 x 7168, rank 16 to 128) the choice is the better
+// one at 99 and within 8 % of it at all but three, where it is 13, 21 and 42 % slower (34 us for 24,
+// 4096 tokens of 32 adapters, 1024 x 1024, rank 128); 4096 tokens of 32 adapters, 4096 x 4096: 29
+// and 35 us at rank 16, 51 and 43 at 64.
 // FGF8_FORCE_TILE=1x16 or 1x128 takes a form where the rows allow it.
 bool wide_form(const LoraArgs& a) {
   // the copy engine counts the rows of all adapters' A in 32 bits
