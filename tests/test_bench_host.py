@@ -36,7 +36,7 @@ def test_recorded_traffic_is_for_a_hash_of_the_right_form():
 
 
 def test_recorded_traffic_is_of_these_sources():
-    """Else the bench prints no traffic: a change of the GEMM's sources takes a new capture with it,
-    by the command in profiles/gemm_mxf8_dense_4096x7168x7168.md."""
+    """Else the bench prints no traffic: a change of the GEMM's sources takes a new capture with it, by
+    the command that stands with the last one in profiles/."""
     b = _bench()
     assert b.NCU_TRAFFIC["src_sha"] == b._src_sha()
